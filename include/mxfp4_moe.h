@@ -304,6 +304,95 @@ int mxfp4_moe_dequant(const uint8_t* packed, const uint8_t* scale, int rows, int
 int mxfp4_moe_dequant_form(const uint8_t* packed, const uint8_t* scale, int rows, int cols,
                            int form, void* out, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Operators around the layer. They follow the conventions above: device
+ * pointers, contiguous rows, host checks before anything is enqueued, no
+ * allocation and no synchronisation, bit-identical repeats. The pages have no
+ * counterpart of them.
+ * ------------------------------------------------------------------------- */
+
+/* Residual addition and root-mean-square norm, with an MXFP8 output. Per row t:
+ *   h = x + residual (fp32)            residual_out = bf16(h)
+ *   y = h * rsqrt(mean(h^2) + eps) * gamma (fp32, from the unrounded h)
+ *   out = bf16(y)
+ *   out8, scale8: MXFP8 of y: per 32 values along the row X = floor(log2(amax)) - 8,
+ *     clamped to [-127, 127], scale byte X + 127, code = E4M3(y / 2^X), nearest
+ *     even, saturating at 448; an all-zero block has scale byte 0, a block with
+ *     a NaN or infinite value byte 255 and codes 0.
+ *     rule 0 = OCP (amax / 2^X lies in [256, 512): values above 448 saturate),
+ *     rule 1 = "nosat": X raised by one when amax / 2^X > 448.
+ *   x            bf16  [T, K]
+ *   residual     bf16  [T, K] or NULL (h = x)
+ *   gamma        bf16  [K]
+ *   residual_out bf16  [T, K] or NULL; may be the same pointer as x or residual
+ *   out          bf16  [T, K] or NULL
+ *   out8         uint8 [T, K] (E4M3) or NULL; scale8 uint8 [T, K/32], both or neither
+ * At least one of out, out8 and residual_out is needed. Limits
+ * (MXFP4_MOE_ERR_SHAPE): 0 <= T, K % 32 == 0, 32 <= K <= 16384. eps finite and
+ * >= 0, rule 0 or 1 (MXFP4_MOE_ERR_ARG). All pointers but scale8 16-byte
+ * aligned (MXFP4_MOE_ERR_ALIGN). T == 0 enqueues nothing. */
+int mxfp4_moe_add_rmsnorm(const void* x, const void* residual, const void* gamma, int T, int K,
+                          float eps, int rule, void* residual_out, void* out, uint8_t* out8,
+                          uint8_t* scale8, void* stream);
+
+/* Router in the score domain (mxfp4_moe_router adds its bias to the logits; a
+ * bias on the scores orders the experts differently). Per token:
+ *   s_e = softmax over all E logits (scoring 0) or sigmoid(logit) (scoring 1)
+ *   c_e = s_e + bias[e]     (bias NULL: the logits decide the choice, which
+ *                            order as the scores do)
+ *   n_group > 1: a group (equal runs of consecutive experts) scores the sum of
+ *     its group_top (1 or 2) largest c; the topk_group best groups stay, ties
+ *     to the lower group
+ *   topk_ids[t]      the k largest c of the groups that stay, in descending
+ *                    order, ties to the lower expert
+ *   topk_weights[t]  s of the chosen (not c), divided by their sum when
+ *                    renormalise is 1, times route_scale; fp32
+ * An expert whose logit or c is NaN or -inf is never chosen; a slot with no
+ * expert left gets id -1 (padding for the forward calls) and weight 0.
+ *   logits fp32 [T, E], bias fp32 [E] or NULL, topk_ids int32 [T, k],
+ *   topk_weights fp32 [T, k]; 4-byte aligned (MXFP4_MOE_ERR_ALIGN)
+ * Limits (MXFP4_MOE_ERR_SHAPE): 1 <= E <= 1024, 1 <= k <= min(32, E), 0 <= T,
+ * 1 <= n_group <= 32, E % n_group == 0, 1 <= topk_group <= n_group,
+ * k <= topk_group * E / n_group. scoring 0 or 1, group_top 1 or 2, renormalise
+ * 0 or 1, route_scale finite (MXFP4_MOE_ERR_ARG). T == 0 enqueues nothing. */
+int mxfp4_moe_router_scored(const float* logits, const float* bias, int T, int E, int topk,
+                            int scoring, int n_group, int topk_group, int group_top,
+                            int renormalise, float route_scale, int32_t* topk_ids,
+                            float* topk_weights, void* stream);
+
+/* A shared projection from packed MXFP4 weights, with the low-rank adapters of
+ * many requests beside it:
+ *   y_t = W x_t + adapter_scale[a] * B[a] (A[a] x_t),   a = adapter_ids[t]
+ * fp32 sums, one rounding to bf16 (the inner product of an adapter, scaled, is
+ * rounded to bf16 once on its way to the second).
+ *   x             bf16 [T, K] (x_scale NULL), or MXFP8 as mxfp4_moe_add_rmsnorm
+ *                 writes it: E4M3 uint8 [T, K] with x_scale E8M0 uint8 [T, K/32]
+ *   w / s         uint8 [N, K/2] / [N, K/32], the packed layout of one expert's w2
+ *   adapter_ids   int32 [T] or NULL (no adapters; the next four are ignored).
+ *                 A negative id: no adapter for this token; an id >= n_adapters:
+ *                 none either, counted in status[0]
+ *   adapter_a     bf16 [n_adapters, rank, K]
+ *   adapter_b     bf16 [n_adapters, N, rank] (adapters of a smaller rank: padded
+ *                 with zeros)
+ *   adapter_scale fp32 [n_adapters] or NULL (1)
+ *   out           bf16 [T, N], written completely
+ *   status        int32 [4] or NULL; status[1] = 0, status[2] and [3] as in the
+ *                 file header (status[2] bit 0: this call's bounded waits)
+ *   workspace     device scratch of mxfp4_moe_linear_workspace_size bytes, no
+ *                 initial contents required, not shared by calls that may run
+ *                 concurrently
+ * Limits (MXFP4_MOE_ERR_SHAPE): 0 <= T <= 2^20, K % 64 == 0, 64 <= K <= 16384,
+ * N % 8 == 0, 8 <= N <= 2^20, and with adapters rank % 8 == 0, 8 <= rank <= 256,
+ * 1 <= n_adapters <= 1024. Pointers 16-byte aligned but adapter_ids,
+ * adapter_scale and status (4 bytes) and the workspace (256 bytes)
+ * (MXFP4_MOE_ERR_ALIGN). T == 0 enqueues nothing. */
+size_t mxfp4_moe_linear_workspace_size(int T, int K, int N, int rank, int x_is_mxfp8);
+int mxfp4_moe_linear(const void* x, const uint8_t* x_scale, const uint8_t* w, const uint8_t* s,
+                     int T, int K, int N, const int32_t* adapter_ids, const void* adapter_a,
+                     const void* adapter_b, const float* adapter_scale, int n_adapters, int rank,
+                     void* out, int32_t* status, void* workspace, size_t workspace_bytes,
+                     void* stream);
+
 /* Profiling hook: when events (host array of n cudaEvent_t handles, n >= 2)
  * is non-NULL, each later forward call on this process records events[0]
  * before its first kernel and events[i] after its i-th kernel (while i < n),

@@ -4,12 +4,14 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
+#include <math.h>
 #include <mutex>
 #include <stdint.h>
 
 #include "../../include/mxfp4_moe.h"
 #include "common.cuh"
 #include "kernels.h"
+#include "ops.h"
 #include "prefill.h"
 
 namespace {
@@ -482,6 +484,135 @@ int mxfp4_moe_dequant_form(const uint8_t* packed, const uint8_t* scale, int rows
 int mxfp4_moe_dequant(const uint8_t* packed, const uint8_t* scale, int rows, int cols, void* out,
                       void* stream) {
   return mxfp4_moe_dequant_form(packed, scale, rows, cols, 1, out, stream);
+}
+
+int mxfp4_moe_add_rmsnorm(const void* x, const void* residual, const void* gamma, int T, int K,
+                          float eps, int rule, void* residual_out, void* out, uint8_t* out8,
+                          uint8_t* scale8, void* stream) {
+  if (T < 0 || K < 32 || K > 16384 || K % 32) return MXFP4_MOE_ERR_SHAPE;
+  if (!(eps >= 0.f) || isinf(eps) || (rule != 0 && rule != 1)) return MXFP4_MOE_ERR_ARG;
+  if (T == 0) return MXFP4_MOE_OK;
+  if ((out8 == nullptr) != (scale8 == nullptr)) return MXFP4_MOE_ERR_ARG;
+  if (out == nullptr && out8 == nullptr && residual_out == nullptr) return MXFP4_MOE_ERR_ARG;
+  if (!x || !gamma) return MXFP4_MOE_ERR_ARG;
+  if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(gamma, 16) ||
+      !aligned(residual_out, 16) || !aligned(out, 16) || !aligned(out8, 16))
+    return MXFP4_MOE_ERR_ALIGN;
+  DeviceInfo* d = nullptr;
+  if (int rc = current_device(&d)) return rc;
+  mxmoe::AddNormArgs a = {};
+  a.x = static_cast<const uint16_t*>(x);
+  a.residual = static_cast<const uint16_t*>(residual);
+  a.gamma = static_cast<const uint16_t*>(gamma);
+  a.residual_out = static_cast<uint16_t*>(residual_out);
+  a.out = static_cast<uint16_t*>(out);
+  a.q8 = out8;
+  a.s8 = scale8;
+  a.T = T;
+  a.K = K;
+  a.nosat = rule;
+  a.eps = eps;
+  return cuda_status(mxmoe::launch_add_rmsnorm(a, d->num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+int mxfp4_moe_router_scored(const float* logits, const float* bias, int T, int E, int topk,
+                            int scoring, int n_group, int topk_group, int group_top,
+                            int renormalise, float route_scale, int32_t* topk_ids,
+                            float* topk_weights, void* stream) {
+  if (T < 0 || E < 1 || E > kRouterMaxExperts || topk < 1 || topk > 32 || topk > E)
+    return MXFP4_MOE_ERR_SHAPE;
+  if (n_group < 1 || n_group > 32 || E % n_group || topk_group < 1 || topk_group > n_group ||
+      topk > topk_group * (E / n_group))
+    return MXFP4_MOE_ERR_SHAPE;
+  if ((scoring != 0 && scoring != 1) || (group_top != 1 && group_top != 2) ||
+      (renormalise != 0 && renormalise != 1) || isnan(route_scale) || isinf(route_scale))
+    return MXFP4_MOE_ERR_ARG;
+  if (T == 0) return MXFP4_MOE_OK;
+  if (!logits || !topk_ids || !topk_weights) return MXFP4_MOE_ERR_ARG;
+  if (!aligned(logits, 4) || !aligned(topk_ids, 4) || !aligned(topk_weights, 4) ||
+      !aligned(bias, 4))
+    return MXFP4_MOE_ERR_ALIGN;
+  DeviceInfo* d = nullptr;
+  if (int rc = current_device(&d)) return rc;
+  mxmoe::RouterScoredArgs a = {};
+  a.logits = logits;
+  a.bias = bias;
+  a.T = T;
+  a.E = E;
+  a.topk = topk;
+  a.scoring = scoring;
+  a.n_group = n_group;
+  a.topk_group = topk_group;
+  a.group_top = group_top;
+  a.renormalise = renormalise;
+  a.route_scale = route_scale;
+  a.ids = topk_ids;
+  a.wts = topk_weights;
+  return cuda_status(mxmoe::launch_router_scored(a, d->num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+constexpr int kLinearMaxDim = 1 << 20;   // tokens and output features
+bool linear_shape_ok(int T, int K, int N) {
+  return T >= 0 && T <= kLinearMaxDim && K >= 64 && K <= 16384 && K % 64 == 0 && N >= 8 &&
+         N <= kLinearMaxDim && N % 8 == 0;
+}
+bool linear_rank_ok(int rank) {
+  return rank >= 8 && rank <= mxmoe::kLinearMaxRank && rank % 8 == 0;
+}
+}  // namespace
+
+size_t mxfp4_moe_linear_workspace_size(int T, int K, int N, int rank, int x_is_mxfp8) {
+  if (!linear_shape_ok(T, K, N) || (rank != 0 && !linear_rank_ok(rank))) return 0;
+  return mxmoe::linear_workspace_bytes(T, K, N, rank, x_is_mxfp8 != 0);
+}
+
+int mxfp4_moe_linear(const void* x, const uint8_t* x_scale, const uint8_t* w, const uint8_t* s,
+                     int T, int K, int N, const int32_t* adapter_ids, const void* adapter_a,
+                     const void* adapter_b, const float* adapter_scale, int n_adapters, int rank,
+                     void* out, int32_t* status, void* workspace, size_t workspace_bytes,
+                     void* stream) {
+  const bool adapters = adapter_ids != nullptr;
+  if (!linear_shape_ok(T, K, N)) return MXFP4_MOE_ERR_SHAPE;
+  if (adapters &&
+      (!linear_rank_ok(rank) || n_adapters < 1 || n_adapters > mxmoe::kLinearMaxAdapters))
+    return MXFP4_MOE_ERR_SHAPE;
+  if (T == 0) return MXFP4_MOE_OK;
+  if (!x || !w || !s || !out || (adapters && (!adapter_a || !adapter_b))) return MXFP4_MOE_ERR_ARG;
+  if (!aligned(x, 16) || !aligned(x_scale, 16) || !aligned(w, 16) || !aligned(s, 16) ||
+      !aligned(out, 16) || !aligned(status, 4))
+    return MXFP4_MOE_ERR_ALIGN;
+  if (adapters && (!aligned(adapter_ids, 4) || !aligned(adapter_a, 16) || !aligned(adapter_b, 16) ||
+                   !aligned(adapter_scale, 4)))
+    return MXFP4_MOE_ERR_ALIGN;
+  const size_t need =
+      mxmoe::linear_workspace_bytes(T, K, N, adapters ? rank : 0, x_scale != nullptr);
+  if (need > 0) {
+    if (workspace == nullptr || workspace_bytes < need) return MXFP4_MOE_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return MXFP4_MOE_ERR_ALIGN;
+  }
+  DeviceInfo* d = nullptr;
+  if (int rc = current_device(&d)) return rc;
+  mxmoe::LinearArgs a = {};
+  a.x = x;
+  a.xs = x_scale;
+  a.w = w;
+  a.s = s;
+  a.T = T;
+  a.K = K;
+  a.N = N;
+  if (adapters) {
+    a.ids = adapter_ids;
+    a.a = static_cast<const uint16_t*>(adapter_a);
+    a.b = static_cast<const uint16_t*>(adapter_b);
+    a.ascale = adapter_scale;
+    a.L = n_adapters;
+    a.rank = rank;
+  }
+  a.out = static_cast<uint16_t*>(out);
+  a.status = status;
+  a.ws = workspace;
+  return cuda_status(mxmoe::launch_linear(a, d->num_sms, static_cast<cudaStream_t>(stream)));
 }
 
 void mxfp4_moe_set_phase_events(void* const* events, int n) {

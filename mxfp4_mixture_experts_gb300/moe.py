@@ -66,6 +66,17 @@ def lib() -> ctypes.CDLL:
     L.mxfp4_moe_dequant.restype = i32
     L.mxfp4_moe_dequant_form.argtypes = [vp, vp, i32, i32, i32, vp, vp]
     L.mxfp4_moe_dequant_form.restype = i32
+    f32 = ctypes.c_float
+    L.mxfp4_moe_add_rmsnorm.argtypes = [vp, vp, vp, i32, i32, f32, i32, vp, vp, vp, vp, vp]
+    L.mxfp4_moe_add_rmsnorm.restype = i32
+    L.mxfp4_moe_router_scored.argtypes = [vp, vp, i32, i32, i32, i32, i32, i32, i32, i32, f32,
+                                          vp, vp, vp]
+    L.mxfp4_moe_router_scored.restype = i32
+    L.mxfp4_moe_linear_workspace_size.argtypes = [i32] * 5
+    L.mxfp4_moe_linear_workspace_size.restype = sz
+    L.mxfp4_moe_linear.argtypes = [vp, vp, vp, vp, i32, i32, i32, vp, vp, vp, vp, i32, i32,
+                                   vp, vp, vp, sz, vp]
+    L.mxfp4_moe_linear.restype = i32
     L.mxfp4_moe_test_skip_grid_arrival.argtypes = [i32]
     L.mxfp4_moe_test_skip_grid_arrival.restype = None
     L.mxfp4_moe_test_decode_form.argtypes = [i32] * 6
@@ -372,6 +383,174 @@ def dequant(packed: torch.Tensor, scale: torch.Tensor, form: str = "decode",
                                       _ptr(out), _stream(stream))
     if rc:
         raise MoEError(rc, "mxfp4_moe_dequant_form")
+    return out
+
+
+MX8_RULES = {"ocp": 0, "nosat": 1}
+
+
+def add_rmsnorm(x: torch.Tensor, gamma: torch.Tensor, residual: Optional[torch.Tensor] = None,
+                eps: float = 1e-5, out8: Optional[str] = None, bf16: bool = True,
+                residual_out: Optional[torch.Tensor] = None,
+                out: Optional[torch.Tensor] = None, stream=None):
+    """h = x + residual, y = h * rsqrt(mean(h^2) + eps) * gamma for bf16 rows [T, K].
+
+    Returns (y bf16 or None, bf16(h), q8, s8): y unless bf16 is False; the new
+    residual stream (x itself when there is no residual; residual_out may be x
+    or residual); with out8 "ocp" or "nosat" y's MXFP8 form, E4M3 [T, K] and
+    E8M0 bytes [T, K/32] (the exponent floor(log2 amax) - 8, under "nosat"
+    raised by one where the block would saturate), else None."""
+    _need(x, "x", torch.bfloat16, 2)
+    _need(gamma, "gamma", torch.bfloat16, 1)
+    T, K = x.shape
+    if gamma.shape[0] != K:
+        raise ValueError("gamma must be [K]")
+    if out8 is not None and out8 not in MX8_RULES:
+        raise ValueError(f"out8 must be None or one of {sorted(MX8_RULES)}")
+    dev = x.device
+    if residual is not None:
+        _need(residual, "residual", torch.bfloat16, 2)
+        if residual.shape != x.shape:
+            raise ValueError("residual must be [T, K]")
+        if residual_out is None:
+            residual_out = torch.empty_like(x)
+    if residual_out is not None:
+        _need(residual_out, "residual_out", torch.bfloat16, 2)
+        if residual_out.shape != x.shape:
+            raise ValueError("residual_out must be [T, K]")
+    if not bf16:
+        if out is not None:
+            raise ValueError("out is not written when bf16 is False")
+    elif out is None:
+        out = torch.empty_like(x)
+    else:
+        _need(out, "out", torch.bfloat16, 2)
+        if out.shape != x.shape:
+            raise ValueError("out must be [T, K]")
+    q = s = None
+    if out8 is not None:
+        q = torch.empty(T, K, dtype=torch.float8_e4m3fn, device=dev)
+        s = torch.empty(T, K // 32, dtype=torch.uint8, device=dev)
+    rc = lib().mxfp4_moe_add_rmsnorm(_ptr(x), _ptr(residual), _ptr(gamma), T, K, eps,
+                                     MX8_RULES[out8 or "ocp"], _ptr(residual_out), _ptr(out),
+                                     _ptr(q), _ptr(s), _stream(stream))
+    if rc:
+        raise MoEError(rc, "mxfp4_moe_add_rmsnorm")
+    return out, (x if residual_out is None else residual_out), q, s
+
+
+SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def router_scored(logits: torch.Tensor, topk: int, scoring: str = "sigmoid",
+                  bias: Optional[torch.Tensor] = None, n_group: int = 1, topk_group: int = 1,
+                  group_top: int = 2, renormalise: bool = True, route_scale: float = 1.0,
+                  topk_ids: Optional[torch.Tensor] = None,
+                  topk_weights: Optional[torch.Tensor] = None, stream=None):
+    """Top-k experts by score: s = sigmoid(logits) or softmax over all experts
+    of fp32 logits [T, E], chosen by s + bias [E] (ties to the lower index)
+    among the topk_group groups with the largest sums of their group_top best;
+    weights from s alone, renormalised over the chosen or not, times
+    route_scale. Experts with a NaN or -inf logit are never chosen; a slot with
+    none left gets id -1 and weight 0. Returns int32 ids and fp32 weights [T, k]."""
+    _need(logits, "logits", torch.float32, 2)
+    T, E = logits.shape
+    if scoring not in SCORES:
+        raise ValueError(f"scoring must be one of {sorted(SCORES)}")
+    if bias is not None:
+        _need(bias, "bias", torch.float32, 1)
+        if bias.shape[0] != E:
+            raise ValueError("bias must be [E]")
+    for name, t, dtype in (("topk_ids", topk_ids, torch.int32),
+                           ("topk_weights", topk_weights, torch.float32)):
+        if t is not None:
+            _need(t, name, dtype, 2)
+            if tuple(t.shape) != (T, topk):
+                raise ValueError(f"{name} must be [T, topk]")
+    if topk_ids is None:
+        topk_ids = torch.empty(T, topk, dtype=torch.int32, device=logits.device)
+    if topk_weights is None:
+        topk_weights = torch.empty(T, topk, dtype=torch.float32, device=logits.device)
+    rc = lib().mxfp4_moe_router_scored(_ptr(logits), _ptr(bias), T, E, topk, SCORES[scoring],
+                                       n_group, topk_group, group_top, int(bool(renormalise)),
+                                       route_scale, _ptr(topk_ids), _ptr(topk_weights),
+                                       _stream(stream))
+    if rc:
+        raise MoEError(rc, "mxfp4_moe_router_scored")
+    return topk_ids, topk_weights
+
+
+def linear_workspace_size(T: int, K: int, N: int, rank: int = 0, x_is_mxfp8: bool = False) -> int:
+    """Bytes of scratch that ``linear`` needs (rank 0: no adapters); 0 also for sizes it does not take."""
+    return int(lib().mxfp4_moe_linear_workspace_size(T, K, N, rank, int(bool(x_is_mxfp8))))
+
+
+def linear(x: torch.Tensor, w: torch.Tensor, s: torch.Tensor,
+           x_scale: Optional[torch.Tensor] = None, adapter_ids: Optional[torch.Tensor] = None,
+           adapter_a: Optional[torch.Tensor] = None, adapter_b: Optional[torch.Tensor] = None,
+           adapter_scale: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+           workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+           stream=None) -> torch.Tensor:
+    """y[T, N] bf16 = W x_t + adapter_scale[a] * B[a] (A[a] x_t), a = adapter_ids[t].
+
+    W is packed MXFP4: w uint8 [N, K/2], s uint8 [N, K/32]. x is bf16 [T, K], or
+    float8_e4m3fn [T, K] with E8M0 bytes x_scale [T, K/32] (``add_rmsnorm``'s
+    out8). adapter_ids int32 [T] (negative: none for this token), adapter_a bf16
+    [L, rank, K], adapter_b bf16 [L, N, rank], adapter_scale fp32 [L] or None
+    (1); without adapter_ids the plain projection. status int32 [4]: [0] counts
+    the ids >= L (no adapter), [2] is non-zero when a bounded wait gave up."""
+    x8 = x_scale is not None
+    _need(x, "x", torch.float8_e4m3fn if x8 else torch.bfloat16, 2)
+    _need(w, "w", torch.uint8, 2)
+    _need(s, "s", torch.uint8, 2)
+    T, K = x.shape
+    N = w.shape[0]
+    if tuple(w.shape) != (N, K // 2) or tuple(s.shape) != (N, K // 32):
+        raise ValueError("w / s shapes must be [N, K/2] / [N, K/32]")
+    if x8:
+        _need(x_scale, "x_scale", torch.uint8, 2)
+        if tuple(x_scale.shape) != (T, K // 32):
+            raise ValueError("x_scale must be [T, K/32]")
+    n_ad = rank = 0
+    if adapter_ids is not None:
+        _need(adapter_ids, "adapter_ids", torch.int32, 1)
+        if adapter_a is None or adapter_b is None:
+            raise ValueError("adapter_ids need adapter_a and adapter_b")
+        _need(adapter_a, "adapter_a", torch.bfloat16, 3)
+        _need(adapter_b, "adapter_b", torch.bfloat16, 3)
+        n_ad, rank, _ = adapter_a.shape
+        if adapter_ids.shape[0] != T:
+            raise ValueError("adapter_ids must be [T]")
+        if adapter_a.shape[2] != K or tuple(adapter_b.shape) != (n_ad, N, rank):
+            raise ValueError("adapter_a / adapter_b must be [L, rank, K] / [L, N, rank]")
+        if adapter_scale is not None:
+            _need(adapter_scale, "adapter_scale", torch.float32, 1)
+            if adapter_scale.shape[0] != n_ad:
+                raise ValueError("adapter_scale must be [L]")
+    elif adapter_a is not None or adapter_b is not None or adapter_scale is not None:
+        raise ValueError("adapters need adapter_ids")
+    if out is None:
+        out = torch.empty(T, N, dtype=torch.bfloat16, device=x.device)
+    else:
+        _need(out, "out", torch.bfloat16, 2)
+        if tuple(out.shape) != (T, N):
+            raise ValueError("out must be [T, N]")
+    if status is not None:
+        _need(status, "status", torch.int32, 1)
+        if status.shape[0] < 4:
+            raise ValueError("status must be [4]")
+    L = lib()
+    if workspace is None:
+        workspace = torch.empty(L.mxfp4_moe_linear_workspace_size(T, K, N, rank, int(x8)),
+                                dtype=torch.uint8, device=x.device)
+    else:
+        _need(workspace, "workspace", torch.uint8, 1)
+    rc = L.mxfp4_moe_linear(_ptr(x), _ptr(x_scale), _ptr(w), _ptr(s), T, K, N, _ptr(adapter_ids),
+                            _ptr(adapter_a), _ptr(adapter_b), _ptr(adapter_scale), n_ad, rank,
+                            _ptr(out), _ptr(status), _ptr(workspace), workspace.numel(),
+                            _stream(stream))
+    if rc:
+        raise MoEError(rc, "mxfp4_moe_linear")
     return out
 
 
