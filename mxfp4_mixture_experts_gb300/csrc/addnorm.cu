@@ -16,8 +16,8 @@
 // once. The 4 threads of a 32-value block share its maximum by two shuffles.
 #include <cstdint>
 
-#include "common.cuh"
 #include "ops.h"
+#include "ops_common.cuh"
 
 namespace mxmoe {
 namespace {
@@ -26,11 +26,6 @@ namespace {
 __device__ __forceinline__ uint32_t e4m3x2_rn_sat(float lo, float hi) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ uint32_t bf16x2_rn(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
 

@@ -1,0 +1,103 @@
+// Device helpers of the operators around the MoE layer (sm_103a).
+#pragma once
+
+#include "common.cuh"
+
+namespace mxmoe {
+
+// Two fp32 -> bf16 pair (first value in the low half), nearest even.
+__device__ __forceinline__ uint32_t bf16x2_rn(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Lets the next kernel of the stream, launched with programmatic
+// serialisation, start before this one has finished.
+__device__ __forceinline__ void grid_launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// Multipliers that turn the placed bits of an E4M3 pair (value * 2^-120, see
+// below) into value * 2^(s - 127): one exact step up to s = 134, two above.
+__device__ __forceinline__ ScaleMul e4m3_scale_mul(uint32_t s) {
+  ScaleMul r;
+  if (s <= 134u) {
+    const uint32_t b = (s + 120u) << 7;   // bf16 bits of 2^(s - 7)
+    r.m1 = b | (b << 16);
+    r.m2 = 0;
+    r.two = false;
+  } else {
+    r.m1 = 0x7B807B80u;                   // 2^120
+    const uint32_t b = (s == 255u) ? 0x7FC0u : (s << 7);
+    r.m2 = b | (b << 16);
+    r.two = true;
+  }
+  return r;
+}
+
+// Four E4M3 bytes (low byte first) times their block's scale -> two bf16 pairs.
+// The sign and the 7 magnitude bits of a code, placed at bit 15 and bits 4..10
+// of a half, are a bf16 of the value times 2^-120, subnormal codes included;
+// the products are rounded once (exact inside bf16's range). Code 0x7F is NaN.
+__device__ __forceinline__ void e4m3x4_to_bf16(uint32_t w, const ScaleMul& sm, uint32_t& o0,
+                                               uint32_t& o1) {
+  const uint32_t p0 = prmt(w, 0u, 0x4140u), p1 = prmt(w, 0u, 0x4342u);
+  uint32_t r0 = ((p0 & 0x00800080u) << 8) | ((p0 & 0x007F007Fu) << 4);
+  uint32_t r1 = ((p1 & 0x00800080u) << 8) | ((p1 & 0x007F007Fu) << 4);
+  if (__builtin_expect((((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0u, 0)) {
+    if ((p0 & 0x7Fu) == 0x7Fu) r0 |= 0x7FC0u;
+    if ((p0 & 0x7F0000u) == 0x7F0000u) r0 |= 0x7FC00000u;
+    if ((p1 & 0x7Fu) == 0x7Fu) r1 |= 0x7FC0u;
+    if ((p1 & 0x7F0000u) == 0x7F0000u) r1 |= 0x7FC00000u;
+  }
+  o0 = bf16x2_mul(r0, sm.m1);
+  o1 = bf16x2_mul(r1, sm.m1);
+  if (__builtin_expect(sm.two, 0)) {
+    o0 = bf16x2_mul(o0, sm.m2);
+    o1 = bf16x2_mul(o1, sm.m2);
+  }
+}
+
+// D += A * B for one m16n8k16 tile, bf16 inputs, fp32 accumulators.
+__device__ __forceinline__ void mma_bf16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                               uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+      "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// D[tmem] (+)= A[smem] * B[smem]^T, both operands K-major with the 128-byte swizzle.
+__device__ __forceinline__ void umma_bf16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                             uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate)
+      : "memory");
+}
+
+// Thread-block clusters: rank, barrier over all threads of the cluster, and
+// 16-byte reads of another CTA's shared memory.
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+__device__ __forceinline__ float4 ld_cluster16(uint32_t smem_addr, uint32_t rank) {
+  uint32_t a;
+  float4 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+
+}  // namespace mxmoe
