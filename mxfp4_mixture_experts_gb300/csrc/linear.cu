@@ -6,31 +6,37 @@
 // fp32, one rounding of y to bf16.
 //
 //   convert  (MXFP8 only) x as bf16 rows: exact but for products beyond bf16's range
-//   down     v_t = bf16(scale_a * A_a x_t): the tokens of a window grouped by
-//            adapter, 16 of one adapter to an m16n8k16 tile, K split over the
-//            warps of a CTA
+//   down     v_t = A_a x_t in fp32: the tokens of a window grouped by adapter, up
+//            to 32 of one adapter to a pass of m16n8k16 tiles, K split over the
+//            warps of a CTA and, for few tokens, over CTAs
 //   linear   the projection on the 5th-generation tensor cores, the second
 //            adapter product as further columns of the same reduction
 //
-// The one rounding of v to bf16 (relative 2^-8 of the adapter's share of y,
-// below the rounding of y itself) is what lets that product run on the same
-// tensor-core accumulators.
+// v is scaled and rounded to bf16 as the projection takes it: the rounding
+// (relative 2^-8 of the adapter's share of y, below the rounding of y itself)
+// is what lets that product run on the same tensor-core accumulators.
 //
-// linear kernel: a tile is 128 weight rows x up to 256 tokens. The MMA computes
-// D[weight row][token] with the dequantised weights as operand A in tensor
-// memory and the tokens as operand B in shared memory. After the K values, the
-// adapters that the tile's tokens name follow as columns: column c stands for
-// (c / rp)-th adapter of the tile, rank index c % rp (rp = rank rounded up to
-// 16); operand A holds B_a[n][r], operand B v_t[r] for the tokens of that
-// adapter and 0 for the others. So tokens need no sorting, and a tile pays for
-// the adapters it has. A B_a value that is not finite would turn the others'
-// zeros into NaN; such values are left out of the tile and added in the
-// epilogue to the tokens of their adapter alone.
+// linear kernel: a pair of CTAs holds a tile of 256 weight rows x up to 256
+// tokens. The MMA computes D[weight row][token] with the dequantised weights as
+// operand A in tensor memory and the tokens as operand B in shared memory, half
+// of them in each CTA. After the K values, the adapters that the tile's tokens
+// name follow as columns: column c stands for (c / rp)-th adapter of the tile,
+// rank index c % rp (rp = rank rounded up to 16); operand A holds B_a[n][r],
+// operand B v_t[r] for the tokens of that adapter and 0 for the others. So
+// tokens need no sorting, and a tile pays for the adapters it has. A B_a value
+// that is not finite would turn the others' zeros into NaN; such values are
+// left out of the tile and added in the epilogue to the tokens of their adapter
+// alone.
 //
-// Warp roles: 0 token copies, 1 MMA issue, 2 packed-weight copies, 8..15
-// dequantisation, 4..7 and 16..19 adapter columns, then the epilogue.
-// Few tiles (small T) split K over a cluster of up to 8 CTAs, whose partial sums meet
-// in shared memory, added in rank order.
+// Why pairs: with one CTA per tile (128 rows x 256 tokens) every stage of 64 K
+// values brought 32 KB of tokens into an SM per 512 clocks of MMAs, the most
+// that the path from L2 carries, and the kernel waited on it; in a pair each SM
+// takes half of the tokens.
+//
+// Warp roles: 0 token copies, 1 MMA issue (the even CTA's), 4..7 adapter
+// columns, 8..19 dequantisation in three groups that take the stages in turn;
+// then 4..19 the epilogue. Few tiles (small T) split K over up to 4 pairs of a
+// cluster, whose partial sums meet in shared memory, added in rank order.
 #include <cuda.h>
 #include <cstdint>
 
@@ -61,19 +67,24 @@ __global__ void __launch_bounds__(256) mx8_to_bf16_kernel(const uint4* __restric
 }
 
 // ---------------------------------------------------------------------------
-// v = bf16(scale * A x): windows of tokens, items of up to 16 tokens of one
-// adapter; gridDim.y CTAs take a window's items in turn.
+// v = A x: windows of tokens, items of up to 32 tokens of one adapter.
+// gridDim.y CTAs take a window's items in turn, gridDim.z CTAs split K; each
+// writes its fp32 part, the projection adds them in order.
 // ---------------------------------------------------------------------------
 constexpr int kDownWin = 128;     // tokens per window
-constexpr int kDownRanks = 64;    // ranks per pass (8 n-tiles)
+constexpr int kDownTok = 32;      // tokens per item (two m16 tiles)
+constexpr int kDownMaxParts = 8;
+constexpr int kDownStep = 64;     // K values per step: 16 a lane
 
+// NT: n-tiles of 8 ranks per pass.
+template <int NT>
 __global__ void __launch_bounds__(256) adapter_down_kernel(const uint16_t* __restrict__ x,
                                                            const LinearArgs a,
-                                                           uint16_t* __restrict__ v) {
-  __shared__ int s_id[kDownWin], s_item[kDownWin], s_leader[kDownWin], s_warp[8];
-  __shared__ int s_tok[kDownWin][16];   // [item][slot]: token of the window, -1 empty
+                                                           float* __restrict__ v) {
+  __shared__ int s_id[kDownWin], s_item[kDownWin], s_warp[8];
+  __shared__ int s_tok[kDownWin][kDownTok];   // [item][slot]: token of the window, -1 empty
   __shared__ int s_ad[kDownWin];
-  __shared__ float part[8][16][kDownRanks + 4];
+  __shared__ float part[8][16][NT * 8 + 4];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int w0 = blockIdx.x * kDownWin;
   grid_launch_dependents();
@@ -83,21 +94,21 @@ __global__ void __launch_bounds__(256) adapter_down_kernel(const uint16_t* __res
   if (tid < kDownWin) {
     if (w0 + tid < a.T) id = a.ids[w0 + tid];
     if (id >= a.L) {
-      if (a.status != nullptr && blockIdx.y == 0) atomicAdd(a.status, 1);
+      if (a.status != nullptr && blockIdx.y == 0 && blockIdx.z == 0) atomicAdd(a.status, 1);
       id = -1;
     }
     s_id[tid] = id < 0 ? -1 : id;
-    for (int j = 0; j < 16; ++j) s_tok[tid][j] = -1;
   }
+  for (int i = tid; i < kDownWin * kDownTok; i += 256) s_tok[i / kDownTok][i % kDownTok] = -1;
   __syncthreads();
   int rank = 0, leader = tid;   // earlier tokens of this adapter; first token of this one's item
   if (tid < kDownWin && id >= 0) {
     for (int j = 0; j < tid; ++j)
       if (s_id[j] == id) {
-        if ((rank & 15) == 0) leader = j;
+        if (rank % kDownTok == 0) leader = j;
         ++rank;
       }
-    if ((rank & 15) == 0) leader = tid;
+    if (rank % kDownTok == 0) leader = tid;
   }
   const bool lead = tid < kDownWin && id >= 0 && leader == tid;
   const uint32_t bal = __ballot_sync(0xffffffffu, lead);
@@ -113,59 +124,80 @@ __global__ void __launch_bounds__(256) adapter_down_kernel(const uint16_t* __res
     s_item[tid] = it;
     s_ad[it] = id;
   }
-  if (tid < kDownWin) s_leader[tid] = leader;
   __syncthreads();
-  if (tid < kDownWin && id >= 0) s_tok[s_item[leader]][rank & 15] = tid;
+  if (tid < kDownWin && id >= 0) s_tok[s_item[leader]][rank % kDownTok] = tid;
   __syncthreads();
 
   const int g = lane >> 2, q = lane & 3;
-  const int steps = a.K / 32;
-  const int k0 = steps * warp / 8, k1 = steps * (warp + 1) / 8;
+  const int slices = 8 * gridDim.z, slice = blockIdx.z * 8 + warp;
+  const int steps = a.K / kDownStep;
+  const int k0 = steps * slice / slices, k1 = steps * (slice + 1) / slices;
   for (int it = blockIdx.y; it < items; it += gridDim.y) {
     const int ad = s_ad[it];
-    const int ta = s_tok[it][g], tb = s_tok[it][g + 8];
-    const uint16_t* xa = x + (size_t)(w0 + (ta < 0 ? 0 : ta)) * a.K + 8 * q;
-    const uint16_t* xb = x + (size_t)(w0 + (tb < 0 ? 0 : tb)) * a.K + 8 * q;
-    for (int r0 = 0; r0 < a.rank; r0 += kDownRanks) {
-      const int nt = min(kDownRanks, a.rank - r0) / 8;
-      const uint16_t* ar = a.a + ((size_t)ad * a.rank + r0 + g) * a.K + 8 * q;
-      float acc[8][4] = {};
-      // each lane holds 8 consecutive values of its rows; both operands take
-      // them in the same order, so the products are those of row order
-#pragma unroll 2
-      for (int k = k0; k < k1; ++k) {
-        uint4 ua = make_uint4(0u, 0u, 0u, 0u), ub = ua;
-        if (ta >= 0) ua = *reinterpret_cast<const uint4*>(xa + 32 * k);
-        if (tb >= 0) ub = *reinterpret_cast<const uint4*>(xb + 32 * k);
+    const bool two = s_tok[it][16] >= 0;   // a second m-tile
+    int tk[4];
+    const uint16_t* xr[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if (j < nt) {
-            const uint4 w = *reinterpret_cast<const uint4*>(ar + (size_t)(8 * j) * a.K + 32 * k);
-            mma_bf16_16816(acc[j], ua.x, ub.x, ua.y, ub.y, w.x, w.y);
-            mma_bf16_16816(acc[j], ua.z, ub.z, ua.w, ub.w, w.z, w.w);
+    for (int i = 0; i < 4; ++i) {
+      tk[i] = s_tok[it][g + 8 * i];
+      xr[i] = x + (size_t)(w0 + max(tk[i], 0)) * a.K + 16 * q;
+    }
+    for (int r0 = 0; r0 < a.rank; r0 += NT * 8) {
+      const int nt = min(NT, (a.rank - r0) / 8);
+      const uint16_t* ar = a.a + ((size_t)ad * a.rank + r0 + g) * a.K + 16 * q;
+      float acc[2][NT][4] = {};
+      // each lane holds 16 consecutive values of its rows; both operands take
+      // them in the same order, so the products are those of row order
+      for (int k = k0; k < k1; ++k) {
+        uint4 u[4][2], w[NT][2];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {   // (past the rank: the last rows again, never stored)
+          const uint16_t* src = ar + (size_t)(8 * (j < nt ? j : nt - 1)) * a.K + kDownStep * k;
+          w[j][0] = *reinterpret_cast<const uint4*>(src);
+          w[j][1] = *reinterpret_cast<const uint4*>(src + 8);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          u[i][0] = u[i][1] = make_uint4(0u, 0u, 0u, 0u);
+          if (tk[i] >= 0) {
+            u[i][0] = *reinterpret_cast<const uint4*>(xr[i] + kDownStep * k);
+            u[i][1] = *reinterpret_cast<const uint4*>(xr[i] + kDownStep * k + 8);
           }
         }
-      }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (j < nt) {
-          part[warp][g][8 * j + 2 * q] = acc[j][0];
-          part[warp][g][8 * j + 2 * q + 1] = acc[j][1];
-          part[warp][g + 8][8 * j + 2 * q] = acc[j][2];
-          part[warp][g + 8][8 * j + 2 * q + 1] = acc[j][3];
+        for (int m = 0; m < 2; ++m) {
+          if (m == 1 && !two) break;
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+              const uint4 ua = u[2 * m][h], ub = u[2 * m + 1][h];
+              mma_bf16_16816(acc[m][j], ua.x, ub.x, ua.y, ub.y, w[j][h].x, w[j][h].y);
+              mma_bf16_16816(acc[m][j], ua.z, ub.z, ua.w, ub.w, w[j][h].z, w[j][h].w);
+            }
         }
       }
-      __syncthreads();
-      const float sc = a.ascale != nullptr ? a.ascale[ad] : 1.f;
-      for (int i = tid; i < 16 * 8 * nt; i += 256) {
-        const int row = i / (8 * nt), r = i - row * (8 * nt);
-        const int t = s_tok[it][row];
-        float z = 0.f;
 #pragma unroll
-        for (int w = 0; w < 8; ++w) z += part[w][row][r];
-        if (t >= 0) v[(size_t)(w0 + t) * a.rank + r0 + r] = f32_to_bf16_rne(z * sc);
+      for (int m = 0; m < 2; ++m) {
+        if (m == 1 && !two) break;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          part[warp][g][8 * j + 2 * q] = acc[m][j][0];
+          part[warp][g][8 * j + 2 * q + 1] = acc[m][j][1];
+          part[warp][g + 8][8 * j + 2 * q] = acc[m][j][2];
+          part[warp][g + 8][8 * j + 2 * q + 1] = acc[m][j][3];
+        }
+        __syncthreads();
+        for (int i = tid; i < 16 * 8 * nt; i += 256) {
+          const int row = i / (8 * nt), r = i - row * (8 * nt);
+          const int t = s_tok[it][16 * m + row];
+          float z = 0.f;
+#pragma unroll
+          for (int w = 0; w < 8; ++w) z += part[w][row][r];
+          if (t >= 0) v[((size_t)blockIdx.z * a.T + w0 + t) * a.rank + r0 + r] = z;
+        }
+        __syncthreads();
       }
-      __syncthreads();
     }
   }
 }
@@ -174,302 +206,389 @@ __global__ void __launch_bounds__(256) adapter_down_kernel(const uint16_t* __res
 // The projection
 // ---------------------------------------------------------------------------
 constexpr int kThreads = 640;
-constexpr int kBM = 128;              // weight rows per tile (MMA M)
-constexpr int kBK = 64;               // K values per stage
+constexpr int kBM = 128;              // weight rows per CTA (half of the pair's MMA M)
+constexpr int kBK = 64;               // K values of a 128-byte swizzled row
+constexpr int kStageK = 2 * kBK;      // K values per stage
 constexpr int kMaxTok = 256;          // tokens per tile (MMA N)
-constexpr int kXBox = 64;             // token rows per tensor copy
-constexpr int kPStage = kBM * kBK / 2;
-constexpr int kPBoxRows = 64;
 constexpr int kBTile = kBM * 128;     // adapter columns of operand A: 128 rows x 64 bf16
-constexpr int kMaxS = 8, kMaxSP = 16, kMaxL = 4;   // ring depths
-constexpr int kWCols = kBK / 2;
+constexpr int kPStage = kBM * kStageK / 2;       // packed bytes of a stage
+constexpr int kMaxS = 8, kMaxSP = 8, kMaxL = 4;  // ring depths
+constexpr int kWCols = kStageK / 2;   // tensor-memory columns of a stage's weights
 constexpr int kTmemCols = 512;
-constexpr int kWarpX = 0, kWarpMma = 1, kWarpW = 2, kWarpEpi = 4, kWarpDeq = 8, kWarpEpi2 = 16;
-constexpr int kDeqWarps = 8, kEpiWarps = 8, kEpiThreads = 256;
-constexpr int kEpiBar = 1;            // named barrier of the epilogue warps
-constexpr int kScaleAhead = 8;
+constexpr int kWarpX = 0, kWarpMma = 1, kWarpW = 2, kWarpAd = 4, kWarpDeq = 8, kWarps = kThreads / 32;
+constexpr int kAdThreads = (kWarpDeq - kWarpAd) * 32;
+constexpr int kDeqGroups = (kWarps - kWarpDeq) / 4;
+constexpr int kAdBar = 1, kEpiBar = 2;   // named barriers: adapter warps; all epilogue warps
+constexpr int kEpiThreads = (kWarps - kWarpAd) * 32;
+constexpr int kAhead = 2;             // own stages of scale bytes in a dequantising thread's registers
 constexpr int kListMax = kMaxTok;     // adapters that one tile can name
 
 struct LinearParams {
-  CUtensorMap tmapX;   // bf16 [T][K], box {64, xbox}, 128-byte swizzle
-  CUtensorMap tmapW;   // u8 [N][K/2], box {32, 64}
+  CUtensorMap tmapX;   // x as bytes {128, T, K / 64}, box {128, cs / 2, 2}, 128-byte swizzle
+  CUtensorMap tmapW;   // packed weights u8 [N][K/2], box {64, 128}, 64-byte swizzle
   LinearArgs a;
-  const uint16_t* v;   // bf16 [T][rank]
+  const float* v;      // fp32 [parts][T][rank]
+  int parts;
   int cs;              // tokens per tile (multiple of 16, at most 256)
-  int xbox;            // rows per token copy
-  int xstage;          // bytes of a token stage (cs * 128)
-  int S, SP, SL;       // ring depths: operand stages, packed bytes, adapter columns
-  int split;           // CTAs of a cluster that share a tile's K
+  int S, SP, SL;       // ring depths: operand stages, packed weights, adapter columns
+  int split;           // pairs of a cluster that share a tile's K
   int rp;              // rank rounded up to 16
 };
 
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity));
 }
-// NaN in either half when a bf16 of the pair is not finite, else +-0.
+// Whether a bf16 of the pair is not finite.
 __device__ __forceinline__ bool nonfinite_bf16x2(uint32_t w) {
   return ((w & 0x7F80u) == 0x7F80u) || ((w & 0x7F800000u) == 0x7F800000u);
+}
+__device__ __forceinline__ uint32_t ldg_u16(const uint8_t* p) {
+  uint16_t v;
+  asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ void tmem_st16_nowait(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+// bf16(scale * v) of token t, ranks r .. r + 7: the parts added in order. v is
+// another kernel's output that may still be written when this one starts, so
+// its loads take no read-only path.
+__device__ __forceinline__ uint4 adapter_inner8(const LinearParams& p, int t, int r, float scale) {
+  float z[8] = {};
+  for (int i = 0; i < p.parts; ++i) {
+    const float* src = p.v + ((size_t)i * p.a.T + t) * p.a.rank + r;
+    const uint4 lo = ldcg16(src), hi = ldcg16(src + 4);
+    z[0] += __uint_as_float(lo.x);
+    z[1] += __uint_as_float(lo.y);
+    z[2] += __uint_as_float(lo.z);
+    z[3] += __uint_as_float(lo.w);
+    z[4] += __uint_as_float(hi.x);
+    z[5] += __uint_as_float(hi.y);
+    z[6] += __uint_as_float(hi.z);
+    z[7] += __uint_as_float(hi.w);
+  }
+  return make_uint4(bf16x2_rn(z[0] * scale, z[1] * scale), bf16x2_rn(z[2] * scale, z[3] * scale),
+                    bf16x2_rn(z[4] * scale, z[5] * scale), bf16x2_rn(z[6] * scale, z[7] * scale));
 }
 
 __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_constant__ LinearParams p) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t full[kMaxS], empty[kMaxS], p_full[kMaxSP], p_empty[kMaxSP], l_full[kMaxL],
-      l_empty[kMaxL], d_full, drain;
+      l_empty[kMaxL], l_list, d_full, drain;
   __shared__ uint32_t tmem_slot, s_bits[kLinearMaxAdapters / 32];
-  __shared__ int s_list[kListMax], s_tokad[kMaxTok], s_count, s_anybad;
+  __shared__ int s_list[kListMax], s_tokad[kMaxTok], s_count, s_anybad, s_fail;
+  static_assert(kAdThreads == kBM, "a pass of 8 rows' chunks a thread covers operand A's rows");
   __shared__ uint8_t s_bad[kListMax];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint8_t* sX = smem;
-  uint8_t* sL = sX + p.S * p.xstage;                 // [SL] of {kBTile, xstage}
-  const int lstage = kBTile + p.xstage;
-  uint8_t* sP = sL + p.SL * lstage;
+  const int hb = p.cs / 2;                           // tokens of the tile in this CTA
+  const int xchunk = hb * 128, xstage = 2 * xchunk;
+  const int lstage = kBTile + xchunk;
+  uint8_t* sX = smem;                                // [S][2 chunks][hb][128 bytes]
+  uint8_t* sL = sX + p.S * xstage;                   // [SL] of {kBTile, hb x 128 bytes}
+  uint8_t* sP = sL + p.SL * lstage;                  // [SP][128 rows][64 bytes]
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = p.split > 1 ? (int)cluster_rank() : 0;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const uint32_t crank = cluster_rank();
+  const int half = crank & 1, part = crank >> 1;     // CTA of the pair, K part of the tile
+  const uint32_t lead = crank & ~1u;                 // rank of the pair's issuing CTA
+  const uint16_t pair = (uint16_t)(3u << lead);
   const int N = p.a.N, K = p.a.K;
-  const int ntile = (N + kBM - 1) / kBM;
-  const int tile = blockIdx.x / p.split;
-  const int nt = tile % ntile;
-  const int t0 = (tile / ntile) * p.cs;
+  const int npair = (N + 2 * kBM - 1) / (2 * kBM);
+  const int tile = blockIdx.x / (2 * p.split);
+  const int t0 = (tile / npair) * p.cs;
   const int n = min(p.cs, p.a.T - t0);               // tokens of this tile
-  const int n16 = (n + 15) & ~15;
-  const int n0 = nt * kBM;
-  const int nKall = K / kBK;
-  const int kc0 = nKall * rank / p.split;
-  const int nK = nKall * (rank + 1) / p.split - kc0;
+  const int n0 = (tile % npair) * 2 * kBM + half * kBM;   // first weight row of this CTA
+  const int nSall = (K + kStageK - 1) / kStageK;
+  const int st0 = nSall * part / p.split;
+  const int nS = nSall * (part + 1) / p.split - st0;
   const bool adapters = p.a.ids != nullptr;
   int fail = 0;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < p.S; ++i) { mbar_init(&full[i], 1 + kDeqWarps); mbar_init(&empty[i], 1); }
-    for (int i = 0; i < p.SP; ++i) { mbar_init(&p_full[i], 1); mbar_init(&p_empty[i], kDeqWarps); }
-    for (int i = 0; i < kMaxL; ++i) { mbar_init(&l_full[i], kEpiWarps); mbar_init(&l_empty[i], 1); }
+    // full and l_full of the issuing CTA count both CTAs' warps; one thread's
+    // expect covers both CTAs' token copies
+    for (int i = 0; i < p.S; ++i) { mbar_init(&full[i], 1 + 2 * 4); mbar_init(&empty[i], 1); }
+    for (int i = 0; i < p.SP; ++i) { mbar_init(&p_full[i], 1); mbar_init(&p_empty[i], 4); }
+    for (int i = 0; i < p.SL; ++i) { mbar_init(&l_full[i], 2 * 4); mbar_init(&l_empty[i], 1); }
+    mbar_init(&l_list, 1);
     mbar_init(&d_full, 1);
     mbar_init(&drain, 1);
     fence_barrier_init();
     prefetch_tensormap(&p.tmapX);
     prefetch_tensormap(&p.tmapW);
+    s_fail = 0;
   }
-  if (warp == kWarpMma) tmem_alloc(&tmem_slot, kTmemCols);
-  if (warp == 3) {
-    s_bits[lane] = 0;
-    if (lane == 0) { s_count = 0; s_anybad = 0; }
-  }
-  __syncthreads();
-  // the adapters that the tile's tokens name, in ascending order
-  if (adapters) {
-    if (threadIdx.x < kMaxTok) {
-      int id = (int)threadIdx.x < n ? p.a.ids[t0 + threadIdx.x] : -1;
-      if (id >= p.a.L) id = -1;
-      s_tokad[threadIdx.x] = id;
-      s_bad[threadIdx.x] = 0;
-      if (id >= 0) atomicOr(&s_bits[id >> 5], 1u << (id & 31));
-    }
-    __syncthreads();
-    if (warp == 3) {
-      uint32_t w = s_bits[lane];
-      int x = __popc(w);
-      const int mine = x;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      int at = x - mine;
-      while (w) {
-        s_list[at++] = lane * 32 + __ffs(w) - 1;
-        w &= w - 1;
-      }
-      if (lane == 31) s_count = x;
-    }
-  }
+  if (warp == kWarpMma) tmem2_alloc(&tmem_slot, kTmemCols);
   tc_fence_before();
   __syncthreads();
+  cluster_sync_relaxed();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
   const uint32_t wcol0 = tmem + (uint32_t)((p.cs + 31) & ~31);   // operand-A ring
-  // adapter columns: stages of 64, taken in turn by the CTAs of the cluster
-  const int lcols = adapters ? s_count * p.rp : 0;
-  const int lstages = (lcols + kBK - 1) / kBK;
 
-  if (warp == kWarpX && lane == 0) {
+  if (warp == kWarpX) {
     // ------------------------------------------------------------ token copies
-    int s = 0, k = 0;
-    uint32_t ph = 0, par = 0;   // parity of each stage's last fill
-    const int nbox = (n16 + p.xbox - 1) / p.xbox;
-    const int boxbytes = p.xbox * 128;
-    for (int kc = 0; kc < nK; ++kc, ++k) {
-      if (k >= p.S && !mbar_wait(&empty[s], ph ^ 1u)) { fail = 1; break; }
-      par = (par & ~(1u << s)) | (ph << s);
-      mbar_arrive_expect_tx(&full[s], nbox * boxbytes);
-      for (int b = 0; b < nbox; ++b)
-        tma_load_2d(sX + s * p.xstage + b * boxbytes, &p.tmapX, (kc0 + kc) * kBK, t0 + b * p.xbox,
-                    &full[s]);
-      if (++s == p.S) { s = 0; ph ^= 1u; }
-    }
-    // no copy may still be landing in shared memory when the CTA exits
-    for (int i = 0; i < p.S && i < k; ++i) mbar_wait(&full[i], (par >> i) & 1u);
-  } else if (warp == kWarpW && lane == 0) {
-    // ------------------------------------------------------------ packed-weight copies
-    int s = 0, k = 0;
-    uint32_t ph = 0, par = 0;
-    for (int kc = 0; kc < nK; ++kc, ++k) {
-      if (k >= p.SP && !mbar_wait(&p_empty[s], ph ^ 1u)) { fail = 1; break; }
-      par = (par & ~(1u << s)) | (ph << s);
-      mbar_arrive_expect_tx(&p_full[s], kPStage);
-      tma_load_2d(sP + s * kPStage, &p.tmapW, (kc0 + kc) * (kBK / 2), n0, &p_full[s]);
-      tma_load_2d(sP + s * kPStage + kPStage / 2, &p.tmapW, (kc0 + kc) * (kBK / 2), n0 + kPBoxRows,
-                  &p_full[s]);
-      if (++s == p.SP) { s = 0; ph ^= 1u; }
-    }
-    for (int i = 0; i < p.SP && i < k; ++i) mbar_wait(&p_full[i], (par >> i) & 1u);
-  } else if (warp == kWarpMma && lane == 0) {
-    // ------------------------------------------------------------ MMA issue
-    const uint64_t desc0 = umma_desc_sw128(smem_u32(sX));
-    const uint32_t idesc = umma_idesc_bf16(kBM, n16);
     int s = 0;
     uint32_t ph = 0;
-    bool acc = false;
-    for (int kc = 0; kc < nK; ++kc) {
-      if (!mbar_wait(&full[s], ph)) { fail = 1; break; }
-      tc_fence_after();
-      const uint64_t dsc = desc0 + (uint64_t)(s * (p.xstage >> 4));
-#pragma unroll
-      for (int k16 = 0; k16 < kBK / 16; ++k16) {
-        umma_bf16_ts(tmem, wcol0 + s * kWCols + k16 * 8, dsc + 2 * k16, idesc, acc);
-        acc = true;
+    for (int i = 0; i < nS; ++i) {
+      if (i >= p.S && !warp_wait_cluster(&empty[s], ph ^ 1u)) { fail = 1; break; }
+      if (elect_one()) {
+        if (half == 0) mbar_arrive_expect_tx(&full[s], 2 * xstage);
+        tma2_load_3d(sX + s * xstage, &p.tmapX, 0, t0 + half * hb, 2 * (st0 + i),
+                     cluster_addr(&full[s], lead));
       }
-      umma_commit(&empty[s]);
+      __syncwarp();
       if (++s == p.S) { s = 0; ph ^= 1u; }
     }
-    int ls = 0;
-    uint32_t lph = 0;
-    for (int i = rank; i < lstages && !fail; i += p.split) {
-      if (!mbar_wait(&l_full[ls], lph)) { fail = 1; break; }
-      tc_fence_after();
-      const uint64_t da = umma_desc_sw128(smem_u32(sL + ls * lstage));
-      const uint64_t db = umma_desc_sw128(smem_u32(sL + ls * lstage + kBTile));
-      const int k16n = min(kBK, lcols - i * kBK) / 16;
-      for (int k16 = 0; k16 < k16n; ++k16) {
-        umma_bf16_ss(tmem, da + 2 * k16, db + 2 * k16, idesc, acc);
-        acc = true;
+  } else if (warp == kWarpW) {
+    // ------------------------------------------------------------ packed-weight copies
+    int s = 0;
+    uint32_t ph = 0;
+    for (int i = 0; i < nS; ++i) {
+      if (i >= p.SP && !warp_wait(&p_empty[s], ph ^ 1u)) { fail = 1; break; }
+      if (elect_one()) {
+        mbar_arrive_expect_tx(&p_full[s], kPStage);
+        tma_load_2d(sP + s * kPStage, &p.tmapW, (st0 + i) * (kStageK / 2), n0, &p_full[s]);
       }
-      umma_commit(&l_empty[ls]);
-      if (++ls == p.SL) { ls = 0; lph ^= 1u; }
+      __syncwarp();
+      if (++s == p.SP) { s = 0; ph ^= 1u; }
     }
-    if (!fail) umma_commit(&d_full);
-    // every issued MMA has finished before tensor memory is released
-    umma_commit(&drain);
-    mbar_wait(&drain, 0);
-  } else if (warp >= kWarpDeq && warp < kWarpDeq + kDeqWarps) {
+  } else if (warp == kWarpMma) {
+    // ------------------------------------------------------------ MMA issue
+    if (half == 0) {
+      const uint64_t desc0 = umma_desc_sw128(smem_u32(sX));
+      const uint32_t idesc = umma_idesc_bf16(2 * kBM, p.cs);
+      int s = 0;
+      uint32_t ph = 0;
+      for (int i = 0; i < nS; ++i) {
+        if (!warp_wait_cluster(&full[s], ph)) { fail = 1; break; }
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t d = desc0 + (uint64_t)(s * (xstage >> 4));
+          const uint32_t a = wcol0 + s * kWCols;
+          umma2_bf16_ts(tmem, a, d, idesc, i > 0);
+          umma2_bf16_ts(tmem, a + 8, d + 2, idesc, true);
+          umma2_bf16_ts(tmem, a + 16, d + 4, idesc, true);
+          umma2_bf16_ts(tmem, a + 24, d + 6, idesc, true);
+          if ((st0 + i) * kStageK + kBK < K) {
+            const uint64_t e = d + (uint64_t)(xchunk >> 4);
+            umma2_bf16_ts(tmem, a + 32, e, idesc, true);
+            umma2_bf16_ts(tmem, a + 40, e + 2, idesc, true);
+            umma2_bf16_ts(tmem, a + 48, e + 4, idesc, true);
+            umma2_bf16_ts(tmem, a + 56, e + 6, idesc, true);
+          }
+          umma2_commit(&empty[s], pair);
+        }
+        __syncwarp();
+        if (++s == p.S) { s = 0; ph ^= 1u; }
+      }
+      if (adapters && !fail && !warp_wait(&l_list, 0)) fail = 1;
+      const int lcols = adapters && !fail ? s_count * p.rp : 0;
+      int ls = 0;
+      uint32_t lph = 0;
+      for (int i = part; i * kBK < lcols; i += p.split) {
+        if (!warp_wait_cluster(&l_full[ls], lph)) { fail = 1; break; }
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t da = umma_desc_sw128(smem_u32(sL + ls * lstage));
+          const uint64_t db = umma_desc_sw128(smem_u32(sL + ls * lstage + kBTile));
+          const int k16n = min(kBK, lcols - i * kBK) / 16;
+          for (int k16 = 0; k16 < k16n; ++k16)
+            umma2_bf16_ss(tmem, da + 2 * k16, db + 2 * k16, idesc, true);   // nS > 0 came before
+          umma2_commit(&l_empty[ls], pair);
+        }
+        __syncwarp();
+        if (++ls == p.SL) { ls = 0; lph ^= 1u; }
+      }
+      if (elect_one()) {
+        if (!fail) umma2_commit(&d_full, pair);
+        umma2_commit(&drain, pair);
+      }
+      __syncwarp();
+    }
+  } else if (warp >= kWarpDeq) {
     // ------------------------------------------------------------ dequantisation
-    const int q = warp & 3;                    // lane quarter
-    const int h = (warp - kWarpDeq) >> 2;      // which 32 of the stage's 64 K values
-    const int m = q * 32 + lane;               // weight row of the tile = TMEM lane
-    const uint32_t wlane = wcol0 + ((uint32_t)(q * 32) << 16) + h * 16;
-    const uint8_t* srow =
-        p.a.s + (size_t)min(n0 + m, N - 1) * (K / kScaleBlock) + 2 * kc0 + h;
-    int sp = 0, sw = 0;
-    uint32_t pp = 0, pw = 0;
-    uint32_t sc[kScaleAhead];
+    // A group of four warps takes a whole stage; a thread holds one weight row
+    // (TMEM lane), its 64 packed bytes of the stage from shared memory and its
+    // four scale bytes straight from global memory, kAhead of its stages early.
+    // (The packed bytes too, straight into registers, cost 3000 clocks a stage:
+    // 32 rows a warp load are 32 requests each.)
+    const int dg = (warp - kWarpDeq) >> 2;   // group: stages dg, dg + kDeqGroups, ..
+    const int m = (warp & 3) * 32 + lane;
+    const uint32_t wlane = wcol0 + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint8_t* srow = p.a.s + (size_t)min(n0 + m, N - 1) * (K / kScaleBlock) +
+                          st0 * (kStageK / kScaleBlock);   // rows past N: the last row, never stored
+    const bool words = K % kStageK == 0;                   // the four bytes are one aligned word
+    uint32_t sc[kAhead];
+    auto load = [&](int slot, int i) {
+      if (i >= nS) return;
+      if (words) {
+        sc[slot] = __ldg(reinterpret_cast<const uint32_t*>(srow + 4 * i));
+      } else {
+        sc[slot] = ldg_u16(srow + 4 * i);
+        if ((st0 + i) * kStageK + kBK < K) sc[slot] |= ldg_u16(srow + 4 * i + 2) << 16;
+      }
+    };
 #pragma unroll
-    for (int i = 0; i < kScaleAhead; ++i) sc[i] = i < nK ? ldg_u8(srow + 2 * i) : 0u;
-    for (int k0 = 0; k0 < nK && !fail; k0 += kScaleAhead) {
-      uint32_t nx[kScaleAhead];   // the next window's scale bytes, loaded one window early
+    for (int j = 0; j < kAhead; ++j) load(j, dg + kDeqGroups * j);
+    int s = dg, sp = dg;
+    uint32_t ph = 0, pp = 0;
+    if (s >= p.S) { s -= p.S; ph = 1; }
+    for (int b = dg; b < nS && !fail; b += kDeqGroups * kAhead) {
 #pragma unroll
-      for (int i = 0; i < kScaleAhead; ++i)
-        nx[i] = k0 + kScaleAhead + i < nK ? ldg_u8(srow + 2 * (k0 + kScaleAhead + i)) : 0u;
-#pragma unroll
-      for (int i = 0; i < kScaleAhead; ++i) {
-        if (k0 + i >= nK || fail) break;
+      for (int j = 0; j < kAhead; ++j) {
+        const int i = b + kDeqGroups * j;
+        if (i >= nS || fail) break;
         if (!warp_wait(&p_full[sp], pp)) { fail = 1; break; }
-        const uint4 qv = *reinterpret_cast<const uint4*>(sP + sp * kPStage + m * (kBK / 2) + h * 16);
-        // the generic read above is ordered before the stage's refill by a tensor copy
+        uint4 w[4];
+        const uint8_t* src = sP + sp * kPStage + m * 64;
+#pragma unroll
+        for (int z = 0; z < 4; ++z)
+          w[z] = *reinterpret_cast<const uint4*>(src + ((z ^ ((m >> 1) & 3)) << 4));
+        // the generic reads above are ordered before the stage's refill by a tensor copy
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_empty[sp]);
-        if (++sp == p.SP) { sp = 0; pp ^= 1u; }
-        const uint32_t wd[4] = {qv.x, qv.y, qv.z, qv.w};
-        uint32_t o[16];
-        dequant32_bf16(wd, scale_mul(sc[i]), o);
-        if (k0 + i >= p.S) {   // the MMAs that read this ring slot have completed
-          if (!warp_wait(&empty[sw], pw ^ 1u)) { fail = 1; break; }
+        if (i >= p.S) {   // the MMAs that read this ring slot have completed
+          if (!warp_wait_cluster(&empty[s], ph ^ 1u)) { fail = 1; break; }
           tc_fence_after();
         }
-        tmem_st16(wlane + sw * kWCols, o);
+        const bool both = (st0 + i) * kStageK + kBK < K;   // K may end inside the stage
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+          if (z == 2 && !both) break;
+          const uint32_t wd[4] = {w[z].x, w[z].y, w[z].z, w[z].w};
+          uint32_t o[16];
+          dequant32_bf16(wd, scale_mul((sc[j] >> (8 * z)) & 255u), o);
+          tmem_st16_nowait(wlane + s * kWCols + 16 * z, o);
+        }
+        load(j, i + kDeqGroups * kAhead);
+        tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&full[sw]);
-        if (++sw == p.S) { sw = 0; pw ^= 1u; }
+        if (lane == 0) mbar_arrive_remote(cluster_addr(&full[s], lead));
+        s += kDeqGroups;
+        if (s >= p.S) { s -= p.S; ph ^= 1u; }
+        sp += kDeqGroups;
+        if (sp >= p.SP) { sp -= p.SP; pp ^= 1u; }
       }
-#pragma unroll
-      for (int i = 0; i < kScaleAhead; ++i) sc[i] = nx[i];
     }
-  } else if ((warp >= kWarpEpi && warp < kWarpEpi + 4) || warp >= kWarpEpi2) {
+  } else if (warp >= kWarpAd) {
     // ------------------------------------------------------------ adapter columns
-    const int q = warp & 3;
-    const int half = warp >= kWarpEpi2;
-    const int et = (half * 4 + q) * 32 + lane;   // 0..255
     if (adapters) {
+      const int et = threadIdx.x - kWarpAd * 32;
+      // the adapters that the tile's tokens name, in ascending order
+      if (et < kLinearMaxAdapters / 32) s_bits[et] = 0;
+      if (et == 0) s_anybad = 0;
+      named_barrier(kAdBar, kAdThreads);
+      for (int i = et; i < kMaxTok; i += kAdThreads) {
+        int id = i < n ? p.a.ids[t0 + i] : -1;
+        if (id >= p.a.L) id = -1;
+        s_tokad[i] = id;
+        s_bad[i] = 0;
+        if (id >= 0) atomicOr(&s_bits[id >> 5], 1u << (id & 31));
+      }
+      named_barrier(kAdBar, kAdThreads);
+      if (warp == kWarpAd) {
+        uint32_t bits = s_bits[lane];
+        int x = __popc(bits);
+        const int mine = x;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, x, o);
+          if (lane >= o) x += y;
+        }
+        int at = x - mine;
+        while (bits) {
+          s_list[at++] = lane * 32 + __ffs(bits) - 1;
+          bits &= bits - 1;
+        }
+        if (lane == 31) s_count = x;
+      }
+      named_barrier(kAdBar, kAdThreads);
+      if (et == 0) mbar_arrive(&l_list);
+      const int count = s_count, lcols = count * p.rp;
+      // stages of 64 columns, taken in turn by the pairs of the cluster
       bool waited = false;
       int ls = 0, use = 0;
       uint32_t lph = 0;
-      for (int i = rank; i < lstages && !fail; i += p.split, ++use) {
-        if (use >= p.SL && !warp_wait(&l_empty[ls], lph ^ 1u)) { fail = 1; break; }
+      for (int i = part; i * kBK < lcols; i += p.split, ++use) {
+        if (use >= p.SL && !warp_wait_cluster(&l_empty[ls], lph ^ 1u)) { fail = 1; break; }
         uint8_t* tb = sL + ls * lstage;
         uint8_t* tv = tb + kBTile;
         // 16-byte chunk j of a row: columns 64 i + 8 j .., one adapter's ranks r ..
         const int j = et & 7;
         const int c = i * kBK + 8 * j;
         const int ai = c / p.rp, r = c - ai * p.rp;
-        const bool live = ai < s_count && r < p.a.rank;
+        const bool live = ai < count && r < p.a.rank;
         const int ad = live ? s_list[ai] : -1;
-        for (int row = et >> 3; row < kBM; row += kEpiThreads / 8) {
-          uint4 w = make_uint4(0u, 0u, 0u, 0u);
+        const float vscale = live && p.a.ascale != nullptr ? p.a.ascale[ad] : 1.f;
+        uint4 b[8];   // in flight together
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int row = (et >> 3) + 16 * u;
+          b[u] = make_uint4(0u, 0u, 0u, 0u);
           if (live && n0 + row < N)
-            w = *reinterpret_cast<const uint4*>(p.a.b + ((size_t)ad * N + n0 + row) * p.a.rank + r);
-          if (nonfinite_bf16x2(w.x) || nonfinite_bf16x2(w.y) || nonfinite_bf16x2(w.z) ||
-              nonfinite_bf16x2(w.w)) {
+            b[u] = *reinterpret_cast<const uint4*>(p.a.b + ((size_t)ad * N + n0 + row) * p.a.rank + r);
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int row = (et >> 3) + 16 * u;
+          uint32_t q[4] = {b[u].x, b[u].y, b[u].z, b[u].w};
+          if (nonfinite_bf16x2(q[0]) || nonfinite_bf16x2(q[1]) || nonfinite_bf16x2(q[2]) ||
+              nonfinite_bf16x2(q[3])) {
             s_bad[ai] = 1;
             s_anybad = 1;
-            uint32_t z[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
             for (int e = 0; e < 4; ++e) {
-              if ((z[e] & 0x7F80u) == 0x7F80u) z[e] &= 0xFFFF0000u;
-              if ((z[e] & 0x7F800000u) == 0x7F800000u) z[e] &= 0xFFFFu;
+              if ((q[e] & 0x7F80u) == 0x7F80u) q[e] &= 0xFFFF0000u;
+              if ((q[e] & 0x7F800000u) == 0x7F800000u) q[e] &= 0xFFFFu;
             }
-            w = make_uint4(z[0], z[1], z[2], z[3]);
           }
-          *reinterpret_cast<uint4*>(tb + row * 128 + ((j ^ (row & 7)) << 4)) = w;
+          *reinterpret_cast<uint4*>(tb + row * 128 + ((j ^ (row & 7)) << 4)) =
+              make_uint4(q[0], q[1], q[2], q[3]);
         }
         if (!waited) {   // v comes from the kernel before this one
           grid_dependency_wait();
           waited = true;
         }
-        for (int t = et >> 3; t < n16; t += kEpiThreads / 8) {
-          uint4 w = make_uint4(0u, 0u, 0u, 0u);
-          if (live && s_tokad[t] == ad)
-            w = *reinterpret_cast<const uint4*>(p.v + (size_t)(t0 + t) * p.a.rank + r);
-          *reinterpret_cast<uint4*>(tv + t * 128 + ((j ^ (t & 7)) << 4)) = w;
+        for (int t = et >> 3; t < hb; t += kAdThreads / 8) {
+          uint4 u = make_uint4(0u, 0u, 0u, 0u);
+          if (live && s_tokad[half * hb + t] == ad)
+            u = adapter_inner8(p, t0 + half * hb + t, r, vscale);
+          *reinterpret_cast<uint4*>(tv + t * 128 + ((j ^ (t & 7)) << 4)) = u;
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&l_full[ls]);
+        if (lane == 0) mbar_arrive_cluster(cluster_addr(&l_full[ls], lead));
         if (++ls == p.SL) { ls = 0; lph ^= 1u; }
       }
       if (!waited) grid_dependency_wait();
-      named_barrier(kEpiBar, kEpiThreads);   // s_bad and s_anybad are complete
     }
+  }
+  __syncwarp();
+  if (warp >= kWarpAd) {
     // ------------------------------------------------------------ epilogue
-    if (!warp_wait(&d_full, 0)) fail = 1;
+    if (adapters) named_barrier(kEpiBar, kEpiThreads);   // s_bad and s_anybad are complete
+    if (!warp_wait_cluster(&d_full, 0)) fail = 1;
     tc_fence_after();
     if (!fail) {
+      const int q = warp & 3;                 // TMEM lane quarter
       const int row = n0 + q * 32 + lane;
       const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16);
-      const int n32 = (n16 + 31) >> 5, lo32 = (n32 + 1) >> 1;
       float* red = reinterpret_cast<float*>(sX);   // [token][128], the token ring is free
       const bool fix = adapters && s_anybad != 0;
 #pragma unroll 1
-      for (int c0 = (half ? lo32 : 0) * 32; c0 < (half ? n32 : lo32) * 32; c0 += 32) {
+      for (int c0 = ((warp - kWarpAd) >> 2) * 32; c0 < n; c0 += (kEpiThreads / 128) * 32) {
         float v[32];
         tmem_ld32(taddr + c0, v);
         if (__builtin_expect(fix, 0) && row < N) {
@@ -481,9 +600,13 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
             float z = 0.f;
             for (int r = 0; r < p.a.rank; ++r) {
               const uint32_t bw = p.a.b[((size_t)ad * N + row) * p.a.rank + r];
-              if ((bw & 0x7F80u) == 0x7F80u)
+              if ((bw & 0x7F80u) == 0x7F80u) {
+                const uint4 u = adapter_inner8(p, t0 + c0 + t, r & ~7,
+                                               p.a.ascale != nullptr ? p.a.ascale[ad] : 1.f);
+                const uint32_t two = (r & 4) ? ((r & 2) ? u.w : u.z) : ((r & 2) ? u.y : u.x);
                 z += __uint_as_float(bw << 16) *
-                     __uint_as_float((uint32_t)p.v[(size_t)(t0 + c0 + t) * p.a.rank + r] << 16);
+                     __uint_as_float((r & 1) ? two & 0xFFFF0000u : two << 16);
+              }
             }
 #pragma unroll
             for (int e = 0; e < 32; ++e)
@@ -495,16 +618,39 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
 #pragma unroll
           for (int e = 0; e < 32; ++e)
             if (e < nv) red[(c0 + e) * kBM + q * 32 + lane] = v[e];
-        } else if (row < N) {
-          uint16_t* dst = p.a.out + (size_t)(t0 + c0) * N + row;
+        } else {
+          // four lanes trade values so that each holds four consecutive rows
+          // of every fourth token: 8-byte stores, 64 bytes a token and warp
+          const int l = lane & 3;
+          const bool inside = n0 + q * 32 + (lane & ~3) < N;   // N % 8 == 0: all four rows or none
+          uint16_t* dst = p.a.out + (size_t)(t0 + c0 + l) * N + n0 + q * 32 + (lane & ~3);
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (e < nv) dst[(size_t)e * N] = f32_to_bf16_rne(v[e]);
+          for (int e = 0; e < 32; e += 4) {
+            // lane l sends token e + l ^ m to lane l ^ m and keeps token e + l
+            float g[4];
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+              const int k = l ^ m;
+              const float send = k == 0 ? v[e] : k == 1 ? v[e + 1] : k == 2 ? v[e + 2] : v[e + 3];
+              g[m] = m == 0 ? send : __shfl_xor_sync(0xffffffffu, send, m);
+            }
+            // g[m] is row (lane & ~3) + (l ^ m) of token e + l
+            const float y0 = l == 0 ? g[0] : l == 1 ? g[1] : l == 2 ? g[2] : g[3];
+            const float y1 = l == 1 ? g[0] : l == 0 ? g[1] : l == 3 ? g[2] : g[3];
+            const float y2 = l == 2 ? g[0] : l == 3 ? g[1] : l == 0 ? g[2] : g[3];
+            const float y3 = l == 3 ? g[0] : l == 2 ? g[1] : l == 1 ? g[2] : g[3];
+            if (inside && e + l < nv)
+              *reinterpret_cast<uint2*>(dst + (size_t)e * N) =
+                  make_uint2(bf16x2_rn(y0, y1), bf16x2_rn(y2, y3));
+          }
         }
       }
     }
   }
+  // no MMA may still read the pair's memory when it is released
+  if (!warp_wait_cluster(&drain, 0)) fail = 1;
   __syncwarp();
+  if (fail) s_fail = 1;
   if (fail && p.a.status != nullptr) {
     if (adapters) grid_dependency_wait();   // the status words belong to that kernel until then
     atomicOr(&p.a.status[2], 1);
@@ -512,23 +658,30 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == kWarpMma) {
-    tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols);
-  }
+  // after a wait that gave up, copies may still be on their way to this CTA's
+  // shared memory: they land within microseconds, a millisecond is waited
+  if (s_fail)
+    for (int i = 0; i < 1000; ++i) __nanosleep(1000);
+  cluster_sync();
+  tc_fence_after();
+  if (warp == kWarpMma) tmem2_dealloc(tmem, kTmemCols);
   if (p.split > 1) {
-    // y of tokens rank, rank + split, ..: the cluster's partial sums in rank order
-    cluster_sync();
+    // y of tokens part, part + split, ..: the pairs' partial sums in rank order
     const uint32_t red = smem_u32(sX);
-    for (int t = rank + p.split * warp; t < n; t += p.split * (kThreads / 32)) {
-      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int c = 0; c < p.split; ++c) {
-        const float4 z = ld_cluster16(red + (t * kBM + lane * 4) * 4, c);
-        y.x += z.x;
-        y.y += z.y;
-        y.z += z.z;
-        y.w += z.w;
-      }
+    for (int t = part + p.split * warp; t < n; t += p.split * kWarps) {
+      float4 z[4];   // all in flight before the first is used
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (c < p.split) z[c] = ld_cluster16(red + (t * kBM + lane * 4) * 4, 2 * c + half);
+      float4 y = z[0];
+#pragma unroll
+      for (int c = 1; c < 4; ++c)
+        if (c < p.split) {
+          y.x += z[c].x;
+          y.y += z[c].y;
+          y.z += z[c].z;
+          y.w += z[c].w;
+        }
       if (n0 + lane * 4 < N)
         *reinterpret_cast<uint2*>(p.a.out + (size_t)(t0 + t) * N + n0 + lane * 4) =
             make_uint2(bf16x2_rn(y.x, y.y), bf16x2_rn(y.z, y.w));
@@ -541,22 +694,71 @@ size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 
 }  // namespace
 
+// CTAs that share an adapter product's K: 8 where the tokens make few items.
+static int down_parts(int T, int K) {
+  constexpr int kSms = 152;   // the workspace's size cannot depend on the device at hand
+  int parts = kSms / ((T + kDownTok - 1) / kDownTok);
+  if (parts > kDownMaxParts) parts = kDownMaxParts;
+  while (parts > 1 && K / kDownStep < 8 * parts) --parts;
+  return parts < 1 ? 1 : parts;
+}
+
 size_t linear_workspace_bytes(int T, int K, int N, int rank, bool x8) {
   (void)N;
-  return up256((size_t)T * rank * 2) + (x8 ? up256((size_t)T * K * 2) : 0);
+  return up256((size_t)down_parts(T, K) * T * rank * 4) + (x8 ? up256((size_t)T * K * 2) : 0);
+}
+
+template <int NT>
+static void launch_down(const uint16_t* x, const LinearArgs& a, float* v, int parts, int num_sms,
+                        cudaStream_t stream) {
+  const int win = (a.T + kDownWin - 1) / kDownWin;
+  int slots = (2 * num_sms + win - 1) / win;
+  if (slots < 4) slots = 4;
+  if (slots > kDownWin) slots = kDownWin;
+  if (slots > a.T) slots = a.T;
+  adapter_down_kernel<NT><<<dim3(win, slots, parts), 256, 0, stream>>>(x, a, v);
+}
+
+// Tokens per tile and pairs per tile that a call takes: the smallest estimate of
+// waves x (stages x clocks of a stage + clocks of a tile's start and end). A
+// stage costs the larger of its dequantisation (about 600 clocks) and its eight
+// MMAs (cs / 2 clocks each).
+static void linear_plan(int T, int N, int K, int num_sms, int& cs, int& split) {
+  const int npair = (N + 2 * kBM - 1) / (2 * kBM), nS = (K + kStageK - 1) / kStageK;
+  const int pairs = num_sms / 2;
+  double best = 0;
+  cs = 0;
+  const int c0 = (T + kMaxTok - 1) / kMaxTok;
+  for (int c = c0; c <= c0 + 8; ++c) {
+    const int tok = ((T + c - 1) / c + 15) & ~15;
+    const int64_t tiles = (int64_t)npair * ((T + tok - 1) / tok);
+    for (int sp = 1; sp <= 4; sp *= 2) {
+      if (sp > 1 && (tiles * sp > pairs || nS < 2 * sp)) break;
+      const double stage = tok > 150 ? 4.0 * tok : 600.0;
+      const double waves = (double)((tiles * sp + pairs - 1) / pairs);
+      const double t = waves * ((double)nS / sp * stage + 5000 + (sp > 1 ? 1500 : 0));
+      if (cs == 0 || t < best) {
+        best = t;
+        cs = tok;
+        split = sp;
+      }
+    }
+    if (tok <= 16) break;
+  }
 }
 
 cudaError_t launch_linear(const LinearArgs& a, int num_sms, cudaStream_t stream) {
   cudaError_t e;
   char* ws = static_cast<char*>(a.ws);
   const bool adapters = a.ids != nullptr;
-  uint16_t* v = reinterpret_cast<uint16_t*>(ws);
+  const int parts = down_parts(a.T, a.K);
+  float* v = reinterpret_cast<float*>(ws);
   const uint16_t* x = static_cast<const uint16_t*>(a.x);
   if (a.status != nullptr &&
       (e = cudaMemsetAsync(a.status, 0, 4 * sizeof(int32_t), stream)) != cudaSuccess)
     return e;
   if (a.xs != nullptr) {
-    uint16_t* xb = reinterpret_cast<uint16_t*>(ws + up256((size_t)a.T * a.rank * 2));
+    uint16_t* xb = reinterpret_cast<uint16_t*>(ws + up256((size_t)parts * a.T * a.rank * 4));
     const int64_t n16 = (int64_t)a.T * a.K / 16;
     const int64_t blocks = (n16 + 255) / 256;
     mx8_to_bf16_kernel<<<(unsigned)(blocks < num_sms * 8 ? blocks : num_sms * 8), 256, 0, stream>>>(
@@ -564,41 +766,32 @@ cudaError_t launch_linear(const LinearArgs& a, int num_sms, cudaStream_t stream)
     x = xb;
   }
   if (adapters) {
-    const int win = (a.T + kDownWin - 1) / kDownWin;
-    int slots = (2 * num_sms + win - 1) / win;
-    if (slots < 8) slots = 8;
-    if (slots > kDownWin) slots = kDownWin;
-    if (slots > a.T) slots = a.T;
-    adapter_down_kernel<<<dim3(win, slots), 256, 0, stream>>>(x, a, v);
+    if (a.rank <= 8) launch_down<1>(x, a, v, parts, num_sms, stream);
+    else if (a.rank <= 16) launch_down<2>(x, a, v, parts, num_sms, stream);
+    else launch_down<4>(x, a, v, parts, num_sms, stream);
   }
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
 
   LinearParams p = {};
   p.a = a;
   p.v = v;
-  const int chunks = (a.T + kMaxTok - 1) / kMaxTok;
-  p.cs = ((a.T + chunks - 1) / chunks + 15) & ~15;
-  p.xbox = p.cs < kXBox ? p.cs : kXBox;
-  const int xrows = (p.cs + p.xbox - 1) / p.xbox * p.xbox;   // whole copies fill a stage
-  p.xstage = xrows * 128;
-  p.S = 96 * 1024 / p.xstage;
-  if (p.S < 4) p.S = 4;
-  if (p.S > kMaxS) p.S = kMaxS;
-  p.SP = p.cs > 32 ? 8 : kMaxSP;
+  p.parts = parts;
+  linear_plan(a.T, a.N, a.K, num_sms, p.cs, p.split);
+  const int xstage = p.cs / 2 * 256;
+  p.S = (kTmemCols - ((p.cs + 31) & ~31)) / kWCols;   // 4 at 256 tokens, 7 at 16
+  p.SP = 6;
   p.SL = !adapters ? 0 : p.cs > 128 ? 1 : p.cs > 64 ? 2 : kMaxL;
   p.rp = (a.rank + 15) & ~15;
-  const int ntile = (a.N + kBM - 1) / kBM, ttile = (a.T + p.cs - 1) / p.cs;
-  const int64_t tiles = (int64_t)ntile * ttile;
-  // a cluster splits K while that still gives every CTA an SM of its own and
-  // at least four stages
-  p.split = 1;
-  while (p.split < 8 && tiles * p.split * 2 <= num_sms && a.K / kBK >= 4 * p.split * 2) p.split *= 2;
-  if (!encode_tiled_2d(&p.tmapX, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, x, (uint64_t)a.K, (uint64_t)a.T,
-                       (uint64_t)a.K * 2, kBK, p.xbox, CU_TENSOR_MAP_SWIZZLE_128B) ||
+  const int npair = (a.N + 2 * kBM - 1) / (2 * kBM), ttile = (a.T + p.cs - 1) / p.cs;
+  const int64_t tiles = (int64_t)npair * ttile;
+  const uint64_t dims[3] = {128, (uint64_t)a.T, (uint64_t)a.K / kBK};
+  const uint64_t strides[2] = {(uint64_t)a.K * 2, 128};
+  const uint32_t box[3] = {128, (uint32_t)p.cs / 2, 2};
+  if (!encode_tiled_u8(&p.tmapX, x, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !encode_tiled_2d(&p.tmapW, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.w, (uint64_t)a.K / 2, (uint64_t)a.N,
-                       (uint64_t)a.K / 2, kBK / 2, kPBoxRows, CU_TENSOR_MAP_SWIZZLE_NONE))
+                       (uint64_t)a.K / 2, kStageK / 2, kBM, CU_TENSOR_MAP_SWIZZLE_64B))
     return cudaErrorInvalidValue;
-  const size_t smem = 1024 + (size_t)p.S * p.xstage + (size_t)p.SL * (kBTile + p.xstage) +
+  const size_t smem = 1024 + (size_t)p.S * xstage + (size_t)p.SL * (kBTile + xstage / 2) +
                       (size_t)p.SP * kPStage;
   static size_t granted[kGrantDevices] = {};
   int dev = 0;
@@ -610,18 +803,16 @@ cudaError_t launch_linear(const LinearArgs& a, int num_sms, cudaStream_t stream)
     granted[dev] = smem;
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(tiles * p.split));
+  cfg.gridDim = dim3((unsigned)(tiles * p.split * 2));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute at[2];
   int na = 0;
-  if (p.split > 1) {
-    at[na].id = cudaLaunchAttributeClusterDimension;
-    at[na].val.clusterDim.x = p.split;
-    at[na].val.clusterDim.y = at[na].val.clusterDim.z = 1;
-    ++na;
-  }
+  at[na].id = cudaLaunchAttributeClusterDimension;
+  at[na].val.clusterDim.x = 2 * p.split;
+  at[na].val.clusterDim.y = at[na].val.clusterDim.z = 1;
+  ++na;
   if (adapters) {   // starts beside the down kernel, whose results it waits for
     at[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[na].val.programmaticStreamSerializationAllowed = 1;

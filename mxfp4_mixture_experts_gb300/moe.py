@@ -116,6 +116,19 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _addr(t: Optional[torch.Tensor]):
+    """The device address as an int (what ctypes makes of a declared pointer argument anyway)."""
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(stream) -> int:
+    """The cudaStream_t of ``stream``, or of the current stream, without the Stream object that
+    torch.cuda.current_stream builds (0.2 against 2.8 us a call)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
+
+
 def _need(t: torch.Tensor, name: str, dtype, ndim: int):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -431,9 +444,9 @@ def add_rmsnorm(x: torch.Tensor, gamma: torch.Tensor, residual: Optional[torch.T
     if out8 is not None:
         q = torch.empty(T, K, dtype=torch.float8_e4m3fn, device=dev)
         s = torch.empty(T, K // 32, dtype=torch.uint8, device=dev)
-    rc = lib().mxfp4_moe_add_rmsnorm(_ptr(x), _ptr(residual), _ptr(gamma), T, K, eps,
-                                     MX8_RULES[out8 or "ocp"], _ptr(residual_out), _ptr(out),
-                                     _ptr(q), _ptr(s), _stream(stream))
+    rc = lib().mxfp4_moe_add_rmsnorm(_addr(x), _addr(residual), _addr(gamma), T, K, eps,
+                                     MX8_RULES[out8 or "ocp"], _addr(residual_out), _addr(out),
+                                     _addr(q), _addr(s), _raw_stream(stream))
     if rc:
         raise MoEError(rc, "mxfp4_moe_add_rmsnorm")
     return out, (x if residual_out is None else residual_out), q, s
@@ -471,10 +484,10 @@ def router_scored(logits: torch.Tensor, topk: int, scoring: str = "sigmoid",
         topk_ids = torch.empty(T, topk, dtype=torch.int32, device=logits.device)
     if topk_weights is None:
         topk_weights = torch.empty(T, topk, dtype=torch.float32, device=logits.device)
-    rc = lib().mxfp4_moe_router_scored(_ptr(logits), _ptr(bias), T, E, topk, SCORES[scoring],
+    rc = lib().mxfp4_moe_router_scored(_addr(logits), _addr(bias), T, E, topk, SCORES[scoring],
                                        n_group, topk_group, group_top, int(bool(renormalise)),
-                                       route_scale, _ptr(topk_ids), _ptr(topk_weights),
-                                       _stream(stream))
+                                       route_scale, _addr(topk_ids), _addr(topk_weights),
+                                       _raw_stream(stream))
     if rc:
         raise MoEError(rc, "mxfp4_moe_router_scored")
     return topk_ids, topk_weights
@@ -545,10 +558,10 @@ def linear(x: torch.Tensor, w: torch.Tensor, s: torch.Tensor,
                                 dtype=torch.uint8, device=x.device)
     else:
         _need(workspace, "workspace", torch.uint8, 1)
-    rc = L.mxfp4_moe_linear(_ptr(x), _ptr(x_scale), _ptr(w), _ptr(s), T, K, N, _ptr(adapter_ids),
-                            _ptr(adapter_a), _ptr(adapter_b), _ptr(adapter_scale), n_ad, rank,
-                            _ptr(out), _ptr(status), _ptr(workspace), workspace.numel(),
-                            _stream(stream))
+    rc = L.mxfp4_moe_linear(_addr(x), _addr(x_scale), _addr(w), _addr(s), T, K, N, _addr(adapter_ids),
+                            _addr(adapter_a), _addr(adapter_b), _addr(adapter_scale), n_ad, rank,
+                            _addr(out), _addr(status), _addr(workspace), workspace.numel(),
+                            _raw_stream(stream))
     if rc:
         raise MoEError(rc, "mxfp4_moe_linear")
     return out
