@@ -33,10 +33,13 @@
 // that the path from L2 carries, and the kernel waited on it; in a pair each SM
 // takes half of the tokens.
 //
-// Warp roles: 0 token copies, 1 MMA issue (the even CTA's), 4..7 adapter
-// columns, 8..19 dequantisation in three groups that take the stages in turn;
-// then 4..19 the epilogue. Few tiles (small T) split K over up to 4 pairs of a
-// cluster, whose partial sums meet in shared memory, added in rank order.
+// Warp roles: 0 token copies, 1 MMA issue (the even CTA's), 2 copies of packed
+// weights, 4..11 adapter columns and epilogue, 12..23 dequantisation in three
+// groups that take the stages in turn. Pairs are persistent: the next tile's
+// operands are made while the epilogue empties the accumulators, and its MMAs
+// run while the output rows go out. Few tiles (small T) split K over up to 4
+// pairs of a cluster, whose partial sums meet in shared memory, added in rank
+// order.
 #include <cuda.h>
 #include <cstdint>
 
@@ -205,7 +208,7 @@ __global__ void __launch_bounds__(256) adapter_down_kernel(const uint16_t* __res
 // ---------------------------------------------------------------------------
 // The projection
 // ---------------------------------------------------------------------------
-constexpr int kThreads = 640;
+constexpr int kThreads = 768;
 constexpr int kBM = 128;              // weight rows per CTA (half of the pair's MMA M)
 constexpr int kBK = 64;               // K values of a 128-byte swizzled row
 constexpr int kStageK = 2 * kBK;      // K values per stage
@@ -215,11 +218,11 @@ constexpr int kPStage = kBM * kStageK / 2;       // packed bytes of a stage
 constexpr int kMaxS = 8, kMaxSP = 8, kMaxL = 4;  // ring depths
 constexpr int kWCols = kStageK / 2;   // tensor-memory columns of a stage's weights
 constexpr int kTmemCols = 512;
-constexpr int kWarpX = 0, kWarpMma = 1, kWarpW = 2, kWarpAd = 4, kWarpDeq = 8, kWarps = kThreads / 32;
-constexpr int kAdThreads = (kWarpDeq - kWarpAd) * 32;
+constexpr int kWarpX = 0, kWarpMma = 1, kWarpW = 2, kWarpEpi = 4, kWarpDeq = 12, kWarps = kThreads / 32;
+constexpr int kEpiWarps = kWarpDeq - kWarpEpi, kEpiThreads = kEpiWarps * 32;
 constexpr int kDeqGroups = (kWarps - kWarpDeq) / 4;
-constexpr int kAdBar = 1, kEpiBar = 2;   // named barriers: adapter warps; all epilogue warps
-constexpr int kEpiThreads = (kWarps - kWarpAd) * 32;
+constexpr int kEpiBar = 1;            // named barrier of the adapter and epilogue warps
+constexpr int kOutPitch = kBM * 2 + 16;   // bytes of a staged output row (128 bf16 and a bank shift)
 constexpr int kAhead = 2;             // own stages of scale bytes in a dequantising thread's registers
 constexpr int kListMax = kMaxTok;     // adapters that one tile can name
 
@@ -233,6 +236,7 @@ struct LinearParams {
   int S, SP, SL;       // ring depths: operand stages, packed weights, adapter columns
   int split;           // pairs of a cluster that share a tile's K
   int rp;              // rank rounded up to 16
+  int tiles;           // (pair of weight blocks, token tile)
 };
 
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
@@ -283,18 +287,20 @@ __device__ __forceinline__ uint4 adapter_inner8(const LinearParams& p, int t, in
 __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_constant__ LinearParams p) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t full[kMaxS], empty[kMaxS], p_full[kMaxSP], p_empty[kMaxSP], l_full[kMaxL],
-      l_empty[kMaxL], l_list, d_full, drain;
+      l_empty[kMaxL], l_list, d_full, d_empty, drain;
   __shared__ uint32_t tmem_slot, s_bits[kLinearMaxAdapters / 32];
-  __shared__ int s_list[kListMax], s_tokad[kMaxTok], s_count, s_anybad, s_fail;
-  static_assert(kAdThreads == kBM, "a pass of 8 rows' chunks a thread covers operand A's rows");
+  __shared__ int s_list[kListMax], s_tokad[kMaxTok], s_count, s_anybad, s_fail, s_efail[2];
+  static_assert(kEpiThreads == kMaxTok, "one thread per token of a tile");
+
   __shared__ uint8_t s_bad[kListMax];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int hb = p.cs / 2;                           // tokens of the tile in this CTA
   const int xchunk = hb * 128, xstage = 2 * xchunk;
   const int lstage = kBTile + xchunk;
   uint8_t* sX = smem;                                // [S][2 chunks][hb][128 bytes]
-  uint8_t* sL = sX + p.S * xstage;                   // [SL] of {kBTile, hb x 128 bytes}
-  uint8_t* sP = sL + p.SL * lstage;                  // [SP][128 rows][64 bytes]
+  uint8_t* sP = sX + p.S * xstage;                   // [SP][128 rows][64 bytes]
+  uint8_t* sL = sP + p.SP * kPStage;                 // [SL] of {kBTile, hb x 128 bytes}; then the
+                                                     // output tile [cs][kOutPitch]
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t crank = cluster_rank();
@@ -303,10 +309,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
   const uint16_t pair = (uint16_t)(3u << lead);
   const int N = p.a.N, K = p.a.K;
   const int npair = (N + 2 * kBM - 1) / (2 * kBM);
-  const int tile = blockIdx.x / (2 * p.split);
-  const int t0 = (tile / npair) * p.cs;
-  const int n = min(p.cs, p.a.T - t0);               // tokens of this tile
-  const int n0 = (tile % npair) * 2 * kBM + half * kBM;   // first weight row of this CTA
+  const int cluster = blockIdx.x / (2 * p.split), clusters = gridDim.x / (2 * p.split);
+  // a tile's first token, and this CTA's first weight row
+  auto tile_t0 = [&](int tile) { return tile / npair * p.cs; };
+  auto tile_n0 = [&](int tile) { return tile % npair * 2 * kBM + half * kBM; };
   const int nSall = (K + kStageK - 1) / kStageK;
   const int st0 = nSall * part / p.split;
   const int nS = nSall * (part + 1) / p.split - st0;
@@ -318,14 +324,15 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
     // expect covers both CTAs' token copies
     for (int i = 0; i < p.S; ++i) { mbar_init(&full[i], 1 + 2 * 4); mbar_init(&empty[i], 1); }
     for (int i = 0; i < p.SP; ++i) { mbar_init(&p_full[i], 1); mbar_init(&p_empty[i], 4); }
-    for (int i = 0; i < p.SL; ++i) { mbar_init(&l_full[i], 2 * 4); mbar_init(&l_empty[i], 1); }
+    for (int i = 0; i < p.SL; ++i) { mbar_init(&l_full[i], 2 * kEpiWarps); mbar_init(&l_empty[i], 1); }
     mbar_init(&l_list, 1);
     mbar_init(&d_full, 1);
+    mbar_init(&d_empty, 2 * kEpiWarps);
     mbar_init(&drain, 1);
     fence_barrier_init();
     prefetch_tensormap(&p.tmapX);
     prefetch_tensormap(&p.tmapW);
-    s_fail = 0;
+    s_fail = s_efail[0] = s_efail[1] = 0;
   }
   if (warp == kWarpMma) tmem2_alloc(&tmem_slot, kTmemCols);
   tc_fence_before();
@@ -337,82 +344,91 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
 
   if (warp == kWarpX) {
     // ------------------------------------------------------------ token copies
-    int s = 0;
+    int s = 0, k = 0;
     uint32_t ph = 0;
-    for (int i = 0; i < nS; ++i) {
-      if (i >= p.S && !warp_wait_cluster(&empty[s], ph ^ 1u)) { fail = 1; break; }
-      if (elect_one()) {
-        if (half == 0) mbar_arrive_expect_tx(&full[s], 2 * xstage);
-        tma2_load_3d(sX + s * xstage, &p.tmapX, 0, t0 + half * hb, 2 * (st0 + i),
-                     cluster_addr(&full[s], lead));
+    for (int tile = cluster; tile < p.tiles && !fail; tile += clusters) {
+      const int row = tile_t0(tile) + half * hb;
+      for (int i = 0; i < nS; ++i, ++k) {
+        if (k >= p.S && !warp_wait_cluster(&empty[s], ph ^ 1u)) { fail = 1; break; }
+        if (elect_one()) {
+          if (half == 0) mbar_arrive_expect_tx(&full[s], 2 * xstage);
+          tma2_load_3d(sX + s * xstage, &p.tmapX, 0, row, 2 * (st0 + i),
+                       cluster_addr(&full[s], lead));
+        }
+        __syncwarp();
+        if (++s == p.S) { s = 0; ph ^= 1u; }
       }
-      __syncwarp();
-      if (++s == p.S) { s = 0; ph ^= 1u; }
     }
   } else if (warp == kWarpW) {
     // ------------------------------------------------------------ packed-weight copies
-    int s = 0;
+    int s = 0, k = 0;
     uint32_t ph = 0;
-    for (int i = 0; i < nS; ++i) {
-      if (i >= p.SP && !warp_wait(&p_empty[s], ph ^ 1u)) { fail = 1; break; }
-      if (elect_one()) {
-        mbar_arrive_expect_tx(&p_full[s], kPStage);
-        tma_load_2d(sP + s * kPStage, &p.tmapW, (st0 + i) * (kStageK / 2), n0, &p_full[s]);
+    for (int tile = cluster; tile < p.tiles && !fail; tile += clusters) {
+      const int n0 = tile_n0(tile);
+      for (int i = 0; i < nS; ++i, ++k) {
+        if (k >= p.SP && !warp_wait(&p_empty[s], ph ^ 1u)) { fail = 1; break; }
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&p_full[s], kPStage);
+          tma_load_2d(sP + s * kPStage, &p.tmapW, (st0 + i) * (kStageK / 2), n0, &p_full[s]);
+        }
+        __syncwarp();
+        if (++s == p.SP) { s = 0; ph ^= 1u; }
       }
-      __syncwarp();
-      if (++s == p.SP) { s = 0; ph ^= 1u; }
     }
   } else if (warp == kWarpMma) {
     // ------------------------------------------------------------ MMA issue
     if (half == 0) {
       const uint64_t desc0 = umma_desc_sw128(smem_u32(sX));
       const uint32_t idesc = umma_idesc_bf16(2 * kBM, p.cs);
-      int s = 0;
-      uint32_t ph = 0;
-      for (int i = 0; i < nS; ++i) {
-        if (!warp_wait_cluster(&full[s], ph)) { fail = 1; break; }
-        tc_fence_after();
-        if (elect_one()) {
-          const uint64_t d = desc0 + (uint64_t)(s * (xstage >> 4));
-          const uint32_t a = wcol0 + s * kWCols;
-          umma2_bf16_ts(tmem, a, d, idesc, i > 0);
-          umma2_bf16_ts(tmem, a + 8, d + 2, idesc, true);
-          umma2_bf16_ts(tmem, a + 16, d + 4, idesc, true);
-          umma2_bf16_ts(tmem, a + 24, d + 6, idesc, true);
-          if ((st0 + i) * kStageK + kBK < K) {
-            const uint64_t e = d + (uint64_t)(xchunk >> 4);
-            umma2_bf16_ts(tmem, a + 32, e, idesc, true);
-            umma2_bf16_ts(tmem, a + 40, e + 2, idesc, true);
-            umma2_bf16_ts(tmem, a + 48, e + 4, idesc, true);
-            umma2_bf16_ts(tmem, a + 56, e + 6, idesc, true);
+      int s = 0, ls = 0, it = 0;
+      uint32_t ph = 0, lph = 0;
+      for (int tile = cluster; tile < p.tiles && !fail; tile += clusters, ++it) {
+        // the epilogues of both CTAs have read the tile before
+        if (it > 0 && !warp_wait_cluster(&d_empty, (it - 1) & 1)) { fail = 1; break; }
+        for (int i = 0; i < nS; ++i) {
+          if (!warp_wait_cluster(&full[s], ph)) { fail = 1; break; }
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t d = desc0 + (uint64_t)(s * (xstage >> 4));
+            const uint32_t a = wcol0 + s * kWCols;
+            umma2_bf16_ts(tmem, a, d, idesc, i > 0);
+            umma2_bf16_ts(tmem, a + 8, d + 2, idesc, true);
+            umma2_bf16_ts(tmem, a + 16, d + 4, idesc, true);
+            umma2_bf16_ts(tmem, a + 24, d + 6, idesc, true);
+            if ((st0 + i) * kStageK + kBK < K) {   // K may end inside the stage
+              const uint64_t e = d + (uint64_t)(xchunk >> 4);
+              umma2_bf16_ts(tmem, a + 32, e, idesc, true);
+              umma2_bf16_ts(tmem, a + 40, e + 2, idesc, true);
+              umma2_bf16_ts(tmem, a + 48, e + 4, idesc, true);
+              umma2_bf16_ts(tmem, a + 56, e + 6, idesc, true);
+            }
+            umma2_commit(&empty[s], pair);
           }
-          umma2_commit(&empty[s], pair);
+          __syncwarp();
+          if (++s == p.S) { s = 0; ph ^= 1u; }
         }
-        __syncwarp();
-        if (++s == p.S) { s = 0; ph ^= 1u; }
-      }
-      if (adapters && !fail && !warp_wait(&l_list, 0)) fail = 1;
-      const int lcols = adapters && !fail ? s_count * p.rp : 0;
-      int ls = 0;
-      uint32_t lph = 0;
-      for (int i = part; i * kBK < lcols; i += p.split) {
-        if (!warp_wait_cluster(&l_full[ls], lph)) { fail = 1; break; }
-        tc_fence_after();
-        if (elect_one()) {
-          const uint64_t da = umma_desc_sw128(smem_u32(sL + ls * lstage));
-          const uint64_t db = umma_desc_sw128(smem_u32(sL + ls * lstage + kBTile));
-          const int k16n = min(kBK, lcols - i * kBK) / 16;
-          for (int k16 = 0; k16 < k16n; ++k16)
-            umma2_bf16_ss(tmem, da + 2 * k16, db + 2 * k16, idesc, true);   // nS > 0 came before
-          umma2_commit(&l_empty[ls], pair);
+        if (adapters && !fail) {
+          if (!warp_wait(&l_list, it & 1)) { fail = 1; break; }
+          const int lcols = s_count * p.rp;
+          for (int i = part; i * kBK < lcols; i += p.split) {
+            if (!warp_wait_cluster(&l_full[ls], lph)) { fail = 1; break; }
+            tc_fence_after();
+            if (elect_one()) {
+              const uint64_t da = umma_desc_sw128(smem_u32(sL + ls * lstage));
+              const uint64_t db = umma_desc_sw128(smem_u32(sL + ls * lstage + kBTile));
+              const int k16n = min(kBK, lcols - i * kBK) / 16;
+              for (int k16 = 0; k16 < k16n; ++k16)
+                umma2_bf16_ss(tmem, da + 2 * k16, db + 2 * k16, idesc, true);   // nS > 0 came before
+              umma2_commit(&l_empty[ls], pair);
+            }
+            __syncwarp();
+            if (++ls == p.SL) { ls = 0; lph ^= 1u; }
+          }
         }
+        if (elect_one() && !fail) umma2_commit(&d_full, pair);
         __syncwarp();
-        if (++ls == p.SL) { ls = 0; lph ^= 1u; }
       }
-      if (elect_one()) {
-        if (!fail) umma2_commit(&d_full, pair);
-        umma2_commit(&drain, pair);
-      }
+      if (elect_one()) umma2_commit(&drain, pair);
       __syncwarp();
     }
   } else if (warp >= kWarpDeq) {
@@ -422,173 +438,185 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
     // four scale bytes straight from global memory, kAhead of its stages early.
     // (The packed bytes too, straight into registers, cost 3000 clocks a stage:
     // 32 rows a warp load are 32 requests each.)
-    const int dg = (warp - kWarpDeq) >> 2;   // group: stages dg, dg + kDeqGroups, ..
+    const int dg = (warp - kWarpDeq) >> 2;   // group: stages dg, dg + kDeqGroups, .. of all tiles
     const int m = (warp & 3) * 32 + lane;
     const uint32_t wlane = wcol0 + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint8_t* srow = p.a.s + (size_t)min(n0 + m, N - 1) * (K / kScaleBlock) +
-                          st0 * (kStageK / kScaleBlock);   // rows past N: the last row, never stored
-    const bool words = K % kStageK == 0;                   // the four bytes are one aligned word
-    uint32_t sc[kAhead];
-    auto load = [&](int slot, int i) {
-      if (i >= nS) return;
-      if (words) {
-        sc[slot] = __ldg(reinterpret_cast<const uint32_t*>(srow + 4 * i));
-      } else {
-        sc[slot] = ldg_u16(srow + 4 * i);
-        if ((st0 + i) * kStageK + kBK < K) sc[slot] |= ldg_u16(srow + 4 * i + 2) << 16;
-      }
-    };
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) load(j, dg + kDeqGroups * j);
-    int s = dg, sp = dg;
+    const bool words = K % kStageK == 0;     // a stage's four scale bytes are one aligned word
+    int s = dg, sp = dg, k = dg;
     uint32_t ph = 0, pp = 0;
     if (s >= p.S) { s -= p.S; ph = 1; }
-    for (int b = dg; b < nS && !fail; b += kDeqGroups * kAhead) {
-#pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        const int i = b + kDeqGroups * j;
-        if (i >= nS || fail) break;
-        if (!warp_wait(&p_full[sp], pp)) { fail = 1; break; }
-        uint4 w[4];
-        const uint8_t* src = sP + sp * kPStage + m * 64;
-#pragma unroll
-        for (int z = 0; z < 4; ++z)
-          w[z] = *reinterpret_cast<const uint4*>(src + ((z ^ ((m >> 1) & 3)) << 4));
-        // the generic reads above are ordered before the stage's refill by a tensor copy
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_empty[sp]);
-        if (i >= p.S) {   // the MMAs that read this ring slot have completed
-          if (!warp_wait_cluster(&empty[s], ph ^ 1u)) { fail = 1; break; }
-          tc_fence_after();
+    if (sp >= p.SP) { sp -= p.SP; pp = 1; }
+    int i0 = dg;   // this group's first stage of the tile
+    for (int tile = cluster; tile < p.tiles && !fail; tile += clusters) {
+      const uint8_t* srow = p.a.s + (size_t)min(tile_n0(tile) + m, N - 1) * (K / kScaleBlock) +
+                            st0 * (kStageK / kScaleBlock);   // rows past N: the last row, never stored
+      uint32_t sc[kAhead];
+      auto load = [&](int slot, int i) {
+        if (i >= nS) return;
+        if (words) {
+          sc[slot] = __ldg(reinterpret_cast<const uint32_t*>(srow + 4 * i));
+        } else {
+          sc[slot] = ldg_u16(srow + 4 * i);
+          if ((st0 + i) * kStageK + kBK < K) sc[slot] |= ldg_u16(srow + 4 * i + 2) << 16;
         }
-        const bool both = (st0 + i) * kStageK + kBK < K;   // K may end inside the stage
+      };
 #pragma unroll
-        for (int z = 0; z < 4; ++z) {
-          if (z == 2 && !both) break;
-          const uint32_t wd[4] = {w[z].x, w[z].y, w[z].z, w[z].w};
-          uint32_t o[16];
-          dequant32_bf16(wd, scale_mul((sc[j] >> (8 * z)) & 255u), o);
-          tmem_st16_nowait(wlane + s * kWCols + 16 * z, o);
-        }
-        load(j, i + kDeqGroups * kAhead);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_remote(cluster_addr(&full[s], lead));
-        s += kDeqGroups;
-        if (s >= p.S) { s -= p.S; ph ^= 1u; }
-        sp += kDeqGroups;
-        if (sp >= p.SP) { sp -= p.SP; pp ^= 1u; }
-      }
-    }
-  } else if (warp >= kWarpAd) {
-    // ------------------------------------------------------------ adapter columns
-    if (adapters) {
-      const int et = threadIdx.x - kWarpAd * 32;
-      // the adapters that the tile's tokens name, in ascending order
-      if (et < kLinearMaxAdapters / 32) s_bits[et] = 0;
-      if (et == 0) s_anybad = 0;
-      named_barrier(kAdBar, kAdThreads);
-      for (int i = et; i < kMaxTok; i += kAdThreads) {
-        int id = i < n ? p.a.ids[t0 + i] : -1;
-        if (id >= p.a.L) id = -1;
-        s_tokad[i] = id;
-        s_bad[i] = 0;
-        if (id >= 0) atomicOr(&s_bits[id >> 5], 1u << (id & 31));
-      }
-      named_barrier(kAdBar, kAdThreads);
-      if (warp == kWarpAd) {
-        uint32_t bits = s_bits[lane];
-        int x = __popc(bits);
-        const int mine = x;
+      for (int j = 0; j < kAhead; ++j) load(j, i0 + kDeqGroups * j);
+      int i = i0;
+      while (i < nS && !fail) {
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int y = __shfl_up_sync(0xffffffffu, x, o);
-          if (lane >= o) x += y;
-        }
-        int at = x - mine;
-        while (bits) {
-          s_list[at++] = lane * 32 + __ffs(bits) - 1;
-          bits &= bits - 1;
-        }
-        if (lane == 31) s_count = x;
-      }
-      named_barrier(kAdBar, kAdThreads);
-      if (et == 0) mbar_arrive(&l_list);
-      const int count = s_count, lcols = count * p.rp;
-      // stages of 64 columns, taken in turn by the pairs of the cluster
-      bool waited = false;
-      int ls = 0, use = 0;
-      uint32_t lph = 0;
-      for (int i = part; i * kBK < lcols; i += p.split, ++use) {
-        if (use >= p.SL && !warp_wait_cluster(&l_empty[ls], lph ^ 1u)) { fail = 1; break; }
-        uint8_t* tb = sL + ls * lstage;
-        uint8_t* tv = tb + kBTile;
-        // 16-byte chunk j of a row: columns 64 i + 8 j .., one adapter's ranks r ..
-        const int j = et & 7;
-        const int c = i * kBK + 8 * j;
-        const int ai = c / p.rp, r = c - ai * p.rp;
-        const bool live = ai < count && r < p.a.rank;
-        const int ad = live ? s_list[ai] : -1;
-        const float vscale = live && p.a.ascale != nullptr ? p.a.ascale[ad] : 1.f;
-        uint4 b[8];   // in flight together
+        for (int j = 0; j < kAhead; ++j) {
+          if (i >= nS || fail) break;
+          if (!warp_wait(&p_full[sp], pp)) { fail = 1; break; }
+          uint4 w[4];
+          const uint8_t* src = sP + sp * kPStage + m * 64;
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const int row = (et >> 3) + 16 * u;
-          b[u] = make_uint4(0u, 0u, 0u, 0u);
-          if (live && n0 + row < N)
-            b[u] = *reinterpret_cast<const uint4*>(p.a.b + ((size_t)ad * N + n0 + row) * p.a.rank + r);
-        }
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const int row = (et >> 3) + 16 * u;
-          uint32_t q[4] = {b[u].x, b[u].y, b[u].z, b[u].w};
-          if (nonfinite_bf16x2(q[0]) || nonfinite_bf16x2(q[1]) || nonfinite_bf16x2(q[2]) ||
-              nonfinite_bf16x2(q[3])) {
-            s_bad[ai] = 1;
-            s_anybad = 1;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              if ((q[e] & 0x7F80u) == 0x7F80u) q[e] &= 0xFFFF0000u;
-              if ((q[e] & 0x7F800000u) == 0x7F800000u) q[e] &= 0xFFFFu;
-            }
+          for (int z = 0; z < 4; ++z)
+            w[z] = *reinterpret_cast<const uint4*>(src + ((z ^ ((m >> 1) & 3)) << 4));
+          // the generic reads above are ordered before the stage's refill by a tensor copy
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_empty[sp]);
+          if (k >= p.S) {   // the MMAs that read this ring slot have completed
+            if (!warp_wait_cluster(&empty[s], ph ^ 1u)) { fail = 1; break; }
+            tc_fence_after();
           }
-          *reinterpret_cast<uint4*>(tb + row * 128 + ((j ^ (row & 7)) << 4)) =
-              make_uint4(q[0], q[1], q[2], q[3]);
+          const bool both = (st0 + i) * kStageK + kBK < K;
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            if (z == 2 && !both) break;
+            const uint32_t wd[4] = {w[z].x, w[z].y, w[z].z, w[z].w};
+            uint32_t o[16];
+            dequant32_bf16(wd, scale_mul((sc[j] >> (8 * z)) & 255u), o);
+            tmem_st16_nowait(wlane + s * kWCols + 16 * z, o);
+          }
+          load(j, i + kDeqGroups * kAhead);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_remote(cluster_addr(&full[s], lead));
+          i += kDeqGroups;
+          k += kDeqGroups;
+          s += kDeqGroups;
+          while (s >= p.S) { s -= p.S; ph ^= 1u; }
+          sp += kDeqGroups;
+          while (sp >= p.SP) { sp -= p.SP; pp ^= 1u; }
         }
-        if (!waited) {   // v comes from the kernel before this one
+      }
+      i0 = i - nS;
+    }
+  } else if (warp >= kWarpEpi) {
+    const int et = threadIdx.x - kWarpEpi * 32;
+    bool waited = false;
+    int ls = 0, use = 0, it = 0;
+    uint32_t lph = 0;
+    for (int tile = cluster; tile < p.tiles && !fail; tile += clusters, ++it) {
+      const int t0 = tile_t0(tile), n0 = tile_n0(tile);
+      const int n = min(p.cs, p.a.T - t0);   // tokens of this tile
+      if (adapters) {
+        // ---------------------------------------------------------- adapter columns
+        // the adapters that the tile's tokens name, in ascending order
+        if (et < kLinearMaxAdapters / 32) s_bits[et] = 0;
+        if (et == 0) s_anybad = 0;
+        named_barrier(kEpiBar, kEpiThreads);
+        {
+          int id = et < n ? p.a.ids[t0 + et] : -1;
+          if (id >= p.a.L) id = -1;
+          s_tokad[et] = id;
+          s_bad[et] = 0;
+          if (id >= 0) atomicOr(&s_bits[id >> 5], 1u << (id & 31));
+        }
+        named_barrier(kEpiBar, kEpiThreads);
+        if (warp == kWarpEpi) {
+          uint32_t bits = s_bits[lane];
+          int x = __popc(bits);
+          const int mine = x;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+          }
+          int at = x - mine;
+          while (bits) {
+            s_list[at++] = lane * 32 + __ffs(bits) - 1;
+            bits &= bits - 1;
+          }
+          if (lane == 31) s_count = x;
+        }
+        named_barrier(kEpiBar, kEpiThreads);
+        if (et == 0) mbar_arrive(&l_list);
+        const int count = s_count, lcols = count * p.rp;
+        // stages of 64 columns, taken in turn by the pairs of the cluster
+        for (int i = part; i * kBK < lcols; i += p.split, ++use) {
+          if (use >= p.SL && !warp_wait_cluster(&l_empty[ls], lph ^ 1u)) { fail = 1; break; }
+          uint8_t* tb = sL + ls * lstage;
+          uint8_t* tv = tb + kBTile;
+          // 16-byte chunk j of a row: columns 64 i + 8 j .., one adapter's ranks r ..
+          const int j = et & 7;
+          const int c = i * kBK + 8 * j;
+          const int ai = c / p.rp, r = c - ai * p.rp;
+          const bool live = ai < count && r < p.a.rank;
+          const int ad = live ? s_list[ai] : -1;
+          const float vscale = live && p.a.ascale != nullptr ? p.a.ascale[ad] : 1.f;
+          constexpr int kPer = kBM * 8 / kEpiThreads;
+          uint4 b[kPer];   // in flight together
+#pragma unroll
+          for (int u = 0; u < kPer; ++u) {
+            const int row = (et >> 3) + kEpiThreads / 8 * u;
+            b[u] = make_uint4(0u, 0u, 0u, 0u);
+            if (live && n0 + row < N)
+              b[u] = *reinterpret_cast<const uint4*>(p.a.b + ((size_t)ad * N + n0 + row) * p.a.rank + r);
+          }
+#pragma unroll
+          for (int u = 0; u < kPer; ++u) {
+            const int row = (et >> 3) + kEpiThreads / 8 * u;
+            uint32_t q[4] = {b[u].x, b[u].y, b[u].z, b[u].w};
+            if (nonfinite_bf16x2(q[0]) || nonfinite_bf16x2(q[1]) || nonfinite_bf16x2(q[2]) ||
+                nonfinite_bf16x2(q[3])) {
+              s_bad[ai] = 1;
+              s_anybad = 1;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                if ((q[e] & 0x7F80u) == 0x7F80u) q[e] &= 0xFFFF0000u;
+                if ((q[e] & 0x7F800000u) == 0x7F800000u) q[e] &= 0xFFFFu;
+              }
+            }
+            *reinterpret_cast<uint4*>(tb + row * 128 + ((j ^ (row & 7)) << 4)) =
+                make_uint4(q[0], q[1], q[2], q[3]);
+          }
+          if (!waited) {   // v comes from the kernel before this one
+            grid_dependency_wait();
+            waited = true;
+          }
+          for (int t = et >> 3; t < hb; t += kEpiThreads / 8) {
+            uint4 u = make_uint4(0u, 0u, 0u, 0u);
+            if (live && s_tokad[half * hb + t] == ad)
+              u = adapter_inner8(p, t0 + half * hb + t, r, vscale);
+            *reinterpret_cast<uint4*>(tv + t * 128 + ((j ^ (t & 7)) << 4)) = u;
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(cluster_addr(&l_full[ls], lead));
+          if (++ls == p.SL) { ls = 0; lph ^= 1u; }
+        }
+        if (!waited) {
           grid_dependency_wait();
           waited = true;
         }
-        for (int t = et >> 3; t < hb; t += kAdThreads / 8) {
-          uint4 u = make_uint4(0u, 0u, 0u, 0u);
-          if (live && s_tokad[half * hb + t] == ad)
-            u = adapter_inner8(p, t0 + half * hb + t, r, vscale);
-          *reinterpret_cast<uint4*>(tv + t * 128 + ((j ^ (t & 7)) << 4)) = u;
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(cluster_addr(&l_full[ls], lead));
-        if (++ls == p.SL) { ls = 0; lph ^= 1u; }
+        named_barrier(kEpiBar, kEpiThreads);   // s_bad and s_anybad are complete
       }
-      if (!waited) grid_dependency_wait();
-    }
-  }
-  __syncwarp();
-  if (warp >= kWarpAd) {
-    // ------------------------------------------------------------ epilogue
-    if (adapters) named_barrier(kEpiBar, kEpiThreads);   // s_bad and s_anybad are complete
-    if (!warp_wait_cluster(&d_full, 0)) fail = 1;
-    tc_fence_after();
-    if (!fail) {
+      // ------------------------------------------------------------ epilogue
+      // accumulators -> a shared-memory tile [token][128 rows]: bf16, or, where K
+      // is split over the cluster, fp32 in the token ring (free by then)
+      if (!warp_wait_cluster(&d_full, it & 1)) fail = 1;
+      tc_fence_after();
       const int q = warp & 3;                 // TMEM lane quarter
       const int row = n0 + q * 32 + lane;
       const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16);
-      float* red = reinterpret_cast<float*>(sX);   // [token][128], the token ring is free
+      float* red = reinterpret_cast<float*>(sX);
       const bool fix = adapters && s_anybad != 0;
 #pragma unroll 1
-      for (int c0 = ((warp - kWarpAd) >> 2) * 32; c0 < n; c0 += (kEpiThreads / 128) * 32) {
+      for (int c0 = (et >> 7) * 32; c0 < n && !fail; c0 += kEpiThreads / 128 * 32) {
         float v[32];
         tmem_ld32(taddr + c0, v);
         if (__builtin_expect(fix, 0) && row < N) {
@@ -619,34 +647,31 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
           for (int e = 0; e < 32; ++e)
             if (e < nv) red[(c0 + e) * kBM + q * 32 + lane] = v[e];
         } else {
-          // four lanes trade values so that each holds four consecutive rows
-          // of every fourth token: 8-byte stores, 64 bytes a token and warp
-          const int l = lane & 3;
-          const bool inside = n0 + q * 32 + (lane & ~3) < N;   // N % 8 == 0: all four rows or none
-          uint16_t* dst = p.a.out + (size_t)(t0 + c0 + l) * N + n0 + q * 32 + (lane & ~3);
+          uint8_t* dst = sL + c0 * kOutPitch + (q * 32 + lane) * 2;
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            // lane l sends token e + l ^ m to lane l ^ m and keeps token e + l
-            float g[4];
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-              const int k = l ^ m;
-              const float send = k == 0 ? v[e] : k == 1 ? v[e + 1] : k == 2 ? v[e + 2] : v[e + 3];
-              g[m] = m == 0 ? send : __shfl_xor_sync(0xffffffffu, send, m);
-            }
-            // g[m] is row (lane & ~3) + (l ^ m) of token e + l
-            const float y0 = l == 0 ? g[0] : l == 1 ? g[1] : l == 2 ? g[2] : g[3];
-            const float y1 = l == 1 ? g[0] : l == 0 ? g[1] : l == 3 ? g[2] : g[3];
-            const float y2 = l == 2 ? g[0] : l == 3 ? g[1] : l == 0 ? g[2] : g[3];
-            const float y3 = l == 3 ? g[0] : l == 2 ? g[1] : l == 1 ? g[2] : g[3];
-            if (inside && e + l < nv)
-              *reinterpret_cast<uint2*>(dst + (size_t)e * N) =
-                  make_uint2(bf16x2_rn(y0, y1), bf16x2_rn(y2, y3));
-          }
+          for (int e = 0; e < 32; ++e)
+            if (e < nv) *reinterpret_cast<uint16_t*>(dst + e * kOutPitch) = f32_to_bf16_rne(v[e]);
         }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote(cluster_addr(&d_empty, lead));
+      if (p.split == 1) {
+        // whole 256-byte rows to global memory, while the next tile's MMAs run
+        named_barrier(kEpiBar, kEpiThreads);
+        const int col = n0 + (et & 15) * 8;
+        if (col < N && !fail)
+          for (int t = et >> 4; t < n; t += kEpiThreads / 16)
+            *reinterpret_cast<uint4*>(p.a.out + (size_t)(t0 + t) * N + col) =
+                *reinterpret_cast<const uint4*>(sL + t * kOutPitch + (et & 15) * 16);
+        // the next tile's adapter columns go there; these warps go on or leave together
+        if (fail) s_efail[it & 1] = 1;
+        named_barrier(kEpiBar, kEpiThreads);
+        if (s_efail[it & 1]) fail = 1;
       }
     }
   }
+  __syncwarp();
   // no MMA may still read the pair's memory when it is released
   if (!warp_wait_cluster(&drain, 0)) fail = 1;
   __syncwarp();
@@ -668,6 +693,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
   if (p.split > 1) {
     // y of tokens part, part + split, ..: the pairs' partial sums in rank order
     const uint32_t red = smem_u32(sX);
+    const int t0 = tile_t0(cluster), n0 = tile_n0(cluster);   // one tile per cluster
+    const int n = min(p.cs, p.a.T - t0);
     for (int t = part + p.split * warp; t < n; t += p.split * kWarps) {
       float4 z[4];   // all in flight before the first is used
 #pragma unroll
@@ -779,7 +806,7 @@ cudaError_t launch_linear(const LinearArgs& a, int num_sms, cudaStream_t stream)
   linear_plan(a.T, a.N, a.K, num_sms, p.cs, p.split);
   const int xstage = p.cs / 2 * 256;
   p.S = (kTmemCols - ((p.cs + 31) & ~31)) / kWCols;   // 4 at 256 tokens, 7 at 16
-  p.SP = 6;
+  p.SP = p.cs > 128 ? 3 : 6;
   p.SL = !adapters ? 0 : p.cs > 128 ? 1 : p.cs > 64 ? 2 : kMaxL;
   p.rp = (a.rank + 15) & ~15;
   const int npair = (a.N + 2 * kBM - 1) / (2 * kBM), ttile = (a.T + p.cs - 1) / p.cs;
@@ -791,8 +818,10 @@ cudaError_t launch_linear(const LinearArgs& a, int num_sms, cudaStream_t stream)
       !encode_tiled_2d(&p.tmapW, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.w, (uint64_t)a.K / 2, (uint64_t)a.N,
                        (uint64_t)a.K / 2, kStageK / 2, kBM, CU_TENSOR_MAP_SWIZZLE_64B))
     return cudaErrorInvalidValue;
-  const size_t smem = 1024 + (size_t)p.S * xstage + (size_t)p.SL * (kBTile + xstage / 2) +
-                      (size_t)p.SP * kPStage;
+  p.tiles = (int)tiles;
+  const size_t lbytes = (size_t)p.SL * (kBTile + xstage / 2), obytes = (size_t)p.cs * kOutPitch;
+  const size_t smem = 1024 + (size_t)p.S * xstage + (size_t)p.SP * kPStage +
+                      (p.split == 1 && obytes > lbytes ? obytes : lbytes);
   static size_t granted[kGrantDevices] = {};
   int dev = 0;
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
@@ -803,7 +832,8 @@ cudaError_t launch_linear(const LinearArgs& a, int num_sms, cudaStream_t stream)
     granted[dev] = smem;
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(tiles * p.split * 2));
+  const int64_t resident = num_sms / (2 * p.split);   // persistent clusters
+  cfg.gridDim = dim3((unsigned)((tiles < resident ? tiles : resident) * p.split * 2));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
