@@ -5,16 +5,17 @@
 // x in bf16, or in MXFP8 (E4M3 with an E8M0 scale per 32 values). Sums in
 // fp32, one rounding of y to bf16.
 //
-//   convert  (MXFP8 only) x as bf16 rows: exact but for products beyond bf16's range
-//   down     v_t = A_a x_t in fp32: the tokens of a window grouped by adapter, up
-//            to 32 of one adapter to a pass of m16n8k16 tiles, K split over the
-//            warps of a CTA and, for few tokens, over CTAs
+//   prepare  v_t = bf16(scale_a * A_a x_t): the tokens of a window grouped by
+//            adapter, up to 32 of one adapter to a pass of m16n8k16 tiles, K split over the
+//            warps of a CTA and, for few tokens, over the CTAs of a cluster.
+//            MXFP8 rows are converted on the way, once, to the bf16 rows that
+//            the projection reads (exact but for products beyond bf16's range)
 //   linear   the projection on the 5th-generation tensor cores, the second
 //            adapter product as further columns of the same reduction
 //
-// v is scaled and rounded to bf16 as the projection takes it: the rounding
-// (relative 2^-8 of the adapter's share of y, below the rounding of y itself)
-// is what lets that product run on the same tensor-core accumulators.
+// The rounding of v to bf16 (relative 2^-8 of the adapter's share of y, below
+// the rounding of y itself) is what lets that product run on the same
+// tensor-core accumulators.
 //
 // linear kernel: a pair of CTAs holds a tile of 256 weight rows x up to 256
 // tokens. The MMA computes D[weight row][token] with the dequantised weights as
@@ -50,29 +51,40 @@
 namespace mxmoe {
 namespace {
 
-// ---------------------------------------------------------------------------
-// MXFP8 rows -> bf16 rows, 16 values a thread
-// ---------------------------------------------------------------------------
+// bf16 rows in pair order (values 0 4 1 5 2 6 3 7 of each group of 8), the order
+// in which the bit placement of dequant32_bf16_pairs makes the weights: saves
+// the projection a quarter of its dequantisation (470 -> 346 clocks a stage)
+__device__ __forceinline__ uint4 pair_order(const uint4& u) {
+  return make_uint4(prmt(u.x, u.z, 0x5410u), prmt(u.x, u.z, 0x7632u), prmt(u.y, u.w, 0x5410u),
+                    prmt(u.y, u.w, 0x7632u));
+}
+// 16 E4M3 values of one scale block -> bf16, in row order.
+__device__ __forceinline__ void e4m3x16_to_bf16(const uint4& u, uint32_t scale, uint4& a, uint4& b) {
+  const ScaleMul sm = e4m3_scale_mul(scale);
+  e4m3x4_to_bf16(u.x, sm, a.x, a.y);
+  e4m3x4_to_bf16(u.y, sm, a.z, a.w);
+  e4m3x4_to_bf16(u.z, sm, b.x, b.y);
+  e4m3x4_to_bf16(u.w, sm, b.z, b.w);
+}
+
+// MXFP8 rows -> bf16 rows in pair order, 16 values a thread (calls without adapters).
 __global__ void __launch_bounds__(256) mx8_to_bf16_kernel(const uint4* __restrict__ q,
                                                           const uint8_t* __restrict__ s, int64_t n16,
                                                           uint4* __restrict__ out) {
+  grid_launch_dependents();
   for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < n16; i += (int64_t)gridDim.x * 256) {
-    const uint4 u = q[i];
-    const ScaleMul sm = e4m3_scale_mul(ldg_u8(s + (i >> 1)));
     uint4 a, b;
-    e4m3x4_to_bf16(u.x, sm, a.x, a.y);
-    e4m3x4_to_bf16(u.y, sm, a.z, a.w);
-    e4m3x4_to_bf16(u.z, sm, b.x, b.y);
-    e4m3x4_to_bf16(u.w, sm, b.z, b.w);
-    out[2 * i] = a;
-    out[2 * i + 1] = b;
+    e4m3x16_to_bf16(q[i], ldg_u8(s + (i >> 1)), a, b);
+    out[2 * i] = pair_order(a);
+    out[2 * i + 1] = pair_order(b);
   }
 }
 
 // ---------------------------------------------------------------------------
-// v = A x: windows of tokens, items of up to 32 tokens of one adapter.
-// gridDim.y CTAs take a window's items in turn, gridDim.z CTAs split K; each
-// writes its fp32 part, the projection adds them in order.
+// v = bf16(scale A x): windows of tokens, items of up to 32 tokens of one
+// adapter (with MXFP8 rows also of none: those are only converted). gridDim.y
+// CTAs take a window's items in turn; the gridDim.z CTAs of a cluster split K
+// and add their parts in rank order through shared memory.
 // ---------------------------------------------------------------------------
 constexpr int kDownWin = 128;     // tokens per window
 constexpr int kDownTok = 32;      // tokens per item (two m16 tiles)
@@ -80,32 +92,38 @@ constexpr int kDownMaxParts = 8;
 constexpr int kDownStep = 64;     // K values per step: 16 a lane
 
 // NT: n-tiles of 8 ranks per pass.
-template <int NT>
-__global__ void __launch_bounds__(256) adapter_down_kernel(const uint16_t* __restrict__ x,
-                                                           const LinearArgs a,
-                                                           float* __restrict__ v) {
+template <int NT, bool X8>
+__global__ void __launch_bounds__(256, 2) adapter_down_kernel(const LinearArgs a, uint16_t* __restrict__ xb,
+                                                           uint16_t* __restrict__ v) {
   __shared__ int s_id[kDownWin], s_item[kDownWin], s_warp[8];
   __shared__ int s_tok[kDownWin][kDownTok];   // [item][slot]: token of the window, -1 empty
   __shared__ int s_ad[kDownWin];
   __shared__ float part[8][16][NT * 8 + 4];
+  __shared__ __align__(16) float s_sum[16][NT * 8];   // this CTA's part of an m-tile
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int w0 = blockIdx.x * kDownWin;
+  const int parts = gridDim.z;
   grid_launch_dependents();
 
-  // group the window's tokens by adapter
-  int id = -1;
+  // group the window's tokens by adapter: id -1 (no adapter) is a class of its
+  // own where rows are converted; -2 stays out
+  constexpr int kNone = X8 ? -1 : -2;
+  int id = -2;
   if (tid < kDownWin) {
-    if (w0 + tid < a.T) id = a.ids[w0 + tid];
-    if (id >= a.L) {
-      if (a.status != nullptr && blockIdx.y == 0 && blockIdx.z == 0) atomicAdd(a.status, 1);
-      id = -1;
+    if (w0 + tid < a.T) {
+      id = a.ids[w0 + tid];
+      if (id >= a.L) {
+        if (a.status != nullptr && blockIdx.y == 0 && blockIdx.z == 0) atomicAdd(a.status, 1);
+        id = kNone;
+      }
+      if (id < 0) id = kNone;
     }
-    s_id[tid] = id < 0 ? -1 : id;
+    s_id[tid] = id;
   }
   for (int i = tid; i < kDownWin * kDownTok; i += 256) s_tok[i / kDownTok][i % kDownTok] = -1;
   __syncthreads();
-  int rank = 0, leader = tid;   // earlier tokens of this adapter; first token of this one's item
-  if (tid < kDownWin && id >= 0) {
+  int rank = 0, leader = tid;   // earlier tokens of this class; first token of this one's item
+  if (tid < kDownWin && id > -2) {
     for (int j = 0; j < tid; ++j)
       if (s_id[j] == id) {
         if (rank % kDownTok == 0) leader = j;
@@ -113,7 +131,7 @@ __global__ void __launch_bounds__(256) adapter_down_kernel(const uint16_t* __res
       }
     if (rank % kDownTok == 0) leader = tid;
   }
-  const bool lead = tid < kDownWin && id >= 0 && leader == tid;
+  const bool lead = tid < kDownWin && id > -2 && leader == tid;
   const uint32_t bal = __ballot_sync(0xffffffffu, lead);
   if (lane == 0) s_warp[warp] = __popc(bal);
   __syncthreads();
@@ -128,45 +146,72 @@ __global__ void __launch_bounds__(256) adapter_down_kernel(const uint16_t* __res
     s_ad[it] = id;
   }
   __syncthreads();
-  if (tid < kDownWin && id >= 0) s_tok[s_item[leader]][rank % kDownTok] = tid;
+  if (tid < kDownWin && id > -2) s_tok[s_item[leader]][rank % kDownTok] = tid;
   __syncthreads();
 
   const int g = lane >> 2, q = lane & 3;
-  const int slices = 8 * gridDim.z, slice = blockIdx.z * 8 + warp;
+  const int slices = 8 * parts, slice = blockIdx.z * 8 + warp;
   const int steps = a.K / kDownStep;
   const int k0 = steps * slice / slices, k1 = steps * (slice + 1) / slices;
   for (int it = blockIdx.y; it < items; it += gridDim.y) {
     const int ad = s_ad[it];
     const bool two = s_tok[it][16] >= 0;   // a second m-tile
     int tk[4];
-    const uint16_t* xr[4];
+    size_t xo[4];                          // value offsets of this lane's rows
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       tk[i] = s_tok[it][g + 8 * i];
-      xr[i] = x + (size_t)(w0 + max(tk[i], 0)) * a.K + 16 * q;
+      xo[i] = (size_t)(w0 + max(tk[i], 0)) * a.K + 16 * q;
     }
-    for (int r0 = 0; r0 < a.rank; r0 += NT * 8) {
-      const int nt = min(NT, (a.rank - r0) / 8);
-      const uint16_t* ar = a.a + ((size_t)ad * a.rank + r0 + g) * a.K + 16 * q;
+    const int passes = ad < 0 ? 1 : (a.rank + NT * 8 - 1) / (NT * 8);
+    for (int pass = 0; pass < passes; ++pass) {
+      const int r0 = pass * NT * 8;
+      const int nt = ad < 0 ? 0 : min(NT, (a.rank - r0) / 8);
+      const uint16_t* ar = a.a + ((size_t)max(ad, 0) * a.rank + r0 + g) * a.K + 16 * q;
       float acc[2][NT][4] = {};
       // each lane holds 16 consecutive values of its rows; both operands take
       // them in the same order, so the products are those of row order
+#pragma unroll NT <= 2 ? 2 : 1
       for (int k = k0; k < k1; ++k) {
-        uint4 u[4][2], w[NT][2];
+        uint4 u[4][2], w[NT][2], e[4];
+        uint32_t sc[4];
+        if (ad >= 0) {
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {   // (past the rank: the last rows again, never stored)
-          const uint16_t* src = ar + (size_t)(8 * (j < nt ? j : nt - 1)) * a.K + kDownStep * k;
-          w[j][0] = *reinterpret_cast<const uint4*>(src);
-          w[j][1] = *reinterpret_cast<const uint4*>(src + 8);
+          for (int j = 0; j < NT; ++j) {   // (past the rank: the last rows again, never stored)
+            const uint16_t* src = ar + (size_t)(8 * (j < nt ? j : nt - 1)) * a.K + kDownStep * k;
+            w[j][0] = *reinterpret_cast<const uint4*>(src);
+            w[j][1] = *reinterpret_cast<const uint4*>(src + 8);
+          }
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          u[i][0] = u[i][1] = make_uint4(0u, 0u, 0u, 0u);
+          u[i][0] = u[i][1] = e[i] = make_uint4(0u, 0u, 0u, 0u);
+          sc[i] = 0;
           if (tk[i] >= 0) {
-            u[i][0] = *reinterpret_cast<const uint4*>(xr[i] + kDownStep * k);
-            u[i][1] = *reinterpret_cast<const uint4*>(xr[i] + kDownStep * k + 8);
+            if (X8) {
+              e[i] = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.x) + xo[i] +
+                                                     kDownStep * k);
+              sc[i] = ldg_u8(a.xs + (xo[i] + kDownStep * k) / kScaleBlock);
+            } else {
+              const uint16_t* x = static_cast<const uint16_t*>(a.x) + xo[i] + kDownStep * k;
+              u[i][0] = *reinterpret_cast<const uint4*>(x);
+              u[i][1] = *reinterpret_cast<const uint4*>(x + 8);
+            }
           }
         }
+        if (X8) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (tk[i] < 0) continue;
+            e4m3x16_to_bf16(e[i], sc[i], u[i][0], u[i][1]);
+            if (pass == 0) {
+              uint4* dst = reinterpret_cast<uint4*>(xb + xo[i] + kDownStep * k);
+              dst[0] = pair_order(u[i][0]);
+              dst[1] = pair_order(u[i][1]);
+            }
+          }
+        }
+        if (ad < 0) continue;
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
           if (m == 1 && !two) break;
@@ -180,6 +225,8 @@ __global__ void __launch_bounds__(256) adapter_down_kernel(const uint16_t* __res
             }
         }
       }
+      if (ad < 0) break;
+      const float scale = a.ascale != nullptr ? a.ascale[ad] : 1.f;
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
         if (m == 1 && !two) break;
@@ -197,9 +244,38 @@ __global__ void __launch_bounds__(256) adapter_down_kernel(const uint16_t* __res
           float z = 0.f;
 #pragma unroll
           for (int w = 0; w < 8; ++w) z += part[w][row][r];
-          if (t >= 0) v[((size_t)blockIdx.z * a.T + w0 + t) * a.rank + r0 + r] = z;
+          if (parts > 1)
+            s_sum[row][r] = z;
+          else if (t >= 0)
+            v[(size_t)(w0 + t) * a.rank + r0 + r] = f32_to_bf16_rne(z * scale);
         }
-        __syncthreads();
+        if (parts > 1) {   // rows cluster rank, rank + parts, ..: the CTAs' parts in order
+          cluster_sync();
+          const uint32_t me = cluster_rank();
+          for (int i = tid; i < 16 * 2 * nt; i += 256) {
+            const int row = i / (2 * nt), r = (i - row * (2 * nt)) * 4;
+            const int t = s_tok[it][16 * m + row];
+            if (row % parts != me || t < 0) continue;
+            float4 z[kDownMaxParts];
+#pragma unroll
+            for (int c = 0; c < kDownMaxParts; ++c)
+              if (c < parts) z[c] = ld_cluster16(smem_u32(&s_sum[row][r]), c);
+            float4 y = z[0];
+#pragma unroll
+            for (int c = 1; c < kDownMaxParts; ++c)
+              if (c < parts) {
+                y.x += z[c].x;
+                y.y += z[c].y;
+                y.z += z[c].z;
+                y.w += z[c].w;
+              }
+            *reinterpret_cast<uint2*>(v + (size_t)(w0 + t) * a.rank + r0 + r) =
+                make_uint2(bf16x2_rn(y.x * scale, y.y * scale), bf16x2_rn(y.z * scale, y.w * scale));
+          }
+          cluster_sync();   // s_sum is read by the whole cluster until here
+        } else {
+          __syncthreads();
+        }
       }
     }
   }
@@ -223,15 +299,14 @@ constexpr int kEpiWarps = kWarpDeq - kWarpEpi, kEpiThreads = kEpiWarps * 32;
 constexpr int kDeqGroups = (kWarps - kWarpDeq) / 4;
 constexpr int kEpiBar = 1;            // named barrier of the adapter and epilogue warps
 constexpr int kOutPitch = kBM * 2 + 16;   // bytes of a staged output row (128 bf16 and a bank shift)
-constexpr int kAhead = 2;             // own stages of scale bytes in a dequantising thread's registers
 constexpr int kListMax = kMaxTok;     // adapters that one tile can name
+constexpr int kMaxSplit = 4;          // pairs of a cluster that share a tile's K
 
 struct LinearParams {
   CUtensorMap tmapX;   // x as bytes {128, T, K / 64}, box {128, cs / 2, 2}, 128-byte swizzle
   CUtensorMap tmapW;   // packed weights u8 [N][K/2], box {64, 128}, 64-byte swizzle
   LinearArgs a;
-  const float* v;      // fp32 [parts][T][rank]
-  int parts;
+  const uint16_t* v;   // bf16 [T][rank]: scale_a A_a x_t, from the kernel before
   int cs;              // tokens per tile (multiple of 16, at most 256)
   int S, SP, SL;       // ring depths: operand stages, packed weights, adapter columns
   int split;           // pairs of a cluster that share a tile's K
@@ -239,9 +314,6 @@ struct LinearParams {
   int tiles;           // (pair of weight blocks, token tile)
 };
 
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity));
-}
 // Whether a bf16 of the pair is not finite.
 __device__ __forceinline__ bool nonfinite_bf16x2(uint32_t w) {
   return ((w & 0x7F80u) == 0x7F80u) || ((w & 0x7F800000u) == 0x7F800000u);
@@ -263,27 +335,9 @@ __device__ __forceinline__ void tmem_st16_nowait(uint32_t taddr, const uint32_t 
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
-// bf16(scale * v) of token t, ranks r .. r + 7: the parts added in order. v is
-// another kernel's output that may still be written when this one starts, so
-// its loads take no read-only path.
-__device__ __forceinline__ uint4 adapter_inner8(const LinearParams& p, int t, int r, float scale) {
-  float z[8] = {};
-  for (int i = 0; i < p.parts; ++i) {
-    const float* src = p.v + ((size_t)i * p.a.T + t) * p.a.rank + r;
-    const uint4 lo = ldcg16(src), hi = ldcg16(src + 4);
-    z[0] += __uint_as_float(lo.x);
-    z[1] += __uint_as_float(lo.y);
-    z[2] += __uint_as_float(lo.z);
-    z[3] += __uint_as_float(lo.w);
-    z[4] += __uint_as_float(hi.x);
-    z[5] += __uint_as_float(hi.y);
-    z[6] += __uint_as_float(hi.z);
-    z[7] += __uint_as_float(hi.w);
-  }
-  return make_uint4(bf16x2_rn(z[0] * scale, z[1] * scale), bf16x2_rn(z[2] * scale, z[3] * scale),
-                    bf16x2_rn(z[4] * scale, z[5] * scale), bf16x2_rn(z[6] * scale, z[7] * scale));
-}
-
+// PAIR: x's rows come in pair order from the kernel before this one (MXFP8);
+// otherwise they are the caller's, in row order.
+template <bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_constant__ LinearParams p) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t full[kMaxS], empty[kMaxS], p_full[kMaxSP], p_empty[kMaxSP], l_full[kMaxL],
@@ -319,20 +373,37 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
   const bool adapters = p.a.ids != nullptr;
   int fail = 0;
 
-  if (threadIdx.x == 0) {
-    // full and l_full of the issuing CTA count both CTAs' warps; one thread's
-    // expect covers both CTAs' token copies
-    for (int i = 0; i < p.S; ++i) { mbar_init(&full[i], 1 + 2 * 4); mbar_init(&empty[i], 1); }
-    for (int i = 0; i < p.SP; ++i) { mbar_init(&p_full[i], 1); mbar_init(&p_empty[i], 4); }
-    for (int i = 0; i < p.SL; ++i) { mbar_init(&l_full[i], 2 * kEpiWarps); mbar_init(&l_empty[i], 1); }
-    mbar_init(&l_list, 1);
-    mbar_init(&d_full, 1);
-    mbar_init(&d_empty, 2 * kEpiWarps);
-    mbar_init(&drain, 1);
+  // full and l_full of the issuing CTA count both CTAs' warps; one thread's
+  // expect covers both CTAs' token copies
+  if (warp == kWarpX) {
+    if (lane < p.S) { mbar_init(&full[lane], 1 + 2 * 4); mbar_init(&empty[lane], 1); }
+    if (lane < p.SL) { mbar_init(&l_full[lane], 2 * kEpiWarps); mbar_init(&l_empty[lane], 1); }
+    if (lane == 8) mbar_init(&l_list, 1);
+    if (lane == 9) mbar_init(&d_full, 1);
+    if (lane == 10) mbar_init(&d_empty, 2 * kEpiWarps);
+    if (lane == 11) mbar_init(&drain, 1);
+    if (lane == 12) {
+      prefetch_tensormap(&p.tmapX);
+      s_fail = s_efail[0] = s_efail[1] = 0;
+    }
     fence_barrier_init();
-    prefetch_tensormap(&p.tmapX);
-    prefetch_tensormap(&p.tmapW);
-    s_fail = s_efail[0] = s_efail[1] = 0;
+  }
+  // the first packed weights need this CTA's barriers alone: under way before
+  // the cluster has met
+  int wk = 0;   // stages of them issued
+  if (warp == kWarpW) {
+    if (lane < p.SP) { mbar_init(&p_full[lane], 1); mbar_init(&p_empty[lane], 4); }
+    fence_barrier_init();
+    fence_proxy_async_smem();
+    __syncwarp();
+    for (; wk < p.SP && wk < nS && cluster < p.tiles; ++wk) {
+      if (elect_one()) {
+        mbar_arrive_expect_tx(&p_full[wk], kPStage);
+        tma_load_2d(sP + wk * kPStage, &p.tmapW, (st0 + wk) * (kStageK / 2), tile_n0(cluster),
+                    &p_full[wk]);
+      }
+      __syncwarp();
+    }
   }
   if (warp == kWarpMma) tmem2_alloc(&tmem_slot, kTmemCols);
   tc_fence_before();
@@ -346,6 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
     // ------------------------------------------------------------ token copies
     int s = 0, k = 0;
     uint32_t ph = 0;
+    if (PAIR) grid_dependency_wait();
     for (int tile = cluster; tile < p.tiles && !fail; tile += clusters) {
       const int row = tile_t0(tile) + half * hb;
       for (int i = 0; i < nS; ++i, ++k) {
@@ -361,12 +433,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
     }
   } else if (warp == kWarpW) {
     // ------------------------------------------------------------ packed-weight copies
-    int s = 0, k = 0;
-    uint32_t ph = 0;
+    int s = wk == p.SP ? 0 : wk, k = wk, first = wk;
+    uint32_t ph = wk == p.SP ? 1 : 0;
     for (int tile = cluster; tile < p.tiles && !fail; tile += clusters) {
       const int n0 = tile_n0(tile);
-      for (int i = 0; i < nS; ++i, ++k) {
-        if (k >= p.SP && !warp_wait(&p_empty[s], ph ^ 1u)) { fail = 1; break; }
+      for (int i = first; i < nS; ++i, ++k) {
+        if (k >= p.SP && !warp_wait_cta(&p_empty[s], ph ^ 1u)) { fail = 1; break; }
         if (elect_one()) {
           mbar_arrive_expect_tx(&p_full[s], kPStage);
           tma_load_2d(sP + s * kPStage, &p.tmapW, (st0 + i) * (kStageK / 2), n0, &p_full[s]);
@@ -374,6 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
         __syncwarp();
         if (++s == p.SP) { s = 0; ph ^= 1u; }
       }
+      first = 0;
     }
   } else if (warp == kWarpMma) {
     // ------------------------------------------------------------ MMA issue
@@ -408,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
           if (++s == p.S) { s = 0; ph ^= 1u; }
         }
         if (adapters && !fail) {
-          if (!warp_wait(&l_list, it & 1)) { fail = 1; break; }
+          if (!warp_wait_cta(&l_list, it & 1)) { fail = 1; break; }
           const int lcols = s_count * p.rp;
           for (int i = part; i * kBK < lcols; i += p.split) {
             if (!warp_wait_cluster(&l_full[ls], lph)) { fail = 1; break; }
@@ -435,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
     // ------------------------------------------------------------ dequantisation
     // A group of four warps takes a whole stage; a thread holds one weight row
     // (TMEM lane), its 64 packed bytes of the stage from shared memory and its
-    // four scale bytes straight from global memory, kAhead of its stages early.
+    // four scale bytes straight from global memory, two of its stages early.
     // (The packed bytes too, straight into registers, cost 3000 clocks a stage:
     // 32 rows a warp load are 32 requests each.)
     const int dg = (warp - kWarpDeq) >> 2;   // group: stages dg, dg + kDeqGroups, .. of all tiles
@@ -450,58 +523,55 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
     for (int tile = cluster; tile < p.tiles && !fail; tile += clusters) {
       const uint8_t* srow = p.a.s + (size_t)min(tile_n0(tile) + m, N - 1) * (K / kScaleBlock) +
                             st0 * (kStageK / kScaleBlock);   // rows past N: the last row, never stored
-      uint32_t sc[kAhead];
-      auto load = [&](int slot, int i) {
-        if (i >= nS) return;
-        if (words) {
-          sc[slot] = __ldg(reinterpret_cast<const uint32_t*>(srow + 4 * i));
-        } else {
-          sc[slot] = ldg_u16(srow + 4 * i);
-          if ((st0 + i) * kStageK + kBK < K) sc[slot] |= ldg_u16(srow + 4 * i + 2) << 16;
-        }
+      auto scales = [&](int i) -> uint32_t {
+        if (i >= nS) return 0u;
+        if (words) return __ldg(reinterpret_cast<const uint32_t*>(srow + 4 * i));
+        uint32_t v = ldg_u16(srow + 4 * i);
+        if ((st0 + i) * kStageK + kBK < K) v |= ldg_u16(srow + 4 * i + 2) << 16;
+        return v;
       };
-#pragma unroll
-      for (int j = 0; j < kAhead; ++j) load(j, i0 + kDeqGroups * j);
       int i = i0;
-      while (i < nS && !fail) {
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-          if (i >= nS || fail) break;
-          if (!warp_wait(&p_full[sp], pp)) { fail = 1; break; }
-          uint4 w[4];
-          const uint8_t* src = sP + sp * kPStage + m * 64;
-#pragma unroll
-          for (int z = 0; z < 4; ++z)
-            w[z] = *reinterpret_cast<const uint4*>(src + ((z ^ ((m >> 1) & 3)) << 4));
-          // the generic reads above are ordered before the stage's refill by a tensor copy
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&p_empty[sp]);
-          if (k >= p.S) {   // the MMAs that read this ring slot have completed
-            if (!warp_wait_cluster(&empty[s], ph ^ 1u)) { fail = 1; break; }
-            tc_fence_after();
-          }
-          const bool both = (st0 + i) * kStageK + kBK < K;
-#pragma unroll
-          for (int z = 0; z < 4; ++z) {
-            if (z == 2 && !both) break;
-            const uint32_t wd[4] = {w[z].x, w[z].y, w[z].z, w[z].w};
-            uint32_t o[16];
-            dequant32_bf16(wd, scale_mul((sc[j] >> (8 * z)) & 255u), o);
-            tmem_st16_nowait(wlane + s * kWCols + 16 * z, o);
-          }
-          load(j, i + kDeqGroups * kAhead);
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_remote(cluster_addr(&full[s], lead));
-          i += kDeqGroups;
-          k += kDeqGroups;
-          s += kDeqGroups;
-          while (s >= p.S) { s -= p.S; ph ^= 1u; }
-          sp += kDeqGroups;
-          while (sp >= p.SP) { sp -= p.SP; pp ^= 1u; }
+      uint32_t sc = scales(i), sc1 = scales(i + kDeqGroups);
+#pragma unroll 1
+      for (; i < nS; i += kDeqGroups) {
+        if (!warp_wait_cta(&p_full[sp], pp)) { fail = 1; break; }
+        const uint8_t* src = sP + sp * kPStage + m * 64;
+        const int swz = (m >> 1) & 3;
+        if (k >= p.S) {   // the MMAs that read this ring slot have completed
+          if (!warp_wait_cluster(&empty[s], ph ^ 1u)) { fail = 1; break; }
+          tc_fence_after();
         }
+        const int blocks = (st0 + i) * kStageK + kBK < K ? 4 : 2;   // K may end inside the stage
+        const uint32_t dst = wlane + s * kWCols;
+        uint4 w = *reinterpret_cast<const uint4*>(src + (swz << 4));
+        // one block's code, run four times: unrolled, the groups' loops outgrew
+        // the instruction cache
+#pragma unroll 1
+        for (int z = 0; z < blocks; ++z) {
+          const uint32_t wd[4] = {w.x, w.y, w.z, w.w};
+          w = *reinterpret_cast<const uint4*>(src + ((((z + 1) & 3) ^ swz) << 4));
+          uint32_t o[16];
+          if (PAIR)
+            dequant32_bf16_pairs(wd, scale_mul((sc >> (8 * z)) & 255u), o);
+          else
+            dequant32_bf16(wd, scale_mul((sc >> (8 * z)) & 255u), o);
+          tmem_st16_nowait(dst + 16 * z, o);
+        }
+        // the generic reads above are ordered before the stage's refill by a tensor copy
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_empty[sp]);
+        sc = sc1;
+        sc1 = scales(i + 2 * kDeqGroups);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(cluster_addr(&full[s], lead));
+        k += kDeqGroups;
+        s += kDeqGroups;
+        while (s >= p.S) { s -= p.S; ph ^= 1u; }
+        sp += kDeqGroups;
+        while (sp >= p.SP) { sp -= p.SP; pp ^= 1u; }
       }
       i0 = i - nS;
     }
@@ -557,7 +627,6 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
           const int ai = c / p.rp, r = c - ai * p.rp;
           const bool live = ai < count && r < p.a.rank;
           const int ad = live ? s_list[ai] : -1;
-          const float vscale = live && p.a.ascale != nullptr ? p.a.ascale[ad] : 1.f;
           constexpr int kPer = kBM * 8 / kEpiThreads;
           uint4 b[kPer];   // in flight together
 #pragma unroll
@@ -591,7 +660,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
           for (int t = et >> 3; t < hb; t += kEpiThreads / 8) {
             uint4 u = make_uint4(0u, 0u, 0u, 0u);
             if (live && s_tokad[half * hb + t] == ad)
-              u = adapter_inner8(p, t0 + half * hb + t, r, vscale);
+              u = ldcg16(p.v + (size_t)(t0 + half * hb + t) * p.a.rank + r);   // (no read-only path:
+                               // v may still be written when this kernel starts)
             *reinterpret_cast<uint4*>(tv + t * 128 + ((j ^ (t & 7)) << 4)) = u;
           }
           fence_proxy_async_smem();
@@ -629,11 +699,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
             for (int r = 0; r < p.a.rank; ++r) {
               const uint32_t bw = p.a.b[((size_t)ad * N + row) * p.a.rank + r];
               if ((bw & 0x7F80u) == 0x7F80u) {
-                const uint4 u = adapter_inner8(p, t0 + c0 + t, r & ~7,
-                                               p.a.ascale != nullptr ? p.a.ascale[ad] : 1.f);
-                const uint32_t two = (r & 4) ? ((r & 2) ? u.w : u.z) : ((r & 2) ? u.y : u.x);
-                z += __uint_as_float(bw << 16) *
-                     __uint_as_float((r & 1) ? two & 0xFFFF0000u : two << 16);
+                const uint32_t vw = p.v[(size_t)(t0 + c0 + t) * p.a.rank + r];
+                z += __uint_as_float(bw << 16) * __uint_as_float(vw << 16);
               }
             }
 #pragma unroll
@@ -677,7 +744,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
   __syncwarp();
   if (fail) s_fail = 1;
   if (fail && p.a.status != nullptr) {
-    if (adapters) grid_dependency_wait();   // the status words belong to that kernel until then
+    if (adapters || PAIR) grid_dependency_wait();   // the status words belong to that kernel until then
     atomicOr(&p.a.status[2], 1);
     atomicCAS(&p.a.status[3], 0, blockIdx.x + 1);
   }
@@ -696,13 +763,13 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
     const int t0 = tile_t0(cluster), n0 = tile_n0(cluster);   // one tile per cluster
     const int n = min(p.cs, p.a.T - t0);
     for (int t = part + p.split * warp; t < n; t += p.split * kWarps) {
-      float4 z[4];   // all in flight before the first is used
+      float4 z[kMaxSplit];   // all in flight before the first is used
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
+      for (int c = 0; c < kMaxSplit; ++c)
         if (c < p.split) z[c] = ld_cluster16(red + (t * kBM + lane * 4) * 4, 2 * c + half);
       float4 y = z[0];
 #pragma unroll
-      for (int c = 1; c < 4; ++c)
+      for (int c = 1; c < kMaxSplit; ++c)
         if (c < p.split) {
           y.x += z[c].x;
           y.y += z[c].y;
@@ -721,49 +788,93 @@ size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 
 }  // namespace
 
-// CTAs that share an adapter product's K: 8 where the tokens make few items.
-static int down_parts(int T, int K) {
-  constexpr int kSms = 152;   // the workspace's size cannot depend on the device at hand
-  int parts = kSms / ((T + kDownTok - 1) / kDownTok);
-  if (parts > kDownMaxParts) parts = kDownMaxParts;
-  while (parts > 1 && K / kDownStep < 8 * parts) --parts;
-  return parts < 1 ? 1 : parts;
-}
-
 size_t linear_workspace_bytes(int T, int K, int N, int rank, bool x8) {
   (void)N;
-  return up256((size_t)down_parts(T, K) * T * rank * 4) + (x8 ? up256((size_t)T * K * 2) : 0);
+  return up256((size_t)T * rank * 2) + (x8 ? up256((size_t)T * K * 2) : 0);
 }
 
-template <int NT>
-static void launch_down(const uint16_t* x, const LinearArgs& a, float* v, int parts, int num_sms,
-                        cudaStream_t stream) {
+// The kernel of the adapters' first product (and of the conversion): CTAs over
+// windows, their items and, while those are few, parts of K.
+template <int NT, bool X8>
+static cudaError_t launch_down(const LinearArgs& a, uint16_t* xb, uint16_t* v, int num_sms,
+                               cudaStream_t stream) {
+  const int items = (a.T + kDownTok - 1) / kDownTok;   // at least
+  int parts = 1;
+  while (parts < kDownMaxParts && items * parts * 2 <= 2 * num_sms &&
+         a.K / kDownStep >= 2 * 8 * parts)
+    parts *= 2;
   const int win = (a.T + kDownWin - 1) / kDownWin;
-  int slots = (2 * num_sms + win - 1) / win;
-  if (slots < 4) slots = 4;
+  int slots = 4 * num_sms / (win * parts);   // CTAs past a window's items leave at once
+  if (slots < 8) slots = 8;
   if (slots > kDownWin) slots = kDownWin;
   if (slots > a.T) slots = a.T;
-  adapter_down_kernel<NT><<<dim3(win, slots, parts), 256, 0, stream>>>(x, a, v);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(win, slots, parts);
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = parts;
+  cfg.attrs = at;
+  cfg.numAttrs = parts > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, adapter_down_kernel<NT, X8>, a, xb, v);
+}
+
+// Clusters of 2 * split CTAs that are resident at once (a cluster stays inside a
+// group of SMs, and those groups are not multiples of every size): asked of the
+// driver once per device.
+static cudaError_t resident_clusters(int dev, int (&out)[kMaxSplit + 1]) {
+  static int known[kGrantDevices][kMaxSplit + 1] = {};
+  if (known[dev][1] == 0) {
+    constexpr int kSmem = 227 * 1024 - 4096;   // one CTA per SM
+    for (auto* k : {linear_kernel<false>, linear_kernel<true>}) {
+      const cudaError_t e =
+          cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+      if (e != cudaSuccess) return e;
+    }
+    for (int sp = kMaxSplit; sp >= 1; --sp) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(2 * sp * 64);
+      cfg.blockDim = dim3(kThreads);
+      cfg.dynamicSmemBytes = kSmem;
+      cudaLaunchAttribute at[1];
+      at[0].id = cudaLaunchAttributeClusterDimension;
+      at[0].val.clusterDim.x = 2 * sp;
+      at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+      cfg.attrs = at;
+      cfg.numAttrs = 1;
+      int n = 0;
+      const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, linear_kernel<false>, &cfg);
+      if (e != cudaSuccess) return e;
+      if (n < 1 && sp == 1) return cudaErrorInvalidConfiguration;
+      known[dev][sp] = n;
+    }
+  }
+  for (int sp = 1; sp <= kMaxSplit; ++sp) out[sp] = known[dev][sp];
+  return cudaSuccess;
 }
 
 // Tokens per tile and pairs per tile that a call takes: the smallest estimate of
 // waves x (stages x clocks of a stage + clocks of a tile's start and end). A
-// stage costs the larger of its dequantisation (about 600 clocks) and its eight
-// MMAs (cs / 2 clocks each).
-static void linear_plan(int T, int N, int K, int num_sms, int& cs, int& split) {
+// stage costs the larger of its dequantisation (measured 500 clocks in row
+// order, 370 in pair order) and its eight MMAs (cs / 2 clocks each).
+static void linear_plan(int T, int N, int K, bool pair_order, const int (&resident)[kMaxSplit + 1],
+                        int& cs, int& split) {
   const int npair = (N + 2 * kBM - 1) / (2 * kBM), nS = (K + kStageK - 1) / kStageK;
-  const int pairs = num_sms / 2;
+  const double deq = pair_order ? 370 : 500;
   double best = 0;
   cs = 0;
   const int c0 = (T + kMaxTok - 1) / kMaxTok;
   for (int c = c0; c <= c0 + 8; ++c) {
     const int tok = ((T + c - 1) / c + 15) & ~15;
     const int64_t tiles = (int64_t)npair * ((T + tok - 1) / tok);
-    for (int sp = 1; sp <= 4; sp *= 2) {
-      if (sp > 1 && (tiles * sp > pairs || nS < 2 * sp)) break;
-      const double stage = tok > 150 ? 4.0 * tok : 600.0;
-      const double waves = (double)((tiles * sp + pairs - 1) / pairs);
-      const double t = waves * ((double)nS / sp * stage + 5000 + (sp > 1 ? 1500 : 0));
+    for (int sp = 1; sp <= kMaxSplit; ++sp) {
+      // split tiles take one pass; parts of at least two stages
+      if (sp > 1 && (tiles > resident[sp] || nS < 2 * sp)) continue;
+      const double stage = 4.0 * tok > deq ? 4.0 * tok : deq;
+      const double waves = (double)((tiles + resident[sp] - 1) / resident[sp]);
+      const double t = 6000 + waves * ((double)((nS + sp - 1) / sp) * stage + 2500) + (sp > 1 ? 1500 : 0);
       if (cs == 0 || t < best) {
         best = t;
         cs = tok;
@@ -778,32 +889,41 @@ cudaError_t launch_linear(const LinearArgs& a, int num_sms, cudaStream_t stream)
   cudaError_t e;
   char* ws = static_cast<char*>(a.ws);
   const bool adapters = a.ids != nullptr;
-  const int parts = down_parts(a.T, a.K);
-  float* v = reinterpret_cast<float*>(ws);
-  const uint16_t* x = static_cast<const uint16_t*>(a.x);
+  uint16_t* v = reinterpret_cast<uint16_t*>(ws);
+  uint16_t* xb = reinterpret_cast<uint16_t*>(ws + up256((size_t)a.T * a.rank * 2));
+  const bool x8 = a.xs != nullptr;
   if (a.status != nullptr &&
       (e = cudaMemsetAsync(a.status, 0, 4 * sizeof(int32_t), stream)) != cudaSuccess)
     return e;
-  if (a.xs != nullptr) {
-    uint16_t* xb = reinterpret_cast<uint16_t*>(ws + up256((size_t)parts * a.T * a.rank * 4));
+  if (adapters) {
+    if (a.rank <= 8)
+      e = x8 ? launch_down<1, true>(a, xb, v, num_sms, stream)
+             : launch_down<1, false>(a, xb, v, num_sms, stream);
+    else if (a.rank <= 16)
+      e = x8 ? launch_down<2, true>(a, xb, v, num_sms, stream)
+             : launch_down<2, false>(a, xb, v, num_sms, stream);
+    else
+      e = x8 ? launch_down<4, true>(a, xb, v, num_sms, stream)
+             : launch_down<4, false>(a, xb, v, num_sms, stream);
+    if (e != cudaSuccess) return e;
+  } else if (x8) {
     const int64_t n16 = (int64_t)a.T * a.K / 16;
     const int64_t blocks = (n16 + 255) / 256;
     mx8_to_bf16_kernel<<<(unsigned)(blocks < num_sms * 8 ? blocks : num_sms * 8), 256, 0, stream>>>(
         static_cast<const uint4*>(a.x), a.xs, n16, reinterpret_cast<uint4*>(xb));
-    x = xb;
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  if (adapters) {
-    if (a.rank <= 8) launch_down<1>(x, a, v, parts, num_sms, stream);
-    else if (a.rank <= 16) launch_down<2>(x, a, v, parts, num_sms, stream);
-    else launch_down<4>(x, a, v, parts, num_sms, stream);
-  }
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  const void* x = x8 ? xb : a.x;
 
   LinearParams p = {};
   p.a = a;
   p.v = v;
-  p.parts = parts;
-  linear_plan(a.T, a.N, a.K, num_sms, p.cs, p.split);
+  int dev = 0;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  if (dev < 0 || dev >= kGrantDevices) return cudaErrorInvalidDevice;
+  int resident[kMaxSplit + 1];
+  if ((e = resident_clusters(dev, resident)) != cudaSuccess) return e;
+  linear_plan(a.T, a.N, a.K, x8, resident, p.cs, p.split);
   const int xstage = p.cs / 2 * 256;
   p.S = (kTmemCols - ((p.cs + 31) & ~31)) / kWCols;   // 4 at 256 tokens, 7 at 16
   p.SP = p.cs > 128 ? 3 : 6;
@@ -822,18 +942,8 @@ cudaError_t launch_linear(const LinearArgs& a, int num_sms, cudaStream_t stream)
   const size_t lbytes = (size_t)p.SL * (kBTile + xstage / 2), obytes = (size_t)p.cs * kOutPitch;
   const size_t smem = 1024 + (size_t)p.S * xstage + (size_t)p.SP * kPStage +
                       (p.split == 1 && obytes > lbytes ? obytes : lbytes);
-  static size_t granted[kGrantDevices] = {};
-  int dev = 0;
-  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
-  if (dev < 0 || dev >= kGrantDevices) return cudaErrorInvalidDevice;
-  if (smem > granted[dev]) {
-    e = cudaFuncSetAttribute(linear_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    granted[dev] = smem;
-  }
   cudaLaunchConfig_t cfg = {};
-  const int64_t resident = num_sms / (2 * p.split);   // persistent clusters
-  cfg.gridDim = dim3((unsigned)((tiles < resident ? tiles : resident) * p.split * 2));
+  cfg.gridDim = dim3((unsigned)((tiles < resident[p.split] ? tiles : resident[p.split]) * p.split * 2));   // persistent
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -843,14 +953,14 @@ cudaError_t launch_linear(const LinearArgs& a, int num_sms, cudaStream_t stream)
   at[na].val.clusterDim.x = 2 * p.split;
   at[na].val.clusterDim.y = at[na].val.clusterDim.z = 1;
   ++na;
-  if (adapters) {   // starts beside the down kernel, whose results it waits for
+  if (adapters || x8) {   // starts beside the kernel before, whose results it waits for
     at[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[na].val.programmaticStreamSerializationAllowed = 1;
     ++na;
   }
   cfg.attrs = at;
   cfg.numAttrs = na;
-  return cudaLaunchKernelEx(&cfg, linear_kernel, p);
+  return cudaLaunchKernelEx(&cfg, x8 ? linear_kernel<true> : linear_kernel<false>, p);
 }
 
 }  // namespace mxmoe

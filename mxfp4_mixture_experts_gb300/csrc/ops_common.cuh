@@ -136,16 +136,33 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t bar) {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// Bounded wait that also acquires what other CTAs released; the whole warp calls it.
+// Bounded wait of a whole warp, which also acquires what other CTAs of the
+// cluster released. The warp sleeps in the hardware until the phase completes or
+// the hint (20 us) runs out, so waiting warps leave the issue slots to the
+// others; it gives up after about a second.
+constexpr uint32_t kSleepHintNs = 20000, kSleepLimit = 50000;
 __device__ __forceinline__ bool warp_wait_cluster(uint64_t* bar, uint32_t parity) {
   uint32_t ok = 0;
-  for (uint32_t i = 0; i < kWaitLimit && !ok; ++i)
+  for (uint32_t i = 0; i < kSleepLimit && !ok; ++i)
     asm volatile(
         "{\n .reg .pred p;\n"
-        " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
         " selp.u32 %0, 1, 0, p;\n}"
         : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(kSleepHintNs)
+        : "memory");
+  return __all_sync(0xffffffffu, ok != 0);
+}
+// The same for barriers of this CTA alone.
+__device__ __forceinline__ bool warp_wait_cta(uint64_t* bar, uint32_t parity) {
+  uint32_t ok = 0;
+  for (uint32_t i = 0; i < kSleepLimit && !ok; ++i)
+    asm volatile(
+        "{\n .reg .pred p;\n"
+        " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+        " selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(kSleepHintNs)
         : "memory");
   return __all_sync(0xffffffffu, ok != 0);
 }
