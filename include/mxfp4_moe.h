@@ -383,9 +383,9 @@ int mxfp4_moe_router_scored(const float* logits, const float* bias, int T, int E
  *                 concurrently
  * Limits (MXFP4_MOE_ERR_SHAPE): 0 <= T <= 2^20, K % 64 == 0, 64 <= K <= 16384,
  * N % 8 == 0, 8 <= N <= 2^20, and with adapters rank % 8 == 0, 8 <= rank <= 256,
- * 1 <= n_adapters <= 1024. Pointers 16-byte aligned but adapter_ids,
- * adapter_scale and status (4 bytes) and the workspace (256 bytes)
- * (MXFP4_MOE_ERR_ALIGN). T == 0 enqueues nothing. */
+ * 1 <= n_adapters <= 1024. x and adapter_a 32-byte aligned (their rows are
+ * read 32 bytes a thread), the workspace 256, adapter_ids, adapter_scale and
+ * status 4, all others 16 (MXFP4_MOE_ERR_ALIGN). T == 0 enqueues nothing. */
 size_t mxfp4_moe_linear_workspace_size(int T, int K, int N, int rank, int x_is_mxfp8);
 int mxfp4_moe_linear(const void* x, const uint8_t* x_scale, const uint8_t* w, const uint8_t* s,
                      int T, int K, int N, const int32_t* adapter_ids, const void* adapter_a,

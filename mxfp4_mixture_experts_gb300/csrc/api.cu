@@ -579,10 +579,10 @@ int mxfp4_moe_linear(const void* x, const uint8_t* x_scale, const uint8_t* w, co
     return MXFP4_MOE_ERR_SHAPE;
   if (T == 0) return MXFP4_MOE_OK;
   if (!x || !w || !s || !out || (adapters && (!adapter_a || !adapter_b))) return MXFP4_MOE_ERR_ARG;
-  if (!aligned(x, 16) || !aligned(x_scale, 16) || !aligned(w, 16) || !aligned(s, 16) ||
+  if (!aligned(x, 32) || !aligned(x_scale, 16) || !aligned(w, 16) || !aligned(s, 16) ||
       !aligned(out, 16) || !aligned(status, 4))
     return MXFP4_MOE_ERR_ALIGN;
-  if (adapters && (!aligned(adapter_ids, 4) || !aligned(adapter_a, 16) || !aligned(adapter_b, 16) ||
+  if (adapters && (!aligned(adapter_ids, 4) || !aligned(adapter_a, 32) || !aligned(adapter_b, 16) ||
                    !aligned(adapter_scale, 4)))
     return MXFP4_MOE_ERR_ALIGN;
   const size_t need =

@@ -61,10 +61,25 @@ __device__ __forceinline__ uint4 pair_order(const uint4& u) {
 // 16 E4M3 values of one scale block -> bf16, in row order.
 __device__ __forceinline__ void e4m3x16_to_bf16(const uint4& u, uint32_t scale, uint4& a, uint4& b) {
   const ScaleMul sm = e4m3_scale_mul(scale);
-  e4m3x4_to_bf16(u.x, sm, a.x, a.y);
-  e4m3x4_to_bf16(u.y, sm, a.z, a.w);
-  e4m3x4_to_bf16(u.z, sm, b.x, b.y);
-  e4m3x4_to_bf16(u.w, sm, b.z, b.w);
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  uint32_t o[8], nan = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    e4m3x4_place(w[i], o[2 * i], o[2 * i + 1]);
+    nan |= (w[i] & 0x7F7F7F7Fu) + 0x01010101u;   // code 0x7F carries into bit 7
+  }
+  if (__builtin_expect((nan & 0x80808080u) != 0u, 0)) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) e4m3x4_nan(w[i], o[2 * i], o[2 * i + 1]);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) o[i] = bf16x2_mul(o[i], sm.m1);
+  if (__builtin_expect(sm.two, 0)) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = bf16x2_mul(o[i], sm.m2);
+  }
+  a = make_uint4(o[0], o[1], o[2], o[3]);
+  b = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
 // MXFP8 rows -> bf16 rows in pair order, 16 values a thread (calls without adapters).
@@ -91,13 +106,34 @@ constexpr int kDownTok = 32;      // tokens per item (two m16 tiles)
 constexpr int kDownMaxParts = 8;
 constexpr int kDownStep = 64;     // K values per step: 16 a lane
 
+__device__ __forceinline__ uint4 ldg16(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+// 32 bytes a lane in one instruction: whole sectors (as two 16-byte halves every
+// sector went through L1 twice).
+__device__ __forceinline__ void ldg32(const void* p, uint4& a, uint4& b) {
+  asm volatile("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z),
+                 "=r"(b.w)
+               : "l"(p));
+}
+__device__ __forceinline__ void stg32(void* p, const uint4& a, const uint4& b) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(a.x), "r"(a.y),
+               "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+               : "memory");
+}
+
 // NT: n-tiles of 8 ranks per pass.
 template <int NT, bool X8>
 __global__ void __launch_bounds__(256, 2) adapter_down_kernel(const LinearArgs a, uint16_t* __restrict__ xb,
                                                            uint16_t* __restrict__ v) {
-  __shared__ int s_id[kDownWin], s_item[kDownWin], s_warp[8];
+  __shared__ int s_cid[kDownWin / 32][32], s_cn[kDownWin / 32][32], s_nc[kDownWin / 32];
+  __shared__ int s_base[kDownWin], s_warp[kDownWin / 32], s_items;
   __shared__ int s_tok[kDownWin][kDownTok];   // [item][slot]: token of the window, -1 empty
-  __shared__ int s_ad[kDownWin];
+  __shared__ int s_ad[kDownWin];              // [item]: adapter, -1 none
   __shared__ float part[8][16][NT * 8 + 4];
   __shared__ __align__(16) float s_sum[16][NT * 8];   // this CTA's part of an m-tile
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -118,36 +154,60 @@ __global__ void __launch_bounds__(256, 2) adapter_down_kernel(const LinearArgs a
       }
       if (id < 0) id = kNone;
     }
-    s_id[tid] = id;
+    // the warp's classes: id and count, listed by their first lanes
+    const uint32_t same = __match_any_sync(0xffffffffu, id);
+    const int first = __ffs(same) - 1;
+    const bool lead = lane == first && id > -2;
+    const uint32_t leads = __ballot_sync(0xffffffffu, lead);
+    const int slot = __popc(leads & lanemask_lt());
+    if (lead) {
+      s_cid[warp][slot] = id;
+      s_cn[warp][slot] = __popc(same);
+    }
+    if (lane == 0) s_nc[warp] = __popc(leads);
+    named_barrier(1, kDownWin);
+    // a class's first warp lists its items; other warps find it there
+    int before = 0, after = 0, root = warp * 32 + slot;
+    if (lead) {
+      for (int w = kDownWin / 32 - 1; w >= 0; --w)
+        for (int j = 0; j < s_nc[w]; ++j)
+          if (w != warp && s_cid[w][j] == id) {
+            if (w < warp) {
+              before += s_cn[w][j];
+              root = w * 32 + j;   // descending: the lowest warp stays
+            } else {
+              after += s_cn[w][j];
+            }
+          }
+    }
+    const int mine =
+        lead && before == 0 ? (__popc(same) + after + kDownTok - 1) / kDownTok : 0;
+    int sum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += y;
+    }
+    if (lane == 31) s_warp[warp] = sum;
+    named_barrier(1, kDownWin);
+    int base = sum - mine, all = 0;
+    for (int w = 0; w < kDownWin / 32; ++w) {
+      if (w < warp) base += s_warp[w];
+      all += s_warp[w];
+    }
+    if (mine > 0) {
+      s_base[root] = base;
+      for (int j = 0; j < mine; ++j) s_ad[base + j] = id;
+    }
+    if (tid == 0) s_items = all;
+    for (int i = tid; i < all * kDownTok; i += kDownWin) s_tok[i / kDownTok][i % kDownTok] = -1;
+    named_barrier(1, kDownWin);
+    const int rank = __shfl_sync(0xffffffffu, before, first) + __popc(same & lanemask_lt());
+    const int at = __shfl_sync(0xffffffffu, lead ? s_base[root] : 0, first);
+    if (id > -2) s_tok[at + rank / kDownTok][rank % kDownTok] = tid;
   }
-  for (int i = tid; i < kDownWin * kDownTok; i += 256) s_tok[i / kDownTok][i % kDownTok] = -1;
   __syncthreads();
-  int rank = 0, leader = tid;   // earlier tokens of this class; first token of this one's item
-  if (tid < kDownWin && id > -2) {
-    for (int j = 0; j < tid; ++j)
-      if (s_id[j] == id) {
-        if (rank % kDownTok == 0) leader = j;
-        ++rank;
-      }
-    if (rank % kDownTok == 0) leader = tid;
-  }
-  const bool lead = tid < kDownWin && id > -2 && leader == tid;
-  const uint32_t bal = __ballot_sync(0xffffffffu, lead);
-  if (lane == 0) s_warp[warp] = __popc(bal);
-  __syncthreads();
-  int base = 0, items = 0;
-  for (int i = 0; i < 8; ++i) {
-    if (i < warp) base += s_warp[i];
-    items += s_warp[i];
-  }
-  if (lead) {
-    const int it = base + __popc(bal & lanemask_lt());
-    s_item[tid] = it;
-    s_ad[it] = id;
-  }
-  __syncthreads();
-  if (tid < kDownWin && id > -2) s_tok[s_item[leader]][rank % kDownTok] = tid;
-  __syncthreads();
+  const int items = s_items;
 
   const int g = lane >> 2, q = lane & 3;
   const int slices = 8 * parts, slice = blockIdx.z * 8 + warp;
@@ -177,26 +237,19 @@ __global__ void __launch_bounds__(256, 2) adapter_down_kernel(const LinearArgs a
         uint32_t sc[4];
         if (ad >= 0) {
 #pragma unroll
-          for (int j = 0; j < NT; ++j) {   // (past the rank: the last rows again, never stored)
-            const uint16_t* src = ar + (size_t)(8 * (j < nt ? j : nt - 1)) * a.K + kDownStep * k;
-            w[j][0] = *reinterpret_cast<const uint4*>(src);
-            w[j][1] = *reinterpret_cast<const uint4*>(src + 8);
-          }
+          for (int j = 0; j < NT; ++j)   // (past the rank: the last rows again, never stored)
+            ldg32(ar + (size_t)(8 * (j < nt ? j : nt - 1)) * a.K + kDownStep * k, w[j][0], w[j][1]);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           u[i][0] = u[i][1] = e[i] = make_uint4(0u, 0u, 0u, 0u);
           sc[i] = 0;
-          if (tk[i] >= 0) {
-            if (X8) {
-              e[i] = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.x) + xo[i] +
-                                                     kDownStep * k);
-              sc[i] = ldg_u8(a.xs + (xo[i] + kDownStep * k) / kScaleBlock);
-            } else {
-              const uint16_t* x = static_cast<const uint16_t*>(a.x) + xo[i] + kDownStep * k;
-              u[i][0] = *reinterpret_cast<const uint4*>(x);
-              u[i][1] = *reinterpret_cast<const uint4*>(x + 8);
-            }
+          if (tk[i] < 0) continue;
+          if (X8) {
+            e[i] = ldg16(static_cast<const uint8_t*>(a.x) + xo[i] + kDownStep * k);
+            sc[i] = ldg_u8(a.xs + (xo[i] + kDownStep * k) / kScaleBlock);
+          } else {
+            ldg32(static_cast<const uint16_t*>(a.x) + xo[i] + kDownStep * k, u[i][0], u[i][1]);
           }
         }
         if (X8) {
@@ -204,11 +257,8 @@ __global__ void __launch_bounds__(256, 2) adapter_down_kernel(const LinearArgs a
           for (int i = 0; i < 4; ++i) {
             if (tk[i] < 0) continue;
             e4m3x16_to_bf16(e[i], sc[i], u[i][0], u[i][1]);
-            if (pass == 0) {
-              uint4* dst = reinterpret_cast<uint4*>(xb + xo[i] + kDownStep * k);
-              dst[0] = pair_order(u[i][0]);
-              dst[1] = pair_order(u[i][1]);
-            }
+            if (pass == 0)
+              stg32(xb + xo[i] + kDownStep * k, pair_order(u[i][0]), pair_order(u[i][1]));
           }
         }
         if (ad < 0) continue;
@@ -232,10 +282,11 @@ __global__ void __launch_bounds__(256, 2) adapter_down_kernel(const LinearArgs a
         if (m == 1 && !two) break;
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-          part[warp][g][8 * j + 2 * q] = acc[m][j][0];
-          part[warp][g][8 * j + 2 * q + 1] = acc[m][j][1];
-          part[warp][g + 8][8 * j + 2 * q] = acc[m][j][2];
-          part[warp][g + 8][8 * j + 2 * q + 1] = acc[m][j][3];
+          float* dst = &part[warp][g][8 * j + 2 * q];
+          dst[0] = acc[m][j][0];
+          dst[1] = acc[m][j][1];
+          dst[8 * (NT * 8 + 4)] = acc[m][j][2];
+          dst[8 * (NT * 8 + 4) + 1] = acc[m][j][3];
         }
         __syncthreads();
         for (int i = tid; i < 16 * 8 * nt; i += 256) {
@@ -300,6 +351,7 @@ constexpr int kDeqGroups = (kWarps - kWarpDeq) / 4;
 constexpr int kEpiBar = 1;            // named barrier of the adapter and epilogue warps
 constexpr int kOutPitch = kBM * 2 + 16;   // bytes of a staged output row (128 bf16 and a bank shift)
 constexpr int kListMax = kMaxTok;     // adapters that one tile can name
+constexpr int kDynSmem = 227 * 1024 - 4096;   // dynamic shared memory of a CTA, one per SM (the rest is static)
 constexpr int kMaxSplit = 4;          // pairs of a cluster that share a tile's K
 
 struct LinearParams {
@@ -827,17 +879,16 @@ static cudaError_t launch_down(const LinearArgs& a, uint16_t* xb, uint16_t* v, i
 static cudaError_t resident_clusters(int dev, int (&out)[kMaxSplit + 1]) {
   static int known[kGrantDevices][kMaxSplit + 1] = {};
   if (known[dev][1] == 0) {
-    constexpr int kSmem = 227 * 1024 - 4096;   // one CTA per SM
     for (auto* k : {linear_kernel<false>, linear_kernel<true>}) {
       const cudaError_t e =
-          cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+          cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kDynSmem);
       if (e != cudaSuccess) return e;
     }
     for (int sp = kMaxSplit; sp >= 1; --sp) {
       cudaLaunchConfig_t cfg = {};
       cfg.gridDim = dim3(2 * sp * 64);
       cfg.blockDim = dim3(kThreads);
-      cfg.dynamicSmemBytes = kSmem;
+      cfg.dynamicSmemBytes = kDynSmem;
       cudaLaunchAttribute at[1];
       at[0].id = cudaLaunchAttributeClusterDimension;
       at[0].val.clusterDim.x = 2 * sp;
@@ -926,7 +977,6 @@ cudaError_t launch_linear(const LinearArgs& a, int num_sms, cudaStream_t stream)
   linear_plan(a.T, a.N, a.K, x8, resident, p.cs, p.split);
   const int xstage = p.cs / 2 * 256;
   p.S = (kTmemCols - ((p.cs + 31) & ~31)) / kWCols;   // 4 at 256 tokens, 7 at 16
-  p.SP = p.cs > 128 ? 3 : 6;
   p.SL = !adapters ? 0 : p.cs > 128 ? 1 : p.cs > 64 ? 2 : kMaxL;
   p.rp = (a.rank + 15) & ~15;
   const int npair = (a.N + 2 * kBM - 1) / (2 * kBM), ttile = (a.T + p.cs - 1) / p.cs;
@@ -940,8 +990,12 @@ cudaError_t launch_linear(const LinearArgs& a, int num_sms, cudaStream_t stream)
     return cudaErrorInvalidValue;
   p.tiles = (int)tiles;
   const size_t lbytes = (size_t)p.SL * (kBTile + xstage / 2), obytes = (size_t)p.cs * kOutPitch;
-  const size_t smem = 1024 + (size_t)p.S * xstage + (size_t)p.SP * kPStage +
-                      (p.split == 1 && obytes > lbytes ? obytes : lbytes);
+  // packed weights take what is left, 3 stages (256 tokens) to 8: with 3 at 144
+  // tokens the dequantisation waited on them, 850 instead of 620 clocks a stage
+  const size_t fixed = 1024 + (size_t)p.S * xstage + (p.split == 1 && obytes > lbytes ? obytes : lbytes);
+  p.SP = (int)((kDynSmem - fixed) / kPStage);
+  if (p.SP > kMaxSP) p.SP = kMaxSP;
+  const size_t smem = fixed + (size_t)p.SP * kPStage;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((tiles < resident[p.split] ? tiles : resident[p.split]) * p.split * 2));   // persistent
   cfg.blockDim = dim3(kThreads);

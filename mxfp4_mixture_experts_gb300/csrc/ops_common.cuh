@@ -36,27 +36,21 @@ __device__ __forceinline__ ScaleMul e4m3_scale_mul(uint32_t s) {
   return r;
 }
 
-// Four E4M3 bytes (low byte first) times their block's scale -> two bf16 pairs.
-// The sign and the 7 magnitude bits of a code, placed at bit 15 and bits 4..10
-// of a half, are a bf16 of the value times 2^-120, subnormal codes included;
-// the products are rounded once (exact inside bf16's range). Code 0x7F is NaN.
-__device__ __forceinline__ void e4m3x4_to_bf16(uint32_t w, const ScaleMul& sm, uint32_t& o0,
-                                               uint32_t& o1) {
+// Four E4M3 bytes (low byte first) -> two bf16 pairs of the values times 2^-120:
+// the sign and the 7 magnitude bits of a code at bit 15 and bits 4..10 of a
+// half, subnormal codes included. Multiplied by e4m3_scale_mul's factors they
+// are rounded once (exact inside bf16's range).
+__device__ __forceinline__ void e4m3x4_place(uint32_t w, uint32_t& o0, uint32_t& o1) {
   const uint32_t p0 = prmt(w, 0u, 0x4140u), p1 = prmt(w, 0u, 0x4342u);
-  uint32_t r0 = ((p0 & 0x00800080u) << 8) | ((p0 & 0x007F007Fu) << 4);
-  uint32_t r1 = ((p1 & 0x00800080u) << 8) | ((p1 & 0x007F007Fu) << 4);
-  if (__builtin_expect((((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0u, 0)) {
-    if ((p0 & 0x7Fu) == 0x7Fu) r0 |= 0x7FC0u;
-    if ((p0 & 0x7F0000u) == 0x7F0000u) r0 |= 0x7FC00000u;
-    if ((p1 & 0x7Fu) == 0x7Fu) r1 |= 0x7FC0u;
-    if ((p1 & 0x7F0000u) == 0x7F0000u) r1 |= 0x7FC00000u;
-  }
-  o0 = bf16x2_mul(r0, sm.m1);
-  o1 = bf16x2_mul(r1, sm.m1);
-  if (__builtin_expect(sm.two, 0)) {
-    o0 = bf16x2_mul(o0, sm.m2);
-    o1 = bf16x2_mul(o1, sm.m2);
-  }
+  o0 = ((p0 << 8) & 0x80008000u) | ((p0 << 4) & 0x07F007F0u);
+  o1 = ((p1 << 8) & 0x80008000u) | ((p1 << 4) & 0x07F007F0u);
+}
+// Code 0x7F (either sign), which the placement above turns into a number, as NaN.
+__device__ __forceinline__ void e4m3x4_nan(uint32_t w, uint32_t& o0, uint32_t& o1) {
+  if ((w & 0x7Fu) == 0x7Fu) o0 |= 0x7FC0u;
+  if ((w & 0x7F00u) == 0x7F00u) o0 |= 0x7FC00000u;
+  if ((w & 0x7F0000u) == 0x7F0000u) o1 |= 0x7FC0u;
+  if ((w & 0x7F000000u) == 0x7F000000u) o1 |= 0x7FC00000u;
 }
 
 // D += A * B for one m16n8k16 tile, bf16 inputs, fp32 accumulators.

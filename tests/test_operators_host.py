@@ -76,8 +76,8 @@ def lin(m, **kw):
     (dict(rank=12), "SHAPE"), (dict(rank=0), "SHAPE"), (dict(rank=264), "SHAPE"),
     (dict(L=0), "SHAPE"), (dict(L=1025), "SHAPE"), (dict(x=None), "ARG"), (dict(w=None), "ARG"),
     (dict(s=None), "ARG"), (dict(out=None), "ARG"), (dict(a=None), "ARG"), (dict(b=None), "ARG"),
-    (dict(x=VP(0x10008)), "ALIGN"), (dict(xs=VP(0x10008)), "ALIGN"), (dict(w=VP(0x20004)), "ALIGN"),
-    (dict(ids=VP(0x40002)), "ALIGN"), (dict(a=VP(0x50008)), "ALIGN"), (dict(out=VP(0x80008)), "ALIGN"),
+    (dict(x=VP(0x10010)), "ALIGN"), (dict(xs=VP(0x10008)), "ALIGN"), (dict(w=VP(0x20004)), "ALIGN"),
+    (dict(ids=VP(0x40002)), "ALIGN"), (dict(a=VP(0x50010)), "ALIGN"), (dict(out=VP(0x80008)), "ALIGN"),
     (dict(ws=VP(0x100080)), "ALIGN"), (dict(ws=None), "WORKSPACE"), (dict(ws_bytes=0), "WORKSPACE"),
     (dict(T=0, x=None, ids=None), "OK"),
 ])
