@@ -129,6 +129,15 @@ def _raw_stream(stream) -> int:
     return stream.cuda_stream
 
 
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """An uninitialised tensor for a call on ``stream``: its memory is not handed out again before
+    that stream has passed the call, also when the tensor is dropped on the current stream first."""
+    t = torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
 def _need(t: torch.Tensor, name: str, dtype, ndim: int):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -426,7 +435,7 @@ def add_rmsnorm(x: torch.Tensor, gamma: torch.Tensor, residual: Optional[torch.T
         if residual.shape != x.shape:
             raise ValueError("residual must be [T, K]")
         if residual_out is None:
-            residual_out = torch.empty_like(x)
+            residual_out = _empty(x.shape, torch.bfloat16, dev, stream)
     if residual_out is not None:
         _need(residual_out, "residual_out", torch.bfloat16, 2)
         if residual_out.shape != x.shape:
@@ -435,15 +444,15 @@ def add_rmsnorm(x: torch.Tensor, gamma: torch.Tensor, residual: Optional[torch.T
         if out is not None:
             raise ValueError("out is not written when bf16 is False")
     elif out is None:
-        out = torch.empty_like(x)
+        out = _empty(x.shape, torch.bfloat16, dev, stream)
     else:
         _need(out, "out", torch.bfloat16, 2)
         if out.shape != x.shape:
             raise ValueError("out must be [T, K]")
     q = s = None
     if out8 is not None:
-        q = torch.empty(T, K, dtype=torch.float8_e4m3fn, device=dev)
-        s = torch.empty(T, K // 32, dtype=torch.uint8, device=dev)
+        q = _empty((T, K), torch.float8_e4m3fn, dev, stream)
+        s = _empty((T, K // 32), torch.uint8, dev, stream)
     rc = lib().mxfp4_moe_add_rmsnorm(_addr(x), _addr(residual), _addr(gamma), T, K, eps,
                                      MX8_RULES[out8 or "ocp"], _addr(residual_out), _addr(out),
                                      _addr(q), _addr(s), _raw_stream(stream))
@@ -481,9 +490,9 @@ def router_scored(logits: torch.Tensor, topk: int, scoring: str = "sigmoid",
             if tuple(t.shape) != (T, topk):
                 raise ValueError(f"{name} must be [T, topk]")
     if topk_ids is None:
-        topk_ids = torch.empty(T, topk, dtype=torch.int32, device=logits.device)
+        topk_ids = _empty((T, topk), torch.int32, logits.device, stream)
     if topk_weights is None:
-        topk_weights = torch.empty(T, topk, dtype=torch.float32, device=logits.device)
+        topk_weights = _empty((T, topk), torch.float32, logits.device, stream)
     rc = lib().mxfp4_moe_router_scored(_addr(logits), _addr(bias), T, E, topk, SCORES[scoring],
                                        n_group, topk_group, group_top, int(bool(renormalise)),
                                        route_scale, _addr(topk_ids), _addr(topk_weights),
@@ -517,8 +526,8 @@ def linear(x: torch.Tensor, w: torch.Tensor, s: torch.Tensor,
     _need(w, "w", torch.uint8, 2)
     _need(s, "s", torch.uint8, 2)
     T, K = x.shape
-    N = w.shape[0]
-    if tuple(w.shape) != (N, K // 2) or tuple(s.shape) != (N, K // 32):
+    N, half = w.shape
+    if 2 * half != K or tuple(s.shape) != (N, K // 32):
         raise ValueError("w / s shapes must be [N, K/2] / [N, K/32]")
     if x8:
         _need(x_scale, "x_scale", torch.uint8, 2)
@@ -531,10 +540,10 @@ def linear(x: torch.Tensor, w: torch.Tensor, s: torch.Tensor,
             raise ValueError("adapter_ids need adapter_a and adapter_b")
         _need(adapter_a, "adapter_a", torch.bfloat16, 3)
         _need(adapter_b, "adapter_b", torch.bfloat16, 3)
-        n_ad, rank, _ = adapter_a.shape
+        n_ad, rank, ka = adapter_a.shape
         if adapter_ids.shape[0] != T:
             raise ValueError("adapter_ids must be [T]")
-        if adapter_a.shape[2] != K or tuple(adapter_b.shape) != (n_ad, N, rank):
+        if ka != K or tuple(adapter_b.shape) != (n_ad, N, rank):
             raise ValueError("adapter_a / adapter_b must be [L, rank, K] / [L, N, rank]")
         if adapter_scale is not None:
             _need(adapter_scale, "adapter_scale", torch.float32, 1)
@@ -543,7 +552,7 @@ def linear(x: torch.Tensor, w: torch.Tensor, s: torch.Tensor,
     elif adapter_a is not None or adapter_b is not None or adapter_scale is not None:
         raise ValueError("adapters need adapter_ids")
     if out is None:
-        out = torch.empty(T, N, dtype=torch.bfloat16, device=x.device)
+        out = _empty((T, N), torch.bfloat16, x.device, stream)
     else:
         _need(out, "out", torch.bfloat16, 2)
         if tuple(out.shape) != (T, N):
@@ -554,13 +563,15 @@ def linear(x: torch.Tensor, w: torch.Tensor, s: torch.Tensor,
             raise ValueError("status must be [4]")
     L = lib()
     if workspace is None:
-        workspace = torch.empty(L.mxfp4_moe_linear_workspace_size(T, K, N, rank, int(x8)),
-                                dtype=torch.uint8, device=x.device)
+        nbytes = L.mxfp4_moe_linear_workspace_size(T, K, N, rank, x8)
+        if nbytes:
+            workspace = _empty(nbytes, torch.uint8, x.device, stream)
     else:
         _need(workspace, "workspace", torch.uint8, 1)
-    rc = L.mxfp4_moe_linear(_addr(x), _addr(x_scale), _addr(w), _addr(s), T, K, N, _addr(adapter_ids),
-                            _addr(adapter_a), _addr(adapter_b), _addr(adapter_scale), n_ad, rank,
-                            _addr(out), _addr(status), _addr(workspace), workspace.numel(),
+    rc = L.mxfp4_moe_linear(x.data_ptr(), _addr(x_scale), w.data_ptr(), s.data_ptr(), T, K, N,
+                            _addr(adapter_ids), _addr(adapter_a), _addr(adapter_b),
+                            _addr(adapter_scale), n_ad, rank, out.data_ptr(), _addr(status),
+                            _addr(workspace), 0 if workspace is None else workspace.numel(),
                             _raw_stream(stream))
     if rc:
         raise MoEError(rc, "mxfp4_moe_linear")
