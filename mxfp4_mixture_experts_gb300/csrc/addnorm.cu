@@ -29,9 +29,42 @@ __device__ __forceinline__ uint32_t e4m3x2_rn_sat(float lo, float hi) {
   return r;
 }
 
+// An fp32 value and its remainder. The warps' sums are added and the scaling is
+// applied with remainders: y then carries one rounding instead of the sums',
+// the root's and two products' (about 4 ulp apart at worst), so the codes made
+// of it are those of the exact y but where that lies within an ulp of a tie.
+struct Two {
+  float hi, lo;
+};
+__device__ __forceinline__ Two add(Two a, Two b) {
+  const float s = __fadd_rn(a.hi, b.hi);
+  const float t = __fsub_rn(s, a.hi);
+  const float e = __fadd_rn(__fsub_rn(a.hi, __fsub_rn(s, t)), __fsub_rn(b.hi, t));
+  return Two{s, e + (a.lo + b.lo)};
+}
+// 1 / sqrt(sum / n + eps): the root's approximation and one Newton step.
+__device__ __forceinline__ Two rsqrt_mean(Two sum, float n, float eps) {
+  const float m = __fdiv_rn(sum.hi, n);
+  const Two v = add(Two{m, (fmaf(-m, n, sum.hi) + sum.lo) / n}, Two{eps, 0.f});
+  const float r = rsqrtf(v.hi);
+  const float p = __fmul_rn(v.hi, r);
+  const float e = fmaf(-p, r, 1.f) - r * (fmaf(v.hi, r, -p) + v.lo * r);
+  const float c = 0.5f * r * e;
+  if (!(fabsf(c) < r)) return Two{r, 0.f};   // sum 0, infinite or NaN: the root as it is
+  const float hi = __fadd_rn(r, c);
+  return Two{hi, c - __fsub_rn(hi, r)};
+}
+// (h * r) * g
+__device__ __forceinline__ float scaled(float h, Two r, float g) {
+  const float t = __fmul_rn(h, r.hi);
+  const float e = fmaf(h, r.hi, -t) + h * r.lo;
+  const float y = fmaf(t, g, e * g);
+  return fabsf(t) < INFINITY ? y : t * g;   // infinite products leave no remainder
+}
+
 // CH: 16-byte chunks per thread (K / 8 <= CH * blockDim.x).
 template <int CH>
-__global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const AddNormArgs a) {
+__global__ void __launch_bounds__(CH <= 2 ? 1024 : 256) add_rmsnorm_kernel(const AddNormArgs a) {
   __shared__ float part[32];
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
   const int n8 = a.K / 8;
@@ -77,10 +110,11 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const AddNormArgs a) 
   for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
   if (lane == 0) part[warp] = ss;
   __syncthreads();
-  ss = lane < (nt >> 5) ? part[lane] : 0.f;
+  Two r = {lane < (nt >> 5) ? part[lane] : 0.f, 0.f};
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  const float r = rsqrtf(ss / (float)a.K + a.eps);
+  for (int o = 16; o > 0; o >>= 1)
+    r = add(r, Two{__shfl_xor_sync(0xffffffffu, r.hi, o), __shfl_xor_sync(0xffffffffu, r.lo, o)});
+  r = rsqrt_mean(r, (float)a.K, a.eps);
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const int c = tid + i * nt;
@@ -92,8 +126,8 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const AddNormArgs a) 
       const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        y[2 * j] = (h[i][2 * j] * r) * __uint_as_float(w[j] << 16);
-        y[2 * j + 1] = (h[i][2 * j + 1] * r) * __uint_as_float(w[j] & 0xFFFF0000u);
+        y[2 * j] = scaled(h[i][2 * j], r, __uint_as_float(w[j] << 16));
+        y[2 * j + 1] = scaled(h[i][2 * j + 1], r, __uint_as_float(w[j] & 0xFFFF0000u));
       }
       if (a.out != nullptr) {
         uint4 o;
@@ -134,14 +168,27 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const AddNormArgs a) 
 }  // namespace
 
 cudaError_t launch_add_rmsnorm(const AddNormArgs& a, int num_sms, cudaStream_t stream) {
-  (void)num_sms;
+  // One row's latency counts for few rows: one chunk a thread, up to 1024
+  // threads. Many rows go faster in CTAs of 128 to 256 threads with up to 8
+  // chunks each, eight or more to an SM, so that some rows load while others wait
+  // at their barrier (T = 8192, K = 6144 with MXFP8: 768 threads 80 us, 256
+  // threads 73 us, the copy rate allows 67).
   const int n8 = a.K / 8;
   int nt = ((n8 + 31) / 32) * 32;
-  if (nt > 1024) nt = 1024;
-  if (n8 <= 1024)
-    add_rmsnorm_kernel<1><<<a.T, nt, 0, stream>>>(a);
-  else
-    add_rmsnorm_kernel<2><<<a.T, nt, 0, stream>>>(a);
+  if (a.T > 2 * num_sms && n8 > 128) {
+    const int ch = n8 <= 1024 ? 4 : 8;
+    nt = ((n8 + ch - 1) / ch + 31) / 32 * 32;
+  } else if (nt > 1024) {
+    nt = 1024;
+  }
+  const int ch = (n8 + nt - 1) / nt;
+#define MXMOE_NORM(C) add_rmsnorm_kernel<C><<<a.T, nt, 0, stream>>>(a)
+  if (ch <= 1) MXMOE_NORM(1);
+  else if (ch <= 2) MXMOE_NORM(2);
+  else if (ch <= 3) MXMOE_NORM(3);
+  else if (ch <= 4) MXMOE_NORM(4);
+  else MXMOE_NORM(8);
+#undef MXMOE_NORM
   return cudaGetLastError();
 }
 
