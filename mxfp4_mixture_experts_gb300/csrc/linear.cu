@@ -105,6 +105,7 @@ constexpr int kDownWin = 128;     // tokens per window
 constexpr int kDownTok = 32;      // tokens per item (two m16 tiles)
 constexpr int kDownMaxParts = 8;
 constexpr int kDownStep = 64;     // K values per step: 16 a lane
+constexpr int kDownSum = 64;      // ranks whose parts a cluster adds at once
 
 __device__ __forceinline__ uint4 ldg16(const void* p) {
   uint4 v;
@@ -135,7 +136,7 @@ __global__ void __launch_bounds__(256, 2) adapter_down_kernel(const LinearArgs a
   __shared__ int s_tok[kDownWin][kDownTok];   // [item][slot]: token of the window, -1 empty
   __shared__ int s_ad[kDownWin];              // [item]: adapter, -1 none
   __shared__ float part[8][16][NT * 8 + 4];
-  __shared__ __align__(16) float s_sum[16][NT * 8];   // this CTA's part of an m-tile
+  __shared__ __align__(16) float s_sum[kDownTok][kDownSum];   // this CTA's part of an item
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int w0 = blockIdx.x * kDownWin;
   const int parts = gridDim.z;
@@ -296,37 +297,39 @@ __global__ void __launch_bounds__(256, 2) adapter_down_kernel(const LinearArgs a
 #pragma unroll
           for (int w = 0; w < 8; ++w) z += part[w][row][r];
           if (parts > 1)
-            s_sum[row][r] = z;
+            s_sum[16 * m + row][r0 % kDownSum + r] = z;
           else if (t >= 0)
             v[(size_t)(w0 + t) * a.rank + r0 + r] = f32_to_bf16_rne(z * scale);
         }
-        if (parts > 1) {   // rows cluster rank, rank + parts, ..: the CTAs' parts in order
-          cluster_sync();
-          const uint32_t me = cluster_rank();
-          for (int i = tid; i < 16 * 2 * nt; i += 256) {
-            const int row = i / (2 * nt), r = (i - row * (2 * nt)) * 4;
-            const int t = s_tok[it][16 * m + row];
-            if (row % parts != me || t < 0) continue;
-            float4 z[kDownMaxParts];
+        __syncthreads();
+      }
+      const int f0 = r0 / kDownSum * kDownSum;   // ranks f0 .. r0 + 8 nt - 1 are complete here
+      if (parts > 1 && (r0 + NT * 8 - f0 == kDownSum || pass == passes - 1)) {
+        // tokens rank, rank + parts, .. of the item: the cluster's parts in order
+        cluster_sync();
+        const int quads = (r0 + 8 * nt - f0) / 4;
+        const int rows = two ? 32 : 16, me = (int)cluster_rank();
+        for (int i = tid; i < rows / parts * quads; i += 256) {
+          const int row = i / quads * parts + me, r = i % quads * 4;
+          const int t = s_tok[it][row];
+          if (t < 0) continue;
+          float4 z[kDownMaxParts];
 #pragma unroll
-            for (int c = 0; c < kDownMaxParts; ++c)
-              if (c < parts) z[c] = ld_cluster16(smem_u32(&s_sum[row][r]), c);
-            float4 y = z[0];
+          for (int c = 0; c < kDownMaxParts; ++c)
+            if (c < parts) z[c] = ld_cluster16(smem_u32(&s_sum[row][r]), c);
+          float4 y = z[0];
 #pragma unroll
-            for (int c = 1; c < kDownMaxParts; ++c)
-              if (c < parts) {
-                y.x += z[c].x;
-                y.y += z[c].y;
-                y.z += z[c].z;
-                y.w += z[c].w;
-              }
-            *reinterpret_cast<uint2*>(v + (size_t)(w0 + t) * a.rank + r0 + r) =
-                make_uint2(bf16x2_rn(y.x * scale, y.y * scale), bf16x2_rn(y.z * scale, y.w * scale));
-          }
-          cluster_sync();   // s_sum is read by the whole cluster until here
-        } else {
-          __syncthreads();
+          for (int c = 1; c < kDownMaxParts; ++c)
+            if (c < parts) {
+              y.x += z[c].x;
+              y.y += z[c].y;
+              y.z += z[c].z;
+              y.w += z[c].w;
+            }
+          *reinterpret_cast<uint2*>(v + (size_t)(w0 + t) * a.rank + f0 + r) =
+              make_uint2(bf16x2_rn(y.x * scale, y.y * scale), bf16x2_rn(y.z * scale, y.w * scale));
         }
+        cluster_sync();   // s_sum is read by the whole cluster until here
       }
     }
   }
