@@ -859,8 +859,10 @@ static cudaError_t launch_down(const LinearArgs& a, uint16_t* xb, uint16_t* v, i
          a.K / kDownStep >= 2 * 8 * parts)
     parts *= 2;
   const int win = (a.T + kDownWin - 1) / kDownWin;
-  int slots = 4 * num_sms / (win * parts);   // CTAs past a window's items leave at once
-  if (slots < 8) slots = 8;
+  // CTAs past a window's items leave after grouping it. One or two windows are a
+  // decode batch, up to an item per token; more are prompts, whose runs make 4
+  // to 8 items a window (more are taken in turns)
+  int slots = win <= 2 ? 4 * num_sms / (win * parts) : 8;
   if (slots > kDownWin) slots = kDownWin;
   if (slots > a.T) slots = a.T;
   cudaLaunchConfig_t cfg = {};
@@ -911,12 +913,13 @@ static cudaError_t resident_clusters(int dev, int (&out)[kMaxSplit + 1]) {
 
 // Tokens per tile and pairs per tile that a call takes: the smallest estimate of
 // waves x (stages x clocks of a stage + clocks of a tile's start and end). A
-// stage costs the larger of its dequantisation (measured 500 clocks in row
-// order, 370 in pair order) and its eight MMAs (cs / 2 clocks each).
+// stage costs the larger of its dequantisation (measured in the running kernel:
+// 750 clocks in row order, 570 in pair order; alone 470 and 346) and its eight
+// MMAs (cs / 2 clocks each).
 static void linear_plan(int T, int N, int K, bool pair_order, const int (&resident)[kMaxSplit + 1],
                         int& cs, int& split) {
   const int npair = (N + 2 * kBM - 1) / (2 * kBM), nS = (K + kStageK - 1) / kStageK;
-  const double deq = pair_order ? 370 : 500;
+  const double deq = pair_order ? 570 : 750;
   double best = 0;
   cs = 0;
   const int c0 = (T + kMaxTok - 1) / kMaxTok;
@@ -980,7 +983,7 @@ cudaError_t launch_linear(const LinearArgs& a, int num_sms, cudaStream_t stream)
   linear_plan(a.T, a.N, a.K, x8, resident, p.cs, p.split);
   const int xstage = p.cs / 2 * 256;
   p.S = (kTmemCols - ((p.cs + 31) & ~31)) / kWCols;   // 4 at 256 tokens, 7 at 16
-  p.SL = !adapters ? 0 : p.cs > 128 ? 1 : p.cs > 64 ? 2 : kMaxL;
+  p.SL = !adapters ? 0 : p.cs > 64 ? 2 : kMaxL;
   p.rp = (a.rank + 15) & ~15;
   const int npair = (a.N + 2 * kBM - 1) / (2 * kBM), ttile = (a.T + p.cs - 1) / p.cs;
   const int64_t tiles = (int64_t)npair * ttile;
