@@ -357,6 +357,52 @@ def test_linear_larger_rows_sampled(moe):
     check_linear(moe, d, rows=[0, 31, 32, 255, 256, 700, 1023, 1024])
 
 
+@pytest.mark.parametrize("ids", ["runs", "random"])
+@pytest.mark.parametrize("K,x8", [(64, False), (192, True), (320, False)])
+def test_linear_many_tiles_per_pair(moe, ids, K, x8):
+    """More tiles than CTA pairs: each pair goes through several, with other adapters in each; K of one
+    stage, of one and a half, and of a number of stages that the dequantising groups do not divide."""
+    d = make_linear(3000, K, 2600, 24, 20, x8, 90 + K, ids)
+    rows = list(range(0, 3000, 97)) + [255, 256, 1499, 2998, 2999]
+    y = check_linear(moe, d, rows=rows)
+    part = {k: (v[1000:1600] if k in ("x", "x_scale", "adapter_ids", "x64") else v) for k, v in d.items()}
+    assert torch.equal(y[1000:1600], call_linear(moe, part))   # another tiling, the same sums
+
+
+def test_linear_offsets_past_32_bits(moe):
+    """2.46e9 outputs: rows around the 2^31st and the last ones."""
+    T, K, N = 600_000, 64, 4096
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(T, K, generator=g, device="cuda").bfloat16()
+    d = make_linear(1, K, N, 16, 3, False, 91, 1)
+    ids = torch.randint(-1, 3, (T,), generator=g, device="cuda", dtype=torch.int32)
+    a = {k: v.cuda() for k, v in d.items() if k not in ("x64", "x", "adapter_ids")}
+    y = moe.linear(x, a.pop("w"), a.pop("s"), adapter_ids=ids, **a)
+    torch.cuda.synchronize()
+    rows = torch.tensor([0, 1, 524287, 524288, 524289, 599_998, 599_999])
+    sub = dict(d, x=x[rows.cuda()].cpu(), adapter_ids=ids[rows.cuda()].cpu())
+    sub["x64"] = f64(sub["x"])
+    z = check_linear(moe, sub)
+    assert torch.equal(y[rows.cuda()], z)
+    del y
+    torch.cuda.empty_cache()
+
+
+def test_add_rmsnorm_offsets_past_32_bits(moe):
+    T, K = 140_000, 16384
+    x = torch.empty(T, K, dtype=torch.bfloat16, device="cuda").normal_()
+    gamma = torch.ones(K).bfloat16()
+    out, _, q, s = moe.add_rmsnorm(x, gamma.cuda(), None, out8="ocp")
+    torch.cuda.synchronize()
+    rows = torch.tensor([0, 131071, 131072, 131073, T - 1], device="cuda")   # 131072 * 16384 = 2^31
+    ref = moe.add_rmsnorm(x[rows].contiguous(), gamma.cuda(), None, out8="ocp")
+    assert torch.equal(out[rows], ref[0]) and torch.equal(s[rows], ref[3])
+    assert torch.equal(q.view(torch.uint8)[rows], ref[2].view(torch.uint8))
+    check_norm(moe, x[rows].cpu(), gamma, None, 1e-5, "ocp")
+    del x, out, q, s
+    torch.cuda.empty_cache()
+
+
 def test_linear_rows_do_not_depend_on_the_batch(moe):
     """A token with the NaN or infinity of another one beside it keeps its values."""
     for T in (20, 300):
