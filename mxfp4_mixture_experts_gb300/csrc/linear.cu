@@ -129,7 +129,7 @@ __device__ __forceinline__ void stg32(void* p, const uint4& a, const uint4& b) {
 
 // NT: n-tiles of 8 ranks per pass.
 template <int NT, bool X8>
-__global__ void __launch_bounds__(256, 2) adapter_down_kernel(const LinearArgs a, uint16_t* __restrict__ xb,
+__global__ void __launch_bounds__(256, 2) adapter_down_kernel(const LinearArgs a, uint16_t* __restrict__ xb /* null: not converted */,
                                                            uint16_t* __restrict__ v) {
   __shared__ int s_cid[kDownWin / 32][32], s_cn[kDownWin / 32][32], s_nc[kDownWin / 32];
   __shared__ int s_base[kDownWin], s_warp[kDownWin / 32], s_items;
@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(256, 2) adapter_down_kernel(const LinearArgs a
 
   // group the window's tokens by adapter: id -1 (no adapter) is a class of its
   // own where rows are converted; -2 stays out
-  constexpr int kNone = X8 ? -1 : -2;
+  const int kNone = X8 && xb != nullptr ? -1 : -2;
   int id = -2;
   if (tid < kDownWin) {
     if (w0 + tid < a.T) {
@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(256, 2) adapter_down_kernel(const LinearArgs a
           for (int i = 0; i < 4; ++i) {
             if (tk[i] < 0) continue;
             e4m3x16_to_bf16(e[i], sc[i], u[i][0], u[i][1]);
-            if (pass == 0)
+            if (xb != nullptr && pass == 0)
               stg32(xb + xo[i] + kDownStep * k, pair_order(u[i][0]), pair_order(u[i][1]));
           }
         }
@@ -839,6 +839,149 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
   }
 }
 
+// ---------------------------------------------------------------------------
+// The projection for few tokens (up to 16)
+// ---------------------------------------------------------------------------
+// Here the packed weights are all there is to move, and the tile kernel's
+// start, its one dequantising pass after another and its cluster-wide sums were most of
+// the time. A CTA takes 32 weight rows, its 16 warps the K values in steps of
+// 128: a lane loads 32 consecutive values (16 bytes, one scale block) of four
+// rows and of its tokens, all steps' loads under way at once, and the bf16
+// products run on m16n8k16 tiles straight from registers -- the order of K in
+// them is free as long as both operands take the same, so pair order costs
+// nothing. The warps' sums meet in shared memory in order; the epilogue adds the adapter's
+// second product from its 32 rows of B_a.
+constexpr int kFewTok = 16;
+constexpr int kFewRows = 32;
+constexpr int kFewWarps = 16;
+constexpr int kFewStep = 128;         // K values a step: 4 scale blocks, one per lane of a quad
+
+struct FewStep {
+  uint4 w[4];        // rows g, g + 8, g + 16, g + 24
+  uint32_t sc[4];
+};
+
+// TT: token tiles of 8.
+template <int TT, bool X8>
+__global__ void __launch_bounds__(kFewWarps * 32) linear_few_kernel(const LinearArgs a,
+                                                                    const uint16_t* __restrict__ v) {
+  __shared__ float part[kFewWarps][kFewRows][8 * TT + 1];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, q = lane & 3;
+  const int n0 = blockIdx.x * kFewRows;
+  const int blocks = a.K / kScaleBlock, steps = (blocks + 3) / 4;
+  const uint8_t* wr[4];
+  const uint8_t* sr[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {   // rows past N: the last row again, never stored
+    const size_t row = (size_t)min(n0 + g + 8 * i, a.N - 1);
+    wr[i] = a.w + row * (a.K / 2);
+    sr[i] = a.s + row * blocks;
+  }
+  auto fetch = [&](FewStep& d, int step) {
+    const int b = 4 * step + q;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      d.w[i] = make_uint4(0u, 0u, 0u, 0u);   // past K: zeros
+      d.sc[i] = 0;
+      if (b < blocks) {
+        d.w[i] = ldg16(wr[i] + (size_t)b * 16);
+        d.sc[i] = ldg_u8(sr[i] + b);
+      }
+    }
+  };
+  float acc[2][TT][4] = {};
+  FewStep buf[2];
+  fetch(buf[0], warp);
+  fetch(buf[1], warp + kFewWarps);
+  for (int s0 = warp; s0 < steps; s0 += 2 * kFewWarps) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int step = s0 + h * kFewWarps;
+      if (step >= steps) break;
+      const int b = 4 * step + q;
+      // this lane's 32 values of token g (and g + 8), in pair order
+      uint4 x[TT][4];
+#pragma unroll
+      for (int t = 0; t < TT; ++t) {
+        const int tok = g + 8 * t;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[t][j] = make_uint4(0u, 0u, 0u, 0u);
+        if (tok < a.T && b < blocks) {
+          const size_t at = (size_t)tok * a.K + (size_t)b * kScaleBlock;
+          if (X8) {
+            const uint8_t* src = static_cast<const uint8_t*>(a.x) + at;
+            const uint4 e0 = ldg16(src), e1 = ldg16(src + 16);
+            const uint32_t sc = ldg_u8(a.xs + (size_t)tok * blocks + b);
+            e4m3x16_to_bf16(e0, sc, x[t][0], x[t][1]);
+            e4m3x16_to_bf16(e1, sc, x[t][2], x[t][3]);
+          } else {
+            const uint16_t* src = static_cast<const uint16_t*>(a.x) + at;
+            ldg32(src, x[t][0], x[t][1]);
+            ldg32(src + 16, x[t][2], x[t][3]);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x[t][j] = pair_order(x[t][j]);
+        }
+      }
+      const FewStep& d = buf[h];
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {   // rows 16 m + g and 16 m + g + 8
+        uint32_t lo[16], hi[16];
+        const uint4 wl = d.w[2 * m], wh = d.w[2 * m + 1];
+        const uint32_t dl[4] = {wl.x, wl.y, wl.z, wl.w}, dh[4] = {wh.x, wh.y, wh.z, wh.w};
+        dequant32_bf16_pairs(dl, scale_mul(d.sc[2 * m]), lo);
+        dequant32_bf16_pairs(dh, scale_mul(d.sc[2 * m + 1]), hi);
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            mma_bf16_16816(acc[m][t], lo[4 * j], hi[4 * j], lo[4 * j + 1], hi[4 * j + 1], x[t][j].x,
+                           x[t][j].y);
+            mma_bf16_16816(acc[m][t], lo[4 * j + 2], hi[4 * j + 2], lo[4 * j + 3], hi[4 * j + 3],
+                           x[t][j].z, x[t][j].w);
+          }
+      }
+      fetch(buf[h], step + 2 * kFewWarps);
+    }
+  }
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+      part[warp][16 * m + g][8 * t + 2 * q] = acc[m][t][0];
+      part[warp][16 * m + g][8 * t + 2 * q + 1] = acc[m][t][1];
+      part[warp][16 * m + g + 8][8 * t + 2 * q] = acc[m][t][2];
+      part[warp][16 * m + g + 8][8 * t + 2 * q + 1] = acc[m][t][3];
+    }
+  if (a.ids != nullptr) grid_dependency_wait();   // v comes from the kernel before this one
+  __syncthreads();
+  for (int i = tid; i < kFewRows * 8 * TT; i += kFewWarps * 32) {
+    const int row = i % kFewRows, t = i / kFewRows, n = n0 + row;
+    if (t >= a.T || n >= a.N) continue;
+    float y = 0.f;
+#pragma unroll
+    for (int w = 0; w < kFewWarps; ++w) y += part[w][row][t];
+    const int ad = a.ids != nullptr ? a.ids[t] : -1;
+    if (ad >= 0 && ad < a.L) {
+      const uint16_t* br = a.b + ((size_t)ad * a.N + n) * a.rank;
+      const uint16_t* vr = v + (size_t)t * a.rank;
+      float z = 0.f;
+      for (int r = 0; r < a.rank; r += 8) {
+        const uint4 bb = ldg16(br + r), vv = ldcg16(vr + r);   // (v: no read-only path)
+        const uint32_t bw[4] = {bb.x, bb.y, bb.z, bb.w}, vw[4] = {vv.x, vv.y, vv.z, vv.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          z = fmaf(__uint_as_float(bw[j] << 16), __uint_as_float(vw[j] << 16), z);
+          z = fmaf(__uint_as_float(bw[j] & 0xFFFF0000u), __uint_as_float(vw[j] & 0xFFFF0000u), z);
+        }
+      }
+      y += z;
+    }
+    a.out[(size_t)t * a.N + n] = f32_to_bf16_rne(y);
+  }
+}
+
 size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 
 }  // namespace
@@ -948,7 +1091,8 @@ cudaError_t launch_linear(const LinearArgs& a, int num_sms, cudaStream_t stream)
   const bool adapters = a.ids != nullptr;
   uint16_t* v = reinterpret_cast<uint16_t*>(ws);
   uint16_t* xb = reinterpret_cast<uint16_t*>(ws + up256((size_t)a.T * a.rank * 2));
-  const bool x8 = a.xs != nullptr;
+  const bool x8 = a.xs != nullptr, few = a.T <= kFewTok;
+  if (few) xb = nullptr;
   if (a.status != nullptr &&
       (e = cudaMemsetAsync(a.status, 0, 4 * sizeof(int32_t), stream)) != cudaSuccess)
     return e;
@@ -963,12 +1107,29 @@ cudaError_t launch_linear(const LinearArgs& a, int num_sms, cudaStream_t stream)
       e = x8 ? launch_down<4, true>(a, xb, v, num_sms, stream)
              : launch_down<4, false>(a, xb, v, num_sms, stream);
     if (e != cudaSuccess) return e;
-  } else if (x8) {
+  } else if (x8 && !few) {
     const int64_t n16 = (int64_t)a.T * a.K / 16;
     const int64_t blocks = (n16 + 255) / 256;
     mx8_to_bf16_kernel<<<(unsigned)(blocks < num_sms * 8 ? blocks : num_sms * 8), 256, 0, stream>>>(
         static_cast<const uint4*>(a.x), a.xs, n16, reinterpret_cast<uint4*>(xb));
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  if (few) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((a.N + kFewRows - 1) / kFewRows);
+    cfg.blockDim = dim3(kFewWarps * 32);
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = adapters ? 1 : 0;
+    const uint16_t* vc = v;
+    if (a.T <= 8)
+      return x8 ? cudaLaunchKernelEx(&cfg, linear_few_kernel<1, true>, a, vc)
+                : cudaLaunchKernelEx(&cfg, linear_few_kernel<1, false>, a, vc);
+    return x8 ? cudaLaunchKernelEx(&cfg, linear_few_kernel<2, true>, a, vc)
+              : cudaLaunchKernelEx(&cfg, linear_few_kernel<2, false>, a, vc);
   }
   const void* x = x8 ? xb : a.x;
 
