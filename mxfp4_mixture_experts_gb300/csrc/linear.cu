@@ -840,11 +840,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
 }
 
 // ---------------------------------------------------------------------------
-// The projection for few tokens (up to 16)
+// The projection for few tokens (up to 16; at 32, whose tokens no longer stay in
+// registers over a step, this form took 16 to 45 us where the tiles take 15 to 19)
 // ---------------------------------------------------------------------------
 // Here the packed weights are all there is to move, and the tile kernel's
 // start, its one dequantising pass after another and its cluster-wide sums were most of
-// the time. A CTA takes 32 weight rows, its 16 warps the K values in steps of
+// the time. A CTA takes 32 weight rows, its warps the K values in steps of
 // 128: a lane loads 32 consecutive values (16 bytes, one scale block) of four
 // rows and of its tokens, all steps' loads under way at once, and the bf16
 // products run on m16n8k16 tiles straight from registers -- the order of K in
@@ -853,7 +854,6 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
 // second product from its 32 rows of B_a.
 constexpr int kFewTok = 16;
 constexpr int kFewRows = 32;
-constexpr int kFewWarps = 16;
 constexpr int kFewStep = 128;         // K values a step: 4 scale blocks, one per lane of a quad
 
 struct FewStep {
@@ -861,11 +861,13 @@ struct FewStep {
   uint32_t sc[4];
 };
 
-// TT: token tiles of 8.
-template <int TT, bool X8>
-__global__ void __launch_bounds__(kFewWarps * 32) linear_few_kernel(const LinearArgs a,
-                                                                    const uint16_t* __restrict__ v) {
-  __shared__ float part[kFewWarps][kFewRows][8 * TT + 1];
+// TT: token tiles of 8. WARPS: 16 where the CTAs do not outnumber the SMs, 8 (two
+// CTAs to an SM) where they do.
+template <int TT, bool X8, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) linear_few_kernel(const LinearArgs a,
+                                                                           const uint16_t* __restrict__ v) {
+  __shared__ float part[WARPS][kFewRows][8 * TT + 1];
+  constexpr int kFewWarps = WARPS;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, q = lane & 3;
   const int n0 = blockIdx.x * kFewRows;
@@ -900,30 +902,30 @@ __global__ void __launch_bounds__(kFewWarps * 32) linear_few_kernel(const Linear
       const int step = s0 + h * kFewWarps;
       if (step >= steps) break;
       const int b = 4 * step + q;
-      // this lane's 32 values of token g (and g + 8), in pair order
-      uint4 x[TT][4];
-#pragma unroll
-      for (int t = 0; t < TT; ++t) {
+      // this lane's 32 values of token 8 t + g, in pair order
+      auto token = [&](int t, uint4 (&x)[4]) {
         const int tok = g + 8 * t;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[t][j] = make_uint4(0u, 0u, 0u, 0u);
-        if (tok < a.T && b < blocks) {
-          const size_t at = (size_t)tok * a.K + (size_t)b * kScaleBlock;
-          if (X8) {
-            const uint8_t* src = static_cast<const uint8_t*>(a.x) + at;
-            const uint4 e0 = ldg16(src), e1 = ldg16(src + 16);
-            const uint32_t sc = ldg_u8(a.xs + (size_t)tok * blocks + b);
-            e4m3x16_to_bf16(e0, sc, x[t][0], x[t][1]);
-            e4m3x16_to_bf16(e1, sc, x[t][2], x[t][3]);
-          } else {
-            const uint16_t* src = static_cast<const uint16_t*>(a.x) + at;
-            ldg32(src, x[t][0], x[t][1]);
-            ldg32(src + 16, x[t][2], x[t][3]);
-          }
-#pragma unroll
-          for (int j = 0; j < 4; ++j) x[t][j] = pair_order(x[t][j]);
+        for (int j = 0; j < 4; ++j) x[j] = make_uint4(0u, 0u, 0u, 0u);
+        if (tok >= a.T || b >= blocks) return;
+        const size_t at = (size_t)tok * a.K + (size_t)b * kScaleBlock;
+        if (X8) {
+          const uint8_t* src = static_cast<const uint8_t*>(a.x) + at;
+          const uint4 e0 = ldg16(src), e1 = ldg16(src + 16);
+          const uint32_t sc = ldg_u8(a.xs + (size_t)tok * blocks + b);
+          e4m3x16_to_bf16(e0, sc, x[0], x[1]);
+          e4m3x16_to_bf16(e1, sc, x[2], x[3]);
+        } else {
+          const uint16_t* src = static_cast<const uint16_t*>(a.x) + at;
+          ldg32(src, x[0], x[1]);
+          ldg32(src + 16, x[2], x[3]);
         }
-      }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = pair_order(x[j]);
+      };
+      uint4 x[TT][4];
+#pragma unroll
+      for (int t = 0; t < TT; ++t) token(t, x[t]);
       const FewStep& d = buf[h];
 #pragma unroll
       for (int m = 0; m < 2; ++m) {   // rows 16 m + g and 16 m + g + 8
@@ -933,7 +935,7 @@ __global__ void __launch_bounds__(kFewWarps * 32) linear_few_kernel(const Linear
         dequant32_bf16_pairs(dl, scale_mul(d.sc[2 * m]), lo);
         dequant32_bf16_pairs(dh, scale_mul(d.sc[2 * m + 1]), hi);
 #pragma unroll
-        for (int t = 0; t < TT; ++t)
+        for (int t = 0; t < TT; ++t) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             mma_bf16_16816(acc[m][t], lo[4 * j], hi[4 * j], lo[4 * j + 1], hi[4 * j + 1], x[t][j].x,
@@ -941,6 +943,7 @@ __global__ void __launch_bounds__(kFewWarps * 32) linear_few_kernel(const Linear
             mma_bf16_16816(acc[m][t], lo[4 * j + 2], hi[4 * j + 2], lo[4 * j + 3], hi[4 * j + 3],
                            x[t][j].z, x[t][j].w);
           }
+        }
       }
       fetch(buf[h], step + 2 * kFewWarps);
     }
@@ -1085,6 +1088,21 @@ static void linear_plan(int T, int N, int K, bool pair_order, const int (&reside
   }
 }
 
+template <int TT, bool X8>
+static cudaError_t launch_few(const LinearArgs& a, const uint16_t* v, bool wide, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((a.N + kFewRows - 1) / kFewRows);
+  cfg.blockDim = dim3((wide ? 8 : 16) * 32);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = a.ids != nullptr ? 1 : 0;
+  return wide ? cudaLaunchKernelEx(&cfg, linear_few_kernel<TT, X8, 8>, a, v)
+              : cudaLaunchKernelEx(&cfg, linear_few_kernel<TT, X8, 16>, a, v);
+}
+
 cudaError_t launch_linear(const LinearArgs& a, int num_sms, cudaStream_t stream) {
   cudaError_t e;
   char* ws = static_cast<char*>(a.ws);
@@ -1115,21 +1133,10 @@ cudaError_t launch_linear(const LinearArgs& a, int num_sms, cudaStream_t stream)
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   if (few) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((a.N + kFewRows - 1) / kFewRows);
-    cfg.blockDim = dim3(kFewWarps * 32);
-    cfg.stream = stream;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = adapters ? 1 : 0;
-    const uint16_t* vc = v;
+    const bool wide = (a.N + kFewRows - 1) / kFewRows > num_sms;
     if (a.T <= 8)
-      return x8 ? cudaLaunchKernelEx(&cfg, linear_few_kernel<1, true>, a, vc)
-                : cudaLaunchKernelEx(&cfg, linear_few_kernel<1, false>, a, vc);
-    return x8 ? cudaLaunchKernelEx(&cfg, linear_few_kernel<2, true>, a, vc)
-              : cudaLaunchKernelEx(&cfg, linear_few_kernel<2, false>, a, vc);
+      return x8 ? launch_few<1, true>(a, v, wide, stream) : launch_few<1, false>(a, v, wide, stream);
+    return x8 ? launch_few<2, true>(a, v, wide, stream) : launch_few<2, false>(a, v, wide, stream);
   }
   const void* x = x8 ? xb : a.x;
 
