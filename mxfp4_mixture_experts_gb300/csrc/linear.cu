@@ -5,19 +5,25 @@
 // x in bf16, or in MXFP8 (E4M3 with an E8M0 scale per 32 values). Sums in
 // fp32, one rounding of y to bf16.
 //
-//   prepare  v_t = bf16(scale_a * A_a x_t): the tokens of a window grouped by
-//            adapter, up to 32 of one adapter to a pass of m16n8k16 tiles, K split over the
-//            warps of a CTA and, for few tokens, over the CTAs of a cluster.
-//            MXFP8 rows are converted on the way, once, to the bf16 rows that
-//            the projection reads (exact but for products beyond bf16's range)
-//   linear   the projection on the 5th-generation tensor cores, the second
-//            adapter product as further columns of the same reduction
+//   down    v_t = bf16(scale_a * A_a x_t): the tokens of a window grouped by
+//           adapter, up to 32 of one adapter to a pass of m16n8k16 tiles, K split
+//           over the warps of a CTA and, for few tokens, over the CTAs of a
+//           cluster. MXFP8 rows are converted on the way, once, to the bf16 rows
+//           that the projection reads (exact but for products beyond bf16's
+//           range). T = 8192, K = 6144, rank 16: 34 us for the 150 MB of the
+//           conversion, 4.5 TB/s
+//   linear  the projection on the 5th-generation tensor cores, the second adapter
+//           product as further columns of the same reduction; or, for up to 16
+//           tokens, register tiles without any of that
+//
+// The two launches overlap: the projection starts beside the kernel before it
+// and waits for it only where it takes its results.
 //
 // The rounding of v to bf16 (relative 2^-8 of the adapter's share of y, below
 // the rounding of y itself) is what lets that product run on the same
 // tensor-core accumulators.
 //
-// linear kernel: a pair of CTAs holds a tile of 256 weight rows x up to 256
+// Tile kernel: a pair of CTAs holds a tile of 256 weight rows x up to 256
 // tokens. The MMA computes D[weight row][token] with the dequantised weights as
 // operand A in tensor memory and the tokens as operand B in shared memory, half
 // of them in each CTA. After the K values, the adapters that the tile's tokens
@@ -41,6 +47,13 @@
 // run while the output rows go out. Few tiles (small T) split K over up to 4
 // pairs of a cluster, whose partial sums meet in shared memory, added in rank
 // order.
+//
+// Measured (T = 8192, K = 6144, N = 4096, rank 16): the tile kernel alone 204 us =
+// 2.0 PFLOP/s, its MMAs back to back (1024 clocks for a stage's eight); with the
+// down kernel and MXFP8 rows 240 us a call. Between 33 and about 1000 tokens the
+// dequantisation bounds a stage (its ALU instructions: 350 to 470 clocks of a
+// stage at best, 570 to 750 beside the other warps), below that the fixed
+// steps of a tile: start 3 us, first operands 2 us, the cluster's addition 2 us.
 #include <cuda.h>
 #include <cstdint>
 
@@ -82,31 +95,6 @@ __device__ __forceinline__ void e4m3x16_to_bf16(const uint4& u, uint32_t scale, 
   b = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
-// MXFP8 rows -> bf16 rows in pair order, 16 values a thread (calls without adapters).
-__global__ void __launch_bounds__(256) mx8_to_bf16_kernel(const uint4* __restrict__ q,
-                                                          const uint8_t* __restrict__ s, int64_t n16,
-                                                          uint4* __restrict__ out) {
-  grid_launch_dependents();
-  for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < n16; i += (int64_t)gridDim.x * 256) {
-    uint4 a, b;
-    e4m3x16_to_bf16(q[i], ldg_u8(s + (i >> 1)), a, b);
-    out[2 * i] = pair_order(a);
-    out[2 * i + 1] = pair_order(b);
-  }
-}
-
-// ---------------------------------------------------------------------------
-// v = bf16(scale A x): windows of tokens, items of up to 32 tokens of one
-// adapter (with MXFP8 rows also of none: those are only converted). gridDim.y
-// CTAs take a window's items in turn; the gridDim.z CTAs of a cluster split K
-// and add their parts in rank order through shared memory.
-// ---------------------------------------------------------------------------
-constexpr int kDownWin = 128;     // tokens per window
-constexpr int kDownTok = 32;      // tokens per item (two m16 tiles)
-constexpr int kDownMaxParts = 8;
-constexpr int kDownStep = 64;     // K values per step: 16 a lane
-constexpr int kDownSum = 64;      // ranks whose parts a cluster adds at once
-
 __device__ __forceinline__ uint4 ldg16(const void* p) {
   uint4 v;
   asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
@@ -127,10 +115,35 @@ __device__ __forceinline__ void stg32(void* p, const uint4& a, const uint4& b) {
                : "memory");
 }
 
+// MXFP8 rows -> bf16 rows in pair order, 16 values a thread (calls without adapters).
+__global__ void __launch_bounds__(256) mx8_to_bf16_kernel(const uint4* __restrict__ q,
+                                                          const uint8_t* __restrict__ s, int64_t n16,
+                                                          uint4* __restrict__ out) {
+  grid_launch_dependents();
+  for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < n16; i += (int64_t)gridDim.x * 256) {
+    uint4 a, b;
+    e4m3x16_to_bf16(q[i], ldg_u8(s + (i >> 1)), a, b);
+    stg32(out + 2 * i, pair_order(a), pair_order(b));
+  }
+}
+
+// ---------------------------------------------------------------------------
+// v = bf16(scale A x): windows of tokens, items of up to 32 tokens of one
+// adapter (with MXFP8 rows also of none: those are only converted). gridDim.y
+// CTAs take a window's items in turn; the gridDim.z CTAs of a cluster split K
+// and add their parts in rank order through shared memory.
+// ---------------------------------------------------------------------------
+constexpr int kDownWin = 128;     // tokens per window
+constexpr int kDownTok = 32;      // tokens per item (two m16 tiles)
+constexpr int kDownMaxParts = 8;
+constexpr int kDownStep = 64;     // K values per step: 16 a lane
+constexpr int kDownSum = 64;      // ranks whose parts a cluster adds at once
+
 // NT: n-tiles of 8 ranks per pass.
 template <int NT, bool X8>
-__global__ void __launch_bounds__(256, 2) adapter_down_kernel(const LinearArgs a, uint16_t* __restrict__ xb /* null: not converted */,
-                                                           uint16_t* __restrict__ v) {
+__global__ void __launch_bounds__(256, 2)
+    adapter_down_kernel(const LinearArgs a, uint16_t* __restrict__ xb /* null: not converted */,
+                        uint16_t* __restrict__ v) {
   __shared__ int s_cid[kDownWin / 32][32], s_cn[kDownWin / 32][32], s_nc[kDownWin / 32];
   __shared__ int s_base[kDownWin], s_warp[kDownWin / 32], s_items;
   __shared__ int s_tok[kDownWin][kDownTok];   // [item][slot]: token of the window, -1 empty
@@ -399,9 +412,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
       l_empty[kMaxL], l_list, d_full, d_empty, drain;
   __shared__ uint32_t tmem_slot, s_bits[kLinearMaxAdapters / 32];
   __shared__ int s_list[kListMax], s_tokad[kMaxTok], s_count, s_anybad, s_fail, s_efail[2];
-  static_assert(kEpiThreads == kMaxTok, "one thread per token of a tile");
-
   __shared__ uint8_t s_bad[kListMax];
+  static_assert(kEpiThreads == kMaxTok, "one thread per token of a tile");
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int hb = p.cs / 2;                           // tokens of the tile in this CTA
   const int xchunk = hb * 128, xstage = 2 * xchunk;
@@ -589,13 +601,20 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
       uint32_t sc = scales(i), sc1 = scales(i + kDeqGroups);
 #pragma unroll 1
       for (; i < nS; i += kDeqGroups) {
-        if (!warp_wait_cta(&p_full[sp], pp)) { fail = 1; break; }
-        const uint8_t* src = sP + sp * kPStage + m * 64;
-        const int swz = (m >> 1) & 3;
-        if (k >= p.S) {   // the MMAs that read this ring slot have completed
+        // A wait by parity tells a phase from the one before it, not from the one
+        // before that, so nobody may wait a whole round of a ring ahead. Order
+        // and depths see to it: the MMAs that read this operand slot (stage k - S)
+        // have completed, and by their order all stages before, so S >= the groups
+        // keeps `empty` in step; the packed slot's fill before this one (stage
+        // k - SP) has then been used too where SP >= S, and was this group's own
+        // where SP is the number of groups.
+        if (k >= p.S) {
           if (!warp_wait_cluster(&empty[s], ph ^ 1u)) { fail = 1; break; }
           tc_fence_after();
         }
+        if (!warp_wait_cta(&p_full[sp], pp)) { fail = 1; break; }
+        const uint8_t* src = sP + sp * kPStage + m * 64;
+        const int swz = (m >> 1) & 3;
         const int blocks = (st0 + i) * kStageK + kBK < K ? 4 : 2;   // K may end inside the stage
         const uint32_t dst = wlane + s * kWCols;
         uint4 w = *reinterpret_cast<const uint4*>(src + (swz << 4));
@@ -840,21 +859,22 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
 }
 
 // ---------------------------------------------------------------------------
-// The projection for few tokens (up to 16; at 32, whose tokens no longer stay in
-// registers over a step, this form took 16 to 45 us where the tiles take 15 to 19)
+// The projection for few tokens
 // ---------------------------------------------------------------------------
-// Here the packed weights are all there is to move, and the tile kernel's
-// start, its one dequantising pass after another and its cluster-wide sums were most of
-// the time. A CTA takes 32 weight rows, its warps the K values in steps of
-// 128: a lane loads 32 consecutive values (16 bytes, one scale block) of four
-// rows and of its tokens, all steps' loads under way at once, and the bf16
-// products run on m16n8k16 tiles straight from registers -- the order of K in
-// them is free as long as both operands take the same, so pair order costs
-// nothing. The warps' sums meet in shared memory in order; the epilogue adds the adapter's
-// second product from its 32 rows of B_a.
+// Up to 16 tokens the packed weights are all there is to move, and the tile
+// kernel's start, its stages one after another and its cluster-wide sums were
+// most of the time (T = 1, K = 6144, N = 4096, rank 16, in a graph: 14.3 us, here
+// 7.5; T = 16: 17 and 13.7). At 32 tokens, which no longer stay in registers over
+// a step, this form took 16 to 45 us where the tiles take 15 to 19.
+//
+// A CTA takes 32 weight rows, its warps the K values in steps of 128 (4 scale
+// blocks, one per lane of a quad): a lane loads 32 consecutive values of four
+// rows and of its tokens, the weights two steps early, and the bf16 products run
+// on m16n8k16 tiles straight from registers -- the order of K in them is free as
+// long as both operands take the same, so pair order costs nothing. The warps' sums meet in shared memory in order; the epilogue adds the
+// adapter's second product from its 32 rows of B_a.
 constexpr int kFewTok = 16;
 constexpr int kFewRows = 32;
-constexpr int kFewStep = 128;         // K values a step: 4 scale blocks, one per lane of a quad
 
 struct FewStep {
   uint4 w[4];        // rows g, g + 8, g + 16, g + 24
@@ -864,10 +884,9 @@ struct FewStep {
 // TT: token tiles of 8. WARPS: 16 where the CTAs do not outnumber the SMs, 8 (two
 // CTAs to an SM) where they do.
 template <int TT, bool X8, int WARPS>
-__global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) linear_few_kernel(const LinearArgs a,
-                                                                           const uint16_t* __restrict__ v) {
+__global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
+    linear_few_kernel(const LinearArgs a, const uint16_t* __restrict__ v) {
   __shared__ float part[WARPS][kFewRows][8 * TT + 1];
-  constexpr int kFewWarps = WARPS;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, q = lane & 3;
   const int n0 = blockIdx.x * kFewRows;
@@ -895,11 +914,11 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) linear_few_kernel(cons
   float acc[2][TT][4] = {};
   FewStep buf[2];
   fetch(buf[0], warp);
-  fetch(buf[1], warp + kFewWarps);
-  for (int s0 = warp; s0 < steps; s0 += 2 * kFewWarps) {
+  fetch(buf[1], warp + WARPS);
+  for (int s0 = warp; s0 < steps; s0 += 2 * WARPS) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int step = s0 + h * kFewWarps;
+      const int step = s0 + h * WARPS;
       if (step >= steps) break;
       const int b = 4 * step + q;
       // this lane's 32 values of token 8 t + g, in pair order
@@ -945,7 +964,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) linear_few_kernel(cons
           }
         }
       }
-      fetch(buf[h], step + 2 * kFewWarps);
+      fetch(buf[h], step + 2 * WARPS);
     }
   }
 #pragma unroll
@@ -959,12 +978,12 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) linear_few_kernel(cons
     }
   if (a.ids != nullptr) grid_dependency_wait();   // v comes from the kernel before this one
   __syncthreads();
-  for (int i = tid; i < kFewRows * 8 * TT; i += kFewWarps * 32) {
+  for (int i = tid; i < kFewRows * 8 * TT; i += WARPS * 32) {
     const int row = i % kFewRows, t = i / kFewRows, n = n0 + row;
     if (t >= a.T || n >= a.N) continue;
     float y = 0.f;
 #pragma unroll
-    for (int w = 0; w < kFewWarps; ++w) y += part[w][row][t];
+    for (int w = 0; w < WARPS; ++w) y += part[w][row][t];
     const int ad = a.ids != nullptr ? a.ids[t] : -1;
     if (ad >= 0 && ad < a.L) {
       const uint16_t* br = a.b + ((size_t)ad * a.N + n) * a.rank;
@@ -991,7 +1010,7 @@ size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 
 size_t linear_workspace_bytes(int T, int K, int N, int rank, bool x8) {
   (void)N;
-  return up256((size_t)T * rank * 2) + (x8 ? up256((size_t)T * K * 2) : 0);
+  return up256((size_t)T * rank * 2) + (x8 && T > kFewTok ? up256((size_t)T * K * 2) : 0);
 }
 
 // The kernel of the adapters' first product (and of the conversion): CTAs over
@@ -1169,6 +1188,8 @@ cudaError_t launch_linear(const LinearArgs& a, int num_sms, cudaStream_t stream)
   const size_t fixed = 1024 + (size_t)p.S * xstage + (p.split == 1 && obytes > lbytes ? obytes : lbytes);
   p.SP = (int)((kDynSmem - fixed) / kPStage);
   if (p.SP > kMaxSP) p.SP = kMaxSP;
+  if (p.SP < p.S) p.SP = kDeqGroups;   // (see the dequantising warps' waits)
+  if (p.S < kDeqGroups || fixed + (size_t)p.SP * kPStage > kDynSmem) return cudaErrorInvalidConfiguration;
   const size_t smem = fixed + (size_t)p.SP * kPStage;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((tiles < resident[p.split] ? tiles : resident[p.split]) * p.split * 2));   // persistent

@@ -424,7 +424,8 @@ def add_rmsnorm(x: torch.Tensor, gamma: torch.Tensor, residual: Optional[torch.T
     raised by one where the block would saturate), else None."""
     _need(x, "x", torch.bfloat16, 2)
     _need(gamma, "gamma", torch.bfloat16, 1)
-    T, K = x.shape
+    shape = x.shape
+    T, K = shape
     if gamma.shape[0] != K:
         raise ValueError("gamma must be [K]")
     if out8 is not None and out8 not in MX8_RULES:
@@ -432,26 +433,25 @@ def add_rmsnorm(x: torch.Tensor, gamma: torch.Tensor, residual: Optional[torch.T
     dev = x.device
     if residual is not None:
         _need(residual, "residual", torch.bfloat16, 2)
-        if residual.shape != x.shape:
+        if residual.shape != shape:
             raise ValueError("residual must be [T, K]")
-        if residual_out is None:
-            residual_out = _empty(x.shape, torch.bfloat16, dev, stream)
     if residual_out is not None:
         _need(residual_out, "residual_out", torch.bfloat16, 2)
-        if residual_out.shape != x.shape:
+        if residual_out.shape != shape:
             raise ValueError("residual_out must be [T, K]")
-    if not bf16:
-        if out is not None:
+    elif residual is not None:
+        residual_out = _empty(shape, torch.bfloat16, dev, stream)
+    if out is not None:
+        if not bf16:
             raise ValueError("out is not written when bf16 is False")
-    elif out is None:
-        out = _empty(x.shape, torch.bfloat16, dev, stream)
-    else:
         _need(out, "out", torch.bfloat16, 2)
-        if out.shape != x.shape:
+        if out.shape != shape:
             raise ValueError("out must be [T, K]")
+    elif bf16:
+        out = _empty(shape, torch.bfloat16, dev, stream)
     q = s = None
     if out8 is not None:
-        q = _empty((T, K), torch.float8_e4m3fn, dev, stream)
+        q = _empty(shape, torch.float8_e4m3fn, dev, stream)
         s = _empty((T, K // 32), torch.uint8, dev, stream)
     rc = lib().mxfp4_moe_add_rmsnorm(_addr(x), _addr(residual), _addr(gamma), T, K, eps,
                                      MX8_RULES[out8 or "ocp"], _addr(residual_out), _addr(out),
@@ -483,16 +483,18 @@ def router_scored(logits: torch.Tensor, topk: int, scoring: str = "sigmoid",
         _need(bias, "bias", torch.float32, 1)
         if bias.shape[0] != E:
             raise ValueError("bias must be [E]")
-    for name, t, dtype in (("topk_ids", topk_ids, torch.int32),
-                           ("topk_weights", topk_weights, torch.float32)):
-        if t is not None:
-            _need(t, name, dtype, 2)
-            if tuple(t.shape) != (T, topk):
-                raise ValueError(f"{name} must be [T, topk]")
     if topk_ids is None:
         topk_ids = _empty((T, topk), torch.int32, logits.device, stream)
+    else:
+        _need(topk_ids, "topk_ids", torch.int32, 2)
+        if tuple(topk_ids.shape) != (T, topk):
+            raise ValueError("topk_ids must be [T, topk]")
     if topk_weights is None:
         topk_weights = _empty((T, topk), torch.float32, logits.device, stream)
+    else:
+        _need(topk_weights, "topk_weights", torch.float32, 2)
+        if tuple(topk_weights.shape) != (T, topk):
+            raise ValueError("topk_weights must be [T, topk]")
     rc = lib().mxfp4_moe_router_scored(_addr(logits), _addr(bias), T, E, topk, SCORES[scoring],
                                        n_group, topk_group, group_top, int(bool(renormalise)),
                                        route_scale, _addr(topk_ids), _addr(topk_weights),
