@@ -40,7 +40,7 @@ constexpr int kRsWarps = 8;
 // Order-preserving map of non-NaN floats to integers >= 1 (-0 as +0), and back.
 __device__ __forceinline__ uint32_t order_key(float x) {
   const uint32_t b = __float_as_uint(__fadd_rn(x, 0.f));
-  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);   // negative: all bits, else the sign
 }
 __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kRsWarps * 32)
   auto score = [&](float v) -> float {
     if (!(v > -INFINITY)) return 0.f;   // NaN too
     if (a.scoring == 0) return __fdiv_rn(v == m ? 1.f : expf(v - m), total);
-    return __fdiv_rn(1.f, __fadd_rn(1.f, expf(-v)));
+    return __frcp_rn(__fadd_rn(1.f, expf(-v)));   // (the rounded 1 / x, as a division gives it)
   };
   uint32_t key[NPL];   // of what the choice goes by; 0: out
   if (biased || a.n_group > 1) {
