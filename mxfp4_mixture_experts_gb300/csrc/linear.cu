@@ -1013,23 +1013,56 @@ size_t linear_workspace_bytes(int T, int K, int N, int rank, bool x8) {
   return up256((size_t)T * rank * 2) + (x8 && T > kFewTok ? up256((size_t)T * K * 2) : 0);
 }
 
-// The kernel of the adapters' first product (and of the conversion): CTAs over
-// windows, their items and, while those are few, parts of K.
-template <int NT, bool X8>
-static cudaError_t launch_down(const LinearArgs& a, uint16_t* xb, uint16_t* v, int num_sms,
-                               cudaStream_t stream) {
-  const int items = (a.T + kDownTok - 1) / kDownTok;   // at least
-  int parts = 1;
-  while (parts < kDownMaxParts && items * parts * 2 <= 2 * num_sms &&
-         a.K / kDownStep >= 2 * 8 * parts)
-    parts *= 2;
+// Grid of the adapters' first product: CTAs over windows, slots for their items
+// (more items are taken in turns, CTAs past a window's items leave after grouping
+// it) and parts of K.
+//
+// On all SMs: parts of K while that makes less than two CTAs to an SM; one or two
+// windows are a decode batch, up to an item per token, more are prompts, whose runs
+// make 4 to 8 items a window. Where the projection needs nothing but the sums from
+// it (`clocks` > 0, what that takes): in the `room` CTAs that leave the projection
+// its SMs, in the most parts that leave a slot for each of a window's items (one
+// for two of a prompt's), if that ends with the projection. Both then start
+// together, and the projection's last steps find the sums ready. us in graphs,
+// against all SMs always (N = 4096; 5760 at K = 2880):
+//   K = 6144, rank 16: T = 8  8.3 (11.4), T = 64 15.7 (19.8), T = 1024 37.8 (43.3)
+//   K = 2880, rank 16: T = 8  8.3  (8.3), T = 64 14.2 (16.5), T = 1024 31.5 (35.5)
+//   K = 7168, rank 64: T = 8 14.4 (16.5), T = 64 20.1 (24.9), T =  256 33.6 (32.4)
+struct DownPlan {
+  int parts, slots;
+};
+static DownPlan down_plan(const LinearArgs& a, double clocks, int room, int num_sms) {
   const int win = (a.T + kDownWin - 1) / kDownWin;
-  // CTAs past a window's items leave after grouping it. One or two windows are a
-  // decode batch, up to an item per token; more are prompts, whose runs make 4
-  // to 8 items a window (more are taken in turns)
+  const int most = a.T < kDownWin ? a.T : kDownWin;   // items of a window, at most
+  int parts = 1;
+  while (parts < kDownMaxParts && a.K / kDownStep >= 2 * 8 * parts) parts *= 2;
+  // a window's items, as a rule: the adapters that its tokens draw, or runs of 32
+  double none = 1;   // the share of them that no token draws
+  for (int t = 0; t < most; ++t) none *= 1 - 1.0 / a.L;
+  int items = (int)(a.L * (1 - none));
+  if (items < 1) items = 1;
+  if (win > 2 || items < most / kDownTok) items = most / kDownTok + 1;
+  for (int p = parts; clocks > 0 && p >= 1; p /= 2) {
+    int slots = room / (win * p);
+    const int turns = slots >= items ? 1 : a.T > kFewTok && p == 1 && 2 * slots >= items ? 2 : 0;
+    // an item: a warp's steps and, in parts, the cluster's sums
+    const int steps = (a.K / kDownStep + 8 * p - 1) / (8 * p);
+    const double item = (p > 1 ? 4500 : 2000) + steps * (a.rank <= 16 ? 700.0 : 2700.0);
+    if (turns == 0 || 5000 + turns * item > clocks) continue;
+    if (turns == 1 && win > 2) slots = 8;   // (a window of more runs than that)
+    return {p, slots < most ? slots : most};
+  }
+  const int total = (a.T + kDownTok - 1) / kDownTok;   // items, at least
+  while (parts > 1 && total * parts > 2 * num_sms) parts /= 2;
   int slots = win <= 2 ? 4 * num_sms / (win * parts) : 8;
-  if (slots > kDownWin) slots = kDownWin;
-  if (slots > a.T) slots = a.T;
+  return {parts, slots < most ? slots : most};
+}
+
+template <int NT, bool X8>
+static cudaError_t launch_down(const LinearArgs& a, uint16_t* xb, uint16_t* v, const DownPlan& plan,
+                               cudaStream_t stream) {
+  const int win = (a.T + kDownWin - 1) / kDownWin;
+  const int parts = plan.parts, slots = plan.slots;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(win, slots, parts);
   cfg.blockDim = dim3(256);
@@ -1082,7 +1115,7 @@ static cudaError_t resident_clusters(int dev, int (&out)[kMaxSplit + 1]) {
 // 750 clocks in row order, 570 in pair order; alone 470 and 346) and its eight
 // MMAs (cs / 2 clocks each).
 static void linear_plan(int T, int N, int K, bool pair_order, const int (&resident)[kMaxSplit + 1],
-                        int& cs, int& split) {
+                        int& cs, int& split, double& clocks) {
   const int npair = (N + 2 * kBM - 1) / (2 * kBM), nS = (K + kStageK - 1) / kStageK;
   const double deq = pair_order ? 570 : 750;
   double best = 0;
@@ -1099,6 +1132,7 @@ static void linear_plan(int T, int N, int K, bool pair_order, const int (&reside
       const double t = 6000 + waves * ((double)((nS + sp - 1) / sp) * stage + 2500) + (sp > 1 ? 1500 : 0);
       if (cs == 0 || t < best) {
         best = t;
+        clocks = t;
         cs = tok;
         split = sp;
       }
@@ -1133,16 +1167,45 @@ cudaError_t launch_linear(const LinearArgs& a, int num_sms, cudaStream_t stream)
   if (a.status != nullptr &&
       (e = cudaMemsetAsync(a.status, 0, 4 * sizeof(int32_t), stream)) != cudaSuccess)
     return e;
+  // the projection's grid, its clocks, and how many CTAs of the kernel before it
+  // leave it all the SMs that it needs
+  LinearParams p = {};
+  const int few_ctas = (a.N + kFewRows - 1) / kFewRows;
+  const bool wide = few_ctas > num_sms;
+  int64_t tiles = 0;
+  int resident[kMaxSplit + 1], room;
+  double clocks;
+  if (few) {
+    room = wide ? 2 * num_sms - few_ctas : num_sms - few_ctas;   // (8-warp CTAs leave half an SM)
+    clocks = 22000;   // (of both, one after the other: it waits for the sums at its end)
+  } else {
+    int dev = 0;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+    if (dev < 0 || dev >= kGrantDevices) return cudaErrorInvalidDevice;
+    if ((e = resident_clusters(dev, resident)) != cudaSuccess) return e;
+    linear_plan(a.T, a.N, a.K, x8, resident, p.cs, p.split, clocks);
+    clocks *= 1.1;   // (hidden but for an end worth less than starting later)
+    tiles = (int64_t)((a.N + 2 * kBM - 1) / (2 * kBM)) * ((a.T + p.cs - 1) / p.cs);
+    // clusters that can start a tile late; of larger clusters what no cluster fits
+    // into may lie next to them
+    const int64_t waves = (tiles + resident[p.split] - 1) / resident[p.split];
+    const int spare = (int)(waves * resident[p.split] - tiles) * p.split;
+    const int rest = num_sms / 2 - resident[p.split] * p.split;
+    room = p.split <= 2 ? 2 * (spare + rest) : spare > 0 ? spare + rest : (rest + 1) / 2;
+    if (x8) clocks = 0;   // it waits for the converted rows
+  }
+  DownPlan plan = {0, 0};
+  if (adapters) plan = down_plan(a, clocks, room, num_sms);
   if (adapters) {
     if (a.rank <= 8)
-      e = x8 ? launch_down<1, true>(a, xb, v, num_sms, stream)
-             : launch_down<1, false>(a, xb, v, num_sms, stream);
+      e = x8 ? launch_down<1, true>(a, xb, v, plan, stream)
+             : launch_down<1, false>(a, xb, v, plan, stream);
     else if (a.rank <= 16)
-      e = x8 ? launch_down<2, true>(a, xb, v, num_sms, stream)
-             : launch_down<2, false>(a, xb, v, num_sms, stream);
+      e = x8 ? launch_down<2, true>(a, xb, v, plan, stream)
+             : launch_down<2, false>(a, xb, v, plan, stream);
     else
-      e = x8 ? launch_down<4, true>(a, xb, v, num_sms, stream)
-             : launch_down<4, false>(a, xb, v, num_sms, stream);
+      e = x8 ? launch_down<4, true>(a, xb, v, plan, stream)
+             : launch_down<4, false>(a, xb, v, plan, stream);
     if (e != cudaSuccess) return e;
   } else if (x8 && !few) {
     const int64_t n16 = (int64_t)a.T * a.K / 16;
@@ -1152,28 +1215,18 @@ cudaError_t launch_linear(const LinearArgs& a, int num_sms, cudaStream_t stream)
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   if (few) {
-    const bool wide = (a.N + kFewRows - 1) / kFewRows > num_sms;
     if (a.T <= 8)
       return x8 ? launch_few<1, true>(a, v, wide, stream) : launch_few<1, false>(a, v, wide, stream);
     return x8 ? launch_few<2, true>(a, v, wide, stream) : launch_few<2, false>(a, v, wide, stream);
   }
   const void* x = x8 ? xb : a.x;
 
-  LinearParams p = {};
   p.a = a;
   p.v = v;
-  int dev = 0;
-  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
-  if (dev < 0 || dev >= kGrantDevices) return cudaErrorInvalidDevice;
-  int resident[kMaxSplit + 1];
-  if ((e = resident_clusters(dev, resident)) != cudaSuccess) return e;
-  linear_plan(a.T, a.N, a.K, x8, resident, p.cs, p.split);
   const int xstage = p.cs / 2 * 256;
   p.S = (kTmemCols - ((p.cs + 31) & ~31)) / kWCols;   // 4 at 256 tokens, 7 at 16
   p.SL = !adapters ? 0 : p.cs > 64 ? 2 : kMaxL;
   p.rp = (a.rank + 15) & ~15;
-  const int npair = (a.N + 2 * kBM - 1) / (2 * kBM), ttile = (a.T + p.cs - 1) / p.cs;
-  const int64_t tiles = (int64_t)npair * ttile;
   const uint64_t dims[3] = {128, (uint64_t)a.T, (uint64_t)a.K / kBK};
   const uint64_t strides[2] = {(uint64_t)a.K * 2, 128};
   const uint32_t box[3] = {128, (uint32_t)p.cs / 2, 2};
