@@ -139,16 +139,21 @@ constexpr int kDownMaxParts = 8;
 constexpr int kDownStep = 64;     // K values per step: 16 a lane
 constexpr int kDownSum = 64;      // ranks whose parts a cluster adds at once
 
-// NT: n-tiles of 8 ranks per pass.
+// NT: n-tiles of 8 ranks per pass. From 17 ranks on one CTA to an SM: its loads and
+// sums want more than 128 registers. With two, and 64 ranks in two passes over x,
+// K = 7168, N = 4096, T = 16 took 20.3 us where this takes 13.6, T = 128 26.4 and
+// 20.6, T = 8192 300 and 287 (of MXFP8 rows 321 and 297); of 32 ranks T = 64 16.5 and
+// 12.1, T = 8192 96 and 103 (K = 4096, N = 2048).
 template <int NT, bool X8>
-__global__ void __launch_bounds__(256, 2)
+__global__ void __launch_bounds__(256, NT <= 2 ? 2 : 1)
     adapter_down_kernel(const LinearArgs a, uint16_t* __restrict__ xb /* null: not converted */,
                         uint16_t* __restrict__ v) {
   __shared__ int s_cid[kDownWin / 32][32], s_cn[kDownWin / 32][32], s_nc[kDownWin / 32];
   __shared__ int s_base[kDownWin], s_warp[kDownWin / 32], s_items;
   __shared__ int s_tok[kDownWin][kDownTok];   // [item][slot]: token of the window, -1 empty
   __shared__ int s_ad[kDownWin];              // [item]: adapter, -1 none
-  __shared__ float part[8][16][NT * 8 + 4];
+  constexpr int NP = NT < 4 ? NT : 4;         // n-tiles that the warps add at once
+  __shared__ float part[8][16][NP * 8 + 4];
   __shared__ __align__(16) float s_sum[kDownTok][kDownSum];   // this CTA's part of an item
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int w0 = blockIdx.x * kDownWin;
@@ -245,7 +250,7 @@ __global__ void __launch_bounds__(256, 2)
       float acc[2][NT][4] = {};
       // each lane holds 16 consecutive values of its rows; both operands take
       // them in the same order, so the products are those of row order
-#pragma unroll NT <= 2 ? 2 : 1
+#pragma unroll NT <= 4 ? 2 : 1
       for (int k = k0; k < k1; ++k) {
         uint4 u[4][2], w[NT][2], e[4];
         uint32_t sc[4];
@@ -292,27 +297,30 @@ __global__ void __launch_bounds__(256, 2)
       if (ad < 0) break;
       const float scale = a.ascale != nullptr ? a.ascale[ad] : 1.f;
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
+      for (int mj = 0; mj < 2 * NT / NP; ++mj) {
+        const int m = mj / (NT / NP), j0 = mj % (NT / NP) * NP;
         if (m == 1 && !two) break;
+        if (j0 >= nt) continue;
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
+        for (int j = 0; j < NP; ++j) {
           float* dst = &part[warp][g][8 * j + 2 * q];
-          dst[0] = acc[m][j][0];
-          dst[1] = acc[m][j][1];
-          dst[8 * (NT * 8 + 4)] = acc[m][j][2];
-          dst[8 * (NT * 8 + 4) + 1] = acc[m][j][3];
+          dst[0] = acc[m][j0 + j][0];
+          dst[1] = acc[m][j0 + j][1];
+          dst[8 * (NP * 8 + 4)] = acc[m][j0 + j][2];
+          dst[8 * (NP * 8 + 4) + 1] = acc[m][j0 + j][3];
         }
         __syncthreads();
-        for (int i = tid; i < 16 * 8 * nt; i += 256) {
-          const int row = i / (8 * nt), r = i - row * (8 * nt);
+        const int n = 8 * min(NP, nt - j0), f = r0 + 8 * j0;
+        for (int i = tid; i < 16 * n; i += 256) {
+          const int row = i / n, r = i - row * n;
           const int t = s_tok[it][16 * m + row];
           float z = 0.f;
 #pragma unroll
           for (int w = 0; w < 8; ++w) z += part[w][row][r];
           if (parts > 1)
-            s_sum[16 * m + row][r0 % kDownSum + r] = z;
+            s_sum[16 * m + row][f % kDownSum + r] = z;
           else if (t >= 0)
-            v[(size_t)(w0 + t) * a.rank + r0 + r] = f32_to_bf16_rne(z * scale);
+            v[(size_t)(w0 + t) * a.rank + f + r] = f32_to_bf16_rne(z * scale);
         }
         __syncthreads();
       }
@@ -1017,17 +1025,18 @@ size_t linear_workspace_bytes(int T, int K, int N, int rank, bool x8) {
 // (more items are taken in turns, CTAs past a window's items leave after grouping
 // it) and parts of K.
 //
-// On all SMs: parts of K while that makes less than two CTAs to an SM; one or two
-// windows are a decode batch, up to an item per token, more are prompts, whose runs
-// make 4 to 8 items a window. Where the projection needs nothing but the sums from
-// it (`clocks` > 0, what that takes): in the `room` CTAs that leave the projection
-// its SMs, in the most parts that leave a slot for each of a window's items (one
-// for two of a prompt's), if that ends with the projection. Both then start
-// together, and the projection's last steps find the sums ready. us in graphs,
-// against all SMs always (N = 4096; 5760 at K = 2880):
+// On all SMs: parts of K while their CTAs run at once (eight parts' sums only from
+// 65 tokens on: T = 32, K = 6144, MXFP8 rows 17.5 us with four, 19.1 with eight);
+// one or two windows are a decode batch, up to an item per token, more are prompts,
+// whose runs make 4 to 8 items a window. Where the projection needs nothing but the
+// sums from it (`clocks` > 0, what that takes): in the `room` CTAs that leave the
+// projection its SMs, in the most parts that leave a slot for each of a window's
+// items (one for two of a prompt's), if that ends with the projection. Both then
+// start together, and the projection's last steps find the sums ready. us in
+// graphs, against all SMs always (N = 4096; 5760 at K = 2880):
 //   K = 6144, rank 16: T = 8  8.3 (11.4), T = 64 15.7 (19.8), T = 1024 37.8 (43.3)
 //   K = 2880, rank 16: T = 8  8.3  (8.3), T = 64 14.2 (16.5), T = 1024 31.5 (35.5)
-//   K = 7168, rank 64: T = 8 14.4 (16.5), T = 64 20.1 (24.9), T =  256 33.6 (32.4)
+//   K = 7168, rank 64: T = 8 10.6 (14.7), T = 64 18   (22),   T =  512 35   (39)
 struct DownPlan {
   int parts, slots;
 };
@@ -1047,14 +1056,16 @@ static DownPlan down_plan(const LinearArgs& a, double clocks, int room, int num_
     const int turns = slots >= items ? 1 : a.T > kFewTok && p == 1 && 2 * slots >= items ? 2 : 0;
     // an item: a warp's steps and, in parts, the cluster's sums
     const int steps = (a.K / kDownStep + 8 * p - 1) / (8 * p);
-    const double item = (p > 1 ? 4500 : 2000) + steps * (a.rank <= 16 ? 700.0 : 2700.0);
+    const double item = (p > 1 ? 4500 : 2000) + steps * (a.rank <= 16 ? 700.0 : 1200.0);
     if (turns == 0 || 5000 + turns * item > clocks) continue;
-    if (turns == 1 && win > 2) slots = 8;   // (a window of more runs than that)
+    if (turns == 1 && win > 2) slots = 16;   // (a window of more runs than that)
     return {p, slots < most ? slots : most};
   }
-  const int total = (a.T + kDownTok - 1) / kDownTok;   // items, at least
-  while (parts > 1 && total * parts > 2 * num_sms) parts /= 2;
-  int slots = win <= 2 ? 4 * num_sms / (win * parts) : 8;
+  // items in all: those of 32 tokens, and where runs end
+  const int total = (a.T + kDownTok - 1) / kDownTok + (win < 3 ? 0 : win < a.L ? win : a.L);
+  const int fit = a.rank <= 16 ? 2 * num_sms : num_sms;   // CTAs at once
+  while (parts > 1 && (total * parts > fit || (parts > 4 && total <= 2))) parts /= 2;
+  int slots = win <= 2 ? fit / (win * parts) : 8;
   return {parts, slots < most ? slots : most};
 }
 
@@ -1203,9 +1214,12 @@ cudaError_t launch_linear(const LinearArgs& a, int num_sms, cudaStream_t stream)
     else if (a.rank <= 16)
       e = x8 ? launch_down<2, true>(a, xb, v, plan, stream)
              : launch_down<2, false>(a, xb, v, plan, stream);
-    else
+    else if (a.rank <= 32)
       e = x8 ? launch_down<4, true>(a, xb, v, plan, stream)
              : launch_down<4, false>(a, xb, v, plan, stream);
+    else
+      e = x8 ? launch_down<8, true>(a, xb, v, plan, stream)
+             : launch_down<8, false>(a, xb, v, plan, stream);
     if (e != cudaSuccess) return e;
   } else if (x8 && !few) {
     const int64_t n16 = (int64_t)a.T * a.K / 16;
