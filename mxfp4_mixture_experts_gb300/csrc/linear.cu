@@ -1030,13 +1030,14 @@ size_t linear_workspace_bytes(int T, int K, int N, int rank, bool x8) {
 // one or two windows are a decode batch, up to an item per token, more are prompts,
 // whose runs make 4 to 8 items a window. Where the projection needs nothing but the
 // sums from it (`clocks` > 0, what that takes): in the `room` CTAs that leave the
-// projection its SMs, in the most parts that leave a slot for each of a window's
-// items (one for two of a prompt's), if that ends with the projection. Both then
-// start together, and the projection's last steps find the sums ready. us in
-// graphs, against all SMs always (N = 4096; 5760 at K = 2880):
-//   K = 6144, rank 16: T = 8  8.3 (11.4), T = 64 15.7 (19.8), T = 1024 37.8 (43.3)
+// projection its SMs, if a grid of them has a slot for each of a window's items
+// (or one for two, without parts) and ends with the projection: the most parts, or,
+// for the tiles, the fewest that end well before (T = 128, K = 6144: one part 16.5
+// us, four 17.0). Both then start together, and the projection's last steps find
+// the sums ready. us in graphs, against all SMs always (N = 4096; 5760 at K = 2880):
+//   K = 6144, rank 16: T = 8  8.3 (11.4), T = 64 15.4 (19.8), T = 1024 37.6 (43.3)
 //   K = 2880, rank 16: T = 8  8.3  (8.3), T = 64 14.2 (16.5), T = 1024 31.5 (35.5)
-//   K = 7168, rank 64: T = 8 10.6 (14.7), T = 64 18   (22),   T =  512 35   (39)
+//   K = 7168, rank 64: T = 8 10.6 (14.7), T = 32 16.8 (21.8), T =  512 34.4 (38.8)
 struct DownPlan {
   int parts, slots;
 };
@@ -1051,16 +1052,20 @@ static DownPlan down_plan(const LinearArgs& a, double clocks, int room, int num_
   int items = (int)(a.L * (1 - none));
   if (items < 1) items = 1;
   if (win > 2 || items < most / kDownTok) items = most / kDownTok + 1;
+  DownPlan beside = {0, 0};
   for (int p = parts; clocks > 0 && p >= 1; p /= 2) {
     int slots = room / (win * p);
-    const int turns = slots >= items ? 1 : a.T > kFewTok && p == 1 && 2 * slots >= items ? 2 : 0;
+    const bool one = slots >= items, two = a.T > kFewTok && p == 1 && 2 * slots >= items;
+    if (!one && (!two || beside.parts > 0)) continue;
     // an item: a warp's steps and, in parts, the cluster's sums
     const int steps = (a.K / kDownStep + 8 * p - 1) / (8 * p);
     const double item = (p > 1 ? 4500 : 2000) + steps * (a.rank <= 16 ? 700.0 : 1200.0);
-    if (turns == 0 || 5000 + turns * item > clocks) continue;
-    if (turns == 1 && win > 2) slots = 16;   // (a window of more runs than that)
-    return {p, slots < most ? slots : most};
+    const double end = 5000 + (one ? 1 : 2) * item;
+    if (end > clocks || (beside.parts > 0 && (a.T <= kFewTok || end > 0.65 * clocks))) continue;
+    if (one && win > 2) slots = 12;   // (a window of more runs than that)
+    beside = {p, slots < most ? slots : most};
   }
+  if (beside.parts > 0) return beside;
   // items in all: those of 32 tokens, and where runs end
   const int total = (a.T + kDownTok - 1) / kDownTok + (win < 3 ? 0 : win < a.L ? win : a.L);
   const int fit = a.rank <= 16 ? 2 * num_sms : num_sms;   // CTAs at once
