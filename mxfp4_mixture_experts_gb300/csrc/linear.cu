@@ -1023,55 +1023,70 @@ size_t linear_workspace_bytes(int T, int K, int N, int rank, bool x8) {
 
 // Grid of the adapters' first product: CTAs over windows, slots for their items
 // (more items are taken in turns, CTAs past a window's items leave after grouping
-// it) and parts of K.
-//
+// it) and parts of K, with its end in clocks.
+struct DownPlan {
+  int parts, slots;   // parts 0: none
+  double end;
+};
+struct DownWork {
+  int win = 0, most = 0;   // windows; the items of one, at most
+  int items = 0;   // the same, as a rule: the adapters that its tokens draw, or runs of 32
+  int total = 0;   // items in all: those of 32 tokens, and where runs end
+  int parts = 0;   // at most: a step or two to a warp; 0: no adapters
+  DownWork() = default;
+  explicit DownWork(const LinearArgs& a) {   // (of a call with adapters)
+    win = (a.T + kDownWin - 1) / kDownWin;
+    most = a.T < kDownWin ? a.T : kDownWin;
+    double none = 1;   // the share of the adapters that no token draws
+    for (int t = 0; t < most; ++t) none *= 1 - 1.0 / a.L;
+    items = (int)(a.L * (1 - none));
+    if (items < 1) items = 1;
+    if (win > 1 || items < most / kDownTok) items = most / kDownTok + 1;
+    total = (a.T + kDownTok - 1) / kDownTok + (win < 3 ? 0 : win < a.L ? win : a.L);
+    for (parts = 1; parts < kDownMaxParts && a.K / kDownStep >= 2 * 8 * parts;) parts *= 2;
+  }
+};
+// Clocks until `turns` items after one another end: a warp's steps of each and, in
+// parts, the cluster's sums.
+static double down_end(const LinearArgs& a, int parts, int turns) {
+  const int steps = (a.K / kDownStep + 8 * parts - 1) / (8 * parts);
+  return 5000 + turns * ((parts > 1 ? 4500 : 2000) + steps * (a.rank <= 16 ? 700.0 : 1200.0));
+}
 // On all SMs: parts of K while their CTAs run at once (eight parts' sums only from
-// 65 tokens on: T = 32, K = 6144, MXFP8 rows 17.5 us with four, 19.1 with eight);
-// one or two windows are a decode batch, up to an item per token, more are prompts,
-// whose runs make 4 to 8 items a window. Where the projection needs nothing but the
-// sums from it (`clocks` > 0, what that takes): in the `room` CTAs that leave the
-// projection its SMs, if a grid of them has a slot for each of a window's items
-// (or one for two, without parts) and ends with the projection: the most parts, or,
-// for the tiles, the fewest that end well before (T = 128, K = 6144: one part 16.5
-// us, four 17.0). Both then start together, and the projection's last steps find
-// the sums ready. us in graphs, against all SMs always (N = 4096; 5760 at K = 2880):
+// 65 tokens on: T = 32, K = 6144, MXFP8 rows 17.5 us with four, 19.1 with eight).
+// One or two windows are a decode batch, up to an item per token, more are prompts,
+// whose runs make 4 to 8 items a window.
+static DownPlan down_alone(const LinearArgs& a, const DownWork& w, int num_sms) {
+  const int fit = a.rank <= 16 ? 2 * num_sms : num_sms;   // CTAs at once
+  int parts = w.parts;
+  while (parts > 1 && (w.total * parts > fit || (parts > 4 && w.total <= 2))) parts /= 2;
+  const int slots = w.win <= 2 ? fit / (w.win * parts) : 8;
+  return {parts, slots < w.most ? slots : w.most,
+          down_end(a, parts, (w.total * parts + fit - 1) / fit)};
+}
+// Beside a projection that needs nothing but the sums, and these after `clocks`:
+// in the `room` CTAs that leave it its SMs, if a grid of them has a slot for each
+// of a window's items (or one for two, without parts) and ends in time. The most
+// parts, or, for the tiles, the fewest that end well before (T = 64, K = 6144: one
+// part 15.4 us, four 15.8). Both kernels then start together, and the projection's
+// last steps find the sums ready. us in graphs, against all SMs always (N = 4096;
+// 5760 at K = 2880):
 //   K = 6144, rank 16: T = 8  8.3 (11.4), T = 64 15.4 (19.8), T = 1024 37.6 (43.3)
 //   K = 2880, rank 16: T = 8  8.3  (8.3), T = 64 14.2 (16.5), T = 1024 31.5 (35.5)
 //   K = 7168, rank 64: T = 8 10.6 (14.7), T = 32 16.8 (21.8), T =  512 34.4 (38.8)
-struct DownPlan {
-  int parts, slots;
-};
-static DownPlan down_plan(const LinearArgs& a, double clocks, int room, int num_sms) {
-  const int win = (a.T + kDownWin - 1) / kDownWin;
-  const int most = a.T < kDownWin ? a.T : kDownWin;   // items of a window, at most
-  int parts = 1;
-  while (parts < kDownMaxParts && a.K / kDownStep >= 2 * 8 * parts) parts *= 2;
-  // a window's items, as a rule: the adapters that its tokens draw, or runs of 32
-  double none = 1;   // the share of them that no token draws
-  for (int t = 0; t < most; ++t) none *= 1 - 1.0 / a.L;
-  int items = (int)(a.L * (1 - none));
-  if (items < 1) items = 1;
-  if (win > 2 || items < most / kDownTok) items = most / kDownTok + 1;
-  DownPlan beside = {0, 0};
-  for (int p = parts; clocks > 0 && p >= 1; p /= 2) {
-    int slots = room / (win * p);
-    const bool one = slots >= items, two = a.T > kFewTok && p == 1 && 2 * slots >= items;
-    if (!one && (!two || beside.parts > 0)) continue;
-    // an item: a warp's steps and, in parts, the cluster's sums
-    const int steps = (a.K / kDownStep + 8 * p - 1) / (8 * p);
-    const double item = (p > 1 ? 4500 : 2000) + steps * (a.rank <= 16 ? 700.0 : 1200.0);
-    const double end = 5000 + (one ? 1 : 2) * item;
-    if (end > clocks || (beside.parts > 0 && (a.T <= kFewTok || end > 0.65 * clocks))) continue;
-    if (one && win > 2) slots = 12;   // (a window of more runs than that)
-    beside = {p, slots < most ? slots : most};
+static DownPlan down_beside(const LinearArgs& a, const DownWork& w, double clocks, int room) {
+  const bool few = a.T <= kFewTok;
+  DownPlan best = {0, 0, 0};
+  for (int p = w.parts; p >= 1; p /= 2) {
+    int slots = room / (w.win * p);
+    const bool one = slots >= w.items, two = !few && p == 1 && 2 * slots >= w.items;
+    if (!one && (!two || best.parts > 0)) continue;
+    const double end = down_end(a, p, one ? 1 : 2);
+    if (end > 1.25 * clocks || (best.parts > 0 && (few || end > 0.76 * clocks))) continue;
+    if (one && w.win > 1) slots = 12;   // (a window of more runs than that)
+    best = {p, slots < w.most ? slots : w.most, end};
   }
-  if (beside.parts > 0) return beside;
-  // items in all: those of 32 tokens, and where runs end
-  const int total = (a.T + kDownTok - 1) / kDownTok + (win < 3 ? 0 : win < a.L ? win : a.L);
-  const int fit = a.rank <= 16 ? 2 * num_sms : num_sms;   // CTAs at once
-  while (parts > 1 && (total * parts > fit || (parts > 4 && total <= 2))) parts /= 2;
-  int slots = win <= 2 ? fit / (win * parts) : 8;
-  return {parts, slots < most ? slots : most};
+  return best;
 }
 
 template <int NT, bool X8>
@@ -1125,36 +1140,58 @@ static cudaError_t resident_clusters(int dev, int (&out)[kMaxSplit + 1]) {
   return cudaSuccess;
 }
 
-// Tokens per tile and pairs per tile that a call takes: the smallest estimate of
-// waves x (stages x clocks of a stage + clocks of a tile's start and end). A
-// stage costs the larger of its dequantisation (measured in the running kernel:
-// 750 clocks in row order, 570 in pair order; alone 470 and 346) and its eight
-// MMAs (cs / 2 clocks each).
-static void linear_plan(int T, int N, int K, bool pair_order, const int (&resident)[kMaxSplit + 1],
-                        int& cs, int& split, double& clocks) {
-  const int npair = (N + 2 * kBM - 1) / (2 * kBM), nS = (K + kStageK - 1) / kStageK;
-  const double deq = pair_order ? 570 : 750;
+// Tokens per tile and pairs per tile that a call takes, and the grid of the
+// adapters' first product before it (`alone`: on all SMs): the
+// smallest estimate of waves x (stages x clocks of a stage + clocks of a tile's
+// start and end), and of that kernel before or beside it. A stage costs the larger
+// of its dequantisation (measured in the running kernel: 750 clocks in row order,
+// 680 in pair order; alone 470 and 346) and its eight MMAs (cs / 2 clocks each);
+// the cluster's addition goes by the tile's tokens. Without adapters this choice
+// was within 5% of the best of all sizes and splits tried by hand (6 shapes, T = 20
+// to 4096), within 11% at N = 512.
+static DownPlan linear_plan(const LinearArgs& a, bool pair_order, const DownWork& w,
+                            const DownPlan& alone, const int (&resident)[kMaxSplit + 1],
+                            int num_sms, int& cs, int& split) {
+  const int npair = (a.N + 2 * kBM - 1) / (2 * kBM), nS = (a.K + kStageK - 1) / kStageK;
+  const double deq = pair_order ? 680 : 750;
+  DownPlan plan = alone;
   double best = 0;
   cs = 0;
-  const int c0 = (T + kMaxTok - 1) / kMaxTok;
+  const int c0 = (a.T + kMaxTok - 1) / kMaxTok;
   for (int c = c0; c <= c0 + 8; ++c) {
-    const int tok = ((T + c - 1) / c + 15) & ~15;
-    const int64_t tiles = (int64_t)npair * ((T + tok - 1) / tok);
+    const int tok = ((a.T + c - 1) / c + 15) & ~15;
+    const int64_t tiles = (int64_t)npair * ((a.T + tok - 1) / tok);
     for (int sp = 1; sp <= kMaxSplit; ++sp) {
       // split tiles take one pass; parts of at least two stages
       if (sp > 1 && (tiles > resident[sp] || nS < 2 * sp)) continue;
       const double stage = 4.0 * tok > deq ? 4.0 * tok : deq;
-      const double waves = (double)((tiles + resident[sp] - 1) / resident[sp]);
-      const double t = 6000 + waves * ((double)((nS + sp - 1) / sp) * stage + 2500) + (sp > 1 ? 1500 : 0);
+      const int64_t waves = (tiles + resident[sp] - 1) / resident[sp];
+      const double clocks = 6000 + (double)waves * ((double)((nS + sp - 1) / sp) * stage + 2500);
+      double t = clocks + alone.end;
+      DownPlan d = alone;
+      if (w.parts > 0 && !pair_order) {   // (pair order: it waits for the converted rows)
+        // clusters that can start a tile late; of larger clusters what no cluster
+        // fits into may lie next to them
+        const int spare = (int)(waves * resident[sp] - tiles) * sp;
+        const int rest = num_sms / 2 - resident[sp] * sp;
+        const DownPlan b = down_beside(
+            a, w, clocks, sp <= 2 ? 2 * (spare + rest) : spare > 0 ? spare + rest : (rest + 1) / 2);
+        if (b.parts > 0) {
+          d = b;
+          t = clocks > b.end ? clocks : b.end;
+        }
+      }
+      if (sp > 1) t += 500 + 25 * tok;
       if (cs == 0 || t < best) {
         best = t;
-        clocks = t;
+        plan = d;
         cs = tok;
         split = sp;
       }
     }
     if (tok <= 16) break;
   }
+  return plan;
 }
 
 template <int TT, bool X8>
@@ -1183,35 +1220,25 @@ cudaError_t launch_linear(const LinearArgs& a, int num_sms, cudaStream_t stream)
   if (a.status != nullptr &&
       (e = cudaMemsetAsync(a.status, 0, 4 * sizeof(int32_t), stream)) != cudaSuccess)
     return e;
-  // the projection's grid, its clocks, and how many CTAs of the kernel before it
-  // leave it all the SMs that it needs
   LinearParams p = {};
   const int few_ctas = (a.N + kFewRows - 1) / kFewRows;
   const bool wide = few_ctas > num_sms;
-  int64_t tiles = 0;
-  int resident[kMaxSplit + 1], room;
-  double clocks;
-  if (few) {
-    room = wide ? 2 * num_sms - few_ctas : num_sms - few_ctas;   // (8-warp CTAs leave half an SM)
-    clocks = 22000;   // (of both, one after the other: it waits for the sums at its end)
-  } else {
+  int resident[kMaxSplit + 1];
+  const DownWork w = adapters ? DownWork(a) : DownWork();
+  DownPlan plan = adapters ? down_alone(a, w, num_sms) : DownPlan{0, 0, 0};
+  if (!few) {
     int dev = 0;
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
     if (dev < 0 || dev >= kGrantDevices) return cudaErrorInvalidDevice;
     if ((e = resident_clusters(dev, resident)) != cudaSuccess) return e;
-    linear_plan(a.T, a.N, a.K, x8, resident, p.cs, p.split, clocks);
-    clocks *= 1.1;   // (hidden but for an end worth less than starting later)
-    tiles = (int64_t)((a.N + 2 * kBM - 1) / (2 * kBM)) * ((a.T + p.cs - 1) / p.cs);
-    // clusters that can start a tile late; of larger clusters what no cluster fits
-    // into may lie next to them
-    const int64_t waves = (tiles + resident[p.split] - 1) / resident[p.split];
-    const int spare = (int)(waves * resident[p.split] - tiles) * p.split;
-    const int rest = num_sms / 2 - resident[p.split] * p.split;
-    room = p.split <= 2 ? 2 * (spare + rest) : spare > 0 ? spare + rest : (rest + 1) / 2;
-    if (x8) clocks = 0;   // it waits for the converted rows
+    plan = linear_plan(a, x8, w, plan, resident, num_sms, p.cs, p.split);
+  } else if (adapters) {
+    // 18500 clocks: both kernels, one after the other (this one waits for the sums
+    // at its end; its CTAs of 8 warps leave half an SM)
+    const int room = wide ? 2 * num_sms - few_ctas : num_sms - few_ctas;
+    const DownPlan beside = down_beside(a, w, 18500, room);
+    if (beside.parts > 0) plan = beside;
   }
-  DownPlan plan = {0, 0};
-  if (adapters) plan = down_plan(a, clocks, room, num_sms);
   if (adapters) {
     if (a.rank <= 8)
       e = x8 ? launch_down<1, true>(a, xb, v, plan, stream)
@@ -1253,7 +1280,7 @@ cudaError_t launch_linear(const LinearArgs& a, int num_sms, cudaStream_t stream)
       !encode_tiled_2d(&p.tmapW, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.w, (uint64_t)a.K / 2, (uint64_t)a.N,
                        (uint64_t)a.K / 2, kStageK / 2, kBM, CU_TENSOR_MAP_SWIZZLE_64B))
     return cudaErrorInvalidValue;
-  p.tiles = (int)tiles;
+  p.tiles = (a.N + 2 * kBM - 1) / (2 * kBM) * ((a.T + p.cs - 1) / p.cs);
   const size_t lbytes = (size_t)p.SL * (kBTile + xstage / 2), obytes = (size_t)p.cs * kOutPitch;
   // packed weights take what is left, 3 stages (256 tokens) to 8: with 3 at 144
   // tokens the dequantisation waited on them, 850 instead of 620 clocks a stage
@@ -1264,7 +1291,7 @@ cudaError_t launch_linear(const LinearArgs& a, int num_sms, cudaStream_t stream)
   if (p.S < kDeqGroups || fixed + (size_t)p.SP * kPStage > kDynSmem) return cudaErrorInvalidConfiguration;
   const size_t smem = fixed + (size_t)p.SP * kPStage;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((tiles < resident[p.split] ? tiles : resident[p.split]) * p.split * 2));   // persistent
+  cfg.gridDim = dim3((unsigned)((p.tiles < resident[p.split] ? p.tiles : resident[p.split]) * p.split * 2));   // persistent
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
