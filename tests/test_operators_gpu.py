@@ -357,6 +357,21 @@ def test_linear_larger_rows_sampled(moe):
     check_linear(moe, d, rows=[0, 31, 32, 255, 256, 700, 1023, 1024])
 
 
+@pytest.mark.parametrize("x8", [False, True])
+@pytest.mark.parametrize("rank", [8, 32, 40, 64, 72, 96, 136, 256])
+@pytest.mark.parametrize("T", [4, 16, 20, 130])
+def test_linear_ranks_with_k_in_parts(moe, T, rank, x8):
+    """K split over clusters of the adapters' first product, ranks of one, two and more passes."""
+    check_linear(moe, make_linear(T, 4096, 136, rank, 5, x8, 700 + T + rank))
+
+
+@pytest.mark.parametrize("N", [4800, 4864, 9728, 10240])
+def test_linear_few_free_sms(moe, N):
+    """Outputs that leave the kernel before the projection few SMs, none, or half of each."""
+    for T in (3, 16):
+        check_linear(moe, make_linear(T, 1024, N, 64, 6, False, 800 + N + T), rows=[0, T - 1])
+
+
 @pytest.mark.parametrize("ids", ["runs", "random"])
 @pytest.mark.parametrize("K,x8", [(64, False), (192, True), (320, False)])
 def test_linear_many_tiles_per_pair(moe, ids, K, x8):
