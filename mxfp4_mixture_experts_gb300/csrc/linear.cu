@@ -5,8 +5,7 @@
 // x in bf16, or in MXFP8 (E4M3 with an E8M0 scale per 32 values). Sums in
 // fp32, one rounding of y to bf16.
 //
-//   down    v_t = bf16(scale_a * A_a x_t): the tokens of a window grouped by
-//           adapter, up to 32 of one adapter to a pass of m16n8k16 tiles, K split
+//   down    v_t = scale_a * A_a x_t: the tokens of a window grouped by adapter, up to 32 of one adapter to a pass of m16n8k16 tiles, K split
 //           over the warps of a CTA and, for few tokens, over the CTAs of a
 //           cluster. MXFP8 rows are converted on the way, once, to the bf16 rows
 //           that the projection reads (exact but for products beyond bf16's
@@ -19,9 +18,12 @@
 // The two launches overlap: the projection starts beside the kernel before it
 // and waits for it only where it takes its results.
 //
-// The rounding of v to bf16 (relative 2^-8 of the adapter's share of y, below
-// the rounding of y itself) is what lets that product run on the same
-// tensor-core accumulators.
+// v is summed in fp32 and rounded to 17 significant bits (2^-17 of each product
+// |B_a[n][r] v_t[r]|): the sum of two bf16 values hi and lo, which the tile kernel's
+// tensor cores take one after the other into the same fp32 accumulators, so both
+// forms multiply the same v. (hi alone leaves 2^-9 of the products, which where
+// they or W x cancel is more than y's own rounding; a third part, for all 24 bits,
+// would cost half as many MMAs again.)
 //
 // Tile kernel: a pair of CTAs holds a tile of 256 weight rows x up to 256
 // tokens. The MMA computes D[weight row][token] with the dequantised weights as
@@ -29,7 +31,8 @@
 // of them in each CTA. After the K values, the adapters that the tile's tokens
 // name follow as columns: column c stands for (c / rp)-th adapter of the tile,
 // rank index c % rp (rp = rank rounded up to 16); operand A holds B_a[n][r],
-// operand B v_t[r] for the tokens of that adapter and 0 for the others. So
+// operand B hi and, in a second tile, lo of v_t[r] for the tokens of that adapter
+// and 0 for the others. So
 // tokens need no sorting, and a tile pays for the adapters it has. A B_a value
 // that is not finite would turn the others' zeros into NaN; such values are
 // left out of the tile and added in the epilogue to the tokens of their adapter
@@ -95,6 +98,31 @@ __device__ __forceinline__ void e4m3x16_to_bf16(const uint4& u, uint32_t scale, 
   b = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
+// v = hi + lo in bf16 but for 2^-17 |v|: hi the nearest bf16 (the next towards 0 where that
+// is infinite), lo the rest, rounded. Infinities and NaN have no rest.
+__device__ __forceinline__ void split_bf16(float v, float& hi, float& lo) {
+  hi = __uint_as_float((uint32_t)f32_to_bf16_rne(v) << 16);
+  lo = 0.f;
+  if (fabsf(v) < INFINITY) {
+    if (!(fabsf(hi) < INFINITY)) hi = __uint_as_float(__float_as_uint(v) & 0xFFFF0000u);
+    lo = __uint_as_float((uint32_t)f32_to_bf16_rne(v - hi) << 16);
+  }
+}
+// v as the sum of its parts: exact, and split into the same sum again.
+__device__ __forceinline__ float two_bf16(float v) {
+  float hi, lo;
+  split_bf16(v, hi, lo);
+  return hi + lo;
+}
+// Two values' parts as bf16 pairs.
+__device__ __forceinline__ void split_bf16x2(float a, float b, uint32_t& hi, uint32_t& lo) {
+  float ha, la, hb, lb;
+  split_bf16(a, ha, la);
+  split_bf16(b, hb, lb);
+  hi = bf16x2_rn(ha, hb);
+  lo = bf16x2_rn(la, lb);
+}
+
 __device__ __forceinline__ uint4 ldg16(const void* p) {
   uint4 v;
   asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
@@ -115,6 +143,13 @@ __device__ __forceinline__ void stg32(void* p, const uint4& a, const uint4& b) {
                : "memory");
 }
 
+// 16 bytes of fp32 from L2: written by a kernel that may still run when this one starts.
+__device__ __forceinline__ float4 ldcg_f4(const float* p) {
+  const uint4 u = ldcg16(p);
+  return make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z),
+                     __uint_as_float(u.w));
+}
+
 // MXFP8 rows -> bf16 rows in pair order, 16 values a thread (calls without adapters).
 __global__ void __launch_bounds__(256) mx8_to_bf16_kernel(const uint4* __restrict__ q,
                                                           const uint8_t* __restrict__ s, int64_t n16,
@@ -128,7 +163,7 @@ __global__ void __launch_bounds__(256) mx8_to_bf16_kernel(const uint4* __restric
 }
 
 // ---------------------------------------------------------------------------
-// v = bf16(scale A x): windows of tokens, items of up to 32 tokens of one
+// v = scale A x, in fp32 of two bf16 values: windows of tokens, items of up to 32 tokens of one
 // adapter (with MXFP8 rows also of none: those are only converted). gridDim.y
 // CTAs take a window's items in turn; the gridDim.z CTAs of a cluster split K
 // and add their parts in rank order through shared memory.
@@ -147,7 +182,7 @@ constexpr int kDownSum = 64;      // ranks whose parts a cluster adds at once
 template <int NT, bool X8>
 __global__ void __launch_bounds__(256, NT <= 2 ? 2 : 1)
     adapter_down_kernel(const LinearArgs a, uint16_t* __restrict__ xb /* null: not converted */,
-                        uint16_t* __restrict__ v) {
+                        float* __restrict__ v) {
   __shared__ int s_cid[kDownWin / 32][32], s_cn[kDownWin / 32][32], s_nc[kDownWin / 32];
   __shared__ int s_base[kDownWin], s_warp[kDownWin / 32], s_items;
   __shared__ int s_tok[kDownWin][kDownTok];   // [item][slot]: token of the window, -1 empty
@@ -320,7 +355,7 @@ __global__ void __launch_bounds__(256, NT <= 2 ? 2 : 1)
           if (parts > 1)
             s_sum[16 * m + row][f % kDownSum + r] = z;
           else if (t >= 0)
-            v[(size_t)(w0 + t) * a.rank + f + r] = f32_to_bf16_rne(z * scale);
+            v[(size_t)(w0 + t) * a.rank + f + r] = two_bf16(z * scale);
         }
         __syncthreads();
       }
@@ -347,8 +382,9 @@ __global__ void __launch_bounds__(256, NT <= 2 ? 2 : 1)
               y.z += z[c].z;
               y.w += z[c].w;
             }
-          *reinterpret_cast<uint2*>(v + (size_t)(w0 + t) * a.rank + f0 + r) =
-              make_uint2(bf16x2_rn(y.x * scale, y.y * scale), bf16x2_rn(y.z * scale, y.w * scale));
+          *reinterpret_cast<float4*>(v + (size_t)(w0 + t) * a.rank + f0 + r) =
+              make_float4(two_bf16(y.x * scale), two_bf16(y.y * scale), two_bf16(y.z * scale),
+                          two_bf16(y.w * scale));
         }
         cluster_sync();   // s_sum is read by the whole cluster until here
       }
@@ -382,7 +418,7 @@ struct LinearParams {
   CUtensorMap tmapX;   // x as bytes {128, T, K / 64}, box {128, cs / 2, 2}, 128-byte swizzle
   CUtensorMap tmapW;   // packed weights u8 [N][K/2], box {64, 128}, 64-byte swizzle
   LinearArgs a;
-  const uint16_t* v;   // bf16 [T][rank]: scale_a A_a x_t, from the kernel before
+  const float* v;      // [T][rank]: scale_a A_a x_t, from the kernel before
   int cs;              // tokens per tile (multiple of 16, at most 256)
   int S, SP, SL;       // ring depths: operand stages, packed weights, adapter columns
   int split;           // pairs of a cluster that share a tile's K
@@ -425,11 +461,11 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int hb = p.cs / 2;                           // tokens of the tile in this CTA
   const int xchunk = hb * 128, xstage = 2 * xchunk;
-  const int lstage = kBTile + xchunk;
+  const int lstage = kBTile + xstage;
   uint8_t* sX = smem;                                // [S][2 chunks][hb][128 bytes]
   uint8_t* sP = sX + p.S * xstage;                   // [SP][128 rows][64 bytes]
-  uint8_t* sL = sP + p.SP * kPStage;                 // [SL] of {kBTile, hb x 128 bytes}; then the
-                                                     // output tile [cs][kOutPitch]
+  uint8_t* sL = sP + p.SP * kPStage;                 // [SL] of {kBTile, 2 x hb x 128 bytes: v's hi and lo};
+                                                     // then the output tile [cs][kOutPitch]
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t crank = cluster_rank();
@@ -564,9 +600,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
             if (elect_one()) {
               const uint64_t da = umma_desc_sw128(smem_u32(sL + ls * lstage));
               const uint64_t db = umma_desc_sw128(smem_u32(sL + ls * lstage + kBTile));
+              const uint64_t dl = db + (uint64_t)(xchunk >> 4);   // v's lo
               const int k16n = min(kBK, lcols - i * kBK) / 16;
-              for (int k16 = 0; k16 < k16n; ++k16)
-                umma2_bf16_ss(tmem, da + 2 * k16, db + 2 * k16, idesc, true);   // nS > 0 came before
+              for (int k16 = 0; k16 < k16n; ++k16) {   // nS > 0 came before
+                umma2_bf16_ss(tmem, da + 2 * k16, db + 2 * k16, idesc, true);
+                umma2_bf16_ss(tmem, da + 2 * k16, dl + 2 * k16, idesc, true);
+              }
               umma2_commit(&l_empty[ls], pair);
             }
             __syncwarp();
@@ -700,7 +739,6 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
         const int count = s_count, lcols = count * p.rp;
         // stages of 64 columns, taken in turn by the pairs of the cluster
         for (int i = part; i * kBK < lcols; i += p.split, ++use) {
-          if (use >= p.SL && !warp_wait_cluster(&l_empty[ls], lph ^ 1u)) { fail = 1; break; }
           uint8_t* tb = sL + ls * lstage;
           uint8_t* tv = tb + kBTile;
           // 16-byte chunk j of a row: columns 64 i + 8 j .., one adapter's ranks r ..
@@ -718,6 +756,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
             if (live && n0 + row < N)
               b[u] = *reinterpret_cast<const uint4*>(p.a.b + ((size_t)ad * N + n0 + row) * p.a.rank + r);
           }
+          // (their way from memory is beside the MMAs that free the slot)
+          if (use >= p.SL && !warp_wait_cluster(&l_empty[ls], lph ^ 1u)) { fail = 1; break; }
 #pragma unroll
           for (int u = 0; u < kPer; ++u) {
             const int row = (et >> 3) + kEpiThreads / 8 * u;
@@ -740,11 +780,18 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
             waited = true;
           }
           for (int t = et >> 3; t < hb; t += kEpiThreads / 8) {
-            uint4 u = make_uint4(0u, 0u, 0u, 0u);
-            if (live && s_tokad[half * hb + t] == ad)
-              u = ldcg16(p.v + (size_t)(t0 + half * hb + t) * p.a.rank + r);   // (no read-only path:
-                               // v may still be written when this kernel starts)
-            *reinterpret_cast<uint4*>(tv + t * 128 + ((j ^ (t & 7)) << 4)) = u;
+            uint4 hi = make_uint4(0u, 0u, 0u, 0u), lo = hi;
+            if (live && s_tokad[half * hb + t] == ad) {
+              const float* src = p.v + (size_t)(t0 + half * hb + t) * p.a.rank + r;
+              const float4 x = ldcg_f4(src), y = ldcg_f4(src + 4);
+              split_bf16x2(x.x, x.y, hi.x, lo.x);
+              split_bf16x2(x.z, x.w, hi.y, lo.y);
+              split_bf16x2(y.x, y.y, hi.z, lo.z);
+              split_bf16x2(y.z, y.w, hi.w, lo.w);
+            }
+            uint8_t* dst = tv + t * 128 + ((j ^ (t & 7)) << 4);
+            *reinterpret_cast<uint4*>(dst) = hi;
+            *reinterpret_cast<uint4*>(dst + xchunk) = lo;
           }
           fence_proxy_async_smem();
           __syncwarp();
@@ -780,10 +827,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
             float z = 0.f;
             for (int r = 0; r < p.a.rank; ++r) {
               const uint32_t bw = p.a.b[((size_t)ad * N + row) * p.a.rank + r];
-              if ((bw & 0x7F80u) == 0x7F80u) {
-                const uint32_t vw = p.v[(size_t)(t0 + c0 + t) * p.a.rank + r];
-                z += __uint_as_float(bw << 16) * __uint_as_float(vw << 16);
-              }
+              if ((bw & 0x7F80u) == 0x7F80u)
+                z += __uint_as_float(bw << 16) * p.v[(size_t)(t0 + c0 + t) * p.a.rank + r];
             }
 #pragma unroll
             for (int e = 0; e < 32; ++e)
@@ -893,7 +938,7 @@ struct FewStep {
 // CTAs to an SM) where they do.
 template <int TT, bool X8, int WARPS>
 __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
-    linear_few_kernel(const LinearArgs a, const uint16_t* __restrict__ v) {
+    linear_few_kernel(const LinearArgs a, const float* __restrict__ v) {
   __shared__ float part[WARPS][kFewRows][8 * TT + 1];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, q = lane & 3;
@@ -995,15 +1040,18 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
     const int ad = a.ids != nullptr ? a.ids[t] : -1;
     if (ad >= 0 && ad < a.L) {
       const uint16_t* br = a.b + ((size_t)ad * a.N + n) * a.rank;
-      const uint16_t* vr = v + (size_t)t * a.rank;
+      const float* vr = v + (size_t)t * a.rank;
       float z = 0.f;
+#pragma unroll 2
       for (int r = 0; r < a.rank; r += 8) {
-        const uint4 bb = ldg16(br + r), vv = ldcg16(vr + r);   // (v: no read-only path)
-        const uint32_t bw[4] = {bb.x, bb.y, bb.z, bb.w}, vw[4] = {vv.x, vv.y, vv.z, vv.w};
+        const uint4 bb = ldg16(br + r);
+        const float4 v0 = ldcg_f4(vr + r), v1 = ldcg_f4(vr + r + 4);
+        const uint32_t bw[4] = {bb.x, bb.y, bb.z, bb.w};
+        const float vw[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          z = fmaf(__uint_as_float(bw[j] << 16), __uint_as_float(vw[j] << 16), z);
-          z = fmaf(__uint_as_float(bw[j] & 0xFFFF0000u), __uint_as_float(vw[j] & 0xFFFF0000u), z);
+          z = fmaf(__uint_as_float(bw[j] << 16), vw[2 * j], z);
+          z = fmaf(__uint_as_float(bw[j] & 0xFFFF0000u), vw[2 * j + 1], z);
         }
       }
       y += z;
@@ -1018,7 +1066,7 @@ size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 
 size_t linear_workspace_bytes(int T, int K, int N, int rank, bool x8) {
   (void)N;
-  return up256((size_t)T * rank * 2) + (x8 && T > kFewTok ? up256((size_t)T * K * 2) : 0);
+  return up256((size_t)T * rank * sizeof(float)) + (x8 && T > kFewTok ? up256((size_t)T * K * 2) : 0);
 }
 
 // Grid of the adapters' first product: CTAs over windows, slots for their items
@@ -1090,7 +1138,7 @@ static DownPlan down_beside(const LinearArgs& a, const DownWork& w, double clock
 }
 
 template <int NT, bool X8>
-static cudaError_t launch_down(const LinearArgs& a, uint16_t* xb, uint16_t* v, const DownPlan& plan,
+static cudaError_t launch_down(const LinearArgs& a, uint16_t* xb, float* v, const DownPlan& plan,
                                cudaStream_t stream) {
   const int win = (a.T + kDownWin - 1) / kDownWin;
   const int parts = plan.parts, slots = plan.slots;
@@ -1195,7 +1243,7 @@ static DownPlan linear_plan(const LinearArgs& a, bool pair_order, const DownWork
 }
 
 template <int TT, bool X8>
-static cudaError_t launch_few(const LinearArgs& a, const uint16_t* v, bool wide, cudaStream_t stream) {
+static cudaError_t launch_few(const LinearArgs& a, const float* v, bool wide, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((a.N + kFewRows - 1) / kFewRows);
   cfg.blockDim = dim3((wide ? 8 : 16) * 32);
@@ -1213,8 +1261,8 @@ cudaError_t launch_linear(const LinearArgs& a, int num_sms, cudaStream_t stream)
   cudaError_t e;
   char* ws = static_cast<char*>(a.ws);
   const bool adapters = a.ids != nullptr;
-  uint16_t* v = reinterpret_cast<uint16_t*>(ws);
-  uint16_t* xb = reinterpret_cast<uint16_t*>(ws + up256((size_t)a.T * a.rank * 2));
+  float* v = reinterpret_cast<float*>(ws);
+  uint16_t* xb = reinterpret_cast<uint16_t*>(ws + up256((size_t)a.T * a.rank * sizeof(float)));
   const bool x8 = a.xs != nullptr, few = a.T <= kFewTok;
   if (few) xb = nullptr;
   if (a.status != nullptr &&
@@ -1271,7 +1319,6 @@ cudaError_t launch_linear(const LinearArgs& a, int num_sms, cudaStream_t stream)
   p.v = v;
   const int xstage = p.cs / 2 * 256;
   p.S = (kTmemCols - ((p.cs + 31) & ~31)) / kWCols;   // 4 at 256 tokens, 7 at 16
-  p.SL = !adapters ? 0 : p.cs > 64 ? 2 : kMaxL;
   p.rp = (a.rank + 15) & ~15;
   const uint64_t dims[3] = {128, (uint64_t)a.T, (uint64_t)a.K / kBK};
   const uint64_t strides[2] = {(uint64_t)a.K * 2, 128};
@@ -1281,11 +1328,19 @@ cudaError_t launch_linear(const LinearArgs& a, int num_sms, cudaStream_t stream)
                        (uint64_t)a.K / 2, kStageK / 2, kBM, CU_TENSOR_MAP_SWIZZLE_64B))
     return cudaErrorInvalidValue;
   p.tiles = (a.N + 2 * kBM - 1) / (2 * kBM) * ((a.T + p.cs - 1) / p.cs);
-  const size_t lbytes = (size_t)p.SL * (kBTile + xstage / 2), obytes = (size_t)p.cs * kOutPitch;
-  // packed weights take what is left, 3 stages (256 tokens) to 8: with 3 at 144
-  // tokens the dequantisation waited on them, 850 instead of 620 clocks a stage
-  const size_t fixed = 1024 + (size_t)p.S * xstage + (p.split == 1 && obytes > lbytes ? obytes : lbytes);
-  p.SP = (int)((kDynSmem - fixed) / kPStage);
+  // The adapter columns take the stages (4 up to 80 tokens, 1 at 256) that leave a
+  // packed-weight ring as deep as the operands', or two with the shortest such ring:
+  // with one, several adapters of a tile followed one another (K = 2880, N = 5760,
+  // rank 16, 48 adapters, MXFP8: T = 1024 46.3 us, here 42.4). Packed weights take what
+  // is left, 3 stages to 8.
+  const size_t obytes = p.split == 1 ? (size_t)p.cs * kOutPitch : 0;
+  size_t fixed = 0;
+  for (p.SL = adapters ? kMaxL : 0;; --p.SL) {
+    const size_t lbytes = (size_t)p.SL * (kBTile + xstage);
+    fixed = 1024 + (size_t)p.S * xstage + (obytes > lbytes ? obytes : lbytes);
+    p.SP = fixed < kDynSmem ? (int)((kDynSmem - fixed) / kPStage) : 0;
+    if (p.SP >= p.S || p.SL <= 1 || (p.SL == 2 && p.SP >= kDeqGroups)) break;
+  }
   if (p.SP > kMaxSP) p.SP = kMaxSP;
   if (p.SP < p.S) p.SP = kDeqGroups;   // (see the dequantising warps' waits)
   if (p.S < kDeqGroups || fixed + (size_t)p.SP * kPStage > kDynSmem) return cudaErrorInvalidConfiguration;

@@ -1,0 +1,67 @@
+"""The operators around the layer where one wrong choice shows: sums that cancel,
+memory and streams, lengths and limits at their ends."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import operators_oracle as P
+from test_operators_gpu import bits, call_linear, f64, gen, make_linear
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def moe():
+    import __graft_entry__
+    __graft_entry__.build()
+    from mxfp4_mixture_experts_gb300 import moe
+    return moe
+
+
+# ------------------------------------------------------------------ the adapters' inner products
+def bf16_values(t):
+    return t.double().numpy()
+
+
+@pytest.mark.parametrize("x8", [False, True])
+@pytest.mark.parametrize("K,rank", [(64, 8), (192, 24), (128, 256), (1024, 40)])
+@pytest.mark.parametrize("T", [1, 16, 17, 40, 130, 300])
+def test_linear_adapter_whose_ranks_cancel(moe, T, K, rank, x8):
+    """Zero weights, and adapters whose ranks come in pairs of almost equal inner products v with
+    opposite signs in B: y is a small difference of large products. The tolerance has the output's
+    rounding (2^-8 |y|), v's two bf16 values (2^-17 of the products' magnitudes) and the fp32 roundings
+    of both sums (2^-23 of their magnitudes each: K / 16 steps, the adding of 8 warps and 8 parts and the
+    factor for v, rank / 8 steps for y); one bf16 rounding of v (2^-9 of the products) is far outside."""
+    d = make_linear(T, K, 136, rank, 3, x8, 1000 + T + K)
+    g = gen(T)
+    d["w"].zero_()
+    a, b = d["adapter_a"], d["adapter_b"]
+    a[:, 1::2] = (a[:, 0::2].float() * (1 + 2.0 ** -6 * torch.randn(3, rank // 2, K, generator=g))).bfloat16()
+    b[:, :, 1::2] = -b[:, :, 0::2]
+    d["adapter_ids"] = torch.randint(0, 3, (T,), generator=g, dtype=torch.int32)
+    y = f64(call_linear(moe, d))
+    n = (K / 16 + rank / 8 + 17) * 2.0 ** -23
+    for t in range(T):
+        j = int(d["adapter_ids"][t])
+        A, B = bf16_values(a[j]), bf16_values(b[j])
+        s, x = float(d["adapter_scale"][j]), d["x64"][t]
+        v = A @ x * s
+        ref = B @ v
+        tol = 2.0 ** -8 * np.abs(ref) + 2.0 ** -17 * (np.abs(B) @ np.abs(v)) \
+            + n * (np.abs(B) @ (np.abs(A) @ np.abs(x) * s)) + 1e-37
+        bad = np.abs(y[t] - ref) > tol
+        assert not bad.any(), (t, y[t][bad][:4], ref[bad][:4], tol[bad][:4])
+
+
+@pytest.mark.parametrize("T", [2, 20, 300])
+def test_linear_inner_product_beyond_bf16(moe, T):
+    """An inner product between the largest bf16 and the largest fp32 value is finite, and so is y."""
+    d = make_linear(T, 64, 16, 8, 1, False, 5, 0)
+    d["w"].zero_()
+    d["x"].fill_(1.0)
+    d["adapter_a"].zero_()
+    d["adapter_a"][0, 0, 0] = 1.0
+    d["adapter_b"].fill_(0.5)
+    d["adapter_scale"].fill_(3.4e38)
+    y = f64(call_linear(moe, d))
+    assert np.all(np.abs(y - 1.7e38) <= 1.7e38 * 2.0 ** -8)
