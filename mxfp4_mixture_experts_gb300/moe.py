@@ -130,11 +130,14 @@ def _raw_stream(stream) -> int:
 
 
 def _empty(shape, dtype, device, stream) -> torch.Tensor:
-    """An uninitialised tensor for a call on ``stream``: its memory is not handed out again before
-    that stream has passed the call, also when the tensor is dropped on the current stream first."""
-    t = torch.empty(shape, dtype=dtype, device=device)
-    if stream is not None:
-        t.record_stream(stream)
+    """An uninitialised tensor for a call on ``stream``, from that stream's own memory: what other
+    streams have freed may still be in use by their queued work. Nor is its memory handed out again
+    before the current stream, where the caller may use it, has passed the point that drops it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream())
     return t
 
 

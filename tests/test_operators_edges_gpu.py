@@ -65,3 +65,78 @@ def test_linear_inner_product_beyond_bf16(moe, T):
     d["adapter_scale"].fill_(3.4e38)
     y = f64(call_linear(moe, d))
     assert np.all(np.abs(y - 1.7e38) <= 1.7e38 * 2.0 ** -8)
+
+
+# ------------------------------------------------------------------ memory of calls on another stream
+def late_writer(shapes, dtype=torch.uint8):
+    """Blocks of these sizes that the current stream will still write to, 20 ms from now, although they are
+    free for its next allocations."""
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    tmp = [torch.empty(n, dtype=dtype, device="cuda") for n in shapes]
+    torch.cuda._sleep(40_000_000)
+    for t in tmp:
+        t.fill_(0xFF)
+
+
+def stream_calls(moe):
+    """name -> (call with a stream, bytes of its outputs and scratch); all larger than the allocator's pool of
+    small blocks, inputs long ready."""
+    g = gen(77)
+    x = torch.randn(1024, 2048, generator=g).bfloat16().cuda()
+    gamma = torch.ones(2048).bfloat16().cuda()
+    logits = torch.randn(70_000, 64, generator=g).cuda()
+    d = {k: v.cuda() for k, v in make_linear(1200, 1024, 2048, 16, 3, True, 78).items() if k != "x64"}
+    lin = lambda st: moe.linear(d["x"], d["w"], d["s"], d["x_scale"], d["adapter_ids"], d["adapter_a"],
+                                d["adapter_b"], d["adapter_scale"], stream=st)
+    return {
+        "add_rmsnorm": (lambda st: moe.add_rmsnorm(x, gamma, x, out8="ocp", stream=st)[:3],
+                        [1024 * 2048 * 2] * 2 + [1024 * 2048]),
+        "router_scored": (lambda st: moe.router_scored(logits, 8, stream=st), [70_000 * 8 * 4] * 2),
+        "linear": (lin, [1200 * 2048 * 2, moe.linear_workspace_size(1200, 1024, 2048, 16, True)]),
+    }
+
+
+@pytest.mark.parametrize("op", ["add_rmsnorm", "router_scored", "linear"])
+def test_call_on_another_stream_does_not_share_memory_with_queued_work(moe, op):
+    call, sizes = stream_calls(moe)[op]
+    as_bytes = lambda r: [t.view(torch.uint8).clone() for t in (r if isinstance(r, tuple) else (r,))]
+    want = as_bytes(call(None))
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    late_writer(sizes)
+    got = call(side)
+    side.synchronize()
+    torch.cuda.synchronize()
+    for a, b in zip(want, as_bytes(got)):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("op", ["add_rmsnorm", "router_scored", "linear"])
+def test_call_on_another_stream_allocates_there(moe, monkeypatch, op):
+    call, sizes = stream_calls(moe)[op]
+    side = torch.cuda.Stream()
+    seen = []
+    empty = torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, **k: (seen.append(torch.cuda.current_stream()), empty(*a, **k))[1])
+    call(side)
+    assert len(seen) >= len(sizes) and all(s == side for s in seen)
+    torch.cuda.synchronize()
+
+
+def test_outputs_of_another_stream_outlive_their_reader(moe):
+    """An output that the current stream still reads when it is dropped is not handed to the side stream's next call."""
+    g = gen(79)
+    x, y = (torch.randn(1024, 2048, generator=g).bfloat16().cuda() for _ in range(2))
+    gamma = torch.ones(2048).bfloat16().cuda()
+    want = moe.add_rmsnorm(x, gamma)[0].clone()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    a = moe.add_rmsnorm(x, gamma, stream=side)[0]
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda._sleep(40_000_000)
+    copy = a.clone()
+    del a
+    moe.add_rmsnorm(y, gamma, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(copy, want)
