@@ -141,6 +141,15 @@ def _empty(shape, dtype, device, stream) -> torch.Tensor:
     return t
 
 
+def _zeros(shape, dtype, device, stream) -> torch.Tensor:
+    """``_empty``, zeroed on ``stream``."""
+    if stream is None:
+        return torch.zeros(shape, dtype=dtype, device=device)
+    t = _empty(shape, dtype, device, stream)
+    with torch.cuda.stream(stream):
+        return t.zero_()
+
+
 def _need(t: torch.Tensor, name: str, dtype, ndim: int):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -164,12 +173,14 @@ def workspace_zero_bytes() -> int:
     return int(lib().mxfp4_moe_workspace_zero_bytes())
 
 
-def new_workspace(T: int, K: int, I: int, E: int, topk: int, device="cuda") -> torch.Tensor:
-    """A zero-filled workspace (the library requires zeros before first use)."""
+def new_workspace(T: int, K: int, I: int, E: int, topk: int, device="cuda",
+                  stream=None) -> torch.Tensor:
+    """A zero-filled workspace (the library requires zeros before first use), zeroed on ``stream``
+    (the current one by default)."""
     n = workspace_size(T, K, I, E, topk)
     if n == 0:
         raise ValueError("unsupported sizes")
-    return torch.zeros(n, dtype=torch.uint8, device=device)
+    return _zeros(n, torch.uint8, device, stream)
 
 
 def route(topk_ids: torch.Tensor, E: int, stream=None, many_ctas: bool = False):
@@ -180,13 +191,13 @@ def route(topk_ids: torch.Tensor, E: int, stream=None, many_ctas: bool = False):
     _need(topk_ids, "topk_ids", torch.int32, 2)
     T, k = topk_ids.shape
     dev = topk_ids.device
-    count = torch.empty(E, dtype=torch.int32, device=dev)
-    offset = torch.empty(E + 1, dtype=torch.int32, device=dev)
-    lst = torch.empty(max(T * k, 1), dtype=torch.int32, device=dev)
-    status = torch.zeros(4, dtype=torch.int32, device=dev)
+    count = _empty(E, torch.int32, dev, stream)
+    offset = _empty(E + 1, torch.int32, dev, stream)
+    lst = _empty(max(T * k, 1), torch.int32, dev, stream)
+    status = _zeros(4, torch.int32, dev, stream)
     if many_ctas:
         n = int(lib().mxfp4_moe_route_workspace_size(T, k, E))
-        ws = torch.empty(max(n, 16), dtype=torch.uint8, device=dev)
+        ws = _empty(max(n, 16), torch.uint8, dev, stream)
         rc = lib().mxfp4_moe_route_ws(_ptr(topk_ids), T, k, E, _ptr(count), _ptr(offset),
                                       _ptr(lst), _ptr(status), _ptr(ws), n, _stream(stream))
         if rc:
@@ -220,11 +231,11 @@ def forward(hidden: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torch.Te
     if tuple(w2.shape) != (E, K, I // 2) or tuple(s2.shape) != (E, K, I // 32):
         raise ValueError("w2 / s2 shapes must be [E, K, I/2] / [E, K, I/32]")
     if out is None:
-        out = torch.empty(T, K, dtype=torch.bfloat16, device=hidden.device)
+        out = _empty((T, K), torch.bfloat16, hidden.device, stream)
     else:
         _need(out, "out", torch.bfloat16, 2)
     if workspace is None:
-        workspace = new_workspace(T, K, I, E, k, hidden.device)
+        workspace = new_workspace(T, K, I, E, k, hidden.device, stream)
     rc = lib().mxfp4_moe_forward(
         _ptr(hidden), _ptr(topk_ids), _ptr(topk_weights), _ptr(w13), _ptr(s13), _ptr(w2),
         _ptr(s2), T, K, I, E, k, _ptr(out), _ptr(status), _ptr(workspace),
@@ -257,13 +268,13 @@ def forward_window(hidden: torch.Tensor, topk_ids: torch.Tensor,
     k = topk_ids.shape[1]
     rows = T * k if per_route else T
     if out is None:
-        out = torch.empty(rows, K, dtype=torch.bfloat16, device=hidden.device)
+        out = _empty((rows, K), torch.bfloat16, hidden.device, stream)
     else:
         _need(out, "out", torch.bfloat16, 2)
         if tuple(out.shape) != (rows, K):
             raise ValueError(f"out must be [{rows}, {K}]")
     if workspace is None:
-        workspace = new_workspace(T, K, I, E, k, hidden.device)
+        workspace = new_workspace(T, K, I, E, k, hidden.device, stream)
     rc = lib().mxfp4_moe_forward_window(
         _ptr(hidden), _ptr(topk_ids), _ptr(topk_weights), _ptr(w13), _ptr(s13), _ptr(w2),
         _ptr(s2), T, K, I, E, k, int(expert_base), int(bool(per_route)), _ptr(out), _ptr(status),
@@ -301,11 +312,11 @@ def forward_oai(hidden: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torc
     if tuple(b13.shape) != (E, 2 * I) or tuple(b2.shape) != (E, K):
         raise ValueError("b13 / b2 shapes must be [E, 2I] / [E, K]")
     if out is None:
-        out = torch.empty(T, K, dtype=torch.bfloat16, device=hidden.device)
+        out = _empty((T, K), torch.bfloat16, hidden.device, stream)
     else:
         _need(out, "out", torch.bfloat16, 2)
     if workspace is None:
-        workspace = new_workspace(T, K, I, E, k, hidden.device)
+        workspace = new_workspace(T, K, I, E, k, hidden.device, stream)
     rc = lib().mxfp4_moe_forward_oai(
         _ptr(hidden), _ptr(topk_ids), _ptr(topk_weights), _ptr(w13), _ptr(s13), _ptr(b13),
         _ptr(w2), _ptr(s2), _ptr(b2), T, K, I, E, k, _ptr(out), _ptr(status), _ptr(workspace),
@@ -318,7 +329,7 @@ def forward_oai(hidden: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torc
 SCORING = {"softmax_topk": 0, "sigmoid_renorm": 1}
 
 
-def _router_args(logits, topk, scoring, bias, topk_ids, topk_weights):
+def _router_args(logits, topk, scoring, bias, topk_ids, topk_weights, stream):
     _need(logits, "logits", torch.float32, 2)
     T, E = logits.shape
     if bias is not None:
@@ -328,9 +339,9 @@ def _router_args(logits, topk, scoring, bias, topk_ids, topk_weights):
     if scoring not in SCORING:
         raise ValueError(f"scoring must be one of {sorted(SCORING)}")
     if topk_ids is None:
-        topk_ids = torch.empty(T, topk, dtype=torch.int32, device=logits.device)
+        topk_ids = _empty((T, topk), torch.int32, logits.device, stream)
     if topk_weights is None:
-        topk_weights = torch.empty(T, topk, dtype=torch.float32, device=logits.device)
+        topk_weights = _empty((T, topk), torch.float32, logits.device, stream)
     return T, E, topk_ids, topk_weights
 
 
@@ -341,7 +352,7 @@ def router(logits: torch.Tensor, topk: int, scoring: str = "softmax_topk",
     int32 [T, k] ids (descending x = logit + bias, ties to the lower index)
     and fp32 [T, k] weights (softmax over the chosen, or renormalised sigmoid)."""
     T, E, topk_ids, topk_weights = _router_args(logits, topk, scoring, bias, topk_ids,
-                                                topk_weights)
+                                                topk_weights, stream)
     rc = lib().mxfp4_moe_router(_ptr(logits), _ptr(bias), T, E, topk, SCORING[scoring],
                                 _ptr(topk_ids), _ptr(topk_weights), _stream(stream))
     if rc:
@@ -358,7 +369,7 @@ def router_grouped(logits: torch.Tensor, topk: int, scoring: str = "sigmoid_reno
     eligible) and, with bias_in_weights=False, a bias that steers the choice
     only (weights from the unbiased logits)."""
     T, E, topk_ids, topk_weights = _router_args(logits, topk, scoring, bias, topk_ids,
-                                                topk_weights)
+                                                topk_weights, stream)
     rc = lib().mxfp4_moe_router_grouped(_ptr(logits), _ptr(bias), T, E, topk, SCORING[scoring],
                                         n_group, topk_group, int(bool(bias_in_weights)),
                                         _ptr(topk_ids), _ptr(topk_weights), _stream(stream))
@@ -378,8 +389,8 @@ def encode(x: torch.Tensor, rule: str = "ocp", stream=None):
     if rule not in RULES:
         raise ValueError(f"rule must be one of {sorted(RULES)}")
     rows, cols = x.shape
-    packed = torch.empty(rows, cols // 2, dtype=torch.uint8, device=x.device)
-    scale = torch.empty(rows, cols // 32, dtype=torch.uint8, device=x.device)
+    packed = _empty((rows, cols // 2), torch.uint8, x.device, stream)
+    scale = _empty((rows, cols // 32), torch.uint8, x.device, stream)
     rc = lib().mxfp4_moe_encode(_ptr(x), rows, cols, RULES[rule], _ptr(packed), _ptr(scale),
                                 _stream(stream))
     if rc:
@@ -403,7 +414,7 @@ def dequant(packed: torch.Tensor, scale: torch.Tensor, form: str = "decode",
     C = 2 * half
     if tuple(scale.shape) != (N, C // 32):
         raise ValueError("scale must be [rows, cols/32]")
-    out = torch.empty(N, C, dtype=torch.bfloat16, device=packed.device)
+    out = _empty((N, C), torch.bfloat16, packed.device, stream)
     rc = lib().mxfp4_moe_dequant_form(_ptr(packed), _ptr(scale), N, C, DEQUANT_FORMS[form],
                                       _ptr(out), _stream(stream))
     if rc:

@@ -140,3 +140,50 @@ def test_outputs_of_another_stream_outlive_their_reader(moe):
     moe.add_rmsnorm(y, gamma, stream=side)
     torch.cuda.synchronize()
     assert torch.equal(copy, want)
+
+
+def layer_calls(moe):
+    """The layer's own calls with a stream, by name, outputs as a tuple."""
+    g = gen(80)
+    u8 = lambda lo, hi, *s: torch.randint(lo, hi, s, generator=g, dtype=torch.uint8).cuda()
+    T, K, I, E = 300, 256, 128, 8
+    h = torch.randn(T, K, generator=g).bfloat16().cuda()
+    logits = torch.randn(T, E, generator=g).cuda()
+    ids, w = moe.router(logits, 2)
+    w13, s13, w2, s2 = u8(0, 256, E, 2 * I, K // 2), u8(118, 124, E, 2 * I, K // 32), \
+        u8(0, 256, E, K, I // 2), u8(118, 124, E, K, I // 32)
+    b13, b2 = torch.zeros(E, 2 * I).cuda(), torch.zeros(E, K).cuda()
+    lay = dict(
+        route=lambda st: moe.route(ids, E, stream=st),
+        route_many=lambda st: moe.route(ids, E, stream=st, many_ctas=True),
+        router=lambda st: moe.router(logits, 2, stream=st),
+        router_grouped=lambda st: moe.router_grouped(logits, 2, n_group=2, topk_group=1, stream=st),
+        encode=lambda st: moe.encode(h, stream=st),
+        dequant=lambda st: (moe.dequant(w2[0], s2[0], stream=st),),
+        forward=lambda st: (moe.forward(h, ids, w, w13, s13, w2, s2, stream=st),),
+        forward_decode=lambda st: (moe.forward(h[:8], ids[:8], w[:8], w13, s13, w2, s2, stream=st),),
+        forward_window=lambda st: (moe.forward_window(h, ids, w, w13, s13, w2, s2, stream=st),),
+        forward_oai=lambda st: (moe.forward_oai(h, ids, w, w13, s13, b13, w2, s2, b2, stream=st),),
+    )
+    return lay
+
+
+@pytest.mark.parametrize("op", ["route", "route_many", "router", "router_grouped", "encode", "dequant", "forward",
+                                "forward_decode", "forward_window", "forward_oai"])
+def test_layer_call_on_another_stream_allocates_and_zeroes_there(moe, monkeypatch, op):
+    call = layer_calls(moe)[op]
+    want = [t.clone() for t in call(None)]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    seen = []
+    empty, zeros = torch.empty, torch.zeros
+    spy = lambda f: lambda *a, **k: (seen.append(torch.cuda.current_stream()), f(*a, **k))[1]
+    monkeypatch.setattr(torch, "empty", spy(empty))
+    monkeypatch.setattr(torch, "zeros", spy(zeros))
+    torch.cuda._sleep(40_000_000)     # the current stream is busy, the call's is not
+    got = call(side)
+    side.synchronize()
+    assert seen and all(s == side for s in seen)
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
