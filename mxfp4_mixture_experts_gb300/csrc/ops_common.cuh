@@ -121,11 +121,13 @@ __device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
   return a;
 }
-// The arrival of a thread whose results are in tensor memory already (after
-// tcgen05.wait::st): no release at cluster scope, which would also wait for the
-// thread's prefetches from global memory (1000 to 10000 clocks a stage).
+// The arrival of a thread whose results are in tensor memory (after tcgen05.wait and
+// the fence before a thread synchronisation; the waiter, which acquires at cluster scope,
+// has the fence after one). Relaxed: those two fences order tensor memory, and a release at
+// cluster scope would also wait for the thread's prefetches from global memory (1000 to
+// 10000 clocks a stage).
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
