@@ -59,6 +59,7 @@
 // steps of a tile: start 3 us, first operands 2 us, the cluster's addition 2 us.
 #include <cuda.h>
 #include <cstdint>
+#include <mutex>
 
 #include "kernels.h"
 #include "ops.h"
@@ -1157,16 +1158,24 @@ static cudaError_t launch_down(const LinearArgs& a, uint16_t* xb, float* v, cons
 
 // Clusters of 2 * split CTAs that are resident at once (a cluster stays inside a
 // group of SMs, and those groups are not multiples of every size): asked of the
-// driver once per device.
+// driver once per device, under a lock: a first call from another thread must not
+// see some of them, which would choose it other tiles.
 static cudaError_t resident_clusters(int dev, int (&out)[kMaxSplit + 1]) {
-  static int known[kGrantDevices][kMaxSplit + 1] = {};
-  if (known[dev][1] == 0) {
+  struct Known {
+    bool set;
+    int n[kMaxSplit + 1];
+  };
+  static Known known[kGrantDevices] = {};
+  static std::mutex mu;
+  std::lock_guard<std::mutex> lk(mu);
+  Known& d = known[dev];
+  if (!d.set) {
     for (auto* k : {linear_kernel<false>, linear_kernel<true>}) {
       const cudaError_t e =
           cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kDynSmem);
       if (e != cudaSuccess) return e;
     }
-    for (int sp = kMaxSplit; sp >= 1; --sp) {
+    for (int sp = 1; sp <= kMaxSplit; ++sp) {
       cudaLaunchConfig_t cfg = {};
       cfg.gridDim = dim3(2 * sp * 64);
       cfg.blockDim = dim3(kThreads);
@@ -1177,14 +1186,13 @@ static cudaError_t resident_clusters(int dev, int (&out)[kMaxSplit + 1]) {
       at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
       cfg.attrs = at;
       cfg.numAttrs = 1;
-      int n = 0;
-      const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, linear_kernel<false>, &cfg);
+      const cudaError_t e = cudaOccupancyMaxActiveClusters(&d.n[sp], linear_kernel<false>, &cfg);
       if (e != cudaSuccess) return e;
-      if (n < 1 && sp == 1) return cudaErrorInvalidConfiguration;
-      known[dev][sp] = n;
     }
+    if (d.n[1] < 1) return cudaErrorInvalidConfiguration;
+    d.set = true;
   }
-  for (int sp = 1; sp <= kMaxSplit; ++sp) out[sp] = known[dev][sp];
+  for (int sp = 1; sp <= kMaxSplit; ++sp) out[sp] = d.n[sp];
   return cudaSuccess;
 }
 

@@ -187,3 +187,46 @@ def test_layer_call_on_another_stream_allocates_and_zeroes_there(moe, monkeypatc
     torch.cuda.synchronize()
     for a, b in zip(want, got):
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+# ------------------------------------------------------------------ threads
+FIRST_CALLS = """
+import sys, threading
+sys.path[:0] = [{root!r}, {root!r} + "/tests"]
+import torch
+from mxfp4_mixture_experts_gb300 import moe
+from test_operators_gpu import make_linear
+d = {{k: v.cuda() for k, v in make_linear(32, 6144, 4096, 16, 5, False, 3).items() if k != "x64"}}
+torch.cuda.synchronize()
+moe.lib()
+n = 12
+start, out, errors = threading.Barrier(n), [None] * n, []
+def first(i):
+    try:
+        st = torch.cuda.Stream()
+        start.wait()
+        out[i] = moe.linear(d["x"], d["w"], d["s"], None, d["adapter_ids"], d["adapter_a"], d["adapter_b"],
+                            d["adapter_scale"], stream=st)
+        st.synchronize()
+    except Exception as e:
+        errors.append(e)
+threads = [threading.Thread(target=first, args=(i,)) for i in range(n)]
+[t.start() for t in threads]
+[t.join() for t in threads]
+torch.cuda.synchronize()
+assert not errors, errors
+again = moe.linear(d["x"], d["w"], d["s"], None, d["adapter_ids"], d["adapter_a"], d["adapter_b"], d["adapter_scale"])
+assert all(torch.equal(o, again) for o in out)
+print("equal")
+"""
+
+
+def test_first_calls_of_several_threads_agree(moe):
+    """The first projections of a process, from twelve threads at once, choose the same tiles: the same bits."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS.format(root=root)], capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and "equal" in r.stdout, r.stderr[-2000:]
