@@ -867,14 +867,15 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
     }
   }
   __syncwarp();
-  // no MMA may still read the pair's memory when it is released
-  if (!warp_wait_cluster(&drain, 0)) fail = 1;
-  __syncwarp();
-  if (fail) s_fail = 1;
-  if (fail && p.a.status != nullptr) {
+  auto report = [&] {
+    if (p.a.status == nullptr) return;
     if (adapters || PAIR) grid_dependency_wait();   // the status words belong to that kernel until then
     atomicOr(&p.a.status[2], 1);
     atomicCAS(&p.a.status[3], 0, blockIdx.x + 1);
+  };
+  if (fail) {
+    s_fail = 1;
+    report();
   }
   tc_fence_before();
   __syncthreads();
@@ -884,7 +885,14 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
     for (int i = 0; i < 1000; ++i) __nanosleep(1000);
   cluster_sync();
   tc_fence_after();
-  if (warp == kWarpMma) tmem2_dealloc(tmem, kTmemCols);
+  if (warp == kWarpMma) {
+    // no MMA may still read the pair's memory when it is released: all have been
+    // issued by now, and this wait's bound covers their end alone (it began with the
+    // kernel for the warps without a role, which reported a call of more than a second)
+    if (!warp_wait_cluster(&drain, 0)) report();
+    __syncwarp();
+    tmem2_dealloc(tmem, kTmemCols);
+  }
   if (p.split > 1) {
     // y of tokens part, part + split, ..: the pairs' partial sums in rank order
     const uint32_t red = smem_u32(sX);

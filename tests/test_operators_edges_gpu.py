@@ -230,3 +230,34 @@ def test_first_calls_of_several_threads_agree(moe):
     r = subprocess.run([sys.executable, "-c", FIRST_CALLS.format(root=root)], capture_output=True, text=True,
                        timeout=300)
     assert r.returncode == 0 and "equal" in r.stdout, r.stderr[-2000:]
+
+
+# ------------------------------------------------------------------ long calls
+def test_linear_call_of_seconds_is_not_reported_as_a_failure(moe):
+    """The waits' bound of about a second is one for each wait, not for the call: a projection of some seconds
+    (every token another adapter of 256 ranks, as many columns to a tile as there can be)."""
+    T, K, N, L, rank = 262_144, 64, 16_384, 256, 256
+    g = torch.Generator(device="cuda").manual_seed(9)
+    rn = lambda *s: torch.empty(s, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    x, a, b = rn(T, K), rn(L, rank, K), rn(L, N, rank)
+    w = torch.randint(0, 256, (N, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+    s = torch.full((N, K // 32), 122, dtype=torch.uint8, device="cuda")
+    ids = (torch.arange(T, device="cuda") * 37 % L).to(torch.int32)
+    out = torch.empty(T, N, dtype=torch.bfloat16, device="cuda")
+    status = torch.full((4,), 7, dtype=torch.int32, device="cuda")
+    start, end = torch.cuda.Event(True), torch.cuda.Event(True)
+    start.record()
+    moe.linear(x, w, s, adapter_ids=ids, adapter_a=a, adapter_b=b, out=out, status=status)
+    end.record()
+    torch.cuda.synchronize()
+    print(f"{start.elapsed_time(end):.0f} ms")
+    assert start.elapsed_time(end) > 1300     # (else this test shows nothing)
+    assert status.tolist() == [0, 0, 0, 0]
+    for t in (0, 1, 255, 256, 131_071, T - 1):
+        j = int(ids[t])
+        ref, mag, low = P.linear(f64(x[t:t + 1]), w.cpu().numpy(), s.cpu().numpy(), [0], bits(a[j:j + 1]),
+                                 bits(b[j:j + 1]))
+        tol = 2.0 ** -8 * np.abs(ref) + (K / 16 + rank / 8 + 17) * 2.0 ** -23 * (mag + 8 * low) + 2.0 ** -17 * low
+        assert np.all(np.abs(f64(out[t:t + 1]) - ref) <= tol)
+    del x, a, b, out
+    torch.cuda.empty_cache()
