@@ -74,13 +74,14 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const AddNormArgs a) 
   __shared__ float part[2][32];
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
   const int n8 = a.K / 8;
+  const unsigned T = (unsigned)a.T;   // unsigned: T + gridDim.x may pass 2^31
   RowLoads<CH> d;
-  auto load = [&](int t) {
+  auto load = [&](unsigned t) {
     const size_t row = (size_t)t * a.K;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const int c = tid + i * nt;
-      if (t < a.T && c < n8) {
+      if (t < T && c < n8) {
         d.x[i] = ld_row16(a.x + row + 8 * c);
         if (a.residual != nullptr) d.res[i] = ld_row16(a.residual + row + 8 * c);
       }
@@ -88,7 +89,7 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const AddNormArgs a) 
   };
   load(blockIdx.x);
   int odd = 0;
-  for (int t = blockIdx.x; t < a.T; t += gridDim.x, odd ^= 1) {
+  for (unsigned t = blockIdx.x; t < T; t += gridDim.x, odd ^= 1) {
     const size_t row = (size_t)t * a.K;
     float h[CH][8];
     float ss = 0.f;

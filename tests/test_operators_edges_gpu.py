@@ -261,3 +261,24 @@ def test_linear_call_of_seconds_is_not_reported_as_a_failure(moe):
         assert np.all(np.abs(f64(out[t:t + 1]) - ref) <= tol)
     del x, a, b, out
     torch.cuda.empty_cache()
+
+
+# ------------------------------------------------------------------ the most rows that a call can name
+def test_add_rmsnorm_of_the_most_rows(moe):
+    """2^31 - 1 rows (137 GB, in place): the row after a CTA's last one is past 2^31."""
+    T, K = 2 ** 31 - 1, 32
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 150e9:
+        pytest.skip("needs 150 GB of free device memory")
+    x = torch.empty(T, K, dtype=torch.bfloat16, device="cuda").fill_(1.0)
+    rows = torch.tensor([0, 1215, 1216, 2 ** 30, 2 ** 31 - 1217, 2 ** 31 - 1216, T - 2, T - 1], device="cuda")
+    vals = torch.arange(len(rows), device="cuda").float()[:, None].expand(-1, K).bfloat16() + 2
+    x[rows] = vals
+    none, h, _, _ = moe.add_rmsnorm(x, torch.ones(K, device="cuda").bfloat16(), x, bf16=False, residual_out=x)
+    torch.cuda.synchronize()
+    assert none is None and h is x
+    assert torch.equal(x[rows], 2 * vals)
+    for r in (2, 2 ** 29 + 1, 2 ** 31 - 5000):
+        assert (x[r:r + 1000] == 2).all()
+    del x, h
+    torch.cuda.empty_cache()
