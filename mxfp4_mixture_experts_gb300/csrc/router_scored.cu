@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(kRsWarps * 32)
 
 cudaError_t launch_router_scored(const RouterScoredArgs& a, int num_sms, cudaStream_t stream) {
   (void)num_sms;
-  const unsigned blocks = (unsigned)((a.T + kRsWarps - 1) / kRsWarps);
+  const unsigned blocks = ((unsigned)a.T + kRsWarps - 1) / kRsWarps;   // (T + 7 may pass 2^31)
   const int lpg = a.n_group > 1 && 32 % a.n_group == 0 ? 32 / a.n_group : 32;
   const int run = lpg < 32 ? a.E / a.n_group : a.E;
   const int per = (run + lpg - 1) / lpg;

@@ -282,3 +282,20 @@ def test_add_rmsnorm_of_the_most_rows(moe):
         assert (x[r:r + 1000] == 2).all()
     del x, h
     torch.cuda.empty_cache()
+
+
+def test_router_scored_of_the_most_rows(moe):
+    """2^31 - 1 rows of one expert (26 GB)."""
+    T = 2 ** 31 - 1
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 40e9:
+        pytest.skip("needs 40 GB of free device memory")
+    x = torch.zeros(T, 1, device="cuda")
+    x[-2] = float("nan")
+    ids = torch.full((T, 1), 7, dtype=torch.int32, device="cuda")
+    ids, w = moe.router_scored(x, 1, "softmax", topk_ids=ids)
+    torch.cuda.synchronize()
+    assert int(ids[-2]) == -1 and float(w[-2]) == 0.0
+    assert int((ids == 0).sum()) == T - 1 and int((w == 1).sum()) == T - 1
+    del x, ids, w
+    torch.cuda.empty_cache()
