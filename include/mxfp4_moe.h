@@ -411,6 +411,13 @@ void mxfp4_moe_set_phase_events(void* const* events, int n);
  * reporting without faulting or hanging a GPU. Not thread-safe. */
 void mxfp4_moe_test_skip_grid_arrival(int cta);
 
+/* Test only: from the next mxfp4_moe_linear call of more than 16 tokens on, CTA
+ * `cta` of its tile kernel leaves out its first copy of packed weights, so the waits
+ * that depend on it run out (0.2 s each) and the call reports it in
+ * status[2] and status[3] instead of computing the output; a negative cta turns
+ * this off (the default). Not thread-safe. */
+void mxfp4_moe_test_skip_linear_copy(int cta);
+
 /* Test only: the warps per CTA of the decode kernel form that a decode call of
  * this shape and T would run on a device with max_smem bytes of opt-in shared
  * memory per block: 12, 11 or 10 (every warp a consumer), 7 (7 consumer warps

@@ -33,6 +33,7 @@ std::mutex g_dev_mu;
 void* const* g_phase_events = nullptr;
 int g_phase_n = 0;
 int g_test_skip_arrival = -1;   // mxfp4_moe_test_skip_grid_arrival
+int g_test_skip_copy = -1;      // mxfp4_moe_test_skip_linear_copy
 
 // cuTensorMapEncodeTiled, fetched from the driver at first use (no link-time
 // dependency on libcuda).
@@ -612,6 +613,7 @@ int mxfp4_moe_linear(const void* x, const uint8_t* x_scale, const uint8_t* w, co
   a.out = static_cast<uint16_t*>(out);
   a.status = status;
   a.ws = workspace;
+  a.skip_copy = g_test_skip_copy;
   return cuda_status(mxmoe::launch_linear(a, d->num_sms, static_cast<cudaStream_t>(stream)));
 }
 
@@ -626,6 +628,7 @@ void mxfp4_moe_set_phase_events(void* const* events, int n) {
 }
 
 void mxfp4_moe_test_skip_grid_arrival(int cta) { g_test_skip_arrival = cta < 0 ? -1 : cta; }
+void mxfp4_moe_test_skip_linear_copy(int cta) { g_test_skip_copy = cta < 0 ? -1 : cta; }
 
 int mxfp4_moe_test_decode_form(int T, int K, int I, int E, int topk, int max_smem) {
   if (T < 1 || T > kDecodeMaxT || topk < 1 || topk > 32 || topk > E || E < 1 || E > kMaxExperts ||

@@ -501,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
     fence_barrier_init();
   }
   // the first packed weights need this CTA's barriers alone: under way before
-  // the cluster has met
+  // the cluster has met (skip_copy: the failure test's call leaves the first one out)
   int wk = 0;   // stages of them issued
   if (warp == kWarpW) {
     if (lane < p.SP) { mbar_init(&p_full[lane], 1); mbar_init(&p_empty[lane], 4); }
@@ -509,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
     fence_proxy_async_smem();
     __syncwarp();
     for (; wk < p.SP && wk < nS && cluster < p.tiles; ++wk) {
-      if (elect_one()) {
+      if (elect_one() && !(wk == 0 && p.a.skip_copy == (int)blockIdx.x)) {
         mbar_arrive_expect_tx(&p_full[wk], kPStage);
         tma_load_2d(sP + wk * kPStage, &p.tmapW, (st0 + wk) * (kStageK / 2), tile_n0(cluster),
                     &p_full[wk]);
@@ -888,7 +888,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
   if (warp == kWarpMma) {
     // no MMA may still read the pair's memory when it is released: all have been
     // issued by now, and this wait's bound covers their end alone (it began with the
-    // kernel for the warps without a role, which reported a call of more than a second)
+    // kernel for the warps without a role, which reported a call of more than 0.19 s)
     if (!warp_wait_cluster(&drain, 0)) report();
     __syncwarp();
     tmem2_dealloc(tmem, kTmemCols);

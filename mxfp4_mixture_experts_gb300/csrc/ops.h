@@ -54,6 +54,7 @@ struct LinearArgs {
   int32_t* status;          // [4] or null
   void* ws;
   int T, K, N, L, rank;
+  int skip_copy;            // test only: this CTA's first copy of weights is left out; -1: none
 };
 size_t linear_workspace_bytes(int T, int K, int N, int rank, bool x8);
 cudaError_t launch_linear(const LinearArgs& a, int num_sms, cudaStream_t stream);

@@ -134,8 +134,9 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
 }
 // Bounded wait of a whole warp, which also acquires what other CTAs of the
 // cluster released. The warp sleeps in the hardware until the phase completes or
-// the hint (20 us) runs out, so waiting warps leave the issue slots to the
-// others; it gives up after about a second.
+// its time runs out (at most the hint of 20 us; 3.7 us measured), so waiting warps
+// leave the issue slots to the others; it gives up after 0.19 s (measured: a call
+// whose first copy never comes ends then).
 constexpr uint32_t kSleepHintNs = 20000, kSleepLimit = 50000;
 __device__ __forceinline__ bool warp_wait_cluster(uint64_t* bar, uint32_t parity) {
   uint32_t ok = 0;

@@ -79,6 +79,8 @@ def lib() -> ctypes.CDLL:
     L.mxfp4_moe_linear.restype = i32
     L.mxfp4_moe_test_skip_grid_arrival.argtypes = [i32]
     L.mxfp4_moe_test_skip_grid_arrival.restype = None
+    L.mxfp4_moe_test_skip_linear_copy.argtypes = [i32]
+    L.mxfp4_moe_test_skip_linear_copy.restype = None
     L.mxfp4_moe_test_decode_form.argtypes = [i32] * 6
     L.mxfp4_moe_test_decode_form.restype = i32
     L.mxfp4_moe_set_phase_events.argtypes = [vp, i32]

@@ -234,9 +234,9 @@ def test_first_calls_of_several_threads_agree(moe):
 
 # ------------------------------------------------------------------ long calls
 def test_linear_call_of_seconds_is_not_reported_as_a_failure(moe):
-    """The waits' bound of about a second is one for each wait, not for the call: a projection of some seconds
+    """The waits' bound of 0.2 s is one for each wait, not for the call: a projection of a second
     (every token another adapter of 256 ranks, as many columns to a tile as there can be)."""
-    T, K, N, L, rank = 262_144, 64, 16_384, 256, 256
+    T, K, N, L, rank = 131_072, 64, 16_384, 256, 256
     g = torch.Generator(device="cuda").manual_seed(9)
     rn = lambda *s: torch.empty(s, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
     x, a, b = rn(T, K), rn(L, rank, K), rn(L, N, rank)
@@ -251,9 +251,9 @@ def test_linear_call_of_seconds_is_not_reported_as_a_failure(moe):
     end.record()
     torch.cuda.synchronize()
     print(f"{start.elapsed_time(end):.0f} ms")
-    assert start.elapsed_time(end) > 1300     # (else this test shows nothing)
+    assert start.elapsed_time(end) > 600     # (else this test shows nothing)
     assert status.tolist() == [0, 0, 0, 0]
-    for t in (0, 1, 255, 256, 131_071, T - 1):
+    for t in (0, 1, 255, 256, 100_003, T - 1):
         j = int(ids[t])
         ref, mag, low = P.linear(f64(x[t:t + 1]), w.cpu().numpy(), s.cpu().numpy(), [0], bits(a[j:j + 1]),
                                  bits(b[j:j + 1]))
@@ -299,3 +299,33 @@ def test_router_scored_of_the_most_rows(moe):
     assert int((ids == 0).sum()) == T - 1 and int((w == 1).sum()) == T - 1
     del x, ids, w
     torch.cuda.empty_cache()
+
+
+# ------------------------------------------------------------------ waits that give up
+@pytest.mark.parametrize("x8", [False, True])
+@pytest.mark.parametrize("rank", [0, 16])
+@pytest.mark.parametrize("T,cta", [(40, 0), (40, 3), (700, 1)])
+def test_linear_missing_copy_is_reported_and_the_next_call_is_right(moe, T, cta, rank, x8):
+    """A copy that never comes (K split over a cluster; one pair a tile): the call ends within its bounds and
+    says so, and the same workspace serves the next one. No GPU fault and no endless wait is involved."""
+    K, N = 2048, 1032
+    d = {k: v.cuda() for k, v in make_linear(T, K, N, rank, 5, x8, 60 + T).items() if k != "x64"}
+    x, w, s, xs = d.pop("x"), d.pop("w"), d.pop("s"), d.pop("x_scale", None)
+    want = moe.linear(x, w, s, xs, **d)
+    ws = torch.empty(max(moe.linear_workspace_size(T, K, N, rank, x8), 1), dtype=torch.uint8, device="cuda")
+    status = torch.full((4,), 7, dtype=torch.int32, device="cuda")
+    start, end = torch.cuda.Event(True), torch.cuda.Event(True)
+    moe.lib().mxfp4_moe_test_skip_linear_copy(cta)
+    try:
+        start.record()
+        moe.linear(x, w, s, xs, workspace=ws, status=status, **d)
+        end.record()
+        torch.cuda.synchronize()
+    finally:
+        moe.lib().mxfp4_moe_test_skip_linear_copy(-1)
+    beyond = int((d["adapter_ids"] >= 5).sum()) if rank else 0
+    assert status[:3].tolist() == [beyond, 0, 1] and 1 <= int(status[3]) <= 152
+    assert start.elapsed_time(end) < 10_000
+    y = moe.linear(x, w, s, xs, workspace=ws, status=status, **d)
+    torch.cuda.synchronize()
+    assert status.tolist() == [beyond, 0, 0, 0] and torch.equal(y, want)
