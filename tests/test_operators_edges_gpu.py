@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from oracle import operators_oracle as P
-from test_operators_gpu import bits, call_linear, f64, gen, make_linear
+from test_operators_gpu import bits, call_linear, check_linear, f64, gen, make_linear
 
 pytestmark = pytest.mark.gpu
 
@@ -329,3 +329,27 @@ def test_linear_missing_copy_is_reported_and_the_next_call_is_right(moe, T, cta,
     y = moe.linear(x, w, s, xs, workspace=ws, status=status, **d)
     torch.cuda.synchronize()
     assert status.tolist() == [beyond, 0, 0, 0] and torch.equal(y, want)
+
+
+# ------------------------------------------------------------------ limits of the projection's sizes
+@pytest.mark.parametrize("x8", [False, True])
+@pytest.mark.parametrize("T", [5, 24, 300])
+def test_linear_longest_rows_and_most_adapters(moe, T, x8):
+    """K = 16384 and 1024 adapters, a token each, the last ones among them."""
+    d = make_linear(T, 16384, 136, 8, 1024, x8, 2000 + T)
+    d["adapter_ids"] = (1023 - torch.arange(T) * 3 % 1024).to(torch.int32)
+    check_linear(moe, d)
+
+
+@pytest.mark.parametrize("T", [3, 40, 300])
+def test_linear_smallest_and_largest_scales_are_exact(moe, T):
+    """Weights and MXFP8 rows whose scales make them bf16's subnormal numbers (rows from scale byte 3 on, below
+    which a code's last bits are under bf16's smallest step), against factors that bring y back into range."""
+    for low in ("x", "w"):
+        d = make_linear(T, 256, 136, 0, 0, True, 31)
+        sx = torch.randint(*((3, 8) if low == "x" else (228, 232)), d["x_scale"].shape, generator=gen(1), dtype=torch.uint8)
+        sw = torch.randint(*((0, 4) if low == "w" else (228, 232)), d["s"].shape, generator=gen(2), dtype=torch.uint8)
+        q = d["x"].double().numpy()
+        d["x_scale"], d["s"] = sx, sw
+        d["x64"] = q * np.repeat(np.exp2(sx.numpy().astype(np.float64) - 127), 32, 1)
+        check_linear(moe, d)
