@@ -365,7 +365,9 @@ int mxfp4_moe_router_scored(const float* logits, const float* bias, int T, int E
  *   y_t = W x_t + adapter_scale[a] * B[a] (A[a] x_t),   a = adapter_ids[t]
  * fp32 sums, one rounding to bf16. The inner products v = adapter_scale (A x)
  * are rounded to 17 significant bits on their way to the second product, an error
- * of at most 2^-17 sum_r |B[n][r] v[r]|.
+ * of at most 2^-17 sum_r |B[n][r] v[r]|. MXFP8 values are taken as bf16: exact,
+ * but for codes of scale bytes 0 to 2 whose last bits are below bf16's smallest
+ * step (2^-133), and infinite past its largest value.
  *   x             bf16 [T, K] (x_scale NULL), or MXFP8 as mxfp4_moe_add_rmsnorm
  *                 writes it: E4M3 uint8 [T, K] with x_scale E8M0 uint8 [T, K/32]
  *   w / s         uint8 [N, K/2] / [N, K/32], the packed layout of one expert's w2

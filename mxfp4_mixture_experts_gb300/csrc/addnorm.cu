@@ -184,8 +184,10 @@ cudaError_t launch_add_rmsnorm(const AddNormArgs& a, int num_sms, cudaStream_t s
   // Few rows: a CTA each, one chunk a thread where 1024 threads suffice (its
   // latency counts). Many rows: two chunks a thread and as many persistent CTAs as
   // fill an SM's threads. T = 8192, K = 6144 with MXFP8 (454.6 MB): 8192 CTAs of
-  // 768 threads 129 us, 608 persistent ones of 384 threads 73 us = 6.2 TB/s; the
-  // copy engine moves as many bytes in 72 us.
+  // 768 threads 129 us, 608 persistent ones of 384 threads 72 us = 6.3 TB/s; the
+  // copy engine moves as many bytes in 72 us. Short rows fill neither a CTA nor, eight
+  // to an SM, its threads: T = 8192 in a graph reaches 5.6 TB/s at K = 2048, 4.7 at
+  // 1024, 3.2 at 512 (12 us) and 2.4 at 256, where half of the CTA's one warp has no chunk.
   const int n8 = a.K / 8;
   const bool many = a.T > 2 * num_sms;
   const int ch = many || n8 > 1024 ? 2 : 1;

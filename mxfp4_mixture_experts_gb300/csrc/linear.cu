@@ -53,7 +53,7 @@
 //
 // Measured (T = 8192, K = 6144, N = 4096, rank 16): the tile kernel alone 204 us =
 // 2.0 PFLOP/s, its MMAs back to back (1024 clocks for a stage's eight); with the
-// down kernel and MXFP8 rows 240 us a call. Between 33 and about 1000 tokens the
+// down kernel and MXFP8 rows 235 us in a graph. Between 33 and about 1000 tokens the
 // dequantisation bounds a stage (its ALU instructions: 350 to 470 clocks of a
 // stage at best, 570 to 750 beside the other warps), below that the fixed
 // steps of a tile: start 3 us, first operands 2 us, the cluster's addition 2 us.
@@ -177,9 +177,12 @@ constexpr int kDownSum = 64;      // ranks whose parts a cluster adds at once
 
 // NT: n-tiles of 8 ranks per pass. From 17 ranks on one CTA to an SM: its loads and
 // sums want more than 128 registers. With two, and 64 ranks in two passes over x,
-// K = 7168, N = 4096, T = 16 took 20.3 us where this takes 13.6, T = 128 26.4 and
-// 20.6, T = 8192 300 and 287 (of MXFP8 rows 321 and 297); of 32 ranks T = 64 16.5 and
-// 12.1, T = 8192 96 and 103 (K = 4096, N = 2048).
+// K = 7168, N = 4096, T = 16 took 19.8 us where this takes 13.9, T = 128 26.8 and
+// 21.1, T = 512 57.1 and 35.5, T = 8192 314 and 298 (of MXFP8 rows 331 and 307); of 32
+// ranks (K = 4096, N = 2048) T = 64 12.2 either way, 15.2 and 13.9 of MXFP8 rows, T = 512
+// 22.8 and 20.1, T = 8192 99.7 and 104, the one size that it loses. Eight ranks have one
+// n-tile: K = 2048, N = 1024, MXFP8, T = 16 6.2 us, with two (half of them unused) 6.8;
+// K = 2880, N = 5760, T = 64 13.9 and 14.6; nothing at T = 8192 (all in graphs).
 template <int NT, bool X8>
 __global__ void __launch_bounds__(256, NT <= 2 ? 2 : 1)
     adapter_down_kernel(const LinearArgs a, uint16_t* __restrict__ xb /* null: not converted */,
@@ -926,7 +929,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
 // Up to 16 tokens the packed weights are all there is to move, and the tile
 // kernel's start, its stages one after another and its cluster-wide sums were
 // most of the time (T = 1, K = 6144, N = 4096, rank 16, in a graph: 14.3 us, here
-// 7.5; T = 16: 17 and 13.7). At 32 tokens, which no longer stay in registers over
+// 7.5; T = 16: 17 and 10.9). At 32 tokens, which no longer stay in registers over
 // a step, this form took 16 to 45 us where the tiles take 15 to 19.
 //
 // A CTA takes 32 weight rows, its warps the K values in steps of 128 (4 scale
@@ -1128,9 +1131,9 @@ static DownPlan down_alone(const LinearArgs& a, const DownWork& w, int num_sms) 
 // part 15.4 us, four 15.8). Both kernels then start together, and the projection's
 // last steps find the sums ready. us in graphs, against all SMs always (N = 4096;
 // 5760 at K = 2880):
-//   K = 6144, rank 16: T = 8  8.3 (11.4), T = 64 15.4 (19.8), T = 1024 37.6 (43.3)
-//   K = 2880, rank 16: T = 8  8.3  (8.3), T = 64 14.2 (16.5), T = 1024 31.5 (35.5)
-//   K = 7168, rank 64: T = 8 10.6 (14.7), T = 32 16.8 (21.8), T =  512 34.4 (38.8)
+//   K = 6144, rank 16: T =  8  8.2  (8.8), T = 64 15.2 (17.3), T = 1024 37.7 (42.6)
+//   K = 2880, rank 16: T =  8  8.3  (8.5), T = 64 14.4 (16.7), T = 1024 32.3 (36.0)
+//   K = 7168, rank 64: T = 16 13.9 (19.6), T = 32 17.3 (17.7), T =  512 35.5 (39.4)
 static DownPlan down_beside(const LinearArgs& a, const DownWork& w, double clocks, int room) {
   const bool few = a.T <= kFewTok;
   DownPlan best = {0, 0, 0};

@@ -14,9 +14,12 @@
 // chosen and a NaN or -inf logit scores 0. A slot with no expert left gets id
 // -1 (padding for the layer) and weight 0; a chosen sum of 0 gives weights 0.
 //
-// The choice has to be the same wherever the fp32 scores are, so they are
-// computed as written: expf, IEEE addition and division, none of them
-// contracted into another operation.
+// Scores are computed as written: expf, IEEE addition and division, none of them
+// contracted into another operation. A choice by logits (no bias, one group) or by
+// sigmoid scores is then the same in every fp32 evaluation of the formula by the same
+// expf. A softmax score has a sum in it whose last bits go by the order of its terms
+// (here a lane's, then a tree): with a bias or groups, experts that lie within 2^-20
+// of one another may change places against another order.
 //
 // One warp per token. Each group gets 32 / n_group neighbouring lanes (all of
 // them without groups), each lane consecutive experts, so of equal candidates
