@@ -91,6 +91,8 @@ def draw(rng):
         gate = rng.choice([None, "channel", "token", "full"])
         scaled = rng.random() < 0.5
         T = min(T, 8192 * 6144 // (K * (2 if gate == "full" or scaled else 1)))
+        if T == 1 and gate == "full":
+            gate = "channel"   # (one row of gates is a channel's)
         ck = rng.choice([None, "ocp", "nosat"])
         args = ("", T, K, gate, rng.choice(["linear", "sigmoid"]), scaled)
         if op == "sandwich_norm":
