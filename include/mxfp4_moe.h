@@ -335,6 +335,63 @@ int mxfp4_moe_add_rmsnorm(const void* x, const void* residual, const void* gamma
                           float eps, int rule, void* residual_out, void* out, uint8_t* out8,
                           uint8_t* scale8, void* stream);
 
+/* The norms after and before a block with the block's gate and the residual's
+ * scale between them. Per row t:
+ *   n = x * r1 * post_gamma, r1 = rsqrt(mean(x^2) + eps)   (post_gamma NULL: n = x)
+ *   h = residual_scale * residual + g * n (fp32)            residual_out = bf16(h)
+ *   y = h * r2 * pre_gamma, r2 = rsqrt(mean(h^2) + eps), from the unrounded h
+ *   out = bf16(y); out8, scale8: MXFP8 of y as mxfp4_moe_add_rmsnorm writes it
+ *   x, residual    bf16 [T, K]
+ *   post_gamma, pre_gamma  bf16 [K]; pre_gamma NULL: no y, out and out8 NULL
+ *   gate           gate_kind 0: NULL (g = 1); 1: bf16 [K], a channel's; 2: fp32 [T],
+ *                  a token's; 3: bf16 [T, K]. gate_act 0: g is the value, 1: its sigmoid
+ *   residual_scale fp32 [1] or NULL (1)
+ *   residual_out   bf16 [T, K] or NULL; may be the same pointer as x or residual
+ *   x8, x8_scale / h8, h8_scale   what a backward pass keeps in 8 bits: MXFP8 of x
+ *                  and of the unrounded h under checkpoint_rule; each pair or NULL
+ *   rstd           fp32 [2, T] or NULL: r1 and r2 (1 where there is no norm)
+ * rule and checkpoint_rule 0 = OCP or 1 = "nosat" as above; at least one output.
+ * Limits, eps, T == 0 and alignment as mxfp4_moe_add_rmsnorm (scale bytes: any;
+ * residual_scale, rstd and a token's gate 4 bytes). */
+int mxfp4_moe_sandwich_norm(const void* x, const void* residual, const void* post_gamma,
+                            const void* pre_gamma, const void* gate, int gate_kind, int gate_act,
+                            const float* residual_scale, int T, int K, float eps, int rule,
+                            int checkpoint_rule, void* residual_out, void* out, uint8_t* out8,
+                            uint8_t* scale8, uint8_t* x8, uint8_t* x8_scale, uint8_t* h8,
+                            uint8_t* h8_scale, float* rstd, void* stream);
+
+/* Its gradient, from what the forward call kept. With H = h r2, X = x r1,
+ * v = pre_gamma * grad_y, means over the row:
+ *   d = grad_h + r2 (v - H mean(v H))       grad_residual = bf16(residual_scale * d)
+ *   u = post_gamma * g * d                  grad_x = bf16(r1 (u - X mean(u X)))
+ *                                           (post_gamma NULL: grad_x = bf16(g * d))
+ *   grad_pre_gamma  fp32 [K]  sum_t grad_y * H
+ *   grad_post_gamma fp32 [K]  sum_t g * d * X
+ *   grad_gate       d * n * g' summed to the gate's shape: fp32 [K], fp32 [T] or bf16 [T, K]
+ *   grad_residual_scale fp32 [1]  sum d * residual
+ *   grad_h, grad_y  bf16 [T, K]; either may be NULL (zero), not both
+ *   x, h            bf16 [T, K] (scale NULL), or E4M3 [T, K] with E8M0 [T, K/32],
+ *                   each by itself; h may be NULL without grad_y
+ *   rstd            fp32 [2, T], needed with post_gamma or grad_y
+ *   post_gamma, pre_gamma, gate, gate_kind, gate_act, residual_scale as forward
+ *   residual        bf16 [T, K], read for grad_residual_scale only
+ * Outputs may be NULL where they are not wanted, at least one is needed, and none may
+ * overlap an input. T == 0 zeroes the sums over rows that are asked for. workspace:
+ * mxfp4_moe_sandwich_norm_backward_workspace_size bytes, 256-byte aligned, no
+ * initial contents required, not shared by calls that may run concurrently. Limits
+ * as forward; bf16 and E4M3 rows and fp32 [K] 16-byte aligned, the rest 4. */
+size_t mxfp4_moe_sandwich_norm_backward_workspace_size(int T, int K);
+int mxfp4_moe_sandwich_norm_backward(const void* grad_h, const void* grad_y, const void* x,
+                                     const uint8_t* x_scale, const void* h, const uint8_t* h_scale,
+                                     const float* rstd, const void* post_gamma,
+                                     const void* pre_gamma, const void* gate, int gate_kind,
+                                     int gate_act, const void* residual,
+                                     const float* residual_scale, int T, int K, void* grad_x,
+                                     void* grad_residual, float* grad_post_gamma,
+                                     float* grad_pre_gamma, void* grad_gate,
+                                     float* grad_residual_scale, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+
 /* Router in the score domain (mxfp4_moe_router adds its bias to the logits; a
  * bias on the scores orders the experts differently). Per token:
  *   s_e = softmax over all E logits (scoring 0) or sigmoid(logit) (scoring 1)
@@ -359,6 +416,63 @@ int mxfp4_moe_router_scored(const float* logits, const float* bias, int T, int E
                             int scoring, int n_group, int topk_group, int group_top,
                             int renormalise, float route_scale, int32_t* topk_ids,
                             float* topk_weights, void* stream);
+
+/* Balance losses and expert counts of a routing. s as mxfp4_moe_router_scored
+ * scores the logits (NaN and -inf: masked, s = 0), p_e = s_e / sum s. A token counts when
+ * it has an id in [0, E) and a logit that is not masked; other ids are skipped,
+ * the same id twice counts twice. Per sequence, over its n counting tokens:
+ *   counts int32 [n_seq, E]  routes to each expert (C: their sum)
+ *   prob   fp32  [n_seq, E]  mean of p
+ *   slope  fp32  [n_seq, E]  E * counts / (C n), the gradient of the sequence's loss
+ *                            E sum_e (counts / C) prob with respect to p of a token
+ * (zeros for a sequence without tokens) and
+ *   stats  fp32  [4]  the mean loss of the sequences that have tokens; the mean over
+ *                     tokens of log(sum exp(logits))^2; tokens; such sequences
+ *   logits fp32 [T, E], topk_ids int32 [T, topk]
+ *   seq_offsets int32 [n_seq + 1], not decreasing: sequence i is the rows from
+ *     seq_offsets[i] up to seq_offsets[i + 1]; rows in none are left out. NULL: all
+ *     rows are one sequence (n_seq 1)
+ * Limits (MXFP4_MOE_ERR_SHAPE): 0 <= T, T * topk < 2^31, 1 <= E <= 1024,
+ * 1 <= topk <= min(32, E), 1 <= n_seq <= 2^20. T == 0 writes zeros. workspace as
+ * mxfp4_moe_sandwich_norm_backward; all other pointers 4-byte aligned. */
+size_t mxfp4_moe_router_balance_workspace_size(int T, int E, int n_seq);
+int mxfp4_moe_router_balance(const float* logits, const int32_t* topk_ids, int T, int E, int topk,
+                             int scoring, const int32_t* seq_offsets, int n_seq, float* stats,
+                             int32_t* counts, float* prob, float* slope, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/* Gradient of the logits of mxfp4_moe_router_scored's weights (the choice is
+ * fixed) and of mxfp4_moe_router_balance's losses (the counts are):
+ *   sum grad_weights * topk_weights + grad_losses[0] * stats[0] + grad_losses[1] * stats[1]
+ *   topk_ids      the chosen experts; an id outside [0, E) or of a masked expert
+ *                 takes no part, the same id twice twice
+ *   grad_weights  fp32 [T, topk] or NULL (zero)
+ *   grad_losses   fp32 [2] or NULL (zero; stats, slope and seq_offsets are then not
+ *                 read); stats, slope, seq_offsets, n_seq as that call's
+ *   grad_logits   fp32 [T, E], written completely (0 for masked logits and for rows
+ *                 without a valid id)
+ * Limits and alignment as mxfp4_moe_router_balance; T == 0 enqueues nothing. */
+int mxfp4_moe_router_backward(const float* logits, const int32_t* topk_ids,
+                              const float* grad_weights, int T, int E, int topk, int scoring,
+                              int renormalise, float route_scale, const float* grad_losses,
+                              const float* stats, const float* slope, const int32_t* seq_offsets,
+                              int n_seq, float* grad_logits, void* stream);
+
+/* Gradient of the layer's combination y_t = sum_j w_tj o_tj of its routes'
+ * outputs o (mxfp4_moe_forward_window with per_route):
+ *   grad_weights fp32 [T, topk]       sum over the row of grad_out_t * o_tj
+ *   grad_routes  bf16 [T * topk, K] or NULL   bf16(w_tj * grad_out_t)
+ *   grad_out bf16 [T, K], routes bf16 [T * topk, K], topk_weights fp32 [T, topk]
+ *   (needed with grad_routes)
+ *   topk_ids int32 [T, topk] or NULL (every route counts). A negative id, or one outside
+ *   expert_base .. expert_base + n_experts - 1 (n_experts 0: no window), is a skipped
+ *   route: its row is not read, its gradients are 0
+ * Limits (MXFP4_MOE_ERR_SHAPE): K as above, 1 <= topk <= 32, T * topk < 2^31.
+ * bf16 rows 16-byte aligned, the rest 4. T == 0 enqueues nothing. */
+int mxfp4_moe_combine_backward(const void* grad_out, const void* routes, const int32_t* topk_ids,
+                               const float* topk_weights, int T, int K, int topk, int expert_base,
+                               int n_experts, float* grad_weights, void* grad_routes,
+                               void* stream);
 
 /* A shared projection from packed MXFP4 weights, with the low-rank adapters of
  * many requests beside it:

@@ -19,49 +19,10 @@
 #include <cstdint>
 
 #include "ops.h"
-#include "ops_common.cuh"
+#include "rows.cuh"
 
 namespace mxmoe {
 namespace {
-
-// Row data (no read-only path: residual_out may be x or residual).
-__device__ __forceinline__ uint4 ld_row16(const uint16_t* p) {
-  return *reinterpret_cast<const uint4*>(p);
-}
-__device__ __forceinline__ void st_row16(uint16_t* p, const uint4& v) {
-  *reinterpret_cast<uint4*>(p) = v;
-}
-__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
-  return make_uint4(bf16x2_rn(v[0], v[1]), bf16x2_rn(v[2], v[3]), bf16x2_rn(v[4], v[5]),
-                    bf16x2_rn(v[6], v[7]));
-}
-// Two fp32 -> two E4M3 bytes (first value in the low byte), nearest even, saturating.
-__device__ __forceinline__ uint32_t e4m3x2_rn_sat(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-// 1 / sqrt(v) as a value and its remainder: the approximation and a Newton step.
-struct Root {
-  float hi, lo;
-};
-__device__ __forceinline__ Root rsqrt2(float v) {
-  const float r = rsqrtf(v);
-  const float p = __fmul_rn(v, r);
-  const float c = 0.5f * r * (fmaf(-p, r, 1.f) - r * fmaf(v, r, -p));
-  if (!(fabsf(c) < r)) return Root{r, 0.f};   // v zero, infinite or NaN: the root as it is
-  const float hi = __fadd_rn(r, c);
-  return Root{hi, c - __fsub_rn(hi, r)};
-}
-// h * r * g with one rounding: the remainders of the root and of the first
-// product go into the second. (Three more operations a value, hidden behind the
-// memory; y is then exact but for the sum's error and half an ulp, and the codes made of it
-// are those of the exact y except next to a tie.)
-__device__ __forceinline__ float scaled(float h, Root r, float g) {
-  const float t = __fmul_rn(h, r.hi);
-  return fmaf(t, g, (fmaf(h, r.hi, -t) + h * r.lo) * g);
-}
 
 template <int CH>
 struct RowLoads {
@@ -157,21 +118,10 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const AddNormArgs a) 
         for (int j = 0; j < 8; ++j) y[j] = 0.f;
       }
       if (a.q8 != nullptr) {
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        const bool nonfinite = m >= 0x7F800000u;
-        int X = max((int)(m >> 23) - 135, -127);
-        // 448 = 1.75 * 2^8: past it the block saturates (never where X is clamped)
-        if (a.nosat && (int)(m >> 23) >= 8 && (m & 0x7FFFFFu) > 0x600000u) ++X;
-        const float inv = __uint_as_float((uint32_t)(127 - X) << 23);   // 2^-X, exact
-        uint2 q;
-        q.x = e4m3x2_rn_sat(y[0] * inv, y[1] * inv) | (e4m3x2_rn_sat(y[2] * inv, y[3] * inv) << 16);
-        q.y = e4m3x2_rn_sat(y[4] * inv, y[5] * inv) | (e4m3x2_rn_sat(y[6] * inv, y[7] * inv) << 16);
-        if (nonfinite) q = make_uint2(0u, 0u);
+        const Mx8 e = mx8_block(y, m, a.nosat);
         if (valid) {
-          *reinterpret_cast<uint2*>(a.q8 + row + 8 * c) = q;
-          if ((c & 3) == 0)
-            a.s8[(size_t)t * (a.K / 32) + (c >> 2)] = nonfinite ? 255u : (uint8_t)(X + 127);
+          *reinterpret_cast<uint2*>(a.q8 + row + 8 * c) = e.q;
+          if ((c & 3) == 0) a.s8[(size_t)t * (a.K / 32) + (c >> 2)] = (uint8_t)e.s;
         }
       }
     }

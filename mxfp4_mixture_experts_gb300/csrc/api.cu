@@ -553,6 +553,255 @@ int mxfp4_moe_router_scored(const float* logits, const float* bias, int T, int E
 }
 
 namespace {
+bool bf16_rows_ok(int T, int K) { return T >= 0 && K >= 32 && K <= 16384 && K % 32 == 0; }
+// A gate of this kind and activation, with its pointer: bf16 rows 16-byte, fp32 4-byte aligned.
+int gate_ok(const void* gate, int kind, int act) {
+  if (kind < 0 || kind > 3 || (act != 0 && act != 1) || (kind == 0) != (gate == nullptr))
+    return MXFP4_MOE_ERR_ARG;
+  return aligned(gate, kind == 2 ? 4 : 16) ? MXFP4_MOE_OK : MXFP4_MOE_ERR_ALIGN;
+}
+}  // namespace
+
+int mxfp4_moe_sandwich_norm(const void* x, const void* residual, const void* post_gamma,
+                            const void* pre_gamma, const void* gate, int gate_kind, int gate_act,
+                            const float* residual_scale, int T, int K, float eps, int rule,
+                            int checkpoint_rule, void* residual_out, void* out, uint8_t* out8,
+                            uint8_t* scale8, uint8_t* x8, uint8_t* x8_scale, uint8_t* h8,
+                            uint8_t* h8_scale, float* rstd, void* stream) {
+  if (!bf16_rows_ok(T, K)) return MXFP4_MOE_ERR_SHAPE;
+  if (!(eps >= 0.f) || isinf(eps) || (rule != 0 && rule != 1) ||
+      (checkpoint_rule != 0 && checkpoint_rule != 1))
+    return MXFP4_MOE_ERR_ARG;
+  if (T == 0) return MXFP4_MOE_OK;
+  if (!x || !residual) return MXFP4_MOE_ERR_ARG;
+  if ((out8 == nullptr) != (scale8 == nullptr) || (x8 == nullptr) != (x8_scale == nullptr) ||
+      (h8 == nullptr) != (h8_scale == nullptr))
+    return MXFP4_MOE_ERR_ARG;
+  if (pre_gamma == nullptr && (out != nullptr || out8 != nullptr)) return MXFP4_MOE_ERR_ARG;
+  if (!residual_out && !out && !out8 && !x8 && !h8 && !rstd) return MXFP4_MOE_ERR_ARG;
+  if (int rc = gate_ok(gate, gate_kind, gate_act)) return rc;
+  if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(post_gamma, 16) ||
+      !aligned(pre_gamma, 16) || !aligned(residual_scale, 4) || !aligned(residual_out, 16) ||
+      !aligned(out, 16) || !aligned(out8, 16) || !aligned(x8, 16) || !aligned(h8, 16) ||
+      !aligned(rstd, 4))
+    return MXFP4_MOE_ERR_ALIGN;
+  DeviceInfo* d = nullptr;
+  if (int rc = current_device(&d)) return rc;
+  mxmoe::SandwichArgs a = {};
+  a.x = static_cast<const uint16_t*>(x);
+  a.residual = static_cast<const uint16_t*>(residual);
+  a.post = static_cast<const uint16_t*>(post_gamma);
+  a.pre = static_cast<const uint16_t*>(pre_gamma);
+  a.gate = gate;
+  a.rscale = residual_scale;
+  a.h_out = static_cast<uint16_t*>(residual_out);
+  a.out = static_cast<uint16_t*>(out);
+  a.q8 = out8;
+  a.s8 = scale8;
+  a.x8 = x8;
+  a.xs8 = x8_scale;
+  a.h8 = h8;
+  a.hs8 = h8_scale;
+  a.rstd = rstd;
+  a.T = T;
+  a.K = K;
+  a.gate_kind = gate_kind;
+  a.gate_act = gate_act;
+  a.nosat = rule;
+  a.ck_nosat = checkpoint_rule;
+  a.eps = eps;
+  return cuda_status(mxmoe::launch_sandwich_norm(a, d->num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+size_t mxfp4_moe_sandwich_norm_backward_workspace_size(int T, int K) {
+  return bf16_rows_ok(T, K) ? mxmoe::sandwich_bwd_workspace_bytes(T, K) : 0;
+}
+
+int mxfp4_moe_sandwich_norm_backward(const void* grad_h, const void* grad_y, const void* x,
+                                     const uint8_t* x_scale, const void* h, const uint8_t* h_scale,
+                                     const float* rstd, const void* post_gamma,
+                                     const void* pre_gamma, const void* gate, int gate_kind,
+                                     int gate_act, const void* residual,
+                                     const float* residual_scale, int T, int K, void* grad_x,
+                                     void* grad_residual, float* grad_post_gamma,
+                                     float* grad_pre_gamma, void* grad_gate,
+                                     float* grad_residual_scale, void* workspace,
+                                     size_t workspace_bytes, void* stream) {
+  if (!bf16_rows_ok(T, K)) return MXFP4_MOE_ERR_SHAPE;
+  if (gate_kind < 0 || gate_kind > 3 || (gate_act != 0 && gate_act != 1)) return MXFP4_MOE_ERR_ARG;
+  if ((grad_post_gamma && !post_gamma) || (grad_pre_gamma && !pre_gamma) ||
+      (grad_gate && gate_kind == 0) || (grad_residual_scale && !residual_scale) ||
+      (grad_y && !pre_gamma))
+    return MXFP4_MOE_ERR_ARG;
+  if (!grad_x && !grad_residual && !grad_post_gamma && !grad_pre_gamma && !grad_gate &&
+      !grad_residual_scale)
+    return MXFP4_MOE_ERR_ARG;
+  if (T > 0) {
+    if ((!grad_h && !grad_y) || !x || (grad_y && !h) || ((post_gamma || grad_y) && !rstd) ||
+        (grad_residual_scale && !residual))
+      return MXFP4_MOE_ERR_ARG;
+  }
+  if (T > 0 || gate_kind == 1) {   // (a channel's gate is read for the sums' factors)
+    if (int rc = gate_ok(gate, gate_kind, gate_act)) return rc;
+  }
+  if (!aligned(grad_h, 16) || !aligned(grad_y, 16) || !aligned(x, 16) || !aligned(h, 16) ||
+      !aligned(rstd, 4) || !aligned(post_gamma, 16) || !aligned(pre_gamma, 16) ||
+      !aligned(residual, 16) || !aligned(residual_scale, 4) || !aligned(grad_x, 16) ||
+      !aligned(grad_residual, 16) || !aligned(grad_post_gamma, 16) ||
+      !aligned(grad_pre_gamma, 16) || !aligned(grad_gate, gate_kind == 2 ? 4 : 16) ||
+      !aligned(grad_residual_scale, 4))
+    return MXFP4_MOE_ERR_ALIGN;
+  const size_t need = mxmoe::sandwich_bwd_workspace_bytes(T, K);
+  if (need > 0) {
+    if (workspace == nullptr || workspace_bytes < need) return MXFP4_MOE_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return MXFP4_MOE_ERR_ALIGN;
+  }
+  DeviceInfo* d = nullptr;
+  if (int rc = current_device(&d)) return rc;
+  mxmoe::SandwichBwdArgs a = {};
+  a.dh = static_cast<const uint16_t*>(grad_h);
+  a.dy = static_cast<const uint16_t*>(grad_y);
+  a.x = x;
+  a.xs = x_scale;
+  a.h = h;
+  a.hs = h_scale;
+  a.rstd = rstd;
+  a.post = static_cast<const uint16_t*>(post_gamma);
+  a.pre = static_cast<const uint16_t*>(pre_gamma);
+  a.gate = gate;
+  a.residual = static_cast<const uint16_t*>(residual);
+  a.rscale = residual_scale;
+  a.dx = static_cast<uint16_t*>(grad_x);
+  a.dres = static_cast<uint16_t*>(grad_residual);
+  a.dpost = grad_post_gamma;
+  a.dpre = grad_pre_gamma;
+  a.dgate = grad_gate;
+  a.dscale = grad_residual_scale;
+  a.ws = static_cast<float*>(workspace);
+  a.T = T;
+  a.K = K;
+  a.gate_kind = gate_kind;
+  a.gate_act = gate_act;
+  return cuda_status(
+      mxmoe::launch_sandwich_norm_backward(a, d->num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+constexpr int kMaxSequences = 1 << 20;
+bool routing_ok(int T, int E, int topk, int S) {
+  return T >= 0 && E >= 1 && E <= kRouterMaxExperts && topk >= 1 && topk <= 32 && topk <= E &&
+         (int64_t)T * topk < ((int64_t)1 << 31) && S >= 1 && S <= kMaxSequences;
+}
+}  // namespace
+
+size_t mxfp4_moe_router_balance_workspace_size(int T, int E, int n_seq) {
+  return routing_ok(T, E, 1, n_seq) ? mxmoe::router_balance_workspace_bytes(T, E, n_seq) : 0;
+}
+
+int mxfp4_moe_router_balance(const float* logits, const int32_t* topk_ids, int T, int E, int topk,
+                             int scoring, const int32_t* seq_offsets, int n_seq, float* stats,
+                             int32_t* counts, float* prob, float* slope, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  if (!routing_ok(T, E, topk, n_seq)) return MXFP4_MOE_ERR_SHAPE;
+  if ((scoring != 0 && scoring != 1) || (seq_offsets == nullptr && n_seq != 1))
+    return MXFP4_MOE_ERR_ARG;
+  if ((T > 0 && (!logits || !topk_ids)) || !stats || !counts || !prob || !slope)
+    return MXFP4_MOE_ERR_ARG;
+  if (!aligned(logits, 4) || !aligned(topk_ids, 4) || !aligned(seq_offsets, 4) ||
+      !aligned(stats, 4) || !aligned(counts, 4) || !aligned(prob, 4) || !aligned(slope, 4))
+    return MXFP4_MOE_ERR_ALIGN;
+  if (workspace == nullptr || workspace_bytes < mxmoe::router_balance_workspace_bytes(T, E, n_seq))
+    return MXFP4_MOE_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return MXFP4_MOE_ERR_ALIGN;
+  DeviceInfo* d = nullptr;
+  if (int rc = current_device(&d)) return rc;
+  mxmoe::RouterBalanceArgs a = {};
+  a.logits = logits;
+  a.ids = topk_ids;
+  a.offsets = seq_offsets;
+  a.T = T;
+  a.E = E;
+  a.topk = topk;
+  a.scoring = scoring;
+  a.S = n_seq;
+  a.stats = stats;
+  a.counts = counts;
+  a.prob = prob;
+  a.slope = slope;
+  a.ws = workspace;
+  return cuda_status(mxmoe::launch_router_balance(a, d->num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+int mxfp4_moe_router_backward(const float* logits, const int32_t* topk_ids,
+                              const float* grad_weights, int T, int E, int topk, int scoring,
+                              int renormalise, float route_scale, const float* grad_losses,
+                              const float* stats, const float* slope, const int32_t* seq_offsets,
+                              int n_seq, float* grad_logits, void* stream) {
+  if (!routing_ok(T, E, topk, n_seq)) return MXFP4_MOE_ERR_SHAPE;
+  if ((scoring != 0 && scoring != 1) || (renormalise != 0 && renormalise != 1) ||
+      isnan(route_scale) || isinf(route_scale) || (seq_offsets == nullptr && n_seq != 1))
+    return MXFP4_MOE_ERR_ARG;
+  if (T == 0) return MXFP4_MOE_OK;
+  if (!logits || !topk_ids || !grad_logits || (!grad_weights && !grad_losses) ||
+      (grad_losses && (!stats || !slope)))
+    return MXFP4_MOE_ERR_ARG;
+  if (!aligned(logits, 4) || !aligned(topk_ids, 4) || !aligned(grad_weights, 4) ||
+      !aligned(grad_losses, 4) || !aligned(stats, 4) || !aligned(slope, 4) ||
+      !aligned(seq_offsets, 4) || !aligned(grad_logits, 4))
+    return MXFP4_MOE_ERR_ALIGN;
+  DeviceInfo* d = nullptr;
+  if (int rc = current_device(&d)) return rc;
+  mxmoe::RouterBackwardArgs a = {};
+  a.logits = logits;
+  a.ids = topk_ids;
+  a.dw = grad_weights;
+  a.dloss = grad_losses;
+  a.stats = stats;
+  a.slope = slope;
+  a.offsets = seq_offsets;
+  a.T = T;
+  a.E = E;
+  a.topk = topk;
+  a.scoring = scoring;
+  a.renormalise = renormalise;
+  a.S = n_seq;
+  a.route_scale = route_scale;
+  a.dlogits = grad_logits;
+  return cuda_status(mxmoe::launch_router_backward(a, static_cast<cudaStream_t>(stream)));
+}
+
+int mxfp4_moe_combine_backward(const void* grad_out, const void* routes, const int32_t* topk_ids,
+                               const float* topk_weights, int T, int K, int topk, int expert_base,
+                               int n_experts, float* grad_weights, void* grad_routes,
+                               void* stream) {
+  if (!bf16_rows_ok(T, K) || topk < 1 || topk > 32 || (int64_t)T * topk >= ((int64_t)1 << 31) ||
+      n_experts < 0)
+    return MXFP4_MOE_ERR_SHAPE;
+  if (expert_base < 0) return MXFP4_MOE_ERR_ARG;
+  if (T == 0) return MXFP4_MOE_OK;
+  if (!grad_out || !routes || !grad_weights || (grad_routes && !topk_weights))
+    return MXFP4_MOE_ERR_ARG;
+  if (!aligned(grad_out, 16) || !aligned(routes, 16) || !aligned(topk_ids, 4) ||
+      !aligned(topk_weights, 4) || !aligned(grad_weights, 4) || !aligned(grad_routes, 16))
+    return MXFP4_MOE_ERR_ALIGN;
+  DeviceInfo* d = nullptr;
+  if (int rc = current_device(&d)) return rc;
+  mxmoe::CombineBwdArgs a = {};
+  a.dy = static_cast<const uint16_t*>(grad_out);
+  a.routes = static_cast<const uint16_t*>(routes);
+  a.ids = topk_ids;
+  a.wts = topk_weights;
+  a.T = T;
+  a.K = K;
+  a.topk = topk;
+  a.ebase = expert_base;
+  a.E = n_experts;
+  a.dw = grad_weights;
+  a.droutes = static_cast<uint16_t*>(grad_routes);
+  return cuda_status(mxmoe::launch_combine_backward(a, static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
 constexpr int kLinearMaxDim = 1 << 20;   // tokens and output features
 bool linear_shape_ok(int T, int K, int N) {
   return T >= 0 && T <= kLinearMaxDim && K >= 64 && K <= 16384 && K % 64 == 0 && N >= 8 &&

@@ -10,7 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -72,6 +72,23 @@ def lib() -> ctypes.CDLL:
     L.mxfp4_moe_router_scored.argtypes = [vp, vp, i32, i32, i32, i32, i32, i32, i32, i32, f32,
                                           vp, vp, vp]
     L.mxfp4_moe_router_scored.restype = i32
+    L.mxfp4_moe_sandwich_norm.argtypes = [vp] * 5 + [i32, i32, vp, i32, i32, f32, i32, i32] + [vp] * 10
+    L.mxfp4_moe_sandwich_norm.restype = i32
+    L.mxfp4_moe_sandwich_norm_backward_workspace_size.argtypes = [i32, i32]
+    L.mxfp4_moe_sandwich_norm_backward_workspace_size.restype = sz
+    L.mxfp4_moe_sandwich_norm_backward.argtypes = [vp] * 10 + [i32, i32, vp, vp, i32, i32] + \
+        [vp] * 7 + [sz, vp]
+    L.mxfp4_moe_sandwich_norm_backward.restype = i32
+    L.mxfp4_moe_router_balance_workspace_size.argtypes = [i32] * 3
+    L.mxfp4_moe_router_balance_workspace_size.restype = sz
+    L.mxfp4_moe_router_balance.argtypes = [vp, vp, i32, i32, i32, i32, vp, i32, vp, vp, vp, vp, vp,
+                                           sz, vp]
+    L.mxfp4_moe_router_balance.restype = i32
+    L.mxfp4_moe_router_backward.argtypes = [vp, vp, vp, i32, i32, i32, i32, i32, f32, vp, vp, vp, vp,
+                                            i32, vp, vp]
+    L.mxfp4_moe_router_backward.restype = i32
+    L.mxfp4_moe_combine_backward.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, vp]
+    L.mxfp4_moe_combine_backward.restype = i32
     L.mxfp4_moe_linear_workspace_size.argtypes = [i32] * 5
     L.mxfp4_moe_linear_workspace_size.restype = sz
     L.mxfp4_moe_linear.argtypes = [vp, vp, vp, vp, i32, i32, i32, vp, vp, vp, vp, i32, i32,
@@ -518,6 +535,340 @@ def router_scored(logits: torch.Tensor, topk: int, scoring: str = "sigmoid",
     if rc:
         raise MoEError(rc, "mxfp4_moe_router_scored")
     return topk_ids, topk_weights
+
+
+def _given(t: Optional[torch.Tensor], name: str, dtype, shape):
+    """``_need`` and the shape, for a tensor that may be left out."""
+    if t is not None:
+        _need(t, name, dtype, len(shape))
+        if t.shape != shape:
+            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _together(*tensors):
+    """One device for all of them, the current one: the library launches there."""
+    dev = torch._C._cuda_getDevice()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("all tensors must be on the current CUDA device")
+
+
+def _scratch(nbytes: int, workspace: Optional[torch.Tensor], device, stream) -> torch.Tensor:
+    if workspace is None:
+        return _empty(nbytes, torch.uint8, device, stream)
+    _need(workspace, "workspace", torch.uint8, 1)
+    return workspace
+
+
+GATE_ACTS = {"linear": 0, "sigmoid": 1}
+
+
+def _gate(gate: Optional[torch.Tensor], gate_act: str, T: int, K: int):
+    """(kind, activation) of a gate: bf16 [1, K], fp32 [T, 1] or bf16 [T, K]."""
+    if gate_act not in GATE_ACTS:
+        raise ValueError(f"gate_act must be one of {sorted(GATE_ACTS)}")
+    if gate is None:
+        return 0, GATE_ACTS[gate_act]
+    if not isinstance(gate, torch.Tensor):
+        raise TypeError("gate must be a torch.Tensor")
+    if gate.dtype == torch.float32:
+        _given(gate, "gate (fp32)", torch.float32, (T, 1))
+        return 2, GATE_ACTS[gate_act]
+    _need(gate, "gate", torch.bfloat16, 2)
+    if gate.shape[1] != K or gate.shape[0] not in (1, T):
+        raise ValueError("gate must be bf16 [1, K], bf16 [T, K] or fp32 [T, 1]")
+    return (1 if gate.shape[0] == 1 else 3), GATE_ACTS[gate_act]
+
+
+class SandwichNorm(NamedTuple):
+    """What ``sandwich_norm`` returns; what was not asked for is None."""
+    y: Optional[torch.Tensor]            # bf16 [T, K]
+    h: torch.Tensor                      # bf16 [T, K], the new residual stream
+    q: Optional[torch.Tensor]            # y in MXFP8: E4M3 [T, K] ...
+    q_scale: Optional[torch.Tensor]      # ... and E8M0 bytes [T, K/32]
+    rstd: Optional[torch.Tensor]         # fp32 [2, T], both norms' factors
+    x8: Optional[torch.Tensor]           # x and h in MXFP8, for the backward pass
+    x8_scale: Optional[torch.Tensor]
+    h8: Optional[torch.Tensor]
+    h8_scale: Optional[torch.Tensor]
+
+
+def sandwich_norm(x: torch.Tensor, residual: torch.Tensor, post_gamma: Optional[torch.Tensor] = None,
+                  pre_gamma: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+                  gate_act: str = "linear", residual_scale: Optional[torch.Tensor] = None,
+                  eps: float = 1e-5, out8: Optional[str] = None, bf16: bool = True,
+                  checkpoint8: Optional[str] = None, rstd: bool = False,
+                  residual_out: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                  stream=None) -> SandwichNorm:
+    """The norm after a block, its gate, the scaled residual and the next block's norm, for bf16 rows
+    [T, K]: n = x * rsqrt(mean(x^2) + eps) * post_gamma, h = residual_scale * residual + g * n,
+    y = h * rsqrt(mean(h^2) + eps) * pre_gamma.
+
+    Without post_gamma n = x; without pre_gamma there is no y. gate: bf16 [1, K] (a
+    channel's), fp32 [T, 1] (a token's) or bf16 [T, K]; with one row a bf16 gate is a channel's.
+    g is the gate, or its sigmoid with gate_act "sigmoid". residual_scale fp32 [1]. residual_out
+    may be x or residual. out8 and bf16 as in ``add_rmsnorm``. For
+    ``sandwich_norm_backward``: rstd True keeps both norms' factors, checkpoint8 "ocp" or "nosat"
+    writes x and the unrounded h in MXFP8 beside the rest."""
+    _need(x, "x", torch.bfloat16, 2)
+    shape = x.shape
+    T, K = shape
+    _need(residual, "residual", torch.bfloat16, 2)
+    if residual.shape != shape:
+        raise ValueError("residual must be [T, K]")
+    _given(post_gamma, "post_gamma", torch.bfloat16, (K,))
+    _given(pre_gamma, "pre_gamma", torch.bfloat16, (K,))
+    _given(residual_scale, "residual_scale", torch.float32, (1,))
+    _given(residual_out, "residual_out", torch.bfloat16, shape)
+    kind, act = _gate(gate, gate_act, T, K)
+    for name, rule in (("out8", out8), ("checkpoint8", checkpoint8)):
+        if rule is not None and rule not in MX8_RULES:
+            raise ValueError(f"{name} must be None or one of {sorted(MX8_RULES)}")
+    if pre_gamma is None:
+        if out8 is not None or out is not None:
+            raise ValueError("out and out8 need pre_gamma")
+        bf16 = False
+    if out is not None:
+        if not bf16:
+            raise ValueError("out is not written when bf16 is False")
+        _given(out, "out", torch.bfloat16, shape)
+    _together(x, residual, post_gamma, pre_gamma, gate, residual_scale, residual_out, out)
+    dev = x.device
+    if residual_out is None:
+        residual_out = _empty(shape, torch.bfloat16, dev, stream)
+    if out is None and bf16:
+        out = _empty(shape, torch.bfloat16, dev, stream)
+    mx8 = lambda: (_empty(shape, torch.float8_e4m3fn, dev, stream),
+                   _empty((T, K // 32), torch.uint8, dev, stream))
+    q, qs = mx8() if out8 is not None else (None, None)
+    (x8, xs), (h8, hs) = (mx8(), mx8()) if checkpoint8 is not None else ((None, None), (None, None))
+    r = _empty((2, T), torch.float32, dev, stream) if rstd else None
+    rc = lib().mxfp4_moe_sandwich_norm(
+        _addr(x), _addr(residual), _addr(post_gamma), _addr(pre_gamma), _addr(gate), kind, act,
+        _addr(residual_scale), T, K, eps, MX8_RULES[out8 or "ocp"], MX8_RULES[checkpoint8 or "ocp"],
+        _addr(residual_out), _addr(out), _addr(q), _addr(qs), _addr(x8), _addr(xs), _addr(h8),
+        _addr(hs), _addr(r), _raw_stream(stream))
+    if rc:
+        raise MoEError(rc, "mxfp4_moe_sandwich_norm")
+    return SandwichNorm(out, residual_out, q, qs, r, x8, xs, h8, hs)
+
+
+class SandwichNormGrads(NamedTuple):
+    """What ``sandwich_norm_backward`` returns; None where the forward call had no such input."""
+    x: torch.Tensor                           # bf16 [T, K]
+    residual: torch.Tensor                    # bf16 [T, K]
+    post_gamma: Optional[torch.Tensor]        # fp32 [K]
+    pre_gamma: Optional[torch.Tensor]         # fp32 [K]
+    gate: Optional[torch.Tensor]              # fp32 [1, K], fp32 [T, 1] or bf16 [T, K]
+    residual_scale: Optional[torch.Tensor]    # fp32 [1], where residual was given
+
+
+def sandwich_norm_backward_workspace_size(T: int, K: int) -> int:
+    """Bytes of scratch that ``sandwich_norm_backward`` needs; 0 also for sizes it does not take."""
+    return int(lib().mxfp4_moe_sandwich_norm_backward_workspace_size(T, K))
+
+
+def sandwich_norm_backward(grad_h: Optional[torch.Tensor], grad_y: Optional[torch.Tensor],
+                           x: torch.Tensor, h: Optional[torch.Tensor], rstd: Optional[torch.Tensor],
+                           post_gamma: Optional[torch.Tensor] = None,
+                           pre_gamma: Optional[torch.Tensor] = None,
+                           gate: Optional[torch.Tensor] = None, gate_act: str = "linear",
+                           residual: Optional[torch.Tensor] = None,
+                           residual_scale: Optional[torch.Tensor] = None,
+                           x_scale: Optional[torch.Tensor] = None,
+                           h_scale: Optional[torch.Tensor] = None,
+                           grad_x: Optional[torch.Tensor] = None,
+                           grad_residual: Optional[torch.Tensor] = None,
+                           workspace: Optional[torch.Tensor] = None,
+                           stream=None) -> SandwichNormGrads:
+    """Gradient of ``sandwich_norm`` from the gradients of its h and y (bf16 [T, K], either None) and
+    from what it kept: x and h in bf16, or as x8 / h8 with x_scale / h_scale, and rstd [2, T]. h is
+    needed with grad_y, rstd with grad_y or post_gamma. gate, gate_act, gammas and residual_scale as
+    in the forward call; with residual (its bf16 rows) residual_scale gets a gradient too.
+    grad_x and grad_residual may be given as outputs that overlap no input."""
+    _need(x, "x", torch.bfloat16 if x_scale is None else torch.float8_e4m3fn, 2)
+    shape = x.shape
+    T, K = shape
+    if grad_h is None and grad_y is None:
+        raise ValueError("grad_h or grad_y is needed")
+    _given(grad_h, "grad_h", torch.bfloat16, shape)
+    _given(post_gamma, "post_gamma", torch.bfloat16, (K,))
+    _given(pre_gamma, "pre_gamma", torch.bfloat16, (K,))
+    if grad_y is not None:
+        _given(grad_y, "grad_y", torch.bfloat16, shape)
+        if pre_gamma is None or h is None:
+            raise ValueError("grad_y needs pre_gamma and h")
+    _given(h, "h", torch.bfloat16 if h_scale is None else torch.float8_e4m3fn, shape)
+    _given(x_scale, "x_scale", torch.uint8, (T, K // 32))
+    _given(h_scale, "h_scale", torch.uint8, (T, K // 32))
+    if h is None and h_scale is not None:
+        raise ValueError("h_scale needs h")
+    if rstd is None:
+        if grad_y is not None or post_gamma is not None:
+            raise ValueError("rstd is needed with grad_y or post_gamma")
+    else:
+        _given(rstd, "rstd", torch.float32, (2, T))
+    _given(residual_scale, "residual_scale", torch.float32, (1,))
+    if residual is not None:
+        if residual_scale is None:
+            raise ValueError("residual is read for residual_scale's gradient")
+        _given(residual, "residual", torch.bfloat16, shape)
+    _given(grad_x, "grad_x", torch.bfloat16, shape)
+    _given(grad_residual, "grad_residual", torch.bfloat16, shape)
+    kind, act = _gate(gate, gate_act, T, K)
+    _together(grad_h, grad_y, x, h, rstd, post_gamma, pre_gamma, gate, residual, residual_scale,
+              x_scale, h_scale, grad_x, grad_residual, workspace)
+    dev = x.device
+    if grad_x is None:
+        grad_x = _empty(shape, torch.bfloat16, dev, stream)
+    if grad_residual is None:
+        grad_residual = _empty(shape, torch.bfloat16, dev, stream)
+    f32 = lambda *n: _empty(n, torch.float32, dev, stream)
+    dpost = f32(K) if post_gamma is not None else None
+    dpre = f32(K) if pre_gamma is not None else None
+    dgate = (None, lambda: f32(1, K), lambda: f32(T, 1),
+             lambda: _empty(shape, torch.bfloat16, dev, stream))[kind]
+    dgate = dgate() if dgate else None
+    dscale = f32(1) if residual is not None else None
+    L = lib()
+    ws = _scratch(L.mxfp4_moe_sandwich_norm_backward_workspace_size(T, K), workspace, dev, stream)
+    rc = L.mxfp4_moe_sandwich_norm_backward(
+        _addr(grad_h), _addr(grad_y), x.data_ptr(), _addr(x_scale), _addr(h), _addr(h_scale),
+        _addr(rstd), _addr(post_gamma), _addr(pre_gamma), _addr(gate), kind, act, _addr(residual),
+        _addr(residual_scale), T, K, grad_x.data_ptr(), grad_residual.data_ptr(), _addr(dpost),
+        _addr(dpre), _addr(dgate), _addr(dscale), ws.data_ptr(), ws.numel(), _raw_stream(stream))
+    if rc:
+        raise MoEError(rc, "mxfp4_moe_sandwich_norm_backward")
+    return SandwichNormGrads(grad_x, grad_residual, dpost, dpre, dgate, dscale)
+
+
+class RouterBalance(NamedTuple):
+    """What ``router_balance`` returns."""
+    stats: torch.Tensor     # fp32 [4]: balance loss, z loss, tokens, sequences with tokens
+    counts: torch.Tensor    # int32 [S, E], routes to each expert
+    prob: torch.Tensor      # fp32 [S, E], mean normalised score
+    slope: torch.Tensor     # fp32 [S, E], a sequence's loss by a token's normalised score
+
+
+def router_balance_workspace_size(T: int, E: int, n_seq: int = 1) -> int:
+    """Bytes of scratch that ``router_balance`` needs; 0 for sizes it does not take."""
+    return int(lib().mxfp4_moe_router_balance_workspace_size(T, E, n_seq))
+
+
+def _routing(logits, topk_ids, scoring, seq_offsets):
+    _need(logits, "logits", torch.float32, 2)
+    _need(topk_ids, "topk_ids", torch.int32, 2)
+    T, E = logits.shape
+    if topk_ids.shape[0] != T:
+        raise ValueError("topk_ids must be [T, topk]")
+    if scoring not in SCORES:
+        raise ValueError(f"scoring must be one of {sorted(SCORES)}")
+    S = 1
+    if seq_offsets is not None:
+        _need(seq_offsets, "seq_offsets", torch.int32, 1)
+        S = seq_offsets.shape[0] - 1
+        if S < 1:
+            raise ValueError("seq_offsets must be [S + 1]")
+    return T, E, topk_ids.shape[1], S
+
+
+def router_balance(logits: torch.Tensor, topk_ids: torch.Tensor, scoring: str = "sigmoid",
+                   seq_offsets: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None, stream=None) -> RouterBalance:
+    """Expert counts and balance losses of a routing (``router_scored``'s ids on fp32 logits [T, E]).
+
+    p is a token's scores over their sum. A sequence's loss is E * sum_e (its share of the routes
+    that went to e) * (its tokens' mean p_e), 1 for an even routing; stats[0] is the mean over the
+    sequences, stats[1] the mean over tokens of logsumexp(logits)^2. seq_offsets int32 [S + 1]: rows
+    of sequence i are seq_offsets[i] up to seq_offsets[i + 1] (not decreasing), None: one of all rows.
+    Rows without an id in [0, E) (padding) or with every logit masked (NaN, -inf) do not count."""
+    T, E, k, S = _routing(logits, topk_ids, scoring, seq_offsets)
+    _together(logits, topk_ids, seq_offsets, workspace)
+    dev = logits.device
+    stats = _empty(4, torch.float32, dev, stream)
+    counts = _empty((S, E), torch.int32, dev, stream)
+    prob = _empty((S, E), torch.float32, dev, stream)
+    slope = _empty((S, E), torch.float32, dev, stream)
+    L = lib()
+    ws = _scratch(L.mxfp4_moe_router_balance_workspace_size(T, E, S), workspace, dev, stream)
+    rc = L.mxfp4_moe_router_balance(logits.data_ptr(), topk_ids.data_ptr(), T, E, k, SCORES[scoring],
+                                    _addr(seq_offsets), S, stats.data_ptr(), counts.data_ptr(),
+                                    prob.data_ptr(), slope.data_ptr(), ws.data_ptr(), ws.numel(),
+                                    _raw_stream(stream))
+    if rc:
+        raise MoEError(rc, "mxfp4_moe_router_balance")
+    return RouterBalance(stats, counts, prob, slope)
+
+
+def router_backward(logits: torch.Tensor, topk_ids: torch.Tensor,
+                    grad_weights: Optional[torch.Tensor] = None, scoring: str = "sigmoid",
+                    renormalise: bool = True, route_scale: float = 1.0,
+                    grad_losses: Optional[torch.Tensor] = None, stats: Optional[torch.Tensor] = None,
+                    slope: Optional[torch.Tensor] = None,
+                    seq_offsets: Optional[torch.Tensor] = None,
+                    grad_logits: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Gradient fp32 [T, E] of the logits: of ``router_scored``'s weights for the ids it chose, by
+    grad_weights fp32 [T, topk], and of ``router_balance``'s two losses, by grad_losses fp32 [2] with
+    that call's stats, slope and seq_offsets. Ids outside [0, E) and masked experts take no part;
+    rows without a valid id get zeros. scoring, renormalise and route_scale as in ``router_scored``."""
+    T, E, k, S = _routing(logits, topk_ids, scoring, seq_offsets)
+    if grad_weights is None and grad_losses is None:
+        raise ValueError("grad_weights or grad_losses is needed")
+    _given(grad_weights, "grad_weights", torch.float32, (T, k))
+    if grad_losses is not None:
+        if stats is None or slope is None:
+            raise ValueError("grad_losses need stats and slope")
+        _given(grad_losses, "grad_losses", torch.float32, (2,))
+        _given(stats, "stats", torch.float32, (4,))
+        _given(slope, "slope", torch.float32, (S, E))
+    _given(grad_logits, "grad_logits", torch.float32, (T, E))
+    _together(logits, topk_ids, grad_weights, grad_losses, stats, slope, seq_offsets, grad_logits)
+    if grad_logits is None:
+        grad_logits = _empty((T, E), torch.float32, logits.device, stream)
+    rc = lib().mxfp4_moe_router_backward(
+        logits.data_ptr(), topk_ids.data_ptr(), _addr(grad_weights), T, E, k, SCORES[scoring],
+        int(bool(renormalise)), route_scale, _addr(grad_losses), _addr(stats), _addr(slope),
+        _addr(seq_offsets), S, grad_logits.data_ptr(), _raw_stream(stream))
+    if rc:
+        raise MoEError(rc, "mxfp4_moe_router_backward")
+    return grad_logits
+
+
+def combine_backward(grad_out: torch.Tensor, routes: torch.Tensor,
+                     topk_ids: Optional[torch.Tensor] = None,
+                     topk_weights: Optional[torch.Tensor] = None, routes_too: bool = False,
+                     expert_base: int = 0, n_experts: int = 0,
+                     grad_routes: Optional[torch.Tensor] = None, stream=None):
+    """Gradient of y_t = sum_j w_tj o_tj by its weights and its routes' outputs o, bf16 [T * topk, K]
+    (``forward_window(per_route=True)``): (fp32 [T, topk], and with routes_too bf16 [T * topk, K],
+    else None). topk is topk_ids' or topk_weights' second size. Routes with a negative id, or
+    outside expert_base .. expert_base + n_experts - 1 when n_experts is not 0, are skipped: gradients
+    0. topk_weights fp32 [T, topk] are needed with routes_too only."""
+    _need(grad_out, "grad_out", torch.bfloat16, 2)
+    _need(routes, "routes", torch.bfloat16, 2)
+    T, K = grad_out.shape
+    if topk_ids is None and topk_weights is None:
+        raise ValueError("topk_ids or topk_weights are needed")
+    k = (topk_ids if topk_ids is not None else topk_weights).shape[-1]
+    _given(topk_ids, "topk_ids", torch.int32, (T, k))
+    _given(topk_weights, "topk_weights", torch.float32, (T, k))
+    _given(routes, "routes", torch.bfloat16, (T * k, K))
+    if grad_routes is not None:
+        routes_too = True
+        _given(grad_routes, "grad_routes", torch.bfloat16, (T * k, K))
+    if routes_too and topk_weights is None:
+        raise ValueError("routes_too needs topk_weights")
+    _together(grad_out, routes, topk_ids, topk_weights, grad_routes)
+    dev = grad_out.device
+    dw = _empty((T, k), torch.float32, dev, stream)
+    if routes_too and grad_routes is None:
+        grad_routes = _empty((T * k, K), torch.bfloat16, dev, stream)
+    rc = lib().mxfp4_moe_combine_backward(
+        grad_out.data_ptr(), routes.data_ptr(), _addr(topk_ids), _addr(topk_weights), T, K, k,
+        int(expert_base), int(n_experts), dw.data_ptr(), _addr(grad_routes), _raw_stream(stream))
+    if rc:
+        raise MoEError(rc, "mxfp4_moe_combine_backward")
+    return dw, grad_routes
 
 
 def linear_workspace_size(T: int, K: int, N: int, rank: int = 0, x_is_mxfp8: bool = False) -> int:
