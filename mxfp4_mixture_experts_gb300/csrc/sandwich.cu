@@ -17,6 +17,7 @@
 // so that one pass over the row and one sum over the CTA give all of it. Every
 // sum is fp32; what is rounded to bf16 is rounded once, on its way out.
 #include <cstdint>
+#include <mutex>
 
 #include "ops.h"
 #include "rows.cuh"
@@ -25,6 +26,7 @@ namespace mxmoe {
 namespace {
 
 constexpr int kSwThreads = 512;   // most threads of a row
+constexpr int kSwRingBytes = 224 * 1024;   // shared memory of a gradient call, beside 448 bytes of sums
 
 __device__ __forceinline__ float gate_value(float g, int act) {
   return act ? __frcp_rn(__fadd_rn(1.f, expf(-g))) : g;
@@ -51,6 +53,31 @@ __device__ __forceinline__ void cta_sums(float (&v)[N], float (*part)[16], int l
     for (int n = 0; n < N; ++n) v[n] += __shfl_xor_sync(0xffffffffu, v[n], o);
 #pragma unroll
   for (int n = 0; n < N; ++n) v[n] = __shfl_sync(0xffffffffu, v[n], 0);
+}
+
+// The same over a team of nt threads of a CTA of at most 16 warps (its own named
+// barrier, none for one warp); part: [N][16], a place a warp of the CTA.
+template <int N>
+__device__ __forceinline__ void team_sums(float (&v)[N], float (*part)[16], int team, int nt, int lane, int warp,
+                                          int warps) {
+  const int base = team * warps;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int n = 0; n < N; ++n) v[n] += __shfl_xor_sync(0xffffffffu, v[n], o);
+  if (warps == 1) return;
+  if (lane == 0) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) part[n][base + warp] = v[n];
+  }
+  named_barrier(team + 1, nt);
+  // both halves of the warp hold the same 16 parts
+#pragma unroll
+  for (int n = 0; n < N; ++n) v[n] = (lane & 15) < warps ? part[n][base + (lane & 15)] : 0.f;
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+    for (int n = 0; n < N; ++n) v[n] += __shfl_xor_sync(0xffffffffu, v[n], o);
 }
 
 // CH: 16-byte chunks per thread (K / 8 <= CH * blockDim.x).
@@ -176,180 +203,324 @@ __global__ void __launch_bounds__(kSwThreads) sandwich_norm_kernel(const Sandwic
 }
 
 // ---------------------------------------------------------------- gradient
-// 8 values of a row in bf16, or in E4M3 with the row's scale bytes.
-__device__ __forceinline__ void load8(const void* rows, const uint8_t* scale, size_t t, int K, int c, float (&v)[8]) {
-  if (scale == nullptr) {
-    unpack8(ld_row16(static_cast<const uint16_t*>(rows) + t * K + 8 * c), v);
+__device__ __forceinline__ float2 dup(float v) { return make_float2(v, v); }
+__device__ __forceinline__ void unpack4(const uint4& u, float2 (&v)[4]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    v[j] = make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u));
+}
+__device__ __forceinline__ uint4 pack4(const float2 (&v)[4]) {
+  return make_uint4(bf16x2_rn(v[0].x, v[0].y), bf16x2_rn(v[1].x, v[1].y), bf16x2_rn(v[2].x, v[2].y),
+                    bf16x2_rn(v[3].x, v[3].y));
+}
+// 8 values from shared memory: bf16, or E4M3 with their block's scale byte.
+__device__ __forceinline__ void slot8(const uint8_t* p, bool e4m3, uint32_t scale, float2 (&v)[4]) {
+  if (!e4m3) {
+    unpack4(*reinterpret_cast<const uint4*>(p), v);
     return;
   }
-  const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(rows) + t * K + 8 * c);
-  const float f = e8m0_to_f32(scale[t * (K / 32) + (c >> 2)]);
-  const uint32_t w[2] = {q.x, q.y};
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float2 p = e4m3x2_values((uint16_t)(w[j >> 1] >> (16 * (j & 1))));
-    v[2 * j] = p.x * f;
-    v[2 * j + 1] = p.y * f;
-  }
+  const uint2 q = *reinterpret_cast<const uint2*>(p);
+  const float2 f = dup(e8m0_to_f32(scale));
+  v[0] = __fmul2_rn(e4m3x2_values((uint16_t)q.x), f);
+  v[1] = __fmul2_rn(e4m3x2_values((uint16_t)(q.x >> 16)), f);
+  v[2] = __fmul2_rn(e4m3x2_values((uint16_t)q.y), f);
+  v[3] = __fmul2_rn(e4m3x2_values((uint16_t)(q.y >> 16)), f);
 }
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy8(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+// All but the latest n (0..3) groups of this thread's copies have landed.
+__device__ __forceinline__ void copies_wait(int n) {
+  if (n == 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
+  else if (n == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else if (n == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+  else asm volatile("cp.async.wait_group 3;" ::: "memory");
+}
+
+// Shared memory of the gradient: a channel gate's values, then for every team a
+// ring of rows. A thread fills and reads its own slots alone.
+struct BwdPlan {
+  int nt, teams, depth;   // threads a row, rows at a time, rows of a ring (1..4)
+  int gate_bytes, stage;  // of a team's row
+  int dy, dh, x, h, res, gate;   // its parts (where they are read at all)
+  int smem;
+};
 
 // Column sums of the CTA's rows go to ws [gridDim.x][2][K]: 0 dy * h^, 1 d x^ with
 // d = dn, or dh_total where the gate is a channel's (its gate and post_gamma take
 // their gradients from the one sum). After them ws holds a float a CTA, sum dh_total * res.
-template <int CH>
-__global__ void __launch_bounds__(kSwThreads) sandwich_bwd_kernel(const SandwichBwdArgs a) {
+// GATE 0: none or a token's, 1: a channel's, 2: one for every value.
+template <int CH, int GATE>
+__global__ void __launch_bounds__(kSwThreads, 1)
+    sandwich_bwd_kernel(const SandwichBwdArgs a, const BwdPlan p) {
+  extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float part[2][3][16];
   __shared__ float last[16];
-  const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
+  constexpr bool kHold = CH <= 2;   // gammas stay in registers
+  const int nt = p.nt, team = threadIdx.x / nt, tid = threadIdx.x - team * nt;
+  const int lane = tid & 31, warp = tid >> 5, warps = nt >> 5;
   const int n8 = a.K / 8;
-  const unsigned T = (unsigned)a.T;
+  const unsigned T = (unsigned)a.T;   // unsigned: T + the step may pass 2^31
+  const unsigned step = gridDim.x * p.teams;
   const float scale = a.rscale != nullptr ? *a.rscale : 1.f;
   const uint16_t* gate16 = static_cast<const uint16_t*>(a.gate);
-  float s_pre[CH][8], s_x[CH][8], s_res = 0.f;
+  const bool has_dy = a.dy != nullptr, has_dh = a.dh != nullptr, has_post = a.post != nullptr;
+  const bool x8 = a.xs != nullptr, h8 = a.hs != nullptr, has_res = a.dscale != nullptr;
+  uint8_t* ring = smem + p.gate_bytes + (size_t)team * p.depth * p.stage;
+  const uint32_t ring_addr = smem_u32(ring);
+  float4* gch = reinterpret_cast<float4*>(smem);   // [K / 4]
+  uint4 gp[kHold ? CH : 1], gn[kHold ? CH : 1];
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int c = tid + i * nt;
+    if (kHold) gp[i] = gn[i] = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);   // 1
+    if (c >= n8) continue;
+    if (kHold && has_post) gp[i] = ld_row16(a.post + 8 * c);
+    if (kHold && has_dy) gn[i] = ld_row16(a.pre + 8 * c);
+    if (GATE == 1 && team == 0) {
+      float g[8];
+      unpack8(ld_row16(gate16 + 8 * c), g);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) g[j] = gate_value(g[j], a.gate_act);
+      gch[2 * c] = make_float4(g[0], g[1], g[2], g[3]);
+      gch[2 * c + 1] = make_float4(g[4], g[5], g[6], g[7]);
+    }
+  }
+  if (GATE == 1) __syncthreads();
+  auto post_of = [&](int i, int c, float2 (&v)[4]) {
+    if (kHold) unpack4(gp[kHold ? i : 0], v);
+    else if (has_post) unpack4(ld_row16(a.post + 8 * c), v);
+    else v[0] = v[1] = v[2] = v[3] = dup(1.f);
+  };
+  auto pre_of = [&](int i, int c, float2 (&v)[4]) {
+    if (kHold) unpack4(gn[kHold ? i : 0], v);
+    else unpack4(ld_row16(a.pre + 8 * c), v);
+  };
+  auto fetch = [&](unsigned t, int st) {
+    if (t < T) {
+      const size_t row = (size_t)t * a.K;
+      const uint32_t base = ring_addr + st * p.stage;
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        const int c = tid + i * nt;
+        if (c >= n8) continue;
+        const size_t at = row + 8 * c;
+        if (has_dh) copy16(base + p.dh + 16 * c, a.dh + at);
+        if (has_dy) {
+          copy16(base + p.dy + 16 * c, a.dy + at);
+          if (h8) copy8(base + p.h + 8 * c, static_cast<const uint8_t*>(a.h) + at);
+          else copy16(base + p.h + 16 * c, static_cast<const uint16_t*>(a.h) + at);
+        }
+        if (x8) copy8(base + p.x + 8 * c, static_cast<const uint8_t*>(a.x) + at);
+        else copy16(base + p.x + 16 * c, static_cast<const uint16_t*>(a.x) + at);
+        if (has_res) copy16(base + p.res + 16 * c, a.residual + at);
+        if (GATE == 2) copy16(base + p.gate + 16 * c, gate16 + at);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  // what is not worth a slot: the row's factors and scale bytes, one row ahead
+  struct RowScalars {
+    float r1, r2, g;
+    uint32_t xs[CH], hs[CH];
+  };
+  auto scalars = [&](unsigned t, RowScalars& r) {
+    if (t >= T) return;
+    r.r1 = has_post ? __ldg(a.rstd + t) : 1.f;
+    r.r2 = has_dy ? __ldg(a.rstd + (size_t)T + t) : 0.f;
+    r.g = GATE == 0 && a.gate_kind == 2 ? __ldg(static_cast<const float*>(a.gate) + t) : 1.f;
+    if (x8 || h8) {
+      const size_t row = (size_t)t * (a.K / 32);
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        const int c = tid + i * nt;
+        if (c >= n8) continue;
+        if (x8) r.xs[i] = __ldg(a.xs + row + (c >> 2));
+        if (h8 && has_dy) r.hs[i] = __ldg(a.hs + row + (c >> 2));
+      }
+    }
+  };
+  float2 s_pre[CH][4], s_x[CH][4], s_res = dup(0.f);
 #pragma unroll
   for (int i = 0; i < CH; ++i)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) s_pre[i][j] = s_x[i][j] = 0.f;
-  int odd = 0;
-  for (unsigned t = blockIdx.x; t < T; t += gridDim.x, odd ^= 1) {
+    for (int j = 0; j < 4; ++j) s_pre[i][j] = s_x[i][j] = dup(0.f);
+  const unsigned first = blockIdx.x * p.teams + team;
+  RowScalars now = {}, next = {};
+  scalars(first, next);
+  for (int d = 0; d < p.depth; ++d) fetch(first + d * step, d);
+  const float inv_k = 1.f / (float)a.K;
+  int odd = 0, st = 0;
+  for (unsigned t = first; t < T; t += step, odd ^= 1) {
     const size_t row = (size_t)t * a.K;
-    const float r1 = a.post != nullptr ? a.rstd[t] : 1.f;
-    const float r2 = a.pre != nullptr ? a.rstd[(size_t)T + t] : 0.f;
-    const float g_raw = a.gate_kind == 2 ? static_cast<const float*>(a.gate)[t] : 1.f;
-    const float gt = a.gate_kind == 2 ? gate_value(g_raw, a.gate_act) : 1.f;
-    float s[3] = {0.f, 0.f, 0.f};   // v h, w x (dh + r2 v), w x h; w without a token's gate
+    now = next;
+    scalars(t + step, next);
+    const float r1 = now.r1, r2 = now.r2;
+    const float gt = GATE == 0 && a.gate_kind == 2 ? gate_value(now.g, a.gate_act) : 1.f;
+    copies_wait(p.depth - 1);
+    const uint8_t* slot = ring + st * p.stage;
+    float2 s2[3] = {dup(0.f), dup(0.f), dup(0.f)};   // v h, w x (dh + r2 v), w x h; w without a token's gate
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const int c = tid + i * nt;
       if (c >= n8) continue;
-      float q[8], h[8], w[8], x[8];
+      float2 q[4], h[4], w[4], x[4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) q[j] = h[j] = 0.f;
-      if (a.dh != nullptr) unpack8(ld_row16(a.dh + row + 8 * c), q);
-      if (a.dy != nullptr) {
-        float v[8], g[8];
-        unpack8(ld_row16(a.dy + row + 8 * c), v);
-        unpack8(ld_row16(a.pre + 8 * c), g);
-        load8(a.h, a.hs, t, a.K, c, h);
+      for (int j = 0; j < 4; ++j) q[j] = h[j] = dup(0.f);
+      if (has_dh) unpack4(*reinterpret_cast<const uint4*>(slot + p.dh + 16 * c), q);
+      if (has_dy) {
+        float2 v[4], g[4];
+        unpack4(*reinterpret_cast<const uint4*>(slot + p.dy + 16 * c), v);
+        pre_of(i, c, g);
+        slot8(slot + p.h + (h8 ? 8 : 16) * c, h8, now.hs[i], h);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          v[j] *= g[j];
-          s[0] = fmaf(v[j], h[j], s[0]);
-          q[j] = fmaf(r2, v[j], q[j]);
+        for (int j = 0; j < 4; ++j) {
+          s_pre[i][j] = __ffma2_rn(v[j], __fmul2_rn(h[j], dup(r2)), s_pre[i][j]);
+          v[j] = __fmul2_rn(v[j], g[j]);
+          s2[0] = __ffma2_rn(v[j], h[j], s2[0]);
+          q[j] = __ffma2_rn(dup(r2), v[j], q[j]);
         }
       }
-      load8(a.x, a.xs, t, a.K, c, x);
-      if (a.post != nullptr) unpack8(ld_row16(a.post + 8 * c), w);
-      else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = 1.f;
+      slot8(slot + p.x + (x8 ? 8 : 16) * c, x8, now.xs[i], x);
+      post_of(i, c, w);
+      if (GATE == 1) {
+        const float4 g0 = gch[2 * c], g1 = gch[2 * c + 1];
+        w[0] = __fmul2_rn(w[0], make_float2(g0.x, g0.y));
+        w[1] = __fmul2_rn(w[1], make_float2(g0.z, g0.w));
+        w[2] = __fmul2_rn(w[2], make_float2(g1.x, g1.y));
+        w[3] = __fmul2_rn(w[3], make_float2(g1.z, g1.w));
       }
-      if (a.gate_kind & 1) {
-        float g[8];
-        unpack8(ld_row16(gate16 + (a.gate_kind == 3 ? row : 0) + 8 * c), g);
+      if (GATE == 2) {
+        float2 g[4];
+        unpack4(*reinterpret_cast<const uint4*>(slot + p.gate + 16 * c), g);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] *= gate_value(g[j], a.gate_act);
+        for (int j = 0; j < 4; ++j)
+          w[j] = __fmul2_rn(w[j], make_float2(gate_value(g[j].x, a.gate_act), gate_value(g[j].y, a.gate_act)));
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float wx = w[j] * x[j];
-        s[1] = fmaf(wx, q[j], s[1]);
-        s[2] = fmaf(wx, h[j], s[2]);
+      for (int j = 0; j < 4; ++j) {
+        const float2 wx = __fmul2_rn(w[j], x[j]);
+        s2[1] = __ffma2_rn(wx, q[j], s2[1]);
+        s2[2] = __ffma2_rn(wx, h[j], s2[2]);
       }
     }
-    cta_sums<3>(s, part[odd], lane, warp, nt >> 5);
-    const float inv_k = 1.f / (float)a.K;
+    float s[3] = {s2[0].x + s2[0].y, s2[1].x + s2[1].y, s2[2].x + s2[2].y};
+    team_sums<3>(s, part[odd], team, nt, lane, warp, warps);
     const float c2 = s[0] * r2 * inv_k * r2;              // r2 mean(v h^)
     const float dot = r1 * (s[1] - c2 * (r2 * s[2]));     // sum of w x^ dh_total
-    const float c1 = a.post != nullptr ? gt * dot * inv_k : 0.f;
-    if (a.gate_kind == 2 && a.dgate != nullptr && tid == 0)
-      static_cast<float*>(a.dgate)[t] = a.gate_act ? dot * gt * gate_value(-g_raw, 1) : dot;
+    const float c1 = has_post ? gt * dot * inv_k : 0.f;
+    if (GATE == 0 && a.gate_kind == 2 && a.dgate != nullptr && tid == 0)
+      static_cast<float*>(a.dgate)[t] = a.gate_act ? dot * gt * gate_value(-now.g, 1) : dot;
+    const float2 kh = dup(-c2 * r2), k1 = dup(-r1 * r1 * c1), xr = dup(r1 * gt);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const int c = tid + i * nt;
       if (c >= n8) continue;
-      float d[8], x[8];   // dh_total
+      float2 d[4], x[4], w[4];   // d: dh_total
 #pragma unroll
-      for (int j = 0; j < 8; ++j) d[j] = 0.f;
-      if (a.dh != nullptr) unpack8(ld_row16(a.dh + row + 8 * c), d);
-      if (a.dy != nullptr) {
-        float v[8], g[8], h[8];
-        unpack8(ld_row16(a.dy + row + 8 * c), v);
-        unpack8(ld_row16(a.pre + 8 * c), g);
-        load8(a.h, a.hs, t, a.K, c, h);
+      for (int j = 0; j < 4; ++j) d[j] = dup(0.f);
+      if (has_dh) unpack4(*reinterpret_cast<const uint4*>(slot + p.dh + 16 * c), d);
+      if (has_dy) {
+        float2 v[4], g[4], h[4];
+        unpack4(*reinterpret_cast<const uint4*>(slot + p.dy + 16 * c), v);
+        pre_of(i, c, g);
+        slot8(slot + p.h + (h8 ? 8 : 16) * c, h8, now.hs[i], h);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float hn = h[j] * r2;
-          s_pre[i][j] = fmaf(v[j], hn, s_pre[i][j]);
-          d[j] = fmaf(-c2, hn, fmaf(r2, v[j] * g[j], d[j]));
-        }
+        for (int j = 0; j < 4; ++j)
+          d[j] = __ffma2_rn(kh, h[j], __ffma2_rn(dup(r2), __fmul2_rn(v[j], g[j]), d[j]));
       }
-      if (a.dscale != nullptr) {
-        float z[8];
-        unpack8(ld_row16(a.residual + row + 8 * c), z);
+      if (has_res) {
+        float2 z[4];
+        unpack4(*reinterpret_cast<const uint4*>(slot + p.res + 16 * c), z);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s_res = fmaf(d[j], z[j], s_res);
+        for (int j = 0; j < 4; ++j) s_res = __ffma2_rn(d[j], z[j], s_res);
       }
       if (a.dres != nullptr) {
-        float z[8];
+        float2 z[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) z[j] = d[j] * scale;
-        st_row16(a.dres + row + 8 * c, pack8(z));
+        for (int j = 0; j < 4; ++j) z[j] = __fmul2_rn(d[j], dup(scale));
+        st_row16(a.dres + row + 8 * c, pack4(z));
       }
-      load8(a.x, a.xs, t, a.K, c, x);
+      slot8(slot + p.x + (x8 ? 8 : 16) * c, x8, now.xs[i], x);
+      post_of(i, c, w);
+      // d becomes the gated gradient but for a channel's gate, whose sums take it without
+      if (GATE == 1) {
+        const float4 g0 = gch[2 * c], g1 = gch[2 * c + 1];
+        w[0] = __fmul2_rn(w[0], make_float2(g0.x, g0.y));
+        w[1] = __fmul2_rn(w[1], make_float2(g0.z, g0.w));
+        w[2] = __fmul2_rn(w[2], make_float2(g1.x, g1.y));
+        w[3] = __fmul2_rn(w[3], make_float2(g1.z, g1.w));
+      }
+      if (GATE == 2) {
+        float2 raw[4], o[4];
+        unpack4(*reinterpret_cast<const uint4*>(slot + p.gate + 16 * c), raw);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] *= r1;
-      float g[8], p[8];   // the gate's values; post_gamma
-#pragma unroll
-      for (int j = 0; j < 8; ++j) g[j] = gt, p[j] = 1.f;
-      if (a.post != nullptr) unpack8(ld_row16(a.post + 8 * c), p);
-      if (a.gate_kind & 1) {
-        float raw[8];
-        unpack8(ld_row16(gate16 + (a.gate_kind == 3 ? row : 0) + 8 * c), raw);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) g[j] = gate_value(raw[j], a.gate_act);
-        if (a.gate_kind == 3 && a.dgate != nullptr) {
-          float o[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            o[j] = d[j] * (x[j] * p[j]);
-            if (a.gate_act) o[j] *= g[j] * gate_value(-raw[j], 1);
-          }
-          st_row16(static_cast<uint16_t*>(a.dgate) + row + 8 * c, pack8(o));
+        for (int j = 0; j < 4; ++j) {
+          const float2 g = make_float2(gate_value(raw[j].x, a.gate_act), gate_value(raw[j].y, a.gate_act));
+          o[j] = __fmul2_rn(d[j], __fmul2_rn(__fmul2_rn(x[j], dup(r1)), w[j]));
+          if (a.gate_act)
+            o[j] = __fmul2_rn(o[j], make_float2(g.x * gate_value(-raw[j].x, 1), g.y * gate_value(-raw[j].y, 1)));
+          d[j] = __fmul2_rn(d[j], g);
         }
+        if (a.dgate != nullptr) st_row16(static_cast<uint16_t*>(a.dgate) + row + 8 * c, pack4(o));
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float dn = d[j] * g[j];
-        s_x[i][j] = fmaf(a.gate_kind == 1 ? d[j] : dn, x[j], s_x[i][j]);
-        d[j] = a.post != nullptr ? r1 * fmaf(-c1, x[j], dn * p[j]) : dn;
+      for (int j = 0; j < 4; ++j) {
+        s_x[i][j] = __ffma2_rn(d[j], __fmul2_rn(x[j], xr), s_x[i][j]);
+        const float2 u = __fmul2_rn(d[j], w[j]);
+        d[j] = __ffma2_rn(k1, x[j], __fmul2_rn(u, xr));   // (no post_gamma: r1 = 1, k1 = 0)
       }
-      if (a.dx != nullptr) st_row16(a.dx + row + 8 * c, pack8(d));
+      if (a.dx != nullptr) st_row16(a.dx + row + 8 * c, pack4(d));
     }
+    fetch(t + p.depth * step, st);
+    if (++st == p.depth) st = 0;
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
   float* mine = a.ws + (size_t)blockIdx.x * 2 * a.K;
+  if (p.teams > 1) __syncthreads();
+  // one team: straight to ws; several: through shared memory, added up in order
+  float* to = p.teams > 1 ? reinterpret_cast<float*>(smem) + (size_t)team * 2 * a.K : mine;
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const int c = tid + i * nt;
     if (c >= n8) continue;
 #pragma unroll
-    for (int j = 0; j < 8; j += 4) {
-      *reinterpret_cast<float4*>(mine + 8 * c + j) =
-          make_float4(s_pre[i][j], s_pre[i][j + 1], s_pre[i][j + 2], s_pre[i][j + 3]);
-      *reinterpret_cast<float4*>(mine + a.K + 8 * c + j) =
-          make_float4(s_x[i][j], s_x[i][j + 1], s_x[i][j + 2], s_x[i][j + 3]);
+    for (int j = 0; j < 4; j += 2) {
+      *reinterpret_cast<float4*>(to + 8 * c + 2 * j) =
+          make_float4(s_pre[i][j].x, s_pre[i][j].y, s_pre[i][j + 1].x, s_pre[i][j + 1].y);
+      *reinterpret_cast<float4*>(to + a.K + 8 * c + 2 * j) =
+          make_float4(s_x[i][j].x, s_x[i][j].y, s_x[i][j + 1].x, s_x[i][j + 1].y);
     }
   }
-  if (a.dscale != nullptr) {
+  float sr = s_res.x + s_res.y;
+  if (has_res) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s_res += __shfl_xor_sync(0xffffffffu, s_res, o);
-    if (lane == 0) last[warp] = s_res;
-    __syncthreads();
-    if (tid == 0) {
-      float sum = 0.f;
-      for (int w = 0; w < (nt >> 5); ++w) sum += last[w];
-      a.ws[(size_t)gridDim.x * 2 * a.K + blockIdx.x] = sum;
+    for (int o = 16; o > 0; o >>= 1) sr += __shfl_xor_sync(0xffffffffu, sr, o);
+    if (lane == 0) last[threadIdx.x >> 5] = sr;
+  }
+  __syncthreads();
+  if (p.teams > 1) {
+    const float4* from = reinterpret_cast<const float4*>(smem);
+    for (int e = threadIdx.x; e < a.K / 2; e += blockDim.x) {
+      float4 v = from[e];
+      for (int m = 1; m < p.teams; ++m) {
+        const float4 o = from[(size_t)m * (a.K / 2) + e];
+        v.x += o.x;
+        v.y += o.y;
+        v.z += o.z;
+        v.w += o.w;
+      }
+      reinterpret_cast<float4*>(mine)[e] = v;
     }
+  }
+  if (has_res && threadIdx.x == 0) {
+    sr = 0.f;
+    for (int w = 0; w < (int)(blockDim.x >> 5); ++w) sr += last[w];
+    a.ws[(size_t)gridDim.x * 2 * a.K + blockIdx.x] = sr;
   }
 }
 
@@ -401,7 +572,64 @@ __global__ void __launch_bounds__(256) sandwich_columns_kernel(const SandwichBwd
 int row_chunks(int n8) { return n8 > 2 * kSwThreads ? 4 : n8 > kSwThreads ? 2 : 1; }
 int row_threads(int n8, int ch) { return ((n8 + ch - 1) / ch + 31) / 32 * 32; }
 
-int bwd_grid(int T, int num_sms) { return T < 2 * num_sms ? T : 2 * num_sms; }
+// Threads, rows at a time and ring of a gradient call. One CTA a SM, so that an SM
+// leaves one row of column sums; short rows share it, several teams to a CTA.
+BwdPlan bwd_plan(const SandwichBwdArgs& a, int num_sms, int* ch) {
+  const int n8 = a.K / 8;
+  BwdPlan p = {};
+  *ch = n8 <= 32 ? 1 : n8 <= 2 * kSwThreads ? 2 : 4;
+  p.nt = row_threads(n8, *ch);
+  p.teams = kSwThreads / p.nt;
+  const int rows = (a.T + num_sms - 1) / num_sms;
+  if (p.teams > rows) p.teams = rows;
+  const int b16 = 16 * n8;
+  auto part = [&](bool there, int bytes) {
+    const int at = p.stage;
+    if (there) p.stage += bytes;
+    return at;
+  };
+  p.dh = part(a.dh != nullptr, b16);
+  p.dy = part(a.dy != nullptr, b16);
+  p.x = part(true, a.xs != nullptr ? b16 / 2 : b16);
+  p.h = part(a.dy != nullptr, a.hs != nullptr ? b16 / 2 : b16);
+  p.res = part(a.dscale != nullptr, b16);
+  p.gate = part(a.gate_kind == 3, b16);
+  p.gate_bytes = a.gate_kind == 1 ? 4 * a.K : 0;
+  p.depth = (kSwRingBytes - p.gate_bytes) / (p.teams * p.stage);
+  if (p.depth > 4) p.depth = 4;
+  p.smem = p.gate_bytes + p.teams * p.depth * p.stage;
+  const int sums = p.teams > 1 ? p.teams * 8 * a.K : 0;
+  if (p.smem < sums) p.smem = sums;
+  return p;
+}
+
+template <int CH, int GATE>
+cudaError_t run_bwd(const SandwichBwdArgs& a, const BwdPlan& p, int grid, cudaStream_t stream) {
+  static bool granted[kGrantDevices] = {};
+  static std::mutex mu;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kGrantDevices) return cudaErrorInvalidDevice;
+  {
+    std::lock_guard<std::mutex> lk(mu);
+    if (!granted[dev]) {
+      e = cudaFuncSetAttribute(sandwich_bwd_kernel<CH, GATE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               kSwRingBytes);
+      if (e != cudaSuccess) return e;
+      granted[dev] = true;
+    }
+  }
+  sandwich_bwd_kernel<CH, GATE><<<grid, p.teams * p.nt, p.smem, stream>>>(a, p);
+  return cudaGetLastError();
+}
+
+template <int CH>
+cudaError_t run_bwd_gate(const SandwichBwdArgs& a, const BwdPlan& p, int grid, cudaStream_t stream) {
+  if (a.gate_kind == 1) return run_bwd<CH, 1>(a, p, grid, stream);
+  if (a.gate_kind == 3) return run_bwd<CH, 2>(a, p, grid, stream);
+  return run_bwd<CH, 0>(a, p, grid, stream);
+}
 
 }  // namespace
 
@@ -422,14 +650,16 @@ size_t sandwich_bwd_workspace_bytes(int T, int K) {
 }
 
 cudaError_t launch_sandwich_norm_backward(const SandwichBwdArgs& a, int num_sms, cudaStream_t stream) {
-  const int n8 = a.K / 8, ch = row_chunks(n8), nt = row_threads(n8, ch);
-  int grid = bwd_grid(a.T, num_sms);
-  if (grid > kSwMaxCtas) grid = kSwMaxCtas;
-  if (grid > 0) {   // (no rows: the sums are zero)
-    if (ch == 1) sandwich_bwd_kernel<1><<<grid, nt, 0, stream>>>(a);
-    else if (ch == 2) sandwich_bwd_kernel<2><<<grid, nt, 0, stream>>>(a);
-    else sandwich_bwd_kernel<4><<<grid, nt, 0, stream>>>(a);
-    const cudaError_t e = cudaGetLastError();
+  int grid = 0;
+  if (a.T > 0) {   // (no rows: the sums are zero)
+    int ch = 0;
+    const BwdPlan p = bwd_plan(a, num_sms, &ch);
+    grid = (a.T + p.teams - 1) / p.teams;
+    if (grid > num_sms) grid = num_sms;
+    if (grid > kSwMaxCtas) grid = kSwMaxCtas;
+    const cudaError_t e = ch == 1   ? run_bwd_gate<1>(a, p, grid, stream)
+                          : ch == 2 ? run_bwd_gate<2>(a, p, grid, stream)
+                                    : run_bwd_gate<4>(a, p, grid, stream);
     if (e != cudaSuccess) return e;
   }
   if (a.dpre != nullptr || a.dpost != nullptr || a.dscale != nullptr || (a.gate_kind == 1 && a.dgate != nullptr))
