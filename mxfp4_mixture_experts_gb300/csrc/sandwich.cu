@@ -80,6 +80,38 @@ __device__ __forceinline__ void team_sums(float (&v)[N], float (*part)[16], int 
     for (int n = 0; n < N; ++n) v[n] += __shfl_xor_sync(0xffffffffu, v[n], o);
 }
 
+// Three sums at once: lanes give up one of two values where a butterfly step would
+// carry both (13 shuffles for 27). Lane 0 ends with the first, 16 the second, 8 the third.
+__device__ __forceinline__ float merge3(float a, float b, float c, int lane) {
+  const bool hi = lane & 16, mid = lane & 8;
+  float k = (hi ? b : a) + __shfl_xor_sync(0xffffffffu, hi ? a : b, 16);
+  c += __shfl_xor_sync(0xffffffffu, c, 16);
+  return (mid ? c : k) + __shfl_xor_sync(0xffffffffu, mid ? k : c, 8);
+}
+__device__ __forceinline__ float fold8(float v) {
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ void team_sum3(float (&v)[3], float (*part)[16], int team, int nt, int lane, int warp,
+                                          int warps) {
+  float r = fold8(merge3(v[0], v[1], v[2], lane));
+  if (warps > 1) {
+    const int base = team * warps, at = lane & 15;
+    if ((lane & 7) == 0 && lane < 24) part[lane == 0 ? 0 : lane == 16 ? 1 : 2][base + warp] = r;
+    named_barrier(team + 1, nt);
+    // the 16 parts of the first sum in the lower half of the warp, of the second in the
+    // upper one, of the third in both
+    const float k = at < warps ? part[lane >> 4][base + at] : 0.f;
+    const float c = at < warps ? part[2][base + at] : 0.f;
+    const bool mid = lane & 8;
+    r = fold8((mid ? c : k) + __shfl_xor_sync(0xffffffffu, mid ? k : c, 8));
+  }
+  v[0] = __shfl_sync(0xffffffffu, r, 0);
+  v[1] = __shfl_sync(0xffffffffu, r, 16);
+  v[2] = __shfl_sync(0xffffffffu, r, 8);
+}
+
 // CH: 16-byte chunks per thread (K / 8 <= CH * blockDim.x).
 template <int CH>
 __global__ void __launch_bounds__(kSwThreads) sandwich_norm_kernel(const SandwichArgs a) {
@@ -241,25 +273,37 @@ __device__ __forceinline__ void copies_wait(int n) {
   else asm volatile("cp.async.wait_group 3;" ::: "memory");
 }
 
-// Shared memory of the gradient: a channel gate's values, then for every team a
-// ring of rows. A thread fills and reads its own slots alone.
+// Shared memory of the gradient: a channel gate's values times post_gamma, then for every team
+// a ring of rows. A row's slots lie by warp and chunk, [dh][dy][x][h][gate][residual] of
+// 32 lanes each; a thread fills and reads its own slots alone. Slots that nothing
+// fills (a gradient that is not there, lanes past the row) hold zeros.
 struct BwdPlan {
   int nt, teams, depth;   // threads a row, rows at a time, rows of a ring (1..4)
-  int gate_bytes, stage;  // of a team's row
-  int dy, dh, x, h, res, gate;   // its parts (where they are read at all)
+  int gate_bytes, stage;  // bytes before the rings; of a team's row
   int smem;
 };
+// E8 0: x and h in bf16, 1: both in E4M3, 2: as the scales tell.
+template <int GATE, int E8>
+struct Slots {   // byte offsets
+  static constexpr int dh = 0, dy = 512, x = 1024, h = x + (E8 == 1 ? 256 : 512), gate = h + (E8 == 1 ? 256 : 512),
+                       res = gate + (GATE == 2 ? 512 : 0);
+};
+// Bytes of a warp's slots of one chunk.
+int slots_bytes(bool full_gate, int e8, bool res) {
+  return 1024 + (e8 == 1 ? 512 : 1024) + (full_gate ? 512 : 0) + (res ? 512 : 0);
+}
 
 // Column sums of the CTA's rows go to ws [gridDim.x][2][K]: 0 dy * h^, 1 d x^ with
 // d = dn, or dh_total where the gate is a channel's (its gate and post_gamma take
 // their gradients from the one sum). After them ws holds a float a CTA, sum dh_total * res.
 // GATE 0: none or a token's, 1: a channel's, 2: one for every value.
-template <int CH, int GATE>
+template <int CH, int GATE, int E8>
 __global__ void __launch_bounds__(kSwThreads, 1)
     sandwich_bwd_kernel(const SandwichBwdArgs a, const BwdPlan p) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float part[2][3][16];
   __shared__ float last[16];
+  using L = Slots<GATE, E8>;
   constexpr bool kHold = CH <= 2;   // gammas stay in registers
   const int nt = p.nt, team = threadIdx.x / nt, tid = threadIdx.x - team * nt;
   const int lane = tid & 31, warp = tid >> 5, warps = nt >> 5;
@@ -269,56 +313,97 @@ __global__ void __launch_bounds__(kSwThreads, 1)
   const float scale = a.rscale != nullptr ? *a.rscale : 1.f;
   const uint16_t* gate16 = static_cast<const uint16_t*>(a.gate);
   const bool has_dy = a.dy != nullptr, has_dh = a.dh != nullptr, has_post = a.post != nullptr;
-  const bool x8 = a.xs != nullptr, h8 = a.hs != nullptr, has_res = a.dscale != nullptr;
-  uint8_t* ring = smem + p.gate_bytes + (size_t)team * p.depth * p.stage;
-  const uint32_t ring_addr = smem_u32(ring);
+  const bool has_res = a.dscale != nullptr;
+  const bool x8 = E8 == 1 || (E8 == 2 && a.xs != nullptr), h8 = E8 == 1 || (E8 == 2 && a.hs != nullptr);
+  const int chunk = L::res + (has_res ? 512 : 0);          // bytes of a warp's slots of a chunk
+  uint8_t* mine = smem + p.gate_bytes + (size_t)team * p.depth * p.stage + warp * chunk;
+  const int lane16 = 16 * lane, lane_x = (x8 ? 8 : 16) * lane, lane_h = (h8 ? 8 : 16) * lane;
   float4* gch = reinterpret_cast<float4*>(smem);   // [K / 4]
+  bool valid[CH];
   uint4 gp[kHold ? CH : 1], gn[kHold ? CH : 1];
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const int c = tid + i * nt;
+    valid[i] = c < n8;
     if (kHold) gp[i] = gn[i] = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);   // 1
-    if (c >= n8) continue;
+    if (!valid[i] || !has_dh || !has_dy) {
+      const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+      for (int d = 0; d < p.depth; ++d) {
+        uint8_t* to = mine + (size_t)d * p.stage + (size_t)i * warps * chunk;
+        if (!valid[i] || !has_dh) *reinterpret_cast<uint4*>(to + L::dh + lane16) = z;
+        if (!valid[i] || !has_dy) {
+          *reinterpret_cast<uint4*>(to + L::dy + lane16) = z;
+          *reinterpret_cast<uint2*>(to + L::h + lane_h) = make_uint2(0u, 0u);
+          if (!h8) *reinterpret_cast<uint4*>(to + L::h + lane_h) = z;
+        }
+        if (!valid[i]) {
+          *reinterpret_cast<uint2*>(to + L::x + lane_x) = make_uint2(0u, 0u);
+          if (!x8) *reinterpret_cast<uint4*>(to + L::x + lane_x) = z;
+          if (GATE == 2) *reinterpret_cast<uint4*>(to + L::gate + lane16) = z;
+          if (has_res) *reinterpret_cast<uint4*>(to + L::res + lane16) = z;
+        }
+      }
+    }
+    if (!valid[i]) continue;
     if (kHold && has_post) gp[i] = ld_row16(a.post + 8 * c);
     if (kHold && has_dy) gn[i] = ld_row16(a.pre + 8 * c);
     if (GATE == 1 && team == 0) {
-      float g[8];
+      float g[8], w[8];
       unpack8(ld_row16(gate16 + 8 * c), g);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) g[j] = gate_value(g[j], a.gate_act);
+      for (int j = 0; j < 8; ++j) w[j] = 1.f;
+      if (has_post) unpack8(ld_row16(a.post + 8 * c), w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) g[j] = gate_value(g[j], a.gate_act) * w[j];
       gch[2 * c] = make_float4(g[0], g[1], g[2], g[3]);
       gch[2 * c + 1] = make_float4(g[4], g[5], g[6], g[7]);
     }
   }
   if (GATE == 1) __syncthreads();
-  auto post_of = [&](int i, int c, float2 (&v)[4]) {
-    if (kHold) unpack4(gp[kHold ? i : 0], v);
-    else if (has_post) unpack4(ld_row16(a.post + 8 * c), v);
-    else v[0] = v[1] = v[2] = v[3] = dup(1.f);
+  // post_gamma, times the channel's gate
+  auto weight_of = [&](int i, float2 (&v)[4]) {
+    const int c = tid + i * nt;
+    if (GATE == 1) {
+      const float4 g0 = valid[i] ? gch[2 * c] : make_float4(0.f, 0.f, 0.f, 0.f);
+      const float4 g1 = valid[i] ? gch[2 * c + 1] : make_float4(0.f, 0.f, 0.f, 0.f);
+      v[0] = make_float2(g0.x, g0.y);
+      v[1] = make_float2(g0.z, g0.w);
+      v[2] = make_float2(g1.x, g1.y);
+      v[3] = make_float2(g1.z, g1.w);
+    } else if (kHold) {
+      unpack4(gp[kHold ? i : 0], v);
+    } else {
+      v[0] = v[1] = v[2] = v[3] = dup(1.f);
+      if (has_post && valid[i]) unpack4(ld_row16(a.post + 8 * c), v);
+    }
   };
-  auto pre_of = [&](int i, int c, float2 (&v)[4]) {
-    if (kHold) unpack4(gn[kHold ? i : 0], v);
-    else unpack4(ld_row16(a.pre + 8 * c), v);
+  auto pre_of = [&](int i, float2 (&v)[4]) {
+    if (kHold) {
+      unpack4(gn[kHold ? i : 0], v);
+    } else {
+      v[0] = v[1] = v[2] = v[3] = dup(1.f);
+      if (has_dy && valid[i]) unpack4(ld_row16(a.pre + 8 * (tid + i * nt)), v);
+    }
   };
   auto fetch = [&](unsigned t, int st) {
     if (t < T) {
-      const size_t row = (size_t)t * a.K;
-      const uint32_t base = ring_addr + st * p.stage;
+      const size_t row = (size_t)t * a.K + 8 * tid;
+      const uint32_t to = smem_u32(mine) + st * p.stage;
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
-        const int c = tid + i * nt;
-        if (c >= n8) continue;
-        const size_t at = row + 8 * c;
-        if (has_dh) copy16(base + p.dh + 16 * c, a.dh + at);
+        if (!valid[i]) continue;
+        const size_t at = row + 8 * i * nt;
+        const uint32_t base = to + i * warps * chunk;
+        if (has_dh) copy16(base + L::dh + lane16, a.dh + at);
         if (has_dy) {
-          copy16(base + p.dy + 16 * c, a.dy + at);
-          if (h8) copy8(base + p.h + 8 * c, static_cast<const uint8_t*>(a.h) + at);
-          else copy16(base + p.h + 16 * c, static_cast<const uint16_t*>(a.h) + at);
+          copy16(base + L::dy + lane16, a.dy + at);
+          if (h8) copy8(base + L::h + lane_h, static_cast<const uint8_t*>(a.h) + at);
+          else copy16(base + L::h + lane_h, static_cast<const uint16_t*>(a.h) + at);
         }
-        if (x8) copy8(base + p.x + 8 * c, static_cast<const uint8_t*>(a.x) + at);
-        else copy16(base + p.x + 16 * c, static_cast<const uint16_t*>(a.x) + at);
-        if (has_res) copy16(base + p.res + 16 * c, a.residual + at);
-        if (GATE == 2) copy16(base + p.gate + 16 * c, gate16 + at);
+        if (x8) copy8(base + L::x + lane_x, static_cast<const uint8_t*>(a.x) + at);
+        else copy16(base + L::x + lane_x, static_cast<const uint16_t*>(a.x) + at);
+        if (has_res) copy16(base + L::res + lane16, a.residual + at);
+        if (GATE == 2) copy16(base + L::gate + lane16, gate16 + at);
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -333,14 +418,14 @@ __global__ void __launch_bounds__(kSwThreads, 1)
     r.r1 = has_post ? __ldg(a.rstd + t) : 1.f;
     r.r2 = has_dy ? __ldg(a.rstd + (size_t)T + t) : 0.f;
     r.g = GATE == 0 && a.gate_kind == 2 ? __ldg(static_cast<const float*>(a.gate) + t) : 1.f;
-    if (x8 || h8) {
+    if (E8 != 0) {
       const size_t row = (size_t)t * (a.K / 32);
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
-        const int c = tid + i * nt;
-        if (c >= n8) continue;
-        if (x8) r.xs[i] = __ldg(a.xs + row + (c >> 2));
-        if (h8 && has_dy) r.hs[i] = __ldg(a.hs + row + (c >> 2));
+        if (!valid[i]) continue;
+        const size_t at = row + ((tid + i * nt) >> 2);
+        if (x8) r.xs[i] = __ldg(a.xs + at);
+        if (h8 && has_dy) r.hs[i] = __ldg(a.hs + at);
       }
     }
   };
@@ -356,50 +441,36 @@ __global__ void __launch_bounds__(kSwThreads, 1)
   const float inv_k = 1.f / (float)a.K;
   int odd = 0, st = 0;
   for (unsigned t = first; t < T; t += step, odd ^= 1) {
-    const size_t row = (size_t)t * a.K;
     now = next;
     scalars(t + step, next);
     const float r1 = now.r1, r2 = now.r2;
     const float gt = GATE == 0 && a.gate_kind == 2 ? gate_value(now.g, a.gate_act) : 1.f;
     copies_wait(p.depth - 1);
-    const uint8_t* slot = ring + st * p.stage;
+    const uint8_t* slot = mine + (size_t)st * p.stage;
     float2 s2[3] = {dup(0.f), dup(0.f), dup(0.f)};   // v h, w x (dh + r2 v), w x h; w without a token's gate
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      const int c = tid + i * nt;
-      if (c >= n8) continue;
-      float2 q[4], h[4], w[4], x[4];
+      const uint8_t* at = slot + i * warps * chunk;
+      float2 q[4], h[4], w[4], x[4], v[4], g[4];
+      unpack4(*reinterpret_cast<const uint4*>(at + L::dh + lane16), q);
+      unpack4(*reinterpret_cast<const uint4*>(at + L::dy + lane16), v);
+      pre_of(i, g);
+      slot8(at + L::h + lane_h, h8, now.hs[i], h);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) q[j] = h[j] = dup(0.f);
-      if (has_dh) unpack4(*reinterpret_cast<const uint4*>(slot + p.dh + 16 * c), q);
-      if (has_dy) {
-        float2 v[4], g[4];
-        unpack4(*reinterpret_cast<const uint4*>(slot + p.dy + 16 * c), v);
-        pre_of(i, c, g);
-        slot8(slot + p.h + (h8 ? 8 : 16) * c, h8, now.hs[i], h);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          s_pre[i][j] = __ffma2_rn(v[j], __fmul2_rn(h[j], dup(r2)), s_pre[i][j]);
-          v[j] = __fmul2_rn(v[j], g[j]);
-          s2[0] = __ffma2_rn(v[j], h[j], s2[0]);
-          q[j] = __ffma2_rn(dup(r2), v[j], q[j]);
-        }
+      for (int j = 0; j < 4; ++j) {
+        s_pre[i][j] = __ffma2_rn(v[j], __fmul2_rn(h[j], dup(r2)), s_pre[i][j]);
+        v[j] = __fmul2_rn(v[j], g[j]);
+        s2[0] = __ffma2_rn(v[j], h[j], s2[0]);
+        q[j] = __ffma2_rn(dup(r2), v[j], q[j]);
       }
-      slot8(slot + p.x + (x8 ? 8 : 16) * c, x8, now.xs[i], x);
-      post_of(i, c, w);
-      if (GATE == 1) {
-        const float4 g0 = gch[2 * c], g1 = gch[2 * c + 1];
-        w[0] = __fmul2_rn(w[0], make_float2(g0.x, g0.y));
-        w[1] = __fmul2_rn(w[1], make_float2(g0.z, g0.w));
-        w[2] = __fmul2_rn(w[2], make_float2(g1.x, g1.y));
-        w[3] = __fmul2_rn(w[3], make_float2(g1.z, g1.w));
-      }
+      slot8(at + L::x + lane_x, x8, now.xs[i], x);
+      weight_of(i, w);
       if (GATE == 2) {
-        float2 g[4];
-        unpack4(*reinterpret_cast<const uint4*>(slot + p.gate + 16 * c), g);
+        float2 f[4];
+        unpack4(*reinterpret_cast<const uint4*>(at + L::gate + lane16), f);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          w[j] = __fmul2_rn(w[j], make_float2(gate_value(g[j].x, a.gate_act), gate_value(g[j].y, a.gate_act)));
+          w[j] = __fmul2_rn(w[j], make_float2(gate_value(f[j].x, a.gate_act), gate_value(f[j].y, a.gate_act)));
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -409,81 +480,64 @@ __global__ void __launch_bounds__(kSwThreads, 1)
       }
     }
     float s[3] = {s2[0].x + s2[0].y, s2[1].x + s2[1].y, s2[2].x + s2[2].y};
-    team_sums<3>(s, part[odd], team, nt, lane, warp, warps);
+    team_sum3(s, part[odd], team, nt, lane, warp, warps);
     const float c2 = s[0] * r2 * inv_k * r2;              // r2 mean(v h^)
     const float dot = r1 * (s[1] - c2 * (r2 * s[2]));     // sum of w x^ dh_total
     const float c1 = has_post ? gt * dot * inv_k : 0.f;
     if (GATE == 0 && a.gate_kind == 2 && a.dgate != nullptr && tid == 0)
       static_cast<float*>(a.dgate)[t] = a.gate_act ? dot * gt * gate_value(-now.g, 1) : dot;
     const float2 kh = dup(-c2 * r2), k1 = dup(-r1 * r1 * c1), xr = dup(r1 * gt);
+    const size_t row = (size_t)t * a.K + 8 * tid;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      const int c = tid + i * nt;
-      if (c >= n8) continue;
-      float2 d[4], x[4], w[4];   // d: dh_total
+      const uint8_t* at = slot + i * warps * chunk;
+      const size_t out = row + 8 * i * nt;
+      float2 d[4], x[4], w[4], v[4], g[4], h[4];   // d: dh_total
+      unpack4(*reinterpret_cast<const uint4*>(at + L::dh + lane16), d);
+      unpack4(*reinterpret_cast<const uint4*>(at + L::dy + lane16), v);
+      pre_of(i, g);
+      slot8(at + L::h + lane_h, h8, now.hs[i], h);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) d[j] = dup(0.f);
-      if (has_dh) unpack4(*reinterpret_cast<const uint4*>(slot + p.dh + 16 * c), d);
-      if (has_dy) {
-        float2 v[4], g[4], h[4];
-        unpack4(*reinterpret_cast<const uint4*>(slot + p.dy + 16 * c), v);
-        pre_of(i, c, g);
-        slot8(slot + p.h + (h8 ? 8 : 16) * c, h8, now.hs[i], h);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          d[j] = __ffma2_rn(kh, h[j], __ffma2_rn(dup(r2), __fmul2_rn(v[j], g[j]), d[j]));
-      }
+      for (int j = 0; j < 4; ++j)
+        d[j] = __ffma2_rn(kh, h[j], __ffma2_rn(dup(r2), __fmul2_rn(v[j], g[j]), d[j]));
       if (has_res) {
-        float2 z[4];
-        unpack4(*reinterpret_cast<const uint4*>(slot + p.res + 16 * c), z);
+        unpack4(*reinterpret_cast<const uint4*>(at + L::res + lane16), v);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s_res = __ffma2_rn(d[j], z[j], s_res);
+        for (int j = 0; j < 4; ++j) s_res = __ffma2_rn(d[j], v[j], s_res);
       }
-      if (a.dres != nullptr) {
-        float2 z[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) z[j] = __fmul2_rn(d[j], dup(scale));
-        st_row16(a.dres + row + 8 * c, pack4(z));
-      }
-      slot8(slot + p.x + (x8 ? 8 : 16) * c, x8, now.xs[i], x);
-      post_of(i, c, w);
+      for (int j = 0; j < 4; ++j) v[j] = __fmul2_rn(d[j], dup(scale));
+      if (a.dres != nullptr && valid[i]) st_row16(a.dres + out, pack4(v));
+      slot8(at + L::x + lane_x, x8, now.xs[i], x);
+      weight_of(i, w);
       // d becomes the gated gradient but for a channel's gate, whose sums take it without
-      if (GATE == 1) {
-        const float4 g0 = gch[2 * c], g1 = gch[2 * c + 1];
-        w[0] = __fmul2_rn(w[0], make_float2(g0.x, g0.y));
-        w[1] = __fmul2_rn(w[1], make_float2(g0.z, g0.w));
-        w[2] = __fmul2_rn(w[2], make_float2(g1.x, g1.y));
-        w[3] = __fmul2_rn(w[3], make_float2(g1.z, g1.w));
-      }
       if (GATE == 2) {
-        float2 raw[4], o[4];
-        unpack4(*reinterpret_cast<const uint4*>(slot + p.gate + 16 * c), raw);
+        unpack4(*reinterpret_cast<const uint4*>(at + L::gate + lane16), v);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float2 g = make_float2(gate_value(raw[j].x, a.gate_act), gate_value(raw[j].y, a.gate_act));
-          o[j] = __fmul2_rn(d[j], __fmul2_rn(__fmul2_rn(x[j], dup(r1)), w[j]));
+          const float2 f = make_float2(gate_value(v[j].x, a.gate_act), gate_value(v[j].y, a.gate_act));
+          g[j] = __fmul2_rn(d[j], __fmul2_rn(__fmul2_rn(x[j], dup(r1)), w[j]));
           if (a.gate_act)
-            o[j] = __fmul2_rn(o[j], make_float2(g.x * gate_value(-raw[j].x, 1), g.y * gate_value(-raw[j].y, 1)));
-          d[j] = __fmul2_rn(d[j], g);
+            g[j] = __fmul2_rn(g[j], make_float2(f.x * gate_value(-v[j].x, 1), f.y * gate_value(-v[j].y, 1)));
+          d[j] = __fmul2_rn(d[j], f);
         }
-        if (a.dgate != nullptr) st_row16(static_cast<uint16_t*>(a.dgate) + row + 8 * c, pack4(o));
+        if (a.dgate != nullptr && valid[i]) st_row16(static_cast<uint16_t*>(a.dgate) + out, pack4(g));
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         s_x[i][j] = __ffma2_rn(d[j], __fmul2_rn(x[j], xr), s_x[i][j]);
-        const float2 u = __fmul2_rn(d[j], w[j]);
-        d[j] = __ffma2_rn(k1, x[j], __fmul2_rn(u, xr));   // (no post_gamma: r1 = 1, k1 = 0)
+        d[j] = __ffma2_rn(k1, x[j], __fmul2_rn(__fmul2_rn(d[j], w[j]), xr));   // (no post_gamma: r1 = 1, k1 = 0)
       }
-      if (a.dx != nullptr) st_row16(a.dx + row + 8 * c, pack4(d));
+      if (a.dx != nullptr && valid[i]) st_row16(a.dx + out, pack4(d));
     }
     fetch(t + p.depth * step, st);
     if (++st == p.depth) st = 0;
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
-  float* mine = a.ws + (size_t)blockIdx.x * 2 * a.K;
+  float* sums = a.ws + (size_t)blockIdx.x * 2 * a.K;
   if (p.teams > 1) __syncthreads();
   // one team: straight to ws; several: through shared memory, added up in order
-  float* to = p.teams > 1 ? reinterpret_cast<float*>(smem) + (size_t)team * 2 * a.K : mine;
+  float* to = p.teams > 1 ? reinterpret_cast<float*>(smem) + (size_t)team * 2 * a.K : sums;
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const int c = tid + i * nt;
@@ -514,7 +568,7 @@ __global__ void __launch_bounds__(kSwThreads, 1)
         v.z += o.z;
         v.w += o.w;
       }
-      reinterpret_cast<float4*>(mine)[e] = v;
+      reinterpret_cast<float4*>(sums)[e] = v;
     }
   }
   if (has_res && threadIdx.x == 0) {
@@ -574,26 +628,13 @@ int row_threads(int n8, int ch) { return ((n8 + ch - 1) / ch + 31) / 32 * 32; }
 
 // Threads, rows at a time and ring of a gradient call. One CTA a SM, so that an SM
 // leaves one row of column sums; short rows share it, several teams to a CTA.
-BwdPlan bwd_plan(const SandwichBwdArgs& a, int num_sms, int* ch) {
-  const int n8 = a.K / 8;
+BwdPlan bwd_plan(const SandwichBwdArgs& a, int num_sms, int ch, int e8) {
   BwdPlan p = {};
-  *ch = n8 <= 32 ? 1 : n8 <= 2 * kSwThreads ? 2 : 4;
-  p.nt = row_threads(n8, *ch);
+  p.nt = row_threads(a.K / 8, ch);
   p.teams = kSwThreads / p.nt;
-  const int rows = (a.T + num_sms - 1) / num_sms;
+  const int rows = (int)(((unsigned)a.T + num_sms - 1) / num_sms);
   if (p.teams > rows) p.teams = rows;
-  const int b16 = 16 * n8;
-  auto part = [&](bool there, int bytes) {
-    const int at = p.stage;
-    if (there) p.stage += bytes;
-    return at;
-  };
-  p.dh = part(a.dh != nullptr, b16);
-  p.dy = part(a.dy != nullptr, b16);
-  p.x = part(true, a.xs != nullptr ? b16 / 2 : b16);
-  p.h = part(a.dy != nullptr, a.hs != nullptr ? b16 / 2 : b16);
-  p.res = part(a.dscale != nullptr, b16);
-  p.gate = part(a.gate_kind == 3, b16);
+  p.stage = p.nt / 32 * ch * slots_bytes(a.gate_kind == 3, e8, a.dscale != nullptr);
   p.gate_bytes = a.gate_kind == 1 ? 4 * a.K : 0;
   p.depth = (kSwRingBytes - p.gate_bytes) / (p.teams * p.stage);
   if (p.depth > 4) p.depth = 4;
@@ -603,8 +644,8 @@ BwdPlan bwd_plan(const SandwichBwdArgs& a, int num_sms, int* ch) {
   return p;
 }
 
-template <int CH, int GATE>
-cudaError_t run_bwd(const SandwichBwdArgs& a, const BwdPlan& p, int grid, cudaStream_t stream) {
+template <int CH, int GATE, int E8>
+cudaError_t run_bwd(const SandwichBwdArgs& a, int num_sms, int* grid, cudaStream_t stream) {
   static bool granted[kGrantDevices] = {};
   static std::mutex mu;
   int dev = 0;
@@ -614,21 +655,31 @@ cudaError_t run_bwd(const SandwichBwdArgs& a, const BwdPlan& p, int grid, cudaSt
   {
     std::lock_guard<std::mutex> lk(mu);
     if (!granted[dev]) {
-      e = cudaFuncSetAttribute(sandwich_bwd_kernel<CH, GATE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      e = cudaFuncSetAttribute(sandwich_bwd_kernel<CH, GATE, E8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                kSwRingBytes);
       if (e != cudaSuccess) return e;
       granted[dev] = true;
     }
   }
-  sandwich_bwd_kernel<CH, GATE><<<grid, p.teams * p.nt, p.smem, stream>>>(a, p);
+  const BwdPlan p = bwd_plan(a, num_sms, CH, E8);
+  *grid = (int)(((unsigned)a.T + p.teams - 1) / p.teams);   // (T + 15 may pass 2^31)
+  if (*grid > num_sms) *grid = num_sms;
+  if (*grid > kSwMaxCtas) *grid = kSwMaxCtas;
+  sandwich_bwd_kernel<CH, GATE, E8><<<*grid, p.teams * p.nt, p.smem, stream>>>(a, p);
   return cudaGetLastError();
 }
 
+template <int CH, int E8>
+cudaError_t run_bwd_gate(const SandwichBwdArgs& a, int num_sms, int* grid, cudaStream_t stream) {
+  if (a.gate_kind == 1) return run_bwd<CH, 1, E8>(a, num_sms, grid, stream);
+  if (a.gate_kind == 3) return run_bwd<CH, 2, E8>(a, num_sms, grid, stream);
+  return run_bwd<CH, 0, E8>(a, num_sms, grid, stream);
+}
 template <int CH>
-cudaError_t run_bwd_gate(const SandwichBwdArgs& a, const BwdPlan& p, int grid, cudaStream_t stream) {
-  if (a.gate_kind == 1) return run_bwd<CH, 1>(a, p, grid, stream);
-  if (a.gate_kind == 3) return run_bwd<CH, 2>(a, p, grid, stream);
-  return run_bwd<CH, 0>(a, p, grid, stream);
+cudaError_t run_bwd_form(const SandwichBwdArgs& a, int num_sms, int* grid, cudaStream_t stream) {
+  const bool x8 = a.xs != nullptr, h8 = a.dy != nullptr ? a.hs != nullptr : x8;   // (without dy h is not read)
+  if (x8 != h8) return run_bwd_gate<CH, 2>(a, num_sms, grid, stream);
+  return x8 ? run_bwd_gate<CH, 1>(a, num_sms, grid, stream) : run_bwd_gate<CH, 0>(a, num_sms, grid, stream);
 }
 
 }  // namespace
@@ -652,14 +703,8 @@ size_t sandwich_bwd_workspace_bytes(int T, int K) {
 cudaError_t launch_sandwich_norm_backward(const SandwichBwdArgs& a, int num_sms, cudaStream_t stream) {
   int grid = 0;
   if (a.T > 0) {   // (no rows: the sums are zero)
-    int ch = 0;
-    const BwdPlan p = bwd_plan(a, num_sms, &ch);
-    grid = (a.T + p.teams - 1) / p.teams;
-    if (grid > num_sms) grid = num_sms;
-    if (grid > kSwMaxCtas) grid = kSwMaxCtas;
-    const cudaError_t e = ch == 1   ? run_bwd_gate<1>(a, p, grid, stream)
-                          : ch == 2 ? run_bwd_gate<2>(a, p, grid, stream)
-                                    : run_bwd_gate<4>(a, p, grid, stream);
+    const cudaError_t e = a.K <= 16 * kSwThreads ? run_bwd_form<2>(a, num_sms, &grid, stream)
+                                                 : run_bwd_form<4>(a, num_sms, &grid, stream);
     if (e != cudaSuccess) return e;
   }
   if (a.dpre != nullptr || a.dpost != nullptr || a.dscale != nullptr || (a.gate_kind == 1 && a.dgate != nullptr))
