@@ -26,7 +26,7 @@ namespace mxmoe {
 namespace {
 
 constexpr int kSwThreads = 512;   // most threads of a row
-constexpr int kSwRingBytes = 224 * 1024;   // shared memory of a gradient call, beside 448 bytes of sums
+constexpr int kSwRingBytes = 224 * 1024;   // shared memory of a gradient call, beside 1.7 KB of sums
 
 __device__ __forceinline__ float gate_value(float g, int act) {
   return act ? __frcp_rn(__fadd_rn(1.f, expf(-g))) : g;
@@ -55,31 +55,6 @@ __device__ __forceinline__ void cta_sums(float (&v)[N], float (*part)[16], int l
   for (int n = 0; n < N; ++n) v[n] = __shfl_sync(0xffffffffu, v[n], 0);
 }
 
-// The same over a team of nt threads of a CTA of at most 16 warps (its own named
-// barrier, none for one warp); part: [N][16], a place a warp of the CTA.
-template <int N>
-__device__ __forceinline__ void team_sums(float (&v)[N], float (*part)[16], int team, int nt, int lane, int warp,
-                                          int warps) {
-  const int base = team * warps;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-    for (int n = 0; n < N; ++n) v[n] += __shfl_xor_sync(0xffffffffu, v[n], o);
-  if (warps == 1) return;
-  if (lane == 0) {
-#pragma unroll
-    for (int n = 0; n < N; ++n) part[n][base + warp] = v[n];
-  }
-  named_barrier(team + 1, nt);
-  // both halves of the warp hold the same 16 parts
-#pragma unroll
-  for (int n = 0; n < N; ++n) v[n] = (lane & 15) < warps ? part[n][base + (lane & 15)] : 0.f;
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1)
-#pragma unroll
-    for (int n = 0; n < N; ++n) v[n] += __shfl_xor_sync(0xffffffffu, v[n], o);
-}
-
 // Three sums at once: lanes give up one of two values where a butterfly step would
 // carry both (13 shuffles for 27). Lane 0 ends with the first, 16 the second, 8 the third.
 __device__ __forceinline__ float merge3(float a, float b, float c, int lane) {
@@ -93,23 +68,33 @@ __device__ __forceinline__ float fold8(float v) {
   for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
-__device__ __forceinline__ void team_sum3(float (&v)[3], float (*part)[16], int team, int nt, int lane, int warp,
-                                          int warps) {
-  float r = fold8(merge3(v[0], v[1], v[2], lane));
+// Over a team of nt threads of the CTA (its own named barrier, none for one warp);
+// part: [3 ROWS][32], a place a warp of the CTA.
+template <int ROWS>
+__device__ __forceinline__ void team_sum3(float (&v)[ROWS][3], float (*part)[32], int team, int nt, int lane,
+                                          int warp, int warps) {
+  float m[ROWS];
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) m[r] = fold8(merge3(v[r][0], v[r][1], v[r][2], lane));
   if (warps > 1) {
-    const int base = team * warps, at = lane & 15;
-    if ((lane & 7) == 0 && lane < 24) part[lane == 0 ? 0 : lane == 16 ? 1 : 2][base + warp] = r;
+    const int base = team * warps;
+    const bool there = lane < warps;
+    if ((lane & 7) == 0 && lane < 24) {
+#pragma unroll
+      for (int r = 0; r < ROWS; ++r) part[3 * r + (lane == 0 ? 0 : lane == 16 ? 1 : 2)][base + warp] = m[r];
+    }
     named_barrier(team + 1, nt);
-    // the 16 parts of the first sum in the lower half of the warp, of the second in the
-    // upper one, of the third in both
-    const float k = at < warps ? part[lane >> 4][base + at] : 0.f;
-    const float c = at < warps ? part[2][base + at] : 0.f;
-    const bool mid = lane & 8;
-    r = fold8((mid ? c : k) + __shfl_xor_sync(0xffffffffu, mid ? k : c, 8));
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r)
+      m[r] = fold8(merge3(there ? part[3 * r][base + lane] : 0.f, there ? part[3 * r + 1][base + lane] : 0.f,
+                          there ? part[3 * r + 2][base + lane] : 0.f, lane));
   }
-  v[0] = __shfl_sync(0xffffffffu, r, 0);
-  v[1] = __shfl_sync(0xffffffffu, r, 16);
-  v[2] = __shfl_sync(0xffffffffu, r, 8);
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) {
+    v[r][0] = __shfl_sync(0xffffffffu, m[r], 0);
+    v[r][1] = __shfl_sync(0xffffffffu, m[r], 16);
+    v[r][2] = __shfl_sync(0xffffffffu, m[r], 8);
+  }
 }
 
 // CH: 16-byte chunks per thread (K / 8 <= CH * blockDim.x).
@@ -246,24 +231,25 @@ __device__ __forceinline__ uint4 pack4(const float2 (&v)[4]) {
   return make_uint4(bf16x2_rn(v[0].x, v[0].y), bf16x2_rn(v[1].x, v[1].y), bf16x2_rn(v[2].x, v[2].y),
                     bf16x2_rn(v[3].x, v[3].y));
 }
-// 8 values from shared memory: bf16, or E4M3 with their block's scale byte.
-__device__ __forceinline__ void slot8(const uint8_t* p, bool e4m3, uint32_t scale, float2 (&v)[4]) {
+// 8 values from shared memory: bf16, or E4M3 with their block's factor.
+__device__ __forceinline__ void slot8(const uint8_t* p, bool e4m3, float scale, float2 (&v)[4]) {
   if (!e4m3) {
     unpack4(*reinterpret_cast<const uint4*>(p), v);
     return;
   }
   const uint2 q = *reinterpret_cast<const uint2*>(p);
-  const float2 f = dup(e8m0_to_f32(scale));
+  const float2 f = dup(scale);
   v[0] = __fmul2_rn(e4m3x2_values((uint16_t)q.x), f);
   v[1] = __fmul2_rn(e4m3x2_values((uint16_t)(q.x >> 16)), f);
   v[2] = __fmul2_rn(e4m3x2_values((uint16_t)q.y), f);
   v[3] = __fmul2_rn(e4m3x2_values((uint16_t)(q.y >> 16)), f);
 }
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// 16 (8) bytes, or zeros where n is 0: nothing is read then.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int n) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
-__device__ __forceinline__ void copy8(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+__device__ __forceinline__ void copy8(uint32_t dst, const void* src, int n) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
 // All but the latest n (0..3) groups of this thread's copies have landed.
 __device__ __forceinline__ void copies_wait(int n) {
@@ -273,20 +259,29 @@ __device__ __forceinline__ void copies_wait(int n) {
   else asm volatile("cp.async.wait_group 3;" ::: "memory");
 }
 
-// Shared memory of the gradient: a channel gate's values times post_gamma, then for every team
-// a ring of rows. A row's slots lie by warp and chunk, [dh][dy][x][h][gate][residual] of
-// 32 lanes each; a thread fills and reads its own slots alone. Slots that nothing
-// fills (a gradient that is not there, lanes past the row) hold zeros.
+// Loads that stay where they are written, ahead of their use.
+__device__ __forceinline__ float ldg_ahead(const float* p) {
+  float v;
+  asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
+}
+
+// Shared memory of the gradient: a channel gate's values times post_gamma (fp32, in two halves of
+// 4 values a chunk), then for every team a ring of rows. A row's slots lie by warp and
+// chunk, [dh][dy][x][h][gate] of 32 lanes each, the residual's after the warp's chunks; a
+// thread fills and reads its own slots alone. What is not there (a gradient, lanes past
+// the row, rows past the last) is filled with zeros.
 struct BwdPlan {
-  int nt, teams, depth;   // threads a row, rows at a time, rows of a ring (1..4)
-  int gate_bytes, stage;  // bytes before the rings; of a team's row
+  int nt, teams, depth;        // threads of a team, teams, stages of a ring (1..4)
+  int gate_bytes, row, stage;  // bytes before the rings; of a row; of a team's rows of one step
   int smem;
+  bool has_dh, has_dy;         // (a gradient that is not there has the other's address)
 };
 // E8 0: x and h in bf16, 1: both in E4M3, 2: as the scales tell.
 template <int GATE, int E8>
 struct Slots {   // byte offsets
   static constexpr int dh = 0, dy = 512, x = 1024, h = x + (E8 == 1 ? 256 : 512), gate = h + (E8 == 1 ? 256 : 512),
-                       res = gate + (GATE == 2 ? 512 : 0);
+                       size = gate + (GATE == 2 ? 512 : 0);
 };
 // Bytes of a warp's slots of one chunk.
 int slots_bytes(bool full_gate, int e8, bool res) {
@@ -297,75 +292,61 @@ int slots_bytes(bool full_gate, int e8, bool res) {
 // d = dn, or dh_total where the gate is a channel's (its gate and post_gamma take
 // their gradients from the one sum). After them ws holds a float a CTA, sum dh_total * res.
 // GATE 0: none or a token's, 1: a channel's, 2: one for every value.
-template <int CH, int GATE, int E8>
-__global__ void __launch_bounds__(kSwThreads, 1)
+// A warp holds CH * 32 chunks in a row, lane after lane, so that the chunks of a thread lie
+// at fixed distances. ROWS: rows that a team takes together, two independent chains of
+// work for a warp and half the waits.
+template <int CH, int GATE, int E8, int ROWS, int MAXT>
+__global__ void __launch_bounds__(MAXT, 1)
     sandwich_bwd_kernel(const SandwichBwdArgs a, const BwdPlan p) {
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ float part[2][3][16];
-  __shared__ float last[16];
+  __shared__ float part[2][3 * ROWS][32];
+  __shared__ float last[32];
   using L = Slots<GATE, E8>;
   constexpr bool kHold = CH <= 2;   // gammas stay in registers
   const int nt = p.nt, team = threadIdx.x / nt, tid = threadIdx.x - team * nt;
   const int lane = tid & 31, warp = tid >> 5, warps = nt >> 5;
-  const int n8 = a.K / 8;
+  const int n8 = a.K / 8, c0 = warp * (32 * CH) + lane;   // this thread's chunks: c0 + 32 i
   const unsigned T = (unsigned)a.T;   // unsigned: T + the step may pass 2^31
-  const unsigned step = gridDim.x * p.teams;
-  const float scale = a.rscale != nullptr ? *a.rscale : 1.f;
+  const bool scaled_res = a.rscale != nullptr;
+  const float scale = scaled_res ? *a.rscale : 1.f;
   const uint16_t* gate16 = static_cast<const uint16_t*>(a.gate);
-  const bool has_dy = a.dy != nullptr, has_dh = a.dh != nullptr, has_post = a.post != nullptr;
+  const bool has_dy = p.has_dy, has_dh = p.has_dh, has_post = a.post != nullptr;
   const bool has_res = a.dscale != nullptr;
   const bool x8 = E8 == 1 || (E8 == 2 && a.xs != nullptr), h8 = E8 == 1 || (E8 == 2 && a.hs != nullptr);
-  const int chunk = L::res + (has_res ? 512 : 0);          // bytes of a warp's slots of a chunk
-  uint8_t* mine = smem + p.gate_bytes + (size_t)team * p.depth * p.stage + warp * chunk;
+  uint8_t* mine = smem + p.gate_bytes + (size_t)team * p.depth * p.stage + warp * (CH * (L::size + (has_res ? 512 : 0)));
   const int lane16 = 16 * lane, lane_x = (x8 ? 8 : 16) * lane, lane_h = (h8 ? 8 : 16) * lane;
-  float4* gch = reinterpret_cast<float4*>(smem);   // [K / 4]
+  const int res0 = CH * L::size + lane16;
+  float4* gch = reinterpret_cast<float4*>(smem);   // [2][chunks of a team]
+  const int gch_half = CH * nt;
   bool valid[CH];
   uint4 gp[kHold ? CH : 1], gn[kHold ? CH : 1];
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
-    const int c = tid + i * nt;
+    const int c = c0 + 32 * i;
     valid[i] = c < n8;
     if (kHold) gp[i] = gn[i] = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);   // 1
-    if (!valid[i] || !has_dh || !has_dy) {
-      const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-      for (int d = 0; d < p.depth; ++d) {
-        uint8_t* to = mine + (size_t)d * p.stage + (size_t)i * warps * chunk;
-        if (!valid[i] || !has_dh) *reinterpret_cast<uint4*>(to + L::dh + lane16) = z;
-        if (!valid[i] || !has_dy) {
-          *reinterpret_cast<uint4*>(to + L::dy + lane16) = z;
-          *reinterpret_cast<uint2*>(to + L::h + lane_h) = make_uint2(0u, 0u);
-          if (!h8) *reinterpret_cast<uint4*>(to + L::h + lane_h) = z;
-        }
-        if (!valid[i]) {
-          *reinterpret_cast<uint2*>(to + L::x + lane_x) = make_uint2(0u, 0u);
-          if (!x8) *reinterpret_cast<uint4*>(to + L::x + lane_x) = z;
-          if (GATE == 2) *reinterpret_cast<uint4*>(to + L::gate + lane16) = z;
-          if (has_res) *reinterpret_cast<uint4*>(to + L::res + lane16) = z;
-        }
+    if (GATE == 1 && team == 0) {
+      float g[8], w[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) g[j] = w[j] = 1.f;
+      if (valid[i]) {
+        unpack8(ld_row16(gate16 + 8 * c), g);
+        if (has_post) unpack8(ld_row16(a.post + 8 * c), w);
       }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) g[j] = gate_value(g[j], a.gate_act) * w[j];
+      gch[c] = make_float4(g[0], g[1], g[2], g[3]);
+      gch[gch_half + c] = make_float4(g[4], g[5], g[6], g[7]);
     }
     if (!valid[i]) continue;
     if (kHold && has_post) gp[i] = ld_row16(a.post + 8 * c);
     if (kHold && has_dy) gn[i] = ld_row16(a.pre + 8 * c);
-    if (GATE == 1 && team == 0) {
-      float g[8], w[8];
-      unpack8(ld_row16(gate16 + 8 * c), g);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] = 1.f;
-      if (has_post) unpack8(ld_row16(a.post + 8 * c), w);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) g[j] = gate_value(g[j], a.gate_act) * w[j];
-      gch[2 * c] = make_float4(g[0], g[1], g[2], g[3]);
-      gch[2 * c + 1] = make_float4(g[4], g[5], g[6], g[7]);
-    }
   }
   if (GATE == 1) __syncthreads();
   // post_gamma, times the channel's gate
   auto weight_of = [&](int i, float2 (&v)[4]) {
-    const int c = tid + i * nt;
     if (GATE == 1) {
-      const float4 g0 = valid[i] ? gch[2 * c] : make_float4(0.f, 0.f, 0.f, 0.f);
-      const float4 g1 = valid[i] ? gch[2 * c + 1] : make_float4(0.f, 0.f, 0.f, 0.f);
+      const float4 g0 = gch[c0 + 32 * i], g1 = gch[gch_half + c0 + 32 * i];
       v[0] = make_float2(g0.x, g0.y);
       v[1] = make_float2(g0.z, g0.w);
       v[2] = make_float2(g1.x, g1.y);
@@ -374,7 +355,7 @@ __global__ void __launch_bounds__(kSwThreads, 1)
       unpack4(gp[kHold ? i : 0], v);
     } else {
       v[0] = v[1] = v[2] = v[3] = dup(1.f);
-      if (has_post && valid[i]) unpack4(ld_row16(a.post + 8 * c), v);
+      if (has_post && valid[i]) unpack4(ld_row16(a.post + 8 * (c0 + 32 * i)), v);
     }
   };
   auto pre_of = [&](int i, float2 (&v)[4]) {
@@ -382,50 +363,60 @@ __global__ void __launch_bounds__(kSwThreads, 1)
       unpack4(gn[kHold ? i : 0], v);
     } else {
       v[0] = v[1] = v[2] = v[3] = dup(1.f);
-      if (has_dy && valid[i]) unpack4(ld_row16(a.pre + 8 * (tid + i * nt)), v);
+      if (has_dy && valid[i]) unpack4(ld_row16(a.pre + 8 * (c0 + 32 * i)), v);
     }
   };
+  // Rows t .. t + ROWS - 1 into stage st. Addresses stay inside the arrays' last row but for
+  // lanes past its end, whose copies read nothing.
+  const uint32_t mine_addr = smem_u32(mine);
+  const int n_dh = has_dh ? 16 : 0, n_dy = has_dy ? 16 : 0;
   auto fetch = [&](unsigned t, int st) {
-    if (t < T) {
-      const size_t row = (size_t)t * a.K + 8 * tid;
-      const uint32_t to = smem_u32(mine) + st * p.stage;
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      const int there = t + r < T ? 16 : 0;
+      const size_t at = (size_t)min(t + r, T - 1) * a.K + 8 * c0;
+      const uint32_t to = mine_addr + st * p.stage + r * p.row;
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
-        if (!valid[i]) continue;
-        const size_t at = row + 8 * i * nt;
-        const uint32_t base = to + i * warps * chunk;
-        if (has_dh) copy16(base + L::dh + lane16, a.dh + at);
-        if (has_dy) {
-          copy16(base + L::dy + lane16, a.dy + at);
-          if (h8) copy8(base + L::h + lane_h, static_cast<const uint8_t*>(a.h) + at);
-          else copy16(base + L::h + lane_h, static_cast<const uint16_t*>(a.h) + at);
-        }
-        if (x8) copy8(base + L::x + lane_x, static_cast<const uint8_t*>(a.x) + at);
-        else copy16(base + L::x + lane_x, static_cast<const uint16_t*>(a.x) + at);
-        if (has_res) copy16(base + L::res + lane16, a.residual + at);
-        if (GATE == 2) copy16(base + L::gate + lane16, gate16 + at);
+        const int n = valid[i] ? there : 0;
+        const uint32_t base = to + i * L::size;
+        copy16(base + L::dh + lane16, a.dh + at + 256 * i, n & n_dh);
+        copy16(base + L::dy + lane16, a.dy + at + 256 * i, n & n_dy);
+        if (h8) copy8(base + L::h + lane_h, static_cast<const uint8_t*>(a.h) + at + 256 * i, (n & n_dy) >> 1);
+        else copy16(base + L::h + lane_h, static_cast<const uint16_t*>(a.h) + at + 256 * i, n & n_dy);
+        if (x8) copy8(base + L::x + lane_x, static_cast<const uint8_t*>(a.x) + at + 256 * i, n >> 1);
+        else copy16(base + L::x + lane_x, static_cast<const uint16_t*>(a.x) + at + 256 * i, n);
+        if (GATE == 2) copy16(base + L::gate + lane16, gate16 + at + 256 * i, n);
+        if (has_res) copy16(to + res0 + 512 * i, a.residual + at + 256 * i, n);
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  // what is not worth a slot: the row's factors and scale bytes, one row ahead
+  // What is not worth a slot, one step ahead: the rows' factors and scale bytes (of the last
+  // row, where a row is not there: its values are zeros).
   struct RowScalars {
-    float r1, r2, g;
-    uint32_t xs[CH], hs[CH];
+    float r1[ROWS], r2[ROWS], g[ROWS];
+    uint32_t xs[ROWS][CH], hs[ROWS][CH];
   };
-  auto scalars = [&](unsigned t, RowScalars& r) {
-    if (t >= T) return;
-    r.r1 = has_post ? __ldg(a.rstd + t) : 1.f;
-    r.r2 = has_dy ? __ldg(a.rstd + (size_t)T + t) : 0.f;
-    r.g = GATE == 0 && a.gate_kind == 2 ? __ldg(static_cast<const float*>(a.gate) + t) : 1.f;
-    if (E8 != 0) {
-      const size_t row = (size_t)t * (a.K / 32);
+  int sc[CH];   // this thread's scale bytes
 #pragma unroll
-      for (int i = 0; i < CH; ++i) {
-        if (!valid[i]) continue;
-        const size_t at = row + ((tid + i * nt) >> 2);
-        if (x8) r.xs[i] = __ldg(a.xs + at);
-        if (h8 && has_dy) r.hs[i] = __ldg(a.hs + at);
+  for (int i = 0; i < CH; ++i) sc[i] = min(c0 + 32 * i, n8 - 1) >> 2;
+  auto scalars = [&](unsigned t0, RowScalars& s) {
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      const unsigned t = min(t0 + r, T - 1);
+      s.r1[r] = s.g[r] = 1.f;
+      s.r2[r] = 0.f;
+      if (has_post) s.r1[r] = ldg_ahead(a.rstd + t);
+      if (has_dy) s.r2[r] = ldg_ahead(a.rstd + (size_t)T + t);
+      if (GATE == 0 && a.gate_kind == 2) s.g[r] = ldg_ahead(static_cast<const float*>(a.gate) + t);
+      if (E8 != 0) {
+        const size_t row = (size_t)t * (a.K / 32);
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+          s.xs[r][i] = x8 ? ldg_u8(a.xs + row + sc[i]) : 127u;
+          s.hs[r][i] = h8 && has_dy ? ldg_u8(a.hs + row + sc[i]) : 127u;
+        }
       }
     }
   };
@@ -434,7 +425,8 @@ __global__ void __launch_bounds__(kSwThreads, 1)
   for (int i = 0; i < CH; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) s_pre[i][j] = s_x[i][j] = dup(0.f);
-  const unsigned first = blockIdx.x * p.teams + team;
+  const unsigned step = gridDim.x * p.teams * ROWS;
+  const unsigned first = (blockIdx.x * p.teams + team) * ROWS;
   RowScalars now = {}, next = {};
   scalars(first, next);
   for (int d = 0; d < p.depth; ++d) fetch(first + d * step, d);
@@ -443,92 +435,130 @@ __global__ void __launch_bounds__(kSwThreads, 1)
   for (unsigned t = first; t < T; t += step, odd ^= 1) {
     now = next;
     scalars(t + step, next);
-    const float r1 = now.r1, r2 = now.r2;
-    const float gt = GATE == 0 && a.gate_kind == 2 ? gate_value(now.g, a.gate_act) : 1.f;
+    float fx[ROWS][CH], fh[ROWS][CH];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        fx[r][i] = E8 != 0 ? e8m0_to_f32(now.xs[r][i]) : 1.f;
+        fh[r][i] = E8 != 0 ? e8m0_to_f32(now.hs[r][i]) : 1.f;
+      }
     copies_wait(p.depth - 1);
-    const uint8_t* slot = mine + (size_t)st * p.stage;
-    float2 s2[3] = {dup(0.f), dup(0.f), dup(0.f)};   // v h, w x (dh + r2 v), w x h; w without a token's gate
+    uint8_t* slot = mine + st * p.stage;
+    float2 s2[ROWS][3];   // v h, w x (dh + r2 v), w x h; w without a token's gate
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) s2[r][0] = s2[r][1] = s2[r][2] = dup(0.f);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      const uint8_t* at = slot + i * warps * chunk;
-      float2 q[4], h[4], w[4], x[4], v[4], g[4];
-      unpack4(*reinterpret_cast<const uint4*>(at + L::dh + lane16), q);
-      unpack4(*reinterpret_cast<const uint4*>(at + L::dy + lane16), v);
+      float2 g[4], w0[4];
       pre_of(i, g);
-      slot8(at + L::h + lane_h, h8, now.hs[i], h);
+      weight_of(i, w0);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        s_pre[i][j] = __ffma2_rn(v[j], __fmul2_rn(h[j], dup(r2)), s_pre[i][j]);
-        v[j] = __fmul2_rn(v[j], g[j]);
-        s2[0] = __ffma2_rn(v[j], h[j], s2[0]);
-        q[j] = __ffma2_rn(dup(r2), v[j], q[j]);
-      }
-      slot8(at + L::x + lane_x, x8, now.xs[i], x);
-      weight_of(i, w);
-      if (GATE == 2) {
-        float2 f[4];
-        unpack4(*reinterpret_cast<const uint4*>(at + L::gate + lane16), f);
+      for (int r = 0; r < ROWS; ++r) {
+        uint8_t* at = slot + r * p.row + i * L::size;
+        float2 q[4], h[4], w[4], x[4], v[4];
+        unpack4(*reinterpret_cast<const uint4*>(at + L::dh + lane16), q);
+        unpack4(*reinterpret_cast<const uint4*>(at + L::dy + lane16), v);
+        slot8(at + L::h + lane_h, h8, fh[r][i], h);
+        slot8(at + L::x + lane_x, x8, fx[r][i], x);
+        const float2 r2 = dup(now.r2[r]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          w[j] = __fmul2_rn(w[j], make_float2(gate_value(f[j].x, a.gate_act), gate_value(f[j].y, a.gate_act)));
-      }
+        for (int j = 0; j < 4; ++j) w[j] = w0[j];
+        if (GATE == 2) {
+          float2 f[4];
+          unpack4(*reinterpret_cast<const uint4*>(at + L::gate + lane16), f);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 wx = __fmul2_rn(w[j], x[j]);
-        s2[1] = __ffma2_rn(wx, q[j], s2[1]);
-        s2[2] = __ffma2_rn(wx, h[j], s2[2]);
-      }
-    }
-    float s[3] = {s2[0].x + s2[0].y, s2[1].x + s2[1].y, s2[2].x + s2[2].y};
-    team_sum3(s, part[odd], team, nt, lane, warp, warps);
-    const float c2 = s[0] * r2 * inv_k * r2;              // r2 mean(v h^)
-    const float dot = r1 * (s[1] - c2 * (r2 * s[2]));     // sum of w x^ dh_total
-    const float c1 = has_post ? gt * dot * inv_k : 0.f;
-    if (GATE == 0 && a.gate_kind == 2 && a.dgate != nullptr && tid == 0)
-      static_cast<float*>(a.dgate)[t] = a.gate_act ? dot * gt * gate_value(-now.g, 1) : dot;
-    const float2 kh = dup(-c2 * r2), k1 = dup(-r1 * r1 * c1), xr = dup(r1 * gt);
-    const size_t row = (size_t)t * a.K + 8 * tid;
-#pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      const uint8_t* at = slot + i * warps * chunk;
-      const size_t out = row + 8 * i * nt;
-      float2 d[4], x[4], w[4], v[4], g[4], h[4];   // d: dh_total
-      unpack4(*reinterpret_cast<const uint4*>(at + L::dh + lane16), d);
-      unpack4(*reinterpret_cast<const uint4*>(at + L::dy + lane16), v);
-      pre_of(i, g);
-      slot8(at + L::h + lane_h, h8, now.hs[i], h);
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        d[j] = __ffma2_rn(kh, h[j], __ffma2_rn(dup(r2), __fmul2_rn(v[j], g[j]), d[j]));
-      if (has_res) {
-        unpack4(*reinterpret_cast<const uint4*>(at + L::res + lane16), v);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) s_res = __ffma2_rn(d[j], v[j], s_res);
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = __fmul2_rn(d[j], dup(scale));
-      if (a.dres != nullptr && valid[i]) st_row16(a.dres + out, pack4(v));
-      slot8(at + L::x + lane_x, x8, now.xs[i], x);
-      weight_of(i, w);
-      // d becomes the gated gradient but for a channel's gate, whose sums take it without
-      if (GATE == 2) {
-        unpack4(*reinterpret_cast<const uint4*>(at + L::gate + lane16), v);
+          for (int j = 0; j < 4; ++j)
+            w[j] = __fmul2_rn(w[j], make_float2(gate_value(f[j].x, a.gate_act), gate_value(f[j].y, a.gate_act)));
+        }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float2 f = make_float2(gate_value(v[j].x, a.gate_act), gate_value(v[j].y, a.gate_act));
-          g[j] = __fmul2_rn(d[j], __fmul2_rn(__fmul2_rn(x[j], dup(r1)), w[j]));
-          if (a.gate_act)
-            g[j] = __fmul2_rn(g[j], make_float2(f.x * gate_value(-v[j].x, 1), f.y * gate_value(-v[j].y, 1)));
-          d[j] = __fmul2_rn(d[j], f);
+          s_pre[i][j] = __ffma2_rn(v[j], __fmul2_rn(h[j], r2), s_pre[i][j]);
+          v[j] = __fmul2_rn(v[j], g[j]);
+          s2[r][0] = __ffma2_rn(v[j], h[j], s2[r][0]);
+          q[j] = __ffma2_rn(r2, v[j], q[j]);
+          const float2 wx = __fmul2_rn(w[j], x[j]);
+          s2[r][1] = __ffma2_rn(wx, q[j], s2[r][1]);
+          s2[r][2] = __ffma2_rn(wx, h[j], s2[r][2]);
         }
-        if (a.dgate != nullptr && valid[i]) st_row16(static_cast<uint16_t*>(a.dgate) + out, pack4(g));
+        // dh + r2 v goes where dh and dy were, for the second pass
+        *reinterpret_cast<float4*>(at + L::dh + lane16) = make_float4(q[0].x, q[0].y, q[1].x, q[1].y);
+        *reinterpret_cast<float4*>(at + L::dy + lane16) = make_float4(q[2].x, q[2].y, q[3].x, q[3].y);
       }
+    }
+    float s[ROWS][3];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        s_x[i][j] = __ffma2_rn(d[j], __fmul2_rn(x[j], xr), s_x[i][j]);
-        d[j] = __ffma2_rn(k1, x[j], __fmul2_rn(__fmul2_rn(d[j], w[j]), xr));   // (no post_gamma: r1 = 1, k1 = 0)
+    for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+      for (int n = 0; n < 3; ++n) s[r][n] = s2[r][n].x + s2[r][n].y;
+    team_sum3<ROWS>(s, part[odd], team, nt, lane, warp, warps);
+    float2 kh[ROWS], k1[ROWS], xr[ROWS];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      const float r1 = now.r1[r], r2 = now.r2[r];
+      const float gt = GATE == 0 && a.gate_kind == 2 ? gate_value(now.g[r], a.gate_act) : 1.f;
+      const float c2 = s[r][0] * r2 * inv_k * r2;                 // r2 mean(v h^)
+      const float dot = r1 * (s[r][1] - c2 * (r2 * s[r][2]));     // sum of w x^ dh_total
+      const float c1 = has_post ? gt * dot * inv_k : 0.f;
+      if (GATE == 0 && a.gate_kind == 2 && a.dgate != nullptr && tid == 0 && t + r < T)
+        static_cast<float*>(a.dgate)[t + r] = a.gate_act ? dot * gt * gate_value(-now.g[r], 1) : dot;
+      kh[r] = dup(-c2 * r2);
+      k1[r] = dup(-r1 * r1 * c1);
+      xr[r] = dup(r1 * gt);
+    }
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      const size_t out = (size_t)(t + r) * a.K + 8 * c0;
+      const bool there = t + r < T;
+      const bool st_res = there && a.dres != nullptr, st_x = there && a.dx != nullptr;
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        const uint8_t* at = slot + r * p.row + i * L::size;
+        float2 d[4], x[4], v[4], h[4], w[4];   // d: dh_total
+        weight_of(i, w);
+        const float4 q0 = *reinterpret_cast<const float4*>(at + L::dh + lane16);
+        const float4 q1 = *reinterpret_cast<const float4*>(at + L::dy + lane16);
+        d[0] = make_float2(q0.x, q0.y);
+        d[1] = make_float2(q0.z, q0.w);
+        d[2] = make_float2(q1.x, q1.y);
+        d[3] = make_float2(q1.z, q1.w);
+        slot8(at + L::h + lane_h, h8, fh[r][i], h);
+        slot8(at + L::x + lane_x, x8, fx[r][i], x);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) d[j] = __ffma2_rn(kh[r], h[j], d[j]);
+        if (has_res) {
+          unpack4(*reinterpret_cast<const uint4*>(slot + r * p.row + res0 + 512 * i), v);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s_res = __ffma2_rn(d[j], v[j], s_res);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = __fmul2_rn(d[j], dup(scale));
+        uint4 o = pack4(v);
+        if (st_res && valid[i]) st_row16(a.dres + out + 256 * i, o);
+        // d becomes the gated gradient but for a channel's gate, whose sums take it without
+        if (GATE == 2) {
+          unpack4(*reinterpret_cast<const uint4*>(at + L::gate + lane16), v);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 f = make_float2(gate_value(v[j].x, a.gate_act), gate_value(v[j].y, a.gate_act));
+            h[j] = __fmul2_rn(d[j], __fmul2_rn(__fmul2_rn(x[j], xr[r]), w[j]));
+            if (a.gate_act)
+              h[j] = __fmul2_rn(h[j], make_float2(f.x * gate_value(-v[j].x, 1), f.y * gate_value(-v[j].y, 1)));
+            d[j] = __fmul2_rn(d[j], f);
+          }
+          o = pack4(h);
+          if (a.dgate != nullptr && there && valid[i])
+            st_row16(static_cast<uint16_t*>(a.dgate) + out + 256 * i, o);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          s_x[i][j] = __ffma2_rn(d[j], __fmul2_rn(x[j], xr[r]), s_x[i][j]);
+          // (no post_gamma: r1 = 1, k1 = 0)
+          d[j] = __ffma2_rn(k1[r], x[j], __fmul2_rn(__fmul2_rn(d[j], w[j]), xr[r]));
+        }
+        o = pack4(d);
+        if (st_x && valid[i]) st_row16(a.dx + out + 256 * i, o);
       }
-      if (a.dx != nullptr && valid[i]) st_row16(a.dx + out, pack4(d));
     }
     fetch(t + p.depth * step, st);
     if (++st == p.depth) st = 0;
@@ -540,7 +570,7 @@ __global__ void __launch_bounds__(kSwThreads, 1)
   float* to = p.teams > 1 ? reinterpret_cast<float*>(smem) + (size_t)team * 2 * a.K : sums;
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
-    const int c = tid + i * nt;
+    const int c = c0 + 32 * i;
     if (c >= n8) continue;
 #pragma unroll
     for (int j = 0; j < 4; j += 2) {
@@ -628,23 +658,26 @@ int row_threads(int n8, int ch) { return ((n8 + ch - 1) / ch + 31) / 32 * 32; }
 
 // Threads, rows at a time and ring of a gradient call. One CTA a SM, so that an SM
 // leaves one row of column sums; short rows share it, several teams to a CTA.
-BwdPlan bwd_plan(const SandwichBwdArgs& a, int num_sms, int ch, int e8) {
+BwdPlan bwd_plan(const SandwichBwdArgs& a, int num_sms, int ch, int e8, int rows, int maxt) {
   BwdPlan p = {};
   p.nt = row_threads(a.K / 8, ch);
-  p.teams = kSwThreads / p.nt;
-  const int rows = (int)(((unsigned)a.T + num_sms - 1) / num_sms);
-  if (p.teams > rows) p.teams = rows;
-  p.stage = p.nt / 32 * ch * slots_bytes(a.gate_kind == 3, e8, a.dscale != nullptr);
-  p.gate_bytes = a.gate_kind == 1 ? 4 * a.K : 0;
+  p.teams = maxt / p.nt;
+  const int most = (int)(((unsigned)a.T + rows * num_sms - 1) / (rows * num_sms));
+  if (p.teams > most) p.teams = most;
+  p.row = p.nt / 32 * ch * slots_bytes(a.gate_kind == 3, e8, a.dscale != nullptr);
+  p.stage = rows * p.row;
+  p.gate_bytes = a.gate_kind == 1 ? 32 * ch * p.nt : 0;
   p.depth = (kSwRingBytes - p.gate_bytes) / (p.teams * p.stage);
   if (p.depth > 4) p.depth = 4;
+  p.has_dh = a.dh != nullptr;
+  p.has_dy = a.dy != nullptr;
   p.smem = p.gate_bytes + p.teams * p.depth * p.stage;
   const int sums = p.teams > 1 ? p.teams * 8 * a.K : 0;
   if (p.smem < sums) p.smem = sums;
   return p;
 }
 
-template <int CH, int GATE, int E8>
+template <int CH, int GATE, int E8, int ROWS, int MAXT>
 cudaError_t run_bwd(const SandwichBwdArgs& a, int num_sms, int* grid, cudaStream_t stream) {
   static bool granted[kGrantDevices] = {};
   static std::mutex mu;
@@ -655,31 +688,39 @@ cudaError_t run_bwd(const SandwichBwdArgs& a, int num_sms, int* grid, cudaStream
   {
     std::lock_guard<std::mutex> lk(mu);
     if (!granted[dev]) {
-      e = cudaFuncSetAttribute(sandwich_bwd_kernel<CH, GATE, E8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      e = cudaFuncSetAttribute(sandwich_bwd_kernel<CH, GATE, E8, ROWS, MAXT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                kSwRingBytes);
       if (e != cudaSuccess) return e;
       granted[dev] = true;
     }
   }
-  const BwdPlan p = bwd_plan(a, num_sms, CH, E8);
-  *grid = (int)(((unsigned)a.T + p.teams - 1) / p.teams);   // (T + 15 may pass 2^31)
+  const BwdPlan p = bwd_plan(a, num_sms, CH, E8, ROWS, MAXT);
+  *grid = (int)(((unsigned)a.T + ROWS * p.teams - 1) / (ROWS * p.teams));   // (T + 15 may pass 2^31)
   if (*grid > num_sms) *grid = num_sms;
   if (*grid > kSwMaxCtas) *grid = kSwMaxCtas;
-  sandwich_bwd_kernel<CH, GATE, E8><<<*grid, p.teams * p.nt, p.smem, stream>>>(a, p);
+  // copies that read nothing still name rows that are there
+  SandwichBwdArgs k = a;
+  if (!p.has_dh) k.dh = a.dy;
+  if (!p.has_dy) {
+    k.dy = a.dh;
+    if (E8 == 1) k.h = a.x;
+    else k.h = a.dh, k.hs = nullptr;
+  }
+  sandwich_bwd_kernel<CH, GATE, E8, ROWS, MAXT><<<*grid, p.teams * p.nt, p.smem, stream>>>(k, p);
   return cudaGetLastError();
 }
 
-template <int CH, int E8>
+template <int CH, int E8, int ROWS, int MAXT>
 cudaError_t run_bwd_gate(const SandwichBwdArgs& a, int num_sms, int* grid, cudaStream_t stream) {
-  if (a.gate_kind == 1) return run_bwd<CH, 1, E8>(a, num_sms, grid, stream);
-  if (a.gate_kind == 3) return run_bwd<CH, 2, E8>(a, num_sms, grid, stream);
-  return run_bwd<CH, 0, E8>(a, num_sms, grid, stream);
+  if (a.gate_kind == 1) return run_bwd<CH, 1, E8, ROWS, MAXT>(a, num_sms, grid, stream);
+  if (a.gate_kind == 3) return run_bwd<CH, 2, E8, ROWS, MAXT>(a, num_sms, grid, stream);
+  return run_bwd<CH, 0, E8, ROWS, MAXT>(a, num_sms, grid, stream);
 }
-template <int CH>
+template <int CH, int ROWS, int MAXT>
 cudaError_t run_bwd_form(const SandwichBwdArgs& a, int num_sms, int* grid, cudaStream_t stream) {
   const bool x8 = a.xs != nullptr, h8 = a.dy != nullptr ? a.hs != nullptr : x8;   // (without dy h is not read)
-  if (x8 != h8) return run_bwd_gate<CH, 2>(a, num_sms, grid, stream);
-  return x8 ? run_bwd_gate<CH, 1>(a, num_sms, grid, stream) : run_bwd_gate<CH, 0>(a, num_sms, grid, stream);
+  if (x8 != h8) return run_bwd_gate<CH, 2, ROWS, MAXT>(a, num_sms, grid, stream);
+  return x8 ? run_bwd_gate<CH, 1, ROWS, MAXT>(a, num_sms, grid, stream) : run_bwd_gate<CH, 0, ROWS, MAXT>(a, num_sms, grid, stream);
 }
 
 }  // namespace
@@ -703,8 +744,9 @@ size_t sandwich_bwd_workspace_bytes(int T, int K) {
 cudaError_t launch_sandwich_norm_backward(const SandwichBwdArgs& a, int num_sms, cudaStream_t stream) {
   int grid = 0;
   if (a.T > 0) {   // (no rows: the sums are zero)
-    const cudaError_t e = a.K <= 16 * kSwThreads ? run_bwd_form<2>(a, num_sms, &grid, stream)
-                                                 : run_bwd_form<4>(a, num_sms, &grid, stream);
+    const cudaError_t e = a.K <= 16 * 384   ? run_bwd_form<2, 2, 384>(a, num_sms, &grid, stream)
+                          : a.K <= 16 * 512 ? run_bwd_form<2, 1, 512>(a, num_sms, &grid, stream)
+                                            : run_bwd_form<4, 1, 512>(a, num_sms, &grid, stream);
     if (e != cudaSuccess) return e;
   }
   if (a.dpre != nullptr || a.dpost != nullptr || a.dscale != nullptr || (a.gate_kind == 1 && a.dgate != nullptr))
