@@ -28,9 +28,20 @@ namespace {
 constexpr int kSwThreads = 512;   // most threads of a row
 constexpr int kSwRingBytes = 224 * 1024;   // shared memory of a gradient call, beside 1.7 KB of sums
 
-__device__ __forceinline__ float gate_value(float g, int act) {
-  return act ? __frcp_rn(__fadd_rn(1.f, expf(-g))) : g;
+// A gate's value and its derivative, (s, s (1 - s)) of a sigmoid: one exponential of -|g|, so that
+// neither overflows nor cancels, and a reciprocal, both approximate: a relative error below
+// 2^-21 + |g| 2^-23 (the exponent's rounding), far under the half step of 2^-8 that a bf16 gate
+// itself carries. (expf and the IEEE reciprocal: T = 4000, K = 2880 with a full gate 73 us for 55.)
+struct Gate {
+  float v, d;
+};
+__device__ __forceinline__ Gate gate_of(float g, int act) {
+  if (!act) return Gate{g, 1.f};
+  const float e = __expf(-fabsf(g));
+  const float hi = __fdividef(1.f, 1.f + e), lo = e * hi;
+  return Gate{g < 0.f ? lo : hi, hi * lo};
 }
+__device__ __forceinline__ float gate_value(float g, int act) { return gate_of(g, act).v; }
 
 // Sum over the CTA of N values, the same in every thread; part: [2][N][16], the
 // two sets in turn.
@@ -266,8 +277,8 @@ __device__ __forceinline__ float ldg_ahead(const float* p) {
   return v;
 }
 
-// Shared memory of the gradient: a channel gate's values times post_gamma (fp32, in two halves of
-// 4 values a chunk), then for every team a ring of rows. A row's slots lie by warp and
+// Shared memory of the gradient: post_gamma, times a channel's gate (fp32, in two halves of
+// 4 values a chunk; not for the longest rows without such a gate), then for every team a ring of rows. A row's slots lie by warp and
 // chunk, [dh][dy][x][h][gate] of 32 lanes each, the residual's after the warp's chunks; a
 // thread fills and reads its own slots alone. What is not there (a gradient, lanes past
 // the row, rows past the last) is filled with zeros.
@@ -302,7 +313,9 @@ __global__ void __launch_bounds__(MAXT, 1)
   __shared__ float part[2][3 * ROWS][32];
   __shared__ float last[32];
   using L = Slots<GATE, E8>;
-  constexpr bool kHold = CH <= 2;   // gammas stay in registers
+  // pre_gamma in registers and the weights in shared memory. A spilled register is dear
+  // here: beside the ring L1 is a few KB, so that it comes back from L2.
+  constexpr bool kHold = CH <= 2, kWeights = kHold || GATE == 1;
   const int nt = p.nt, team = threadIdx.x / nt, tid = threadIdx.x - team * nt;
   const int lane = tid & 31, warp = tid >> 5, warps = nt >> 5;
   const int n8 = a.K / 8, c0 = warp * (32 * CH) + lane;   // this thread's chunks: c0 + 32 i
@@ -319,40 +332,37 @@ __global__ void __launch_bounds__(MAXT, 1)
   float4* gch = reinterpret_cast<float4*>(smem);   // [2][chunks of a team]
   const int gch_half = CH * nt;
   bool valid[CH];
-  uint4 gp[kHold ? CH : 1], gn[kHold ? CH : 1];
+  uint4 gn[kHold ? CH : 1];
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const int c = c0 + 32 * i;
     valid[i] = c < n8;
-    if (kHold) gp[i] = gn[i] = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);   // 1
-    if (GATE == 1 && team == 0) {
+    if (kHold) gn[i] = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);   // 1
+    if (kWeights && team == 0) {
       float g[8], w[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) g[j] = w[j] = 1.f;
       if (valid[i]) {
-        unpack8(ld_row16(gate16 + 8 * c), g);
+        if (GATE == 1) unpack8(ld_row16(gate16 + 8 * c), g);
         if (has_post) unpack8(ld_row16(a.post + 8 * c), w);
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) g[j] = gate_value(g[j], a.gate_act) * w[j];
+      for (int j = 0; j < 8; ++j) g[j] = GATE == 1 ? gate_value(g[j], a.gate_act) * w[j] : w[j];
       gch[c] = make_float4(g[0], g[1], g[2], g[3]);
       gch[gch_half + c] = make_float4(g[4], g[5], g[6], g[7]);
     }
     if (!valid[i]) continue;
-    if (kHold && has_post) gp[i] = ld_row16(a.post + 8 * c);
     if (kHold && has_dy) gn[i] = ld_row16(a.pre + 8 * c);
   }
-  if (GATE == 1) __syncthreads();
+  if (kWeights) __syncthreads();
   // post_gamma, times the channel's gate
   auto weight_of = [&](int i, float2 (&v)[4]) {
-    if (GATE == 1) {
+    if (kWeights) {
       const float4 g0 = gch[c0 + 32 * i], g1 = gch[gch_half + c0 + 32 * i];
       v[0] = make_float2(g0.x, g0.y);
       v[1] = make_float2(g0.z, g0.w);
       v[2] = make_float2(g1.x, g1.y);
       v[3] = make_float2(g1.z, g1.w);
-    } else if (kHold) {
-      unpack4(gp[kHold ? i : 0], v);
     } else {
       v[0] = v[1] = v[2] = v[3] = dup(1.f);
       if (has_post && valid[i]) unpack4(ld_row16(a.post + 8 * (c0 + 32 * i)), v);
@@ -427,6 +437,7 @@ __global__ void __launch_bounds__(MAXT, 1)
     for (int j = 0; j < 4; ++j) s_pre[i][j] = s_x[i][j] = dup(0.f);
   const unsigned step = gridDim.x * p.teams * ROWS;
   const unsigned first = (blockIdx.x * p.teams + team) * ROWS;
+  grid_launch_dependents();
   RowScalars now = {}, next = {};
   scalars(first, next);
   for (int d = 0; d < p.depth; ++d) fetch(first + d * step, d);
@@ -501,7 +512,7 @@ __global__ void __launch_bounds__(MAXT, 1)
       const float dot = r1 * (s[r][1] - c2 * (r2 * s[r][2]));     // sum of w x^ dh_total
       const float c1 = has_post ? gt * dot * inv_k : 0.f;
       if (GATE == 0 && a.gate_kind == 2 && a.dgate != nullptr && tid == 0 && t + r < T)
-        static_cast<float*>(a.dgate)[t + r] = a.gate_act ? dot * gt * gate_value(-now.g[r], 1) : dot;
+        static_cast<float*>(a.dgate)[t + r] = dot * gate_of(now.g[r], a.gate_act).d;
       kh[r] = dup(-c2 * r2);
       k1[r] = dup(-r1 * r1 * c1);
       xr[r] = dup(r1 * gt);
@@ -540,11 +551,10 @@ __global__ void __launch_bounds__(MAXT, 1)
           unpack4(*reinterpret_cast<const uint4*>(at + L::gate + lane16), v);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float2 f = make_float2(gate_value(v[j].x, a.gate_act), gate_value(v[j].y, a.gate_act));
-            h[j] = __fmul2_rn(d[j], __fmul2_rn(__fmul2_rn(x[j], xr[r]), w[j]));
-            if (a.gate_act)
-              h[j] = __fmul2_rn(h[j], make_float2(f.x * gate_value(-v[j].x, 1), f.y * gate_value(-v[j].y, 1)));
-            d[j] = __fmul2_rn(d[j], f);
+            const Gate fx = gate_of(v[j].x, a.gate_act), fy = gate_of(v[j].y, a.gate_act);
+            h[j] = __fmul2_rn(__fmul2_rn(d[j], make_float2(fx.d, fy.d)),
+                              __fmul2_rn(__fmul2_rn(x[j], xr[r]), w[j]));
+            d[j] = __fmul2_rn(d[j], make_float2(fx.v, fy.v));
           }
           o = pack4(h);
           if (a.dgate != nullptr && there && valid[i])
@@ -609,13 +619,17 @@ __global__ void __launch_bounds__(MAXT, 1)
 }
 
 // The columns' sums over the CTAs' rows of ws, in the order of the CTAs; 32
-// columns a CTA, a row group a warp.
-__global__ void __launch_bounds__(256) sandwich_columns_kernel(const SandwichBwdArgs a, int rows) {
-  __shared__ float part[2][8][32];
+// columns a CTA, every 16th row a warp, so that few loads follow one another. Launched
+// while the rows' kernel still runs; waits for its end before it reads.
+constexpr int kColWarps = 16;
+__global__ void __launch_bounds__(32 * kColWarps) sandwich_columns_kernel(const SandwichBwdArgs a, int rows) {
+  __shared__ float part[2][kColWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int k = blockIdx.x * 32 + lane;   // K is a multiple of 32
+  grid_dependency_wait();
   float s0 = 0.f, s1 = 0.f;
-  for (int r = warp; r < rows; r += 8) {
+#pragma unroll 8
+  for (int r = warp; r < rows; r += kColWarps) {
     const float* p = a.ws + (size_t)r * 2 * a.K + k;
     s0 += p[0];
     s1 += p[a.K];
@@ -626,21 +640,18 @@ __global__ void __launch_bounds__(256) sandwich_columns_kernel(const SandwichBwd
   if (warp == 0) {
     s0 = s1 = 0.f;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) {
+    for (int w = 0; w < kColWarps; ++w) {
       s0 += part[0][w][lane];
       s1 += part[1][w][lane];
     }
     if (a.dpre != nullptr) a.dpre[k] = s0;
-    float gv = 1.f, dv = 1.f;
-    if (a.gate_kind == 1) {
-      const float g = __uint_as_float((uint32_t)static_cast<const uint16_t*>(a.gate)[k] << 16);
-      gv = gate_value(g, a.gate_act);
-      if (a.gate_act) dv = gv * gate_value(-g, 1);
-    }
-    if (a.dpost != nullptr) a.dpost[k] = gv * s1;
+    Gate g = {1.f, 1.f};
+    if (a.gate_kind == 1)
+      g = gate_of(__uint_as_float((uint32_t)static_cast<const uint16_t*>(a.gate)[k] << 16), a.gate_act);
+    if (a.dpost != nullptr) a.dpost[k] = g.v * s1;
     if (a.gate_kind == 1 && a.dgate != nullptr) {
       const float p = a.post != nullptr ? __uint_as_float((uint32_t)a.post[k] << 16) : 1.f;
-      static_cast<float*>(a.dgate)[k] = dv * (p * s1);
+      static_cast<float*>(a.dgate)[k] = g.d * (p * s1);
     }
   }
   if (a.dscale != nullptr && blockIdx.x == 0 && warp == 1) {
@@ -666,7 +677,7 @@ BwdPlan bwd_plan(const SandwichBwdArgs& a, int num_sms, int ch, int e8, int rows
   if (p.teams > most) p.teams = most;
   p.row = p.nt / 32 * ch * slots_bytes(a.gate_kind == 3, e8, a.dscale != nullptr);
   p.stage = rows * p.row;
-  p.gate_bytes = a.gate_kind == 1 ? 32 * ch * p.nt : 0;
+  p.gate_bytes = ch <= 2 || a.gate_kind == 1 ? 32 * ch * p.nt : 0;
   p.depth = (kSwRingBytes - p.gate_bytes) / (p.teams * p.stage);
   if (p.depth > 4) p.depth = 4;
   p.has_dh = a.dh != nullptr;
@@ -723,6 +734,19 @@ cudaError_t run_bwd_form(const SandwichBwdArgs& a, int num_sms, int* grid, cudaS
   return x8 ? run_bwd_gate<CH, 1, ROWS, MAXT>(a, num_sms, grid, stream) : run_bwd_gate<CH, 0, ROWS, MAXT>(a, num_sms, grid, stream);
 }
 
+cudaError_t run_columns(const SandwichBwdArgs& a, int rows, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.K / 32);
+  cfg.blockDim = dim3(32 * kColWarps);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = rows > 0 ? 1 : 0;   // (no rows: nothing of this call runs before it)
+  return cudaLaunchKernelEx(&cfg, sandwich_columns_kernel, a, rows);
+}
+
 }  // namespace
 
 cudaError_t launch_sandwich_norm(const SandwichArgs& a, int num_sms, cudaStream_t stream) {
@@ -744,14 +768,14 @@ size_t sandwich_bwd_workspace_bytes(int T, int K) {
 cudaError_t launch_sandwich_norm_backward(const SandwichBwdArgs& a, int num_sms, cudaStream_t stream) {
   int grid = 0;
   if (a.T > 0) {   // (no rows: the sums are zero)
-    const cudaError_t e = a.K <= 16 * 384   ? run_bwd_form<2, 2, 384>(a, num_sms, &grid, stream)
+    const cudaError_t e = a.K <= 16 * 384 && a.T > num_sms / 2 ? run_bwd_form<2, 2, 384>(a, num_sms, &grid, stream)
                           : a.K <= 16 * 512 ? run_bwd_form<2, 1, 512>(a, num_sms, &grid, stream)
                                             : run_bwd_form<4, 1, 512>(a, num_sms, &grid, stream);
     if (e != cudaSuccess) return e;
   }
   if (a.dpre != nullptr || a.dpost != nullptr || a.dscale != nullptr || (a.gate_kind == 1 && a.dgate != nullptr))
-    sandwich_columns_kernel<<<a.K / 32, 256, 0, stream>>>(a, grid);
-  return cudaGetLastError();
+    return run_columns(a, grid, stream);
+  return cudaSuccess;
 }
 
 }  // namespace mxmoe
