@@ -25,7 +25,6 @@
 namespace mxmoe {
 namespace {
 
-constexpr int kSwThreads = 512;   // most threads of a row
 constexpr int kSwRingBytes = 224 * 1024;   // shared memory of a gradient call, beside 1.7 KB of sums
 
 // A gate's value and its derivative, (s, s (1 - s)) of a sigmoid: one exponential of -|g|, so that
@@ -43,29 +42,213 @@ __device__ __forceinline__ Gate gate_of(float g, int act) {
 }
 __device__ __forceinline__ float gate_value(float g, int act) { return gate_of(g, act).v; }
 
-// Sum over the CTA of N values, the same in every thread; part: [2][N][16], the
-// two sets in turn.
-template <int N>
-__device__ __forceinline__ void cta_sums(float (&v)[N], float (*part)[16], int lane, int warp, int warps) {
+__device__ __forceinline__ float2 dup(float v) { return make_float2(v, v); }
+__device__ __forceinline__ void unpack4(const uint4& u, float2 (&v)[4]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-    for (int n = 0; n < N; ++n) v[n] += __shfl_xor_sync(0xffffffffu, v[n], o);
-  if (lane == 0) {
-#pragma unroll
-    for (int n = 0; n < N; ++n) part[n][warp] = v[n];
-  }
-  __syncthreads();
-#pragma unroll
-  for (int n = 0; n < N; ++n) v[n] = lane < warps ? part[n][lane] : 0.f;
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1)
-#pragma unroll
-    for (int n = 0; n < N; ++n) v[n] += __shfl_xor_sync(0xffffffffu, v[n], o);
-#pragma unroll
-  for (int n = 0; n < N; ++n) v[n] = __shfl_sync(0xffffffffu, v[n], 0);
+  for (int j = 0; j < 4; ++j)
+    v[j] = make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u));
+}
+__device__ __forceinline__ uint4 pack4(const float2 (&v)[4]) {
+  return make_uint4(bf16x2_rn(v[0].x, v[0].y), bf16x2_rn(v[1].x, v[1].y), bf16x2_rn(v[2].x, v[2].y),
+                    bf16x2_rn(v[3].x, v[3].y));
+}
+// 16 (8) bytes, or zeros where n is 0: nothing is read then.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int n) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void copy8(uint32_t dst, const void* src, int n) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+// All but the latest n (0..3) groups of this thread's copies have landed.
+__device__ __forceinline__ void copies_wait(int n) {
+  if (n == 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
+  else if (n == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else if (n == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+  else asm volatile("cp.async.wait_group 3;" ::: "memory");
 }
 
+// Loads that stay where they are written, ahead of their use.
+__device__ __forceinline__ float ldg_ahead(const float* p) {
+  float v;
+  asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
+}
+
+// Sum of v over a team of nt threads of the CTA (its own named barrier, none for one
+// warp); part: [32], a place a warp of the CTA.
+__device__ __forceinline__ float team_sum(float v, float* part, int team, int nt, int lane, int warp, int warps) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (warps == 1) return v;
+  const int base = team * warps, at = lane & 15;   // at most 16 warps
+  if (lane == 0) part[base + warp] = v;
+  named_barrier(team + 1, nt);
+  v = at < warps ? part[base + at] : 0.f;
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Shared memory of a forward call: the gammas (bf16), a channel's gate (fp32, in two halves of 4
+// values a chunk), then for every team a ring of rows. A row's slots lie by warp and chunk,
+// [x][residual][gate] of 32 lanes each; a thread fills and reads its own slots alone.
+struct FwdPlan {
+  int nt, teams, depth;   // threads of a team, teams, rows of a ring (1..4)
+  int pre, gate, ring;    // byte offsets (post_gamma at 0)
+  int slot, row;          // bytes of a warp's slots of a chunk, of a row
+  int smem;
+};
+
+// MXFP8 of 8 values: the 4 lanes of a block call together.
+__device__ __forceinline__ void store_mx8(const float2 (&v)[4], int nosat, bool valid, uint8_t* q, uint8_t* scale,
+                                          bool first) {
+  const float f[8] = {v[0].x, v[0].y, v[1].x, v[1].y, v[2].x, v[2].y, v[3].x, v[3].y};
+  const Mx8 e = mx8_block(f, max_bits8(f), nosat);
+  if (valid) {
+    *reinterpret_cast<uint2*>(q) = e.q;
+    if (first) *scale = (uint8_t)e.s;
+  }
+}
+
+// A team of warps to a row, CH * 32 chunks in a row to a warp; short rows share a CTA.
+template <int CH, int MAXT, int PER_SM>
+__global__ void __launch_bounds__(MAXT, PER_SM) sandwich_norm_kernel(const SandwichArgs a, const FwdPlan p) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ float part[2][2][32];
+  const int nt = p.nt, team = threadIdx.x / nt, tid = threadIdx.x - team * nt;
+  const int lane = tid & 31, warp = tid >> 5, warps = nt >> 5;
+  const int n8 = a.K / 8, c0 = warp * (32 * CH) + lane;   // this thread's chunks: c0 + 32 i
+  const unsigned T = (unsigned)a.T;   // unsigned: T + the step may pass 2^31
+  const bool has_post = a.post != nullptr, has_pre = a.pre != nullptr, scaled_res = a.rscale != nullptr;
+  const float scale = scaled_res ? *a.rscale : 1.f;
+  const uint16_t* gate16 = static_cast<const uint16_t*>(a.gate);
+  uint8_t* mine = smem + p.ring + (size_t)team * p.depth * p.row + warp * (CH * p.slot) + 16 * lane;
+  const uint32_t mine_addr = smem_u32(mine);
+  uint4* post = reinterpret_cast<uint4*>(smem);
+  uint4* pre = reinterpret_cast<uint4*>(smem + p.pre);
+  float4* gch = reinterpret_cast<float4*>(smem + p.gate);
+  const int half = CH * nt;
+  bool valid[CH];
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int c = c0 + 32 * i;
+    valid[i] = c < n8;
+    if (team != 0) continue;
+    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+    if (has_post) post[c] = valid[i] ? ld_row16(a.post + 8 * c) : z;
+    if (has_pre) pre[c] = valid[i] ? ld_row16(a.pre + 8 * c) : z;
+    if (a.gate_kind == 1) {
+      float g[8];
+      unpack8(valid[i] ? ld_row16(gate16 + 8 * c) : z, g);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) g[j] = gate_value(g[j], a.gate_act);
+      gch[c] = make_float4(g[0], g[1], g[2], g[3]);
+      gch[half + c] = make_float4(g[4], g[5], g[6], g[7]);
+    }
+  }
+  // row t into stage st; lanes past its end copy nothing
+  auto fetch = [&](unsigned t, int st) {
+    const size_t at = (size_t)min(t, T - 1) * a.K + 8 * c0;
+    const uint32_t to = mine_addr + st * p.row;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int n = t < T && valid[i] ? 16 : 0;
+      copy16(to + i * p.slot, a.x + at + 256 * i, n);
+      copy16(to + i * p.slot + 512, a.residual + at + 256 * i, n);
+      if (a.gate_kind == 3) copy16(to + i * p.slot + 1024, gate16 + at + 256 * i, n);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  const unsigned step = gridDim.x * p.teams;
+  const unsigned first = blockIdx.x * p.teams + team;
+  for (int d = 0; d < p.depth; ++d) fetch(first + d * step, d);
+  float g_next = a.gate_kind == 2 && first < T ? ldg_ahead(static_cast<const float*>(a.gate) + first) : 1.f;
+  __syncthreads();
+  const float inv_k = 1.f / (float)a.K;
+  int odd = 0, st = 0;
+  for (unsigned t = first; t < T; t += step, odd ^= 1) {
+    const size_t out = (size_t)t * a.K + 8 * c0;
+    const size_t sout = (size_t)t * (a.K / 32) + (c0 >> 2);
+    const float g_raw = g_next;
+    if (a.gate_kind == 2 && t + step < T) g_next = ldg_ahead(static_cast<const float*>(a.gate) + t + step);
+    copies_wait(p.depth - 1);
+    const uint8_t* slot = mine + st * p.row;
+    float2 h[CH][4], ss = dup(0.f);
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      unpack4(*reinterpret_cast<const uint4*>(slot + i * p.slot), h[i]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) ss = __ffma2_rn(h[i][j], h[i][j], ss);
+      if (a.x8 != nullptr)
+        store_mx8(h[i], a.ck_nosat, valid[i], a.x8 + out + 256 * i, a.xs8 + sout + 8 * i, (lane & 3) == 0);
+    }
+    float r1 = 1.f;
+    if (has_post) r1 = rsqrt2(team_sum(ss.x + ss.y, part[odd][0], team, nt, lane, warp, warps) * inv_k + a.eps).hi;
+    const float gt = a.gate_kind == 2 ? gate_value(g_raw, a.gate_act) : 1.f;
+    ss = dup(0.f);
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      float2 z[4];
+      unpack4(*reinterpret_cast<const uint4*>(slot + i * p.slot + 512), z);
+      if (has_post) {
+        float2 g[4];
+        unpack4(post[c0 + 32 * i], g);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h[i][j] = __fmul2_rn(__fmul2_rn(h[i][j], dup(r1)), g[j]);
+      }
+      if (scaled_res) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) z[j] = __fmul2_rn(z[j], dup(scale));
+      }
+      float2 g[4] = {dup(gt), dup(gt), dup(gt), dup(gt)};
+      if (a.gate_kind == 1) {
+        const float4 g0 = gch[c0 + 32 * i], g1 = gch[half + c0 + 32 * i];
+        g[0] = make_float2(g0.x, g0.y);
+        g[1] = make_float2(g0.z, g0.w);
+        g[2] = make_float2(g1.x, g1.y);
+        g[3] = make_float2(g1.z, g1.w);
+      } else if (a.gate_kind == 3) {
+        unpack4(*reinterpret_cast<const uint4*>(slot + i * p.slot + 1024), g);
+        if (a.gate_act) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) g[j] = make_float2(gate_value(g[j].x, 1), gate_value(g[j].y, 1));
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        h[i][j] = __ffma2_rn(g[j], h[i][j], z[j]);
+        ss = __ffma2_rn(h[i][j], h[i][j], ss);
+      }
+      if (a.h_out != nullptr && valid[i]) st_row16(a.h_out + out + 256 * i, pack4(h[i]));
+      if (a.h8 != nullptr)
+        store_mx8(h[i], a.ck_nosat, valid[i], a.h8 + out + 256 * i, a.hs8 + sout + 8 * i, (lane & 3) == 0);
+    }
+    fetch(t + p.depth * step, st);
+    if (++st == p.depth) st = 0;
+    float r2 = 1.f;
+    if (has_pre) {
+      r2 = rsqrt2(team_sum(ss.x + ss.y, part[odd][1], team, nt, lane, warp, warps) * inv_k + a.eps).hi;
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        float2 g[4];
+        unpack4(pre[c0 + 32 * i], g);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h[i][j] = __fmul2_rn(__fmul2_rn(h[i][j], dup(r2)), g[j]);
+        if (a.out != nullptr && valid[i]) st_row16(a.out + out + 256 * i, pack4(h[i]));
+        if (a.q8 != nullptr)
+          store_mx8(h[i], a.nosat, valid[i], a.q8 + out + 256 * i, a.s8 + sout + 8 * i, (lane & 3) == 0);
+      }
+    }
+    if (a.rstd != nullptr && tid == 0) {
+      a.rstd[t] = r1;
+      a.rstd[(size_t)T + t] = r2;
+    }
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+// ---------------------------------------------------------------- gradient
 // Three sums at once: lanes give up one of two values where a butterfly step would
 // carry both (13 shuffles for 27). Lane 0 ends with the first, 16 the second, 8 the third.
 __device__ __forceinline__ float merge3(float a, float b, float c, int lane) {
@@ -108,140 +291,6 @@ __device__ __forceinline__ void team_sum3(float (&v)[ROWS][3], float (*part)[32]
   }
 }
 
-// CH: 16-byte chunks per thread (K / 8 <= CH * blockDim.x).
-template <int CH>
-__global__ void __launch_bounds__(kSwThreads) sandwich_norm_kernel(const SandwichArgs a) {
-  __shared__ float part[2][2][16];
-  const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
-  const int n8 = a.K / 8;
-  const unsigned T = (unsigned)a.T;   // unsigned: T + gridDim.x may pass 2^31
-  const float scale = a.rscale != nullptr ? *a.rscale : 1.f;
-  int odd = 0;
-  for (unsigned t = blockIdx.x; t < T; t += gridDim.x, odd ^= 1) {
-    const size_t row = (size_t)t * a.K;
-    float h[CH][8];
-    float ss[1] = {0.f};
-#pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      const int c = tid + i * nt;
-      const bool valid = c < n8;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) h[i][j] = 0.f;
-      if (valid) unpack8(ld_row16(a.x + row + 8 * c), h[i]);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) ss[0] += h[i][j] * h[i][j];
-      if (a.x8 != nullptr) {
-        const Mx8 e = mx8_block(h[i], max_bits8(h[i]), a.ck_nosat);
-        if (valid) {
-          *reinterpret_cast<uint2*>(a.x8 + row + 8 * c) = e.q;
-          if ((c & 3) == 0) a.xs8[(size_t)t * (a.K / 32) + (c >> 2)] = (uint8_t)e.s;
-        }
-      }
-    }
-    Root r1 = {1.f, 0.f};
-    if (a.post != nullptr) {
-      cta_sums<1>(ss, part[odd], lane, warp, nt >> 5);
-      r1 = rsqrt2(ss[0] / (float)a.K + a.eps);
-    }
-    const float gt = a.gate_kind == 2 ? gate_value(static_cast<const float*>(a.gate)[t], a.gate_act) : 1.f;
-    ss[0] = 0.f;
-#pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      const int c = tid + i * nt;
-      const bool valid = c < n8;
-      if (valid) {
-        if (a.post != nullptr) {
-          float g[8], n[8];
-          unpack8(ld_row16(a.post + 8 * c), g);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) n[j] = scaled(h[i][j], r1, g[j]);
-          if (__builtin_expect(max_bits8(n) >= 0x7F800000u, 0)) {   // infinities leave no remainder
-#pragma unroll
-            for (int j = 0; j < 8; ++j) n[j] = (h[i][j] * r1.hi) * g[j];
-          }
-#pragma unroll
-          for (int j = 0; j < 8; ++j) h[i][j] = n[j];
-        }
-        float z[8];
-        unpack8(ld_row16(a.residual + row + 8 * c), z);
-        if (a.rscale != nullptr) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) z[j] = __fmul_rn(z[j], scale);
-        }
-        if (a.gate_kind == 0) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) h[i][j] += z[j];
-        } else if (a.gate_kind == 2) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) h[i][j] = fmaf(gt, h[i][j], z[j]);
-        } else {
-          float g[8];
-          unpack8(ld_row16(static_cast<const uint16_t*>(a.gate) + (a.gate_kind == 3 ? row : 0) + 8 * c), g);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) h[i][j] = fmaf(gate_value(g[j], a.gate_act), h[i][j], z[j]);
-        }
-        if (a.h_out != nullptr) st_row16(a.h_out + row + 8 * c, pack8(h[i]));
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) ss[0] += h[i][j] * h[i][j];
-      if (a.h8 != nullptr) {
-        const Mx8 e = mx8_block(h[i], max_bits8(h[i]), a.ck_nosat);
-        if (valid) {
-          *reinterpret_cast<uint2*>(a.h8 + row + 8 * c) = e.q;
-          if ((c & 3) == 0) a.hs8[(size_t)t * (a.K / 32) + (c >> 2)] = (uint8_t)e.s;
-        }
-      }
-    }
-    Root r2 = {1.f, 0.f};
-    if (a.pre != nullptr) {
-      cta_sums<1>(ss, part[odd] + 1, lane, warp, nt >> 5);
-      r2 = rsqrt2(ss[0] / (float)a.K + a.eps);
-#pragma unroll
-      for (int i = 0; i < CH; ++i) {
-        const int c = tid + i * nt;
-        const bool valid = c < n8;
-        float y[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = 0.f;
-        if (valid) {
-          float g[8];
-          unpack8(ld_row16(a.pre + 8 * c), g);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) y[j] = scaled(h[i][j], r2, g[j]);
-          if (__builtin_expect(max_bits8(y) >= 0x7F800000u, 0)) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = (h[i][j] * r2.hi) * g[j];
-          }
-          if (a.out != nullptr) st_row16(a.out + row + 8 * c, pack8(y));
-        }
-        if (a.q8 != nullptr) {
-          const Mx8 e = mx8_block(y, max_bits8(y), a.nosat);
-          if (valid) {
-            *reinterpret_cast<uint2*>(a.q8 + row + 8 * c) = e.q;
-            if ((c & 3) == 0) a.s8[(size_t)t * (a.K / 32) + (c >> 2)] = (uint8_t)e.s;
-          }
-        }
-      }
-    }
-    if (a.rstd != nullptr && tid == 0) {
-      a.rstd[t] = r1.hi;
-      a.rstd[(size_t)T + t] = r2.hi;
-    }
-  }
-}
-
-// ---------------------------------------------------------------- gradient
-__device__ __forceinline__ float2 dup(float v) { return make_float2(v, v); }
-__device__ __forceinline__ void unpack4(const uint4& u, float2 (&v)[4]) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    v[j] = make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u));
-}
-__device__ __forceinline__ uint4 pack4(const float2 (&v)[4]) {
-  return make_uint4(bf16x2_rn(v[0].x, v[0].y), bf16x2_rn(v[1].x, v[1].y), bf16x2_rn(v[2].x, v[2].y),
-                    bf16x2_rn(v[3].x, v[3].y));
-}
 // 8 values from shared memory: bf16, or E4M3 with their block's factor.
 __device__ __forceinline__ void slot8(const uint8_t* p, bool e4m3, float scale, float2 (&v)[4]) {
   if (!e4m3) {
@@ -255,28 +304,6 @@ __device__ __forceinline__ void slot8(const uint8_t* p, bool e4m3, float scale, 
   v[2] = __fmul2_rn(e4m3x2_values((uint16_t)q.y), f);
   v[3] = __fmul2_rn(e4m3x2_values((uint16_t)(q.y >> 16)), f);
 }
-// 16 (8) bytes, or zeros where n is 0: nothing is read then.
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int n) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void copy8(uint32_t dst, const void* src, int n) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-// All but the latest n (0..3) groups of this thread's copies have landed.
-__device__ __forceinline__ void copies_wait(int n) {
-  if (n == 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
-  else if (n == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
-  else if (n == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
-  else asm volatile("cp.async.wait_group 3;" ::: "memory");
-}
-
-// Loads that stay where they are written, ahead of their use.
-__device__ __forceinline__ float ldg_ahead(const float* p) {
-  float v;
-  asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
-  return v;
-}
-
 // Shared memory of the gradient: post_gamma, times a channel's gate (fp32, in two halves of
 // 4 values a chunk; not for the longest rows without such a gate), then for every team a ring of rows. A row's slots lie by warp and
 // chunk, [dh][dy][x][h][gate] of 32 lanes each, the residual's after the warp's chunks; a
@@ -663,9 +690,49 @@ __global__ void __launch_bounds__(32 * kColWarps) sandwich_columns_kernel(const 
   }
 }
 
-// Chunks a thread and threads a row.
-int row_chunks(int n8) { return n8 > 2 * kSwThreads ? 4 : n8 > kSwThreads ? 2 : 1; }
+// Threads of a row of n8 chunks, ch a thread.
 int row_threads(int n8, int ch) { return ((n8 + ch - 1) / ch + 31) / 32 * 32; }
+
+// Lets a kernel have this much dynamic shared memory, once a device.
+cudaError_t grant_smem(const void* kernel, int bytes, bool (&granted)[kGrantDevices], std::mutex& mu) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kGrantDevices) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lk(mu);
+  if (granted[dev]) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  granted[dev] = e == cudaSuccess;
+  return e;
+}
+
+template <int CH, int MAXT, int PER_SM>
+cudaError_t run_fwd(const SandwichArgs& a, int num_sms, cudaStream_t stream) {
+  constexpr int kRing = PER_SM == 2 ? 110 * 1024 : kSwRingBytes;
+  static bool granted[kGrantDevices] = {};
+  static std::mutex mu;
+  const auto kernel = sandwich_norm_kernel<CH, MAXT, PER_SM>;
+  const cudaError_t e = grant_smem(reinterpret_cast<const void*>(kernel), kRing, granted, mu);
+  if (e != cudaSuccess) return e;
+  FwdPlan p = {};
+  p.nt = row_threads(a.K / 8, CH);
+  p.teams = MAXT / p.nt;
+  const int ctas = PER_SM * num_sms, most = (int)(((unsigned)a.T + ctas - 1) / ctas);
+  if (p.teams > most) p.teams = most;
+  const int chunks = CH * p.nt;
+  p.pre = a.post != nullptr ? 16 * chunks : 0;
+  p.gate = p.pre + (a.pre != nullptr ? 16 * chunks : 0);
+  p.ring = p.gate + (a.gate_kind == 1 ? 32 * chunks : 0);
+  p.slot = a.gate_kind == 3 ? 1536 : 1024;
+  p.row = chunks / 32 * p.slot;
+  p.depth = (kRing - p.ring) / (p.teams * p.row);
+  if (p.depth > 4) p.depth = 4;
+  p.smem = p.ring + p.teams * p.depth * p.row;
+  const unsigned want = ((unsigned)a.T + p.teams - 1) / p.teams;
+  const int grid = want < (unsigned)ctas ? (int)want : ctas;
+  kernel<<<grid, p.teams * p.nt, p.smem, stream>>>(a, p);
+  return cudaGetLastError();
+}
 
 // Threads, rows at a time and ring of a gradient call. One CTA a SM, so that an SM
 // leaves one row of column sums; short rows share it, several teams to a CTA.
@@ -692,19 +759,9 @@ template <int CH, int GATE, int E8, int ROWS, int MAXT>
 cudaError_t run_bwd(const SandwichBwdArgs& a, int num_sms, int* grid, cudaStream_t stream) {
   static bool granted[kGrantDevices] = {};
   static std::mutex mu;
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  const auto kernel = sandwich_bwd_kernel<CH, GATE, E8, ROWS, MAXT>;
+  const cudaError_t e = grant_smem(reinterpret_cast<const void*>(kernel), kSwRingBytes, granted, mu);
   if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= kGrantDevices) return cudaErrorInvalidDevice;
-  {
-    std::lock_guard<std::mutex> lk(mu);
-    if (!granted[dev]) {
-      e = cudaFuncSetAttribute(sandwich_bwd_kernel<CH, GATE, E8, ROWS, MAXT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               kSwRingBytes);
-      if (e != cudaSuccess) return e;
-      granted[dev] = true;
-    }
-  }
   const BwdPlan p = bwd_plan(a, num_sms, CH, E8, ROWS, MAXT);
   *grid = (int)(((unsigned)a.T + ROWS * p.teams - 1) / (ROWS * p.teams));   // (T + 15 may pass 2^31)
   if (*grid > num_sms) *grid = num_sms;
@@ -717,7 +774,7 @@ cudaError_t run_bwd(const SandwichBwdArgs& a, int num_sms, int* grid, cudaStream
     if (E8 == 1) k.h = a.x;
     else k.h = a.dh, k.hs = nullptr;
   }
-  sandwich_bwd_kernel<CH, GATE, E8, ROWS, MAXT><<<*grid, p.teams * p.nt, p.smem, stream>>>(k, p);
+  kernel<<<*grid, p.teams * p.nt, p.smem, stream>>>(k, p);
   return cudaGetLastError();
 }
 
@@ -750,14 +807,8 @@ cudaError_t run_columns(const SandwichBwdArgs& a, int rows, cudaStream_t stream)
 }  // namespace
 
 cudaError_t launch_sandwich_norm(const SandwichArgs& a, int num_sms, cudaStream_t stream) {
-  const int n8 = a.K / 8, ch = row_chunks(n8), nt = row_threads(n8, ch);
-  int per_sm = 1024 / nt;
-  if (per_sm > 8) per_sm = 8;
-  const int grid = a.T < per_sm * num_sms ? a.T : per_sm * num_sms;
-  if (ch == 1) sandwich_norm_kernel<1><<<grid, nt, 0, stream>>>(a);
-  else if (ch == 2) sandwich_norm_kernel<2><<<grid, nt, 0, stream>>>(a);
-  else sandwich_norm_kernel<4><<<grid, nt, 0, stream>>>(a);
-  return cudaGetLastError();
+  if (a.K <= 16 * 384) return run_fwd<2, 384, 2>(a, num_sms, stream);
+  return run_fwd<4, 512, 1>(a, num_sms, stream);
 }
 
 size_t sandwich_bwd_workspace_bytes(int T, int K) {
