@@ -81,12 +81,12 @@ __device__ __forceinline__ float team_sum(float v, float* part, int team, int nt
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   if (warps == 1) return v;
-  const int base = team * warps, at = lane & 15;   // at most 16 warps
+  const int base = team * warps;
   if (lane == 0) part[base + warp] = v;
   named_barrier(team + 1, nt);
-  v = at < warps ? part[base + at] : 0.f;
+  v = lane < warps ? part[base + lane] : 0.f;
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 
@@ -807,6 +807,7 @@ cudaError_t run_columns(const SandwichBwdArgs& a, int rows, cudaStream_t stream)
 }  // namespace
 
 cudaError_t launch_sandwich_norm(const SandwichArgs& a, int num_sms, cudaStream_t stream) {
+  if (a.T <= num_sms && a.K <= 8 * 1024) return run_fwd<1, 1024, 1>(a, num_sms, stream);
   if (a.K <= 16 * 384) return run_fwd<2, 384, 2>(a, num_sms, stream);
   return run_fwd<4, 512, 1>(a, num_sms, stream);
 }

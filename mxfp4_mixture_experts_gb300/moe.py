@@ -545,25 +545,46 @@ def _given(t: Optional[torch.Tensor], name: str, dtype, shape):
             raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
 
 
-def _together(*tensors):
-    """One device for all of them, the current one: the library launches there."""
+def _want(t: Optional[torch.Tensor], name: str, dtype, shape, dev: int):
+    """``_given``, on the current device too (the library launches there). One expression where all is
+    well: a small call's time is the host's, and a gradient's call has a dozen tensors."""
+    if t is None or (type(t) is torch.Tensor and t.dtype == dtype and t.shape == shape
+                     and t.is_contiguous() and t.get_device() == dev):
+        return
+    _given(t, name, dtype, shape)
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the current CUDA device")
+
+
+def _first(t: torch.Tensor, name: str, dtype) -> int:
+    """``_need`` for the matrix that sets a call's sizes; the current device's index."""
+    _need(t, name, dtype, 2)
     dev = torch._C._cuda_getDevice()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError("all tensors must be on the current CUDA device")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the current CUDA device")
+    return dev
 
 
-def _scratch(nbytes: int, workspace: Optional[torch.Tensor], device, stream) -> torch.Tensor:
+def _like(t: torch.Tensor, stream) -> torch.Tensor:
+    """``_empty`` of t's shape and type."""
+    if stream is None:
+        return torch.empty_like(t)
+    return _empty(t.shape, t.dtype, t.device, stream)
+
+
+def _scratch(nbytes: int, workspace: Optional[torch.Tensor], device, stream, dev: int) -> torch.Tensor:
     if workspace is None:
         return _empty(nbytes, torch.uint8, device, stream)
     _need(workspace, "workspace", torch.uint8, 1)
+    if workspace.get_device() != dev:
+        raise ValueError("workspace must be on the current CUDA device")
     return workspace
 
 
 GATE_ACTS = {"linear": 0, "sigmoid": 1}
 
 
-def _gate(gate: Optional[torch.Tensor], gate_act: str, T: int, K: int):
+def _gate(gate: Optional[torch.Tensor], gate_act: str, T: int, K: int, dev: int):
     """(kind, activation) of a gate: bf16 [1, K], fp32 [T, 1] or bf16 [T, K]."""
     if gate_act not in GATE_ACTS:
         raise ValueError(f"gate_act must be one of {sorted(GATE_ACTS)}")
@@ -572,11 +593,13 @@ def _gate(gate: Optional[torch.Tensor], gate_act: str, T: int, K: int):
     if not isinstance(gate, torch.Tensor):
         raise TypeError("gate must be a torch.Tensor")
     if gate.dtype == torch.float32:
-        _given(gate, "gate (fp32)", torch.float32, (T, 1))
+        _want(gate, "gate (fp32)", torch.float32, (T, 1), dev)
         return 2, GATE_ACTS[gate_act]
     _need(gate, "gate", torch.bfloat16, 2)
     if gate.shape[1] != K or gate.shape[0] not in (1, T):
         raise ValueError("gate must be bf16 [1, K], bf16 [T, K] or fp32 [T, 1]")
+    if gate.get_device() != dev:
+        raise ValueError("gate must be on the current CUDA device")
     return (1 if gate.shape[0] == 1 else 3), GATE_ACTS[gate_act]
 
 
@@ -610,17 +633,17 @@ def sandwich_norm(x: torch.Tensor, residual: torch.Tensor, post_gamma: Optional[
     may be x or residual. out8 and bf16 as in ``add_rmsnorm``. For
     ``sandwich_norm_backward``: rstd True keeps both norms' factors, checkpoint8 "ocp" or "nosat"
     writes x and the unrounded h in MXFP8 beside the rest."""
-    _need(x, "x", torch.bfloat16, 2)
+    dev = _first(x, "x", torch.bfloat16)
     shape = x.shape
     T, K = shape
-    _need(residual, "residual", torch.bfloat16, 2)
-    if residual.shape != shape:
-        raise ValueError("residual must be [T, K]")
-    _given(post_gamma, "post_gamma", torch.bfloat16, (K,))
-    _given(pre_gamma, "pre_gamma", torch.bfloat16, (K,))
-    _given(residual_scale, "residual_scale", torch.float32, (1,))
-    _given(residual_out, "residual_out", torch.bfloat16, shape)
-    kind, act = _gate(gate, gate_act, T, K)
+    if residual is None:
+        raise TypeError("residual must be a torch.Tensor")
+    _want(residual, "residual", torch.bfloat16, shape, dev)
+    _want(post_gamma, "post_gamma", torch.bfloat16, (K,), dev)
+    _want(pre_gamma, "pre_gamma", torch.bfloat16, (K,), dev)
+    _want(residual_scale, "residual_scale", torch.float32, (1,), dev)
+    _want(residual_out, "residual_out", torch.bfloat16, shape, dev)
+    kind, act = _gate(gate, gate_act, T, K, dev)
     for name, rule in (("out8", out8), ("checkpoint8", checkpoint8)):
         if rule is not None and rule not in MX8_RULES:
             raise ValueError(f"{name} must be None or one of {sorted(MX8_RULES)}")
@@ -631,18 +654,21 @@ def sandwich_norm(x: torch.Tensor, residual: torch.Tensor, post_gamma: Optional[
     if out is not None:
         if not bf16:
             raise ValueError("out is not written when bf16 is False")
-        _given(out, "out", torch.bfloat16, shape)
-    _together(x, residual, post_gamma, pre_gamma, gate, residual_scale, residual_out, out)
-    dev = x.device
+        _want(out, "out", torch.bfloat16, shape, dev)
+    device = x.device
     if residual_out is None:
-        residual_out = _empty(shape, torch.bfloat16, dev, stream)
+        residual_out = _like(x, stream)
     if out is None and bf16:
-        out = _empty(shape, torch.bfloat16, dev, stream)
-    mx8 = lambda: (_empty(shape, torch.float8_e4m3fn, dev, stream),
-                   _empty((T, K // 32), torch.uint8, dev, stream))
-    q, qs = mx8() if out8 is not None else (None, None)
-    (x8, xs), (h8, hs) = (mx8(), mx8()) if checkpoint8 is not None else ((None, None), (None, None))
-    r = _empty((2, T), torch.float32, dev, stream) if rstd else None
+        out = _like(x, stream)
+    q = qs = x8 = xs = h8 = hs = r = None
+    if out8 is not None:
+        q = _empty(shape, torch.float8_e4m3fn, device, stream)
+        qs = _empty((T, K // 32), torch.uint8, device, stream)
+    if checkpoint8 is not None:
+        x8, h8 = _empty((2, T, K), torch.float8_e4m3fn, device, stream)
+        xs, hs = _empty((2, T, K // 32), torch.uint8, device, stream)
+    if rstd:
+        r = _empty((2, T), torch.float32, device, stream)
     rc = lib().mxfp4_moe_sandwich_norm(
         _addr(x), _addr(residual), _addr(post_gamma), _addr(pre_gamma), _addr(gate), kind, act,
         _addr(residual_scale), T, K, eps, MX8_RULES[out8 or "ocp"], MX8_RULES[checkpoint8 or "ocp"],
@@ -686,52 +712,51 @@ def sandwich_norm_backward(grad_h: Optional[torch.Tensor], grad_y: Optional[torc
     needed with grad_y, rstd with grad_y or post_gamma. gate, gate_act, gammas and residual_scale as
     in the forward call; with residual (its bf16 rows) residual_scale gets a gradient too.
     grad_x and grad_residual may be given as outputs that overlap no input."""
-    _need(x, "x", torch.bfloat16 if x_scale is None else torch.float8_e4m3fn, 2)
+    dev = _first(x, "x", torch.bfloat16 if x_scale is None else torch.float8_e4m3fn)
     shape = x.shape
     T, K = shape
     if grad_h is None and grad_y is None:
         raise ValueError("grad_h or grad_y is needed")
-    _given(grad_h, "grad_h", torch.bfloat16, shape)
-    _given(post_gamma, "post_gamma", torch.bfloat16, (K,))
-    _given(pre_gamma, "pre_gamma", torch.bfloat16, (K,))
-    if grad_y is not None:
-        _given(grad_y, "grad_y", torch.bfloat16, shape)
-        if pre_gamma is None or h is None:
-            raise ValueError("grad_y needs pre_gamma and h")
-    _given(h, "h", torch.bfloat16 if h_scale is None else torch.float8_e4m3fn, shape)
-    _given(x_scale, "x_scale", torch.uint8, (T, K // 32))
-    _given(h_scale, "h_scale", torch.uint8, (T, K // 32))
+    _want(grad_h, "grad_h", torch.bfloat16, shape, dev)
+    _want(grad_y, "grad_y", torch.bfloat16, shape, dev)
+    _want(post_gamma, "post_gamma", torch.bfloat16, (K,), dev)
+    _want(pre_gamma, "pre_gamma", torch.bfloat16, (K,), dev)
+    if grad_y is not None and (pre_gamma is None or h is None):
+        raise ValueError("grad_y needs pre_gamma and h")
+    _want(h, "h", torch.bfloat16 if h_scale is None else torch.float8_e4m3fn, shape, dev)
+    _want(x_scale, "x_scale", torch.uint8, (T, K // 32), dev)
+    _want(h_scale, "h_scale", torch.uint8, (T, K // 32), dev)
     if h is None and h_scale is not None:
         raise ValueError("h_scale needs h")
-    if rstd is None:
-        if grad_y is not None or post_gamma is not None:
-            raise ValueError("rstd is needed with grad_y or post_gamma")
-    else:
-        _given(rstd, "rstd", torch.float32, (2, T))
-    _given(residual_scale, "residual_scale", torch.float32, (1,))
-    if residual is not None:
-        if residual_scale is None:
-            raise ValueError("residual is read for residual_scale's gradient")
-        _given(residual, "residual", torch.bfloat16, shape)
-    _given(grad_x, "grad_x", torch.bfloat16, shape)
-    _given(grad_residual, "grad_residual", torch.bfloat16, shape)
-    kind, act = _gate(gate, gate_act, T, K)
-    _together(grad_h, grad_y, x, h, rstd, post_gamma, pre_gamma, gate, residual, residual_scale,
-              x_scale, h_scale, grad_x, grad_residual, workspace)
-    dev = x.device
+    if rstd is None and (grad_y is not None or post_gamma is not None):
+        raise ValueError("rstd is needed with grad_y or post_gamma")
+    _want(rstd, "rstd", torch.float32, (2, T), dev)
+    _want(residual_scale, "residual_scale", torch.float32, (1,), dev)
+    if residual is not None and residual_scale is None:
+        raise ValueError("residual is read for residual_scale's gradient")
+    _want(residual, "residual", torch.bfloat16, shape, dev)
+    _want(grad_x, "grad_x", torch.bfloat16, shape, dev)
+    _want(grad_residual, "grad_residual", torch.bfloat16, shape, dev)
+    kind, act = _gate(gate, gate_act, T, K, dev)
+    device = x.device
+    rows = grad_h if grad_h is not None else grad_y
     if grad_x is None:
-        grad_x = _empty(shape, torch.bfloat16, dev, stream)
+        grad_x = _like(rows, stream)
     if grad_residual is None:
-        grad_residual = _empty(shape, torch.bfloat16, dev, stream)
-    f32 = lambda *n: _empty(n, torch.float32, dev, stream)
-    dpost = f32(K) if post_gamma is not None else None
-    dpre = f32(K) if pre_gamma is not None else None
-    dgate = (None, lambda: f32(1, K), lambda: f32(T, 1),
-             lambda: _empty(shape, torch.bfloat16, dev, stream))[kind]
-    dgate = dgate() if dgate else None
-    dscale = f32(1) if residual is not None else None
+        grad_residual = _like(rows, stream)
+    dpost = dpre = dgate = dscale = None
+    if post_gamma is not None:
+        dpost = _empty(K, torch.float32, device, stream)
+    if pre_gamma is not None:
+        dpre = _empty(K, torch.float32, device, stream)
+    if kind == 1:
+        dgate = _empty((1, K), torch.float32, device, stream)
+    elif kind:
+        dgate = _like(gate, stream)
+    if residual is not None:
+        dscale = _empty(1, torch.float32, device, stream)
     L = lib()
-    ws = _scratch(L.mxfp4_moe_sandwich_norm_backward_workspace_size(T, K), workspace, dev, stream)
+    ws = _scratch(L.mxfp4_moe_sandwich_norm_backward_workspace_size(T, K), workspace, device, stream, dev)
     rc = L.mxfp4_moe_sandwich_norm_backward(
         _addr(grad_h), _addr(grad_y), x.data_ptr(), _addr(x_scale), _addr(h), _addr(h_scale),
         _addr(rstd), _addr(post_gamma), _addr(pre_gamma), _addr(gate), kind, act, _addr(residual),
@@ -756,8 +781,8 @@ def router_balance_workspace_size(T: int, E: int, n_seq: int = 1) -> int:
 
 
 def _routing(logits, topk_ids, scoring, seq_offsets):
-    _need(logits, "logits", torch.float32, 2)
-    _need(topk_ids, "topk_ids", torch.int32, 2)
+    dev = _first(logits, "logits", torch.float32)
+    _first(topk_ids, "topk_ids", torch.int32)
     T, E = logits.shape
     if topk_ids.shape[0] != T:
         raise ValueError("topk_ids must be [T, topk]")
@@ -769,7 +794,9 @@ def _routing(logits, topk_ids, scoring, seq_offsets):
         S = seq_offsets.shape[0] - 1
         if S < 1:
             raise ValueError("seq_offsets must be [S + 1]")
-    return T, E, topk_ids.shape[1], S
+        if seq_offsets.get_device() != dev:
+            raise ValueError("seq_offsets must be on the current CUDA device")
+    return T, E, topk_ids.shape[1], S, dev
 
 
 def router_balance(logits: torch.Tensor, topk_ids: torch.Tensor, scoring: str = "sigmoid",
@@ -782,15 +809,14 @@ def router_balance(logits: torch.Tensor, topk_ids: torch.Tensor, scoring: str = 
     sequences, stats[1] the mean over tokens of logsumexp(logits)^2. seq_offsets int32 [S + 1]: rows
     of sequence i are seq_offsets[i] up to seq_offsets[i + 1] (not decreasing), None: one of all rows.
     Rows without an id in [0, E) (padding) or with every logit masked (NaN, -inf) do not count."""
-    T, E, k, S = _routing(logits, topk_ids, scoring, seq_offsets)
-    _together(logits, topk_ids, seq_offsets, workspace)
-    dev = logits.device
-    stats = _empty(4, torch.float32, dev, stream)
-    counts = _empty((S, E), torch.int32, dev, stream)
-    prob = _empty((S, E), torch.float32, dev, stream)
-    slope = _empty((S, E), torch.float32, dev, stream)
+    T, E, k, S, dev = _routing(logits, topk_ids, scoring, seq_offsets)
+    device = logits.device
+    stats = _empty(4, torch.float32, device, stream)
+    counts = _empty((S, E), torch.int32, device, stream)
+    prob = _empty((S, E), torch.float32, device, stream)
+    slope = _like(prob, stream)
     L = lib()
-    ws = _scratch(L.mxfp4_moe_router_balance_workspace_size(T, E, S), workspace, dev, stream)
+    ws = _scratch(L.mxfp4_moe_router_balance_workspace_size(T, E, S), workspace, device, stream, dev)
     rc = L.mxfp4_moe_router_balance(logits.data_ptr(), topk_ids.data_ptr(), T, E, k, SCORES[scoring],
                                     _addr(seq_offsets), S, stats.data_ptr(), counts.data_ptr(),
                                     prob.data_ptr(), slope.data_ptr(), ws.data_ptr(), ws.numel(),
@@ -811,20 +837,20 @@ def router_backward(logits: torch.Tensor, topk_ids: torch.Tensor,
     grad_weights fp32 [T, topk], and of ``router_balance``'s two losses, by grad_losses fp32 [2] with
     that call's stats, slope and seq_offsets. Ids outside [0, E) and masked experts take no part;
     rows without a valid id get zeros. scoring, renormalise and route_scale as in ``router_scored``."""
-    T, E, k, S = _routing(logits, topk_ids, scoring, seq_offsets)
+    T, E, k, S, dev = _routing(logits, topk_ids, scoring, seq_offsets)
     if grad_weights is None and grad_losses is None:
         raise ValueError("grad_weights or grad_losses is needed")
-    _given(grad_weights, "grad_weights", torch.float32, (T, k))
+    _want(grad_weights, "grad_weights", torch.float32, (T, k), dev)
     if grad_losses is not None:
         if stats is None or slope is None:
             raise ValueError("grad_losses need stats and slope")
-        _given(grad_losses, "grad_losses", torch.float32, (2,))
-        _given(stats, "stats", torch.float32, (4,))
-        _given(slope, "slope", torch.float32, (S, E))
-    _given(grad_logits, "grad_logits", torch.float32, (T, E))
-    _together(logits, topk_ids, grad_weights, grad_losses, stats, slope, seq_offsets, grad_logits)
+        _want(grad_losses, "grad_losses", torch.float32, (2,), dev)
+        _want(stats, "stats", torch.float32, (4,), dev)
+        _want(slope, "slope", torch.float32, (S, E), dev)
     if grad_logits is None:
-        grad_logits = _empty((T, E), torch.float32, logits.device, stream)
+        grad_logits = _like(logits, stream)
+    else:
+        _want(grad_logits, "grad_logits", torch.float32, (T, E), dev)
     rc = lib().mxfp4_moe_router_backward(
         logits.data_ptr(), topk_ids.data_ptr(), _addr(grad_weights), T, E, k, SCORES[scoring],
         int(bool(renormalise)), route_scale, _addr(grad_losses), _addr(stats), _addr(slope),
@@ -844,25 +870,24 @@ def combine_backward(grad_out: torch.Tensor, routes: torch.Tensor,
     else None). topk is topk_ids' or topk_weights' second size. Routes with a negative id, or
     outside expert_base .. expert_base + n_experts - 1 when n_experts is not 0, are skipped: gradients
     0. topk_weights fp32 [T, topk] are needed with routes_too only."""
-    _need(grad_out, "grad_out", torch.bfloat16, 2)
-    _need(routes, "routes", torch.bfloat16, 2)
+    dev = _first(grad_out, "grad_out", torch.bfloat16)
+    _first(routes, "routes", torch.bfloat16)
     T, K = grad_out.shape
     if topk_ids is None and topk_weights is None:
         raise ValueError("topk_ids or topk_weights are needed")
     k = (topk_ids if topk_ids is not None else topk_weights).shape[-1]
-    _given(topk_ids, "topk_ids", torch.int32, (T, k))
-    _given(topk_weights, "topk_weights", torch.float32, (T, k))
-    _given(routes, "routes", torch.bfloat16, (T * k, K))
+    _want(topk_ids, "topk_ids", torch.int32, (T, k), dev)
+    _want(topk_weights, "topk_weights", torch.float32, (T, k), dev)
+    _want(routes, "routes", torch.bfloat16, (T * k, K), dev)
     if grad_routes is not None:
         routes_too = True
-        _given(grad_routes, "grad_routes", torch.bfloat16, (T * k, K))
+        _want(grad_routes, "grad_routes", torch.bfloat16, (T * k, K), dev)
     if routes_too and topk_weights is None:
         raise ValueError("routes_too needs topk_weights")
-    _together(grad_out, routes, topk_ids, topk_weights, grad_routes)
-    dev = grad_out.device
-    dw = _empty((T, k), torch.float32, dev, stream)
+    dw = _empty((T, k), torch.float32, grad_out.device, stream) if topk_weights is None \
+        else _like(topk_weights, stream)
     if routes_too and grad_routes is None:
-        grad_routes = _empty((T * k, K), torch.bfloat16, dev, stream)
+        grad_routes = _like(routes, stream)
     rc = lib().mxfp4_moe_combine_backward(
         grad_out.data_ptr(), routes.data_ptr(), _addr(topk_ids), _addr(topk_weights), T, K, k,
         int(expert_base), int(n_experts), dw.data_ptr(), _addr(grad_routes), _raw_stream(stream))
