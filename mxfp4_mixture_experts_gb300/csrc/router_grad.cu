@@ -21,15 +21,20 @@
 // Nothing is divided by a sum that could have gone to zero before the product:
 // q and p are at most 1.
 //
-// One warp per token, lane l holding experts l, l + 32, ... in registers: the
-// logits are read once (coalesced 128 bytes a load), 4 T E bytes and as many
-// written by the gradient. The losses' sums are per tile of tokens and sequence (a
-// piece), written to scratch and added up in a fixed order: no floating-point
-// atomics, every repeat gives the same bits.
+// One warp per token, its logits in registers, four neighbours a lane and 16-byte load where rows
+// allow it: the logits are read once, 4 T E bytes and as many written by the gradient. Both
+// kernels are bound by their instructions, so exponentials and reciprocals are the
+// hardware's (2^-22 and 1 ulp; the argument's rounding adds |x| 2^-24), a sigmoid and its
+// complement come from one exponential, and a chosen expert's gradient is put
+// together in its slot's lane and written over the rest's, not searched for in the registers.
+// The losses' sums are per tile of tokens and sequence (a piece), written to scratch and added
+// up in a fixed order: no floating-point atomics, every repeat gives the same bits.
+#include <cfloat>
 #include <cstdint>
 
 #include "common.cuh"
 #include "ops.h"
+#include "ops_common.cuh"
 
 namespace mxmoe {
 namespace {
@@ -41,52 +46,72 @@ __device__ __forceinline__ float warp_sum(float v) {
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
-__device__ __forceinline__ float sigmoid(float x) { return __frcp_rn(__fadd_rn(1.f, expf(-x))); }
+// exp(v) and 1 / v; exp(-inf) = 0, 1 / inf = 0
+__device__ __forceinline__ float fast_exp(float v) { return __expf(v); }
+__device__ __forceinline__ float fast_rcp(float v) { return __fdividef(1.f, v); }
+// sigmoid(x) and sigmoid(-x), neither of which loses its last bits where the other is near 1
+struct Sigmoid {
+  float s, rest;
+};
+__device__ __forceinline__ Sigmoid sigmoid(float x) {
+  const float e = fast_exp(-fabsf(x)), hi = fast_rcp(1.f + e), lo = e * hi;
+  return x < 0.f ? Sigmoid{lo, hi} : Sigmoid{hi, lo};
+}
 
-// A token's logits in registers, masked ones as -inf, and what its softmax needs.
-template <int NPL>
+// A token's logits in registers, masked ones as -inf, and what its softmax needs. Values
+// 4 i .. 4 i + 3 are neighbours (VEC), or 32 experts apart.
+template <int NPL, bool VEC>
 struct Token {
   float x[NPL];
-  float m, total;   // largest logit; sum of exp(x - m)
+  float m;   // largest logit, an infinite one as the largest number
+  static __device__ __forceinline__ int expert(int j, int lane) {
+    return VEC ? (j / 4) * 128 + lane * 4 + j % 4 : lane + 32 * j;
+  }
   __device__ __forceinline__ void load(const float* row, int E, int lane) {
 #pragma unroll
-    for (int j = 0; j < NPL; ++j) {
-      const int e = lane + 32 * j;
-      x[j] = e < E ? __ldg(row + e) : -INFINITY;
+    for (int j = 0; j < NPL; j += VEC ? 4 : 1) {
+      const int e = expert(j, lane);
+      if (VEC) {
+        float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        if (e < E) v = __ldg(reinterpret_cast<const float4*>(row + e));
+        x[j] = v.x;
+        x[j + (VEC ? 1 : 0)] = v.y;
+        x[j + (VEC ? 2 : 0)] = v.z;
+        x[j + (VEC ? 3 : 0)] = v.w;
+      } else {
+        x[j] = e < E ? __ldg(row + e) : -INFINITY;
+      }
     }
   }
   __device__ __forceinline__ void largest() {
     m = -INFINITY;
 #pragma unroll
     for (int j = 0; j < NPL; ++j) {
-      if (!(x[j] > -INFINITY)) x[j] = -INFINITY;   // NaN too
+      x[j] = fmaxf(x[j], -INFINITY);   // NaN becomes -inf
       m = fmaxf(m, x[j]);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  }
-  // exp(x - m): 1 at the largest, also where it is infinite
-  __device__ __forceinline__ float power(float v) const {
-    return v == m ? 1.f : v > -INFINITY ? expf(v - m) : 0.f;
-  }
-  // the exponentials into ex, their sum into total
-  __device__ __forceinline__ void powers(float (&ex)[NPL]) {
-    total = 0.f;
+    if (m == INFINITY) {
+      m = FLT_MAX;
 #pragma unroll
-    for (int j = 0; j < NPL; ++j) total += ex[j] = power(x[j]);
-    total = warp_sum(total);
+      for (int j = 0; j < NPL; ++j) x[j] = fminf(x[j], FLT_MAX);
+    }
   }
-  __device__ __forceinline__ float lse() const { return m + logf(total); }
+  __device__ __forceinline__ float power(float v) const { return fast_exp(v - m); }
 };
 
 __device__ __forceinline__ unsigned clamp_row(int v, unsigned T) { return v < 0 ? 0u : min((unsigned)v, T); }
-// The last sequence that begins at or before row t (offsets[0] is taken as such).
-__device__ __forceinline__ int sequence_of(const int32_t* offsets, int S, unsigned t, unsigned T) {
-  int lo = 0, hi = S - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (clamp_row(__ldg(offsets + mid), T) <= t) lo = mid;
-    else hi = mid - 1;
+// The last sequence that begins at or before row t (the first one is taken as such); 32
+// offsets at a time, the whole warp calls.
+__device__ __forceinline__ int sequence_of(const int32_t* offsets, int S, unsigned t, unsigned T, int lane) {
+  int lo = 0, n = S;   // the answer is one of lo .. lo + n - 1
+  while (n > 1) {
+    const int stride = (n + 31) / 32, i = (lane + 1) * stride;
+    const bool past = i < n && clamp_row(__ldg(offsets + lo + i), T) <= t;
+    const int c = __popc(__ballot_sync(0xffffffffu, past));
+    lo += c * stride;
+    n = min(stride, n - c * stride);
   }
   return lo;
 }
@@ -96,11 +121,13 @@ struct BalanceScratch {
   float* p;          // [rows, E] sums of p
   int* c;            // [rows, E] counts
   float* z;          // [rows] sums of lse^2
-  int* n;            // [rows] tokens
-  float *loss, *zs;  // [S]
+  int *n, *ct;       // [rows] tokens, routes
+  float *loss, *zs;  // [S, blocks of columns], [S]
   int* ns;           // [S]
-  unsigned* done;    // sequences finished
+  unsigned* done;    // CTAs that have finished
 };
+constexpr int kColumns = 32;   // experts of a CTA of the second kernel
+__host__ __device__ inline size_t column_blocks(size_t E) { return (E + kColumns - 1) / kColumns; }
 __host__ __device__ inline size_t balance_layout(size_t rows, size_t E, size_t S, char* base, BalanceScratch* b) {
   size_t o = 0;
   auto take = [&](size_t n) { const size_t at = o; o += (n * 4 + 255) & ~size_t(255); return base + at; };
@@ -109,7 +136,8 @@ __host__ __device__ inline size_t balance_layout(size_t rows, size_t E, size_t S
   b->c = reinterpret_cast<int*>(take(rows * E));
   b->z = reinterpret_cast<float*>(take(rows));
   b->n = reinterpret_cast<int*>(take(rows));
-  b->loss = reinterpret_cast<float*>(take(S));
+  b->ct = reinterpret_cast<int*>(take(rows));
+  b->loss = reinterpret_cast<float*>(take(S * column_blocks(E)));
   b->zs = reinterpret_cast<float*>(take(S));
   b->ns = reinterpret_cast<int*>(take(S));
   return o;
@@ -125,58 +153,79 @@ unsigned tile_count(int T) { return ((unsigned)T + tile_tokens(T) - 1) / tile_to
 template <int NPL>
 constexpr int kBalanceWarps = NPL > 16 ? 4 : 8;   // 32 KB of shared memory either way
 
-template <int NPL>
+template <int NPL, bool VEC>
 __global__ void __launch_bounds__(kBalanceWarps<NPL> * 32)
     balance_pieces_kernel(const RouterBalanceArgs a, const BalanceScratch b, unsigned tile) {
+  using Tok = Token<NPL, VEC>;
   constexpr int W = kBalanceWarps<NPL>;
   __shared__ float sp[W][32 * NPL];
   __shared__ int sc[W][32 * NPL];
   __shared__ float sz[W];
-  __shared__ int sn[W];
+  __shared__ int sn[W], sr[W];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int E = a.E;
   const unsigned T = (unsigned)a.T;
   if (blockIdx.x == 0 && threadIdx.x == 0) *b.done = 0;
+  grid_launch_dependents();
 #pragma unroll
   for (int j = 0; j < NPL; ++j) sc[warp][lane + 32 * j] = 0;
   __syncwarp();
   const unsigned t0 = blockIdx.x * tile, t1 = min(T, t0 + tile);
   float acc[NPL], z = 0.f;
-  int n = 0;
+  int n = 0, routes = 0;
   auto clear = [&]() {
 #pragma unroll
     for (int j = 0; j < NPL; ++j) acc[j] = 0.f;
     z = 0.f;
-    n = 0;
+    n = routes = 0;
   };
-  // rows first, first + step, ... below last into this warp's sums
+  // rows first, first + step, ... below last into this warp's sums, the next one's loads under way
   auto rows = [&](unsigned first, unsigned last, unsigned step) {
+    Tok next;
+    int next_id = -1;
+    auto load = [&](unsigned t) {
+      if (t >= last) return;
+      next.load(a.logits + (size_t)t * E, E, lane);
+      next_id = lane < a.topk ? __ldg(a.ids + (size_t)t * a.topk + lane) : -1;
+    };
+    load(first);
     for (unsigned t = first; t < last; t += step) {
-      Token<NPL> k;
-      k.load(a.logits + (size_t)t * E, E, lane);
-      const int id = lane < a.topk ? __ldg(a.ids + (size_t)t * a.topk + lane) : -1;
-      const bool hit = id >= 0 && id < E;
+      Tok k = next;
+      const int id = next_id;
+      load(t + step);
+      const unsigned hit = __ballot_sync(0xffffffffu, id >= 0 && id < E);
       k.largest();
-      if (!__any_sync(0xffffffffu, hit) || k.m == -INFINITY) continue;
-      if (hit) atomicAdd(&sc[warp][id], 1);
-      float ex[NPL];
-      k.powers(ex);
-      const float lse = k.lse();
-      z = fmaf(lse, lse, z);
+      if (hit == 0 || k.m == -INFINITY) continue;
+      if (id >= 0 && id < E) atomicAdd(&sc[warp][id], 1);
+      routes += __popc(hit);
       ++n;
+      float s[NPL], total = 0.f;
+#pragma unroll
+      for (int j = 0; j < NPL; ++j) total += s[j] = k.power(k.x[j]);
       if (a.scoring == 0) {
-        const float inv = __frcp_rn(k.total);
-#pragma unroll
-        for (int j = 0; j < NPL; ++j) acc[j] = fmaf(ex[j], inv, acc[j]);
+        total = warp_sum(total);
       } else {
-        float s[NPL], sum = 0.f;
+        float sum = 0.f;
 #pragma unroll
-        for (int j = 0; j < NPL; ++j) sum += s[j] = sigmoid(k.x[j]);   // (0 at -inf)
-        sum = warp_sum(sum);
-        const float inv = sum > 0.f ? __frcp_rn(sum) : 0.f;
+        for (int j = 0; j < NPL; ++j) sum += s[j] = fast_rcp(1.f + fast_exp(-k.x[j]));   // (0 at -inf)
+        // both sums in one butterfly: the lower half of the warp ends with the first, the upper with the second
+        const bool hi = lane & 16;
+        float v = (hi ? sum : total) + __shfl_xor_sync(0xffffffffu, hi ? total : sum, 16);
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        total = __shfl_sync(0xffffffffu, v, 0);
+        sum = __shfl_sync(0xffffffffu, v, 16);
+        const float lse = k.m + __logf(total);
+        z = fmaf(lse, lse, z);
+        const float inv = sum > 0.f ? fast_rcp(sum) : 0.f;
 #pragma unroll
         for (int j = 0; j < NPL; ++j) acc[j] = fmaf(s[j], inv, acc[j]);
+        continue;
       }
+      const float lse = k.m + __logf(total), inv = fast_rcp(total);
+      z = fmaf(lse, lse, z);
+#pragma unroll
+      for (int j = 0; j < NPL; ++j) acc[j] = fmaf(s[j], inv, acc[j]);
     }
   };
   auto piece = [&](int s, unsigned lo, unsigned hi) {
@@ -188,7 +237,7 @@ __global__ void __launch_bounds__(kBalanceWarps<NPL> * 32)
       __syncwarp();
 #pragma unroll
       for (int j = 0; j < NPL; ++j) {
-        const int e = lane + 32 * j;
+        const int e = Tok::expert(j, lane);
         if (e < E) {
           b.p[at * E + e] = acc[j];
           b.c[at * E + e] = sc[warp][e];
@@ -199,16 +248,18 @@ __global__ void __launch_bounds__(kBalanceWarps<NPL> * 32)
       if (lane == 0) {
         b.z[at] = z;
         b.n[at] = n;
+        b.ct[at] = routes;
       }
       return;
     }
     clear();
     rows(lo + warp, hi, W);
 #pragma unroll
-    for (int j = 0; j < NPL; ++j) sp[warp][lane + 32 * j] = acc[j];
+    for (int j = 0; j < NPL; ++j) sp[warp][Tok::expert(j, lane)] = acc[j];
     if (lane == 0) {
       sz[warp] = z;
       sn[warp] = n;
+      sr[warp] = routes;
     }
     __syncthreads();
     for (int e = threadIdx.x; e < E; e += 32 * W) {
@@ -225,13 +276,16 @@ __global__ void __launch_bounds__(kBalanceWarps<NPL> * 32)
     }
     if (threadIdx.x == 0) {
       float zz = 0.f;
-      int nn = 0;
+      int nn = 0, rr = 0;
+#pragma unroll
       for (int w = 0; w < W; ++w) {
         zz += sz[w];
         nn += sn[w];
+        rr += sr[w];
       }
       b.z[at] = zz;
       b.n[at] = nn;
+      b.ct[at] = rr;
     }
     __syncthreads();
   };
@@ -240,7 +294,7 @@ __global__ void __launch_bounds__(kBalanceWarps<NPL> * 32)
     return;
   }
   // 32 sequences a step, so that runs of empty ones cost little
-  for (int s0 = sequence_of(a.offsets, a.S, t0, T); s0 < a.S; s0 += 32) {
+  for (int s0 = sequence_of(a.offsets, a.S, t0, T, lane); s0 < a.S; s0 += 32) {
     const int s = s0 + lane;
     unsigned lo = T, hi = 0;
     if (s < a.S) {
@@ -257,17 +311,18 @@ __global__ void __launch_bounds__(kBalanceWarps<NPL> * 32)
   }
 }
 
-// A CTA per sequence: its pieces added up in order, its share, slope and loss;
-// the last CTA to finish adds up the sequences, in order again.
-__global__ void __launch_bounds__(1024)
-    balance_sequences_kernel(const RouterBalanceArgs a, const BalanceScratch b, unsigned tile, unsigned tiles) {
-  __shared__ float tp[1024], part[32][32];
-  __shared__ int tc[1024], partc[32][32];
-  __shared__ float red[3][32];
-  __shared__ long long redn[2][32];
+// A CTA per sequence and 32 experts: the sequence's pieces added up in order (every 16th a
+// warp), the share, mean, slope and loss of its experts; the last CTA to finish adds up
+// the losses, in order again. Launched while the first kernel still runs.
+constexpr int kSeqWarps = 16;
+__global__ void __launch_bounds__(32 * kSeqWarps)
+    balance_sequences_kernel(const RouterBalanceArgs a, const BalanceScratch b, unsigned tile) {
+  __shared__ float part[kSeqWarps][32], pz[kSeqWarps], pl[kSeqWarps];
+  __shared__ int partc[kSeqWarps][32], pn[kSeqWarps], pr[kSeqWarps];
   __shared__ bool last;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  const int E = a.E, s = blockIdx.x;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int E = a.E, blocks = (int)column_blocks(E), s = blockIdx.x / blocks, cb = blockIdx.x % blocks;
+  const int e = cb * kColumns + lane;
   const unsigned T = (unsigned)a.T;
   unsigned lo = 0, hi = T;
   if (a.offsets != nullptr) {
@@ -275,227 +330,260 @@ __global__ void __launch_bounds__(1024)
     hi = clamp_row(__ldg(a.offsets + s + 1), T);
   }
   const unsigned b0 = lo / tile, b1 = lo < hi ? (hi - 1) / tile + 1 : b0;   // its tiles
-  const int blocks = (E + 31) / 32;                      // of 32 columns
-  const int across = blocks < warps ? blocks : warps;    // taken at a time
-  const int groups = warps / across;                     // row groups of each
-  const int cb = warp % across, rg = warp / across;
-  for (int c0 = 0; c0 < blocks; c0 += across) {
-    const int e = (c0 + cb) * 32 + lane;
-    float p = 0.f;
-    int c = 0;
-    if (e < E && rg < groups) {
-#pragma unroll 4
-      for (unsigned r = b0 + rg; r < b1; r += groups) {
-        const size_t at = ((size_t)r + s) * E + e;
-        p += b.p[at];
-        c += b.c[at];
-      }
-    }
-    part[warp][lane] = p;
-    partc[warp][lane] = c;
-    __syncthreads();
-    if (rg == 0 && e < E) {
-      for (int g = 1; g < groups; ++g) {
-        p += part[g * across + cb][lane];
-        c += partc[g * across + cb][lane];
-      }
-      tp[e] = p;
-      tc[e] = c;
-    }
-    __syncthreads();
-  }
-  float z = 0.f;
-  long long n = 0, total = 0;
-  for (unsigned r = b0 + threadIdx.x; r < b1; r += blockDim.x) {
+  grid_dependency_wait();
+  float p = 0.f, z = 0.f;
+  int c = 0, n = 0, routes = 0;
+  for (unsigned r = b0 + threadIdx.x; r < b1; r += 32 * kSeqWarps) {
     z += b.z[(size_t)r + s];
     n += b.n[(size_t)r + s];
+    routes += b.ct[(size_t)r + s];
   }
-  for (int e = threadIdx.x; e < E; e += blockDim.x) total += tc[e];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    z += __shfl_xor_sync(0xffffffffu, z, o);
-    n += __shfl_xor_sync(0xffffffffu, n, o);
-    total += __shfl_xor_sync(0xffffffffu, total, o);
+  if (e < E) {
+#pragma unroll 8
+    for (unsigned r = b0 + warp; r < b1; r += kSeqWarps) {
+      const size_t at = ((size_t)r + s) * E + e;
+      p += b.p[at];
+      c += b.c[at];
+    }
   }
+  part[warp][lane] = p;
+  partc[warp][lane] = c;
+  z = warp_sum(z);
+  n = __reduce_add_sync(0xffffffffu, n);
+  routes = __reduce_add_sync(0xffffffffu, routes);
   if (lane == 0) {
-    red[0][warp] = z;
-    redn[0][warp] = n;
-    redn[1][warp] = total;
+    pz[warp] = z;
+    pn[warp] = n;
+    pr[warp] = routes;
   }
   __syncthreads();
-  z = 0.f;
-  n = total = 0;
-  for (int w = 0; w < warps; ++w) {
-    z += red[0][w];
-    n += redn[0][w];
-    total += redn[1][w];
-  }
-  float loss = 0.f;
-  for (int e = threadIdx.x; e < E; e += blockDim.x) {
-    const size_t at = (size_t)s * E + e;
-    const float share = n > 0 ? (float)E * (float)tc[e] / (float)total : 0.f;
-    const float prob = n > 0 ? tp[e] / (float)n : 0.f;
-    a.counts[at] = tc[e];
-    a.prob[at] = prob;
-    a.slope[at] = n > 0 ? share / (float)n : 0.f;
-    loss = fmaf(share, prob, loss);
-  }
-  loss = warp_sum(loss);
-  if (lane == 0) red[1][warp] = loss;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    loss = 0.f;
-    for (int w = 0; w < warps; ++w) loss += red[1][w];
-    b.loss[s] = loss;
-    b.zs[s] = z;
-    b.ns[s] = (int)n;
-    __threadfence();
-    last = atomicAdd(b.done, 1u) == (unsigned)a.S - 1;
+  if (warp == 0) {
+    p = z = 0.f;
+    c = n = routes = 0;
+#pragma unroll
+    for (int w = 0; w < kSeqWarps; ++w) {
+      p += part[w][lane];
+      c += partc[w][lane];
+      z += pz[w];
+      n += pn[w];
+      routes += pr[w];
+    }
+    float loss = 0.f;
+    if (e < E) {
+      const size_t at = (size_t)s * E + e;
+      const float share = n > 0 ? (float)E * (float)c / (float)routes : 0.f;
+      const float prob = n > 0 ? p / (float)n : 0.f;
+      a.counts[at] = c;
+      a.prob[at] = prob;
+      a.slope[at] = n > 0 ? share / (float)n : 0.f;
+      loss = share * prob;
+    }
+    loss = warp_sum(loss);
+    if (lane == 0) {
+      b.loss[(size_t)s * blocks + cb] = loss;
+      if (cb == 0) {
+        b.zs[s] = z;
+        b.ns[s] = n;
+      }
+      __threadfence();
+      last = atomicAdd(b.done, 1u) == gridDim.x - 1;
+    }
   }
   __syncthreads();
   if (!last) return;
   __threadfence();
-  float l = 0.f;
-  long long seen = 0;
+  float l = 0.f, tokens = 0.f;
+  int seen = 0;
   z = 0.f;
   n = 0;
-  for (int i = threadIdx.x; i < a.S; i += blockDim.x) {
-    l += __ldcg(b.loss + i);
+  for (int i = threadIdx.x; i < a.S * blocks; i += 32 * kSeqWarps) l += __ldcg(b.loss + i);
+  for (int i = threadIdx.x; i < a.S; i += 32 * kSeqWarps) {
     z += __ldcg(b.zs + i);
     const int ni = __ldcg(b.ns + i);
-    n += ni;
+    n += ni;   // (at most T)
     seen += ni > 0;
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    l += __shfl_xor_sync(0xffffffffu, l, o);
-    z += __shfl_xor_sync(0xffffffffu, z, o);
-    n += __shfl_xor_sync(0xffffffffu, n, o);
-    seen += __shfl_xor_sync(0xffffffffu, seen, o);
-  }
-  __syncthreads();
+  l = warp_sum(l);
+  z = warp_sum(z);
+  n = __reduce_add_sync(0xffffffffu, n);
+  seen = __reduce_add_sync(0xffffffffu, seen);
   if (lane == 0) {
-    red[0][warp] = z;
-    red[1][warp] = l;
-    redn[0][warp] = n;
-    redn[1][warp] = seen;
+    pz[warp] = z;
+    pl[warp] = l;
+    pn[warp] = n;
+    pr[warp] = seen;
   }
   __syncthreads();
   if (threadIdx.x == 0) {
     l = z = 0.f;
     n = seen = 0;
-    for (int w = 0; w < warps; ++w) {
-      z += red[0][w];
-      l += red[1][w];
-      n += redn[0][w];
-      seen += redn[1][w];
+#pragma unroll
+    for (int w = 0; w < kSeqWarps; ++w) {
+      z += pz[w];
+      l += pl[w];
+      n += pn[w];
+      seen += pr[w];
     }
+    tokens = (float)n;
     a.stats[0] = seen > 0 ? l / (float)seen : 0.f;
-    a.stats[1] = n > 0 ? z / (float)n : 0.f;
-    a.stats[2] = (float)n;
+    a.stats[1] = n > 0 ? z / tokens : 0.f;
+    a.stats[2] = tokens;
     a.stats[3] = (float)seen;
   }
 }
 
 constexpr int kRbWarps = 8;
 
-template <int NPL>
+template <int NPL, bool VEC>
 __global__ void __launch_bounds__(kRbWarps * 32) router_backward_kernel(const RouterBackwardArgs a) {
+  using Tok = Token<NPL, VEC>;
   const int lane = threadIdx.x & 31;
   const unsigned T = (unsigned)a.T;
   const unsigned t = blockIdx.x * kRbWarps + (threadIdx.x >> 5);
   if (t >= T) return;
   const int E = a.E;
   const float* row = a.logits + (size_t)t * E;
-  Token<NPL> k;
+  float* out = a.dlogits + (size_t)t * E;
+  Tok k;
   k.load(row, E, lane);
   int id = lane < a.topk ? __ldg(a.ids + (size_t)t * a.topk + lane) : -1;
   if (id >= E) id = -1;
+  const float w = a.dw != nullptr && id >= 0 ? __ldg(a.dw + (size_t)t * a.topk + lane) : 0.f;
+  float v = id >= 0 ? __ldg(row + id) : -INFINITY;   // lane r: slot r's logit
+  // the losses' parts: gb, gz 0 where they do not count
+  float gb = 0.f, gz = 0.f;
+  const float* slope = a.slope;
+  if (a.dloss != nullptr) {
+    int s = 0;
+    bool inside = true;
+    if (a.offsets != nullptr) {
+      s = sequence_of(a.offsets, a.S, t, T, lane);
+      inside = t >= clamp_row(__ldg(a.offsets + s), T) && t < clamp_row(__ldg(a.offsets + s + 1), T);
+    }
+    if (inside) {
+      gb = __ldg(a.dloss) / fmaxf(__ldg(a.stats + 3), 1.f);
+      gz = 2.f * __ldg(a.dloss + 1) / fmaxf(__ldg(a.stats + 2), 1.f);
+      slope += (size_t)s * E;
+    }
+  }
+  const bool losses = gb != 0.f || gz != 0.f;   // (the same in the whole warp)
   k.largest();
+  v = fminf(fmaxf(v, -INFINITY), k.m);   // masked: -inf; an infinite one as in the registers
   float d[NPL];
 #pragma unroll
   for (int j = 0; j < NPL; ++j) d[j] = 0.f;
-  if (__any_sync(0xffffffffu, id >= 0) && k.m > -INFINITY) {
-    float ex[NPL];
-    k.powers(ex);
-    const float inv = __frcp_rn(k.total);
+  const bool live = __any_sync(0xffffffffu, id >= 0) && k.m > -INFINITY;
+  float val = 0.f;   // lane r: slot r's part of the gradient of its expert, then all of it
+  if (live) {
+    float ex[NPL], total = 0.f;
+    const float vx = k.power(v);
+#pragma unroll
+    for (int j = 0; j < NPL; ++j) total += ex[j] = k.power(k.x[j]);
+    total = warp_sum(total);
+    const float inv = fast_rcp(total);
+    const Sigmoid sv = sigmoid(v);   // (-inf: 0 and 1)
+    const bool soft = a.scoring == 0, there = v > -INFINITY;
+    float common = 0.f;
     if (a.dw != nullptr) {
-      // lane r: slot r's score and its part of the gradient
-      float s = 0.f, val = 0.f, w = 0.f;
-      if (id >= 0) {
-        const float v = __ldg(row + id);
-        if (v > -INFINITY) {
-          s = a.scoring == 0 ? k.power(v) * inv : sigmoid(v);
-          w = __ldg(a.dw + (size_t)t * a.topk + lane);
-          if (a.scoring == 1) val = sigmoid(-v);   // 1 - s
-          else val = 1.f;
-        }
-      }
+      const float s = soft ? vx * inv : sv.s;
+      const float wv = there ? w : 0.f;   // (what is no part's gradient may be anything)
       if (a.renormalise) {
-        const float D = warp_sum(s);
-        const float q = D > 0.f ? s / D : 0.f;
-        val *= q * (w - warp_sum(q * w));
+        const float D = warp_sum(s), q = D > 0.f ? s / D : 0.f;
+        val = q * (wv - warp_sum(q * wv));
       } else {
-        val *= s * w;
+        val = s * wv;
       }
+      if (!soft) val *= sv.rest;
       val *= a.route_scale;
-      const float common = a.scoring == 0 && !a.renormalise ? warp_sum(val) * inv : 0.f;
-#pragma unroll
-      for (int j = 0; j < NPL; ++j) d[j] = -common * ex[j];
-      for (int r = 0; r < a.topk; ++r) {   // also the same expert twice
-        const int e = __shfl_sync(0xffffffffu, id, r);
-        const float v = __shfl_sync(0xffffffffu, val, r);
-        if (e >= 0 && (e & 31) == lane) {
-#pragma unroll
-          for (int j = 0; j < NPL; ++j)
-            if (j == (e >> 5)) d[j] += v;
-        }
-      }
+      if (soft && !a.renormalise) common = warp_sum(val) * inv;
     }
-    if (a.dloss != nullptr) {
-      int s = 0;
-      bool inside = true;
-      if (a.offsets != nullptr) {
-        s = sequence_of(a.offsets, a.S, t, T);
-        inside = t >= clamp_row(__ldg(a.offsets + s), T) && t < clamp_row(__ldg(a.offsets + s + 1), T);
+    // the same expert in several slots: the first one takes all
+    const unsigned twins = __match_any_sync(0xffffffffu, id);
+    if (__any_sync(0xffffffffu, id >= 0 && (twins & (twins - 1)) != 0)) {
+      float sum = 0.f;
+      for (int r = 0; r < a.topk; ++r) {
+        const float o = __shfl_sync(0xffffffffu, val, r);
+        if ((twins >> r) & 1u) sum += o;
       }
-      if (inside) {
-        const float gb = __ldg(a.dloss) / fmaxf(__ldg(a.stats + 3), 1.f);
-        const float gz = 2.f * __ldg(a.dloss + 1) / fmaxf(__ldg(a.stats + 2), 1.f);
-        const float* slope = a.slope + (size_t)s * E;
-        float sl[NPL], p[NPL], dot = 0.f;
+      val = sum;
+    }
+    float vbase = -common * vx;
 #pragma unroll
-        for (int j = 0; j < NPL; ++j) sl[j] = lane + 32 * j < E ? __ldg(slope + lane + 32 * j) : 0.f;
-        if (a.scoring == 0) {
+    for (int j = 0; j < NPL; ++j) d[j] = -common * ex[j];
+    if (losses) {
+      float sl[NPL], p[NPL], rest[NPL], dot = 0.f, is = inv;
+      if (VEC) {
 #pragma unroll
-          for (int j = 0; j < NPL; ++j) p[j] = ex[j] * inv;
-        } else {
-          float sum = 0.f;
-#pragma unroll
-          for (int j = 0; j < NPL; ++j) sum += p[j] = sigmoid(k.x[j]);
-          sum = warp_sum(sum);
-          const float is = sum > 0.f ? __frcp_rn(sum) : 0.f;
-#pragma unroll
-          for (int j = 0; j < NPL; ++j) p[j] *= is;
+        for (int j = 0; j < NPL; j += VEC ? 4 : 1) {
+          const int e = Tok::expert(j, lane);
+          float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (e < E) q = __ldg(reinterpret_cast<const float4*>(slope + e));
+          sl[j] = q.x;
+          sl[j + (VEC ? 1 : 0)] = q.y;
+          sl[j + (VEC ? 2 : 0)] = q.z;
+          sl[j + (VEC ? 3 : 0)] = q.w;
         }
-#pragma unroll
-        for (int j = 0; j < NPL; ++j) dot = fmaf(p[j], sl[j], dot);
-        dot = warp_sum(dot);
-        const float zc = gz * k.lse() * inv;
+      } else {
 #pragma unroll
         for (int j = 0; j < NPL; ++j) {
-          float u = gb * p[j] * (sl[j] - dot);
-          if (a.scoring == 1 && p[j] > 0.f) u *= sigmoid(-k.x[j]);
-          d[j] += u;
-          if (gz != 0.f && ex[j] > 0.f) d[j] = fmaf(zc, ex[j], d[j]);
+          const int e = Tok::expert(j, lane);
+          sl[j] = e < E ? __ldg(slope + e) : 0.f;
         }
       }
+      const float vsl = id >= 0 ? __ldg(slope + id) : 0.f;
+      if (soft) {
+#pragma unroll
+        for (int j = 0; j < NPL; ++j) {
+          p[j] = ex[j];
+          rest[j] = 1.f;
+        }
+      } else {
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < NPL; ++j) {
+          const Sigmoid g = sigmoid(k.x[j]);
+          sum += p[j] = g.s;
+          rest[j] = g.rest;
+        }
+        sum = warp_sum(sum);
+        is = sum > 0.f ? fast_rcp(sum) : 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < NPL; ++j) dot = fmaf(p[j], sl[j], dot);
+      dot = warp_sum(dot) * is;
+      const float gp = gb * is;
+      const float zc = gz != 0.f ? gz * (k.m + __logf(total)) * inv : 0.f;
+#pragma unroll
+      for (int j = 0; j < NPL; ++j) {
+        const float u = gp * p[j] * (sl[j] - dot);
+        d[j] = fmaf(u, rest[j], d[j]);
+        d[j] = ex[j] > 0.f ? fmaf(zc, ex[j], d[j]) : d[j];   // (an infinite zc stays at the logits that have a part)
+      }
+      const float u = gp * (soft ? vx : sv.s) * (vsl - dot);
+      vbase = fmaf(u, soft ? 1.f : sv.rest, vbase);
+      vbase = vx > 0.f ? fmaf(zc, vx, vbase) : vbase;
+    }
+    val = there ? val + vbase : 0.f;
+  }
+#pragma unroll
+  for (int j = 0; j < NPL; j += VEC ? 4 : 1) {
+    const int e = Tok::expert(j, lane);
+    if (e >= E) continue;
+    if (VEC) {
+      *reinterpret_cast<float4*>(out + e) =
+          make_float4(d[j], d[j + (VEC ? 1 : 0)], d[j + (VEC ? 2 : 0)], d[j + (VEC ? 3 : 0)]);
+    } else {
+      out[e] = d[j];
     }
   }
-  float* out = a.dlogits + (size_t)t * E;
-#pragma unroll
-  for (int j = 0; j < NPL; ++j)
-    if (lane + 32 * j < E) out[lane + 32 * j] = d[j];
+  __syncwarp();
+  if (live && id >= 0) out[id] = val;   // after the rest's
+}
+
+// Rows that four neighbours of a lane can be read from.
+bool rows_vec(int E, const void* a, const void* b, const void* c) {
+  return E % 4 == 0 && ((reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b) |
+                         reinterpret_cast<uintptr_t>(c)) & 15) == 0;
 }
 
 }  // namespace
@@ -512,30 +600,40 @@ cudaError_t launch_router_balance(const RouterBalanceArgs& a, int num_sms, cudaS
   balance_layout((size_t)tiles + a.S, a.E, a.S, static_cast<char*>(a.ws), &b);
   const int per = (a.E + 31) / 32;
   const unsigned grid = tiles > 0 ? tiles : 1;   // (no rows: the counter all the same)
-#define MXMOE_BP(N) balance_pieces_kernel<N><<<grid, kBalanceWarps<N> * 32, 0, stream>>>(a, b, tile)
-  if (per <= 1) MXMOE_BP(1);
-  else if (per <= 2) MXMOE_BP(2);
-  else if (per <= 4) MXMOE_BP(4);
-  else if (per <= 8) MXMOE_BP(8);
-  else if (per <= 16) MXMOE_BP(16);
-  else MXMOE_BP(32);
+  const bool vec = rows_vec(a.E, a.logits, nullptr, nullptr);
+#define MXMOE_BP(N, V) balance_pieces_kernel<N, V><<<grid, kBalanceWarps<N> * 32, 0, stream>>>(a, b, tile)
+  if (per <= 1) MXMOE_BP(1, false);
+  else if (per <= 2) MXMOE_BP(2, false);
+  else if (per <= 4) { if (vec) MXMOE_BP(4, true); else MXMOE_BP(4, false); }
+  else if (per <= 8) { if (vec) MXMOE_BP(8, true); else MXMOE_BP(8, false); }
+  else if (per <= 16) { if (vec) MXMOE_BP(16, true); else MXMOE_BP(16, false); }
+  else { if (vec) MXMOE_BP(32, true); else MXMOE_BP(32, false); }
 #undef MXMOE_BP
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  balance_sequences_kernel<<<a.S, a.S < 128 ? 1024 : 256, 0, stream>>>(a, b, tile, tiles);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(a.S * column_blocks(a.E)));
+  cfg.blockDim = dim3(32 * kSeqWarps);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, balance_sequences_kernel, a, b, tile);
 }
 
 cudaError_t launch_router_backward(const RouterBackwardArgs& a, cudaStream_t stream) {
   const unsigned blocks = ((unsigned)a.T + kRbWarps - 1) / kRbWarps;
   const int per = (a.E + 31) / 32;
-#define MXMOE_RB(N) router_backward_kernel<N><<<blocks, kRbWarps * 32, 0, stream>>>(a)
-  if (per <= 1) MXMOE_RB(1);
-  else if (per <= 2) MXMOE_RB(2);
-  else if (per <= 4) MXMOE_RB(4);
-  else if (per <= 8) MXMOE_RB(8);
-  else if (per <= 16) MXMOE_RB(16);
-  else MXMOE_RB(32);
+  const bool vec = rows_vec(a.E, a.logits, a.slope, a.dlogits);
+#define MXMOE_RB(N, V) router_backward_kernel<N, V><<<blocks, kRbWarps * 32, 0, stream>>>(a)
+  if (per <= 1) MXMOE_RB(1, false);
+  else if (per <= 2) MXMOE_RB(2, false);
+  else if (per <= 4) { if (vec) MXMOE_RB(4, true); else MXMOE_RB(4, false); }
+  else if (per <= 8) { if (vec) MXMOE_RB(8, true); else MXMOE_RB(8, false); }
+  else if (per <= 16) { if (vec) MXMOE_RB(16, true); else MXMOE_RB(16, false); }
+  else { if (vec) MXMOE_RB(32, true); else MXMOE_RB(32, false); }
 #undef MXMOE_RB
   return cudaGetLastError();
 }
