@@ -100,15 +100,22 @@ struct FwdPlan {
   int smem;
 };
 
-// MXFP8 of 8 values: the 4 lanes of a block call together.
+// MXFP8 of 8 values: the 4 lanes of a block call together. The largest magnitude comes from
+// maxima of three magnitudes that keep a NaN (its bits are above infinity's).
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ void store_mx8(const float2 (&v)[4], int nosat, bool valid, uint8_t* q, uint8_t* scale,
                                           bool first) {
+  float m = max3_abs(v[0].x, v[0].y, v[1].x);
+  m = max3_abs(m, v[1].y, v[2].x);
+  m = max3_abs(m, v[2].y, v[3].x);
   const float f[8] = {v[0].x, v[0].y, v[1].x, v[1].y, v[2].x, v[2].y, v[3].x, v[3].y};
-  const Mx8 e = mx8_block(f, max_bits8(f), nosat);
-  if (valid) {
-    *reinterpret_cast<uint2*>(q) = e.q;
-    if (first) *scale = (uint8_t)e.s;
-  }
+  const Mx8 e = mx8_block(f, max(__float_as_uint(m), __float_as_uint(v[3].y) & 0x7FFFFFFFu), nosat);
+  if (valid) *reinterpret_cast<uint2*>(q) = e.q;
+  if (first && valid) *scale = (uint8_t)e.s;
 }
 
 // A team of warps to a row, CH * 32 chunks in a row to a warp; short rows share a CTA.
@@ -291,18 +298,17 @@ __device__ __forceinline__ void team_sum3(float (&v)[ROWS][3], float (*part)[32]
   }
 }
 
-// 8 values from shared memory: bf16, or E4M3 with their block's factor.
-__device__ __forceinline__ void slot8(const uint8_t* p, bool e4m3, float scale, float2 (&v)[4]) {
+// 8 values from shared memory: bf16, or E4M3 without their block's factor.
+__device__ __forceinline__ void slot8(const uint8_t* p, bool e4m3, float2 (&v)[4]) {
   if (!e4m3) {
     unpack4(*reinterpret_cast<const uint4*>(p), v);
     return;
   }
   const uint2 q = *reinterpret_cast<const uint2*>(p);
-  const float2 f = dup(scale);
-  v[0] = __fmul2_rn(e4m3x2_values((uint16_t)q.x), f);
-  v[1] = __fmul2_rn(e4m3x2_values((uint16_t)(q.x >> 16)), f);
-  v[2] = __fmul2_rn(e4m3x2_values((uint16_t)q.y), f);
-  v[3] = __fmul2_rn(e4m3x2_values((uint16_t)(q.y >> 16)), f);
+  v[0] = e4m3x2_values((uint16_t)q.x);
+  v[1] = e4m3x2_values((uint16_t)(q.x >> 16));
+  v[2] = e4m3x2_values((uint16_t)q.y);
+  v[3] = e4m3x2_values((uint16_t)(q.y >> 16));
 }
 // Shared memory of the gradient: post_gamma, times a channel's gate (fp32, in two halves of
 // 4 values a chunk; not for the longest rows without such a gate), then for every team a ring of rows. A row's slots lie by warp and
@@ -483,7 +489,9 @@ __global__ void __launch_bounds__(MAXT, 1)
       }
     copies_wait(p.depth - 1);
     uint8_t* slot = mine + st * p.stage;
-    float2 s2[ROWS][3];   // v h, w x (dh + r2 v), w x h; w without a token's gate
+    // v h, w x (dh + r2 v), w x h; w without a token's gate. An 8-bit block's factor is taken
+    // into the sums of its chunk and into the row's factors, not into every value.
+    float2 s2[ROWS][3];
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) s2[r][0] = s2[r][1] = s2[r][2] = dup(0.f);
 #pragma unroll
@@ -497,9 +505,10 @@ __global__ void __launch_bounds__(MAXT, 1)
         float2 q[4], h[4], w[4], x[4], v[4];
         unpack4(*reinterpret_cast<const uint4*>(at + L::dh + lane16), q);
         unpack4(*reinterpret_cast<const uint4*>(at + L::dy + lane16), v);
-        slot8(at + L::h + lane_h, h8, fh[r][i], h);
-        slot8(at + L::x + lane_x, x8, fx[r][i], x);
-        const float2 r2 = dup(now.r2[r]);
+        slot8(at + L::h + lane_h, h8, h);
+        slot8(at + L::x + lane_x, x8, x);
+        const float2 r2 = dup(now.r2[r]), hr2 = dup(now.r2[r] * fh[r][i]);
+        float2 c2[3] = {dup(0.f), dup(0.f), dup(0.f)};
 #pragma unroll
         for (int j = 0; j < 4; ++j) w[j] = w0[j];
         if (GATE == 2) {
@@ -511,13 +520,19 @@ __global__ void __launch_bounds__(MAXT, 1)
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          s_pre[i][j] = __ffma2_rn(v[j], __fmul2_rn(h[j], r2), s_pre[i][j]);
+          s_pre[i][j] = __ffma2_rn(v[j], __fmul2_rn(h[j], hr2), s_pre[i][j]);
           v[j] = __fmul2_rn(v[j], g[j]);
-          s2[r][0] = __ffma2_rn(v[j], h[j], s2[r][0]);
           q[j] = __ffma2_rn(r2, v[j], q[j]);
           const float2 wx = __fmul2_rn(w[j], x[j]);
-          s2[r][1] = __ffma2_rn(wx, q[j], s2[r][1]);
-          s2[r][2] = __ffma2_rn(wx, h[j], s2[r][2]);
+          float2(&to)[3] = E8 != 0 ? c2 : s2[r];
+          to[0] = __ffma2_rn(v[j], h[j], to[0]);
+          to[1] = __ffma2_rn(wx, q[j], to[1]);
+          to[2] = __ffma2_rn(wx, h[j], to[2]);
+        }
+        if (E8 != 0) {
+          s2[r][0] = __ffma2_rn(c2[0], dup(fh[r][i]), s2[r][0]);
+          s2[r][1] = __ffma2_rn(c2[1], dup(fx[r][i]), s2[r][1]);
+          s2[r][2] = __ffma2_rn(__fmul2_rn(c2[2], dup(fx[r][i])), dup(fh[r][i]), s2[r][2]);
         }
         // dh + r2 v goes where dh and dy were, for the second pass
         *reinterpret_cast<float4*>(at + L::dh + lane16) = make_float4(q[0].x, q[0].y, q[1].x, q[1].y);
@@ -530,19 +545,18 @@ __global__ void __launch_bounds__(MAXT, 1)
 #pragma unroll
       for (int n = 0; n < 3; ++n) s[r][n] = s2[r][n].x + s2[r][n].y;
     team_sum3<ROWS>(s, part[odd], team, nt, lane, warp, warps);
-    float2 kh[ROWS], k1[ROWS], xr[ROWS];
+    float kh[ROWS], k1[ROWS], xr[ROWS];   // of h^, of x^ times the token's gate, of x
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
       const float r1 = now.r1[r], r2 = now.r2[r];
       const float gt = GATE == 0 && a.gate_kind == 2 ? gate_value(now.g[r], a.gate_act) : 1.f;
       const float c2 = s[r][0] * r2 * inv_k * r2;                 // r2 mean(v h^)
       const float dot = r1 * (s[r][1] - c2 * (r2 * s[r][2]));     // sum of w x^ dh_total
-      const float c1 = has_post ? gt * dot * inv_k : 0.f;
       if (GATE == 0 && a.gate_kind == 2 && a.dgate != nullptr && tid == 0 && t + r < T)
         static_cast<float*>(a.dgate)[t + r] = dot * gate_of(now.g[r], a.gate_act).d;
-      kh[r] = dup(-c2 * r2);
-      k1[r] = dup(-r1 * r1 * c1);
-      xr[r] = dup(r1 * gt);
+      kh[r] = -c2;
+      k1[r] = has_post ? -r1 * (dot * inv_k) : 0.f;
+      xr[r] = r1 * gt;
     }
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
@@ -553,6 +567,7 @@ __global__ void __launch_bounds__(MAXT, 1)
       for (int i = 0; i < CH; ++i) {
         const uint8_t* at = slot + r * p.row + i * L::size;
         float2 d[4], x[4], v[4], h[4], w[4];   // d: dh_total
+        const float2 hr2 = dup(now.r2[r] * fh[r][i]), xrf = dup(xr[r] * fx[r][i]);
         weight_of(i, w);
         const float4 q0 = *reinterpret_cast<const float4*>(at + L::dh + lane16);
         const float4 q1 = *reinterpret_cast<const float4*>(at + L::dy + lane16);
@@ -560,10 +575,10 @@ __global__ void __launch_bounds__(MAXT, 1)
         d[1] = make_float2(q0.z, q0.w);
         d[2] = make_float2(q1.x, q1.y);
         d[3] = make_float2(q1.z, q1.w);
-        slot8(at + L::h + lane_h, h8, fh[r][i], h);
-        slot8(at + L::x + lane_x, x8, fx[r][i], x);
+        slot8(at + L::h + lane_h, h8, h);
+        slot8(at + L::x + lane_x, x8, x);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) d[j] = __ffma2_rn(kh[r], h[j], d[j]);
+        for (int j = 0; j < 4; ++j) d[j] = __ffma2_rn(dup(kh[r]), __fmul2_rn(h[j], hr2), d[j]);
         if (has_res) {
           unpack4(*reinterpret_cast<const uint4*>(slot + r * p.row + res0 + 512 * i), v);
 #pragma unroll
@@ -578,10 +593,10 @@ __global__ void __launch_bounds__(MAXT, 1)
           unpack4(*reinterpret_cast<const uint4*>(at + L::gate + lane16), v);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const Gate fx = gate_of(v[j].x, a.gate_act), fy = gate_of(v[j].y, a.gate_act);
-            h[j] = __fmul2_rn(__fmul2_rn(d[j], make_float2(fx.d, fy.d)),
-                              __fmul2_rn(__fmul2_rn(x[j], xr[r]), w[j]));
-            d[j] = __fmul2_rn(d[j], make_float2(fx.v, fy.v));
+            const Gate gx = gate_of(v[j].x, a.gate_act), gy = gate_of(v[j].y, a.gate_act);
+            h[j] = __fmul2_rn(__fmul2_rn(d[j], make_float2(gx.d, gy.d)),
+                              __fmul2_rn(__fmul2_rn(x[j], xrf), w[j]));
+            d[j] = __fmul2_rn(d[j], make_float2(gx.v, gy.v));
           }
           o = pack4(h);
           if (a.dgate != nullptr && there && valid[i])
@@ -589,9 +604,10 @@ __global__ void __launch_bounds__(MAXT, 1)
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          s_x[i][j] = __ffma2_rn(d[j], __fmul2_rn(x[j], xr[r]), s_x[i][j]);
+          const float2 xn = __fmul2_rn(x[j], xrf);
+          s_x[i][j] = __ffma2_rn(d[j], xn, s_x[i][j]);
           // (no post_gamma: r1 = 1, k1 = 0)
-          d[j] = __ffma2_rn(k1[r], x[j], __fmul2_rn(__fmul2_rn(d[j], w[j]), xr[r]));
+          d[j] = __ffma2_rn(dup(k1[r]), xn, __fmul2_rn(__fmul2_rn(d[j], w[j]), dup(xr[r])));
         }
         o = pack4(d);
         if (st_x && valid[i]) st_row16(a.dx + out + 256 * i, o);
@@ -719,6 +735,7 @@ cudaError_t run_fwd(const SandwichArgs& a, int num_sms, cudaStream_t stream) {
   p.teams = MAXT / p.nt;
   const int ctas = PER_SM * num_sms, most = (int)(((unsigned)a.T + ctas - 1) / ctas);
   if (p.teams > most) p.teams = most;
+  if (p.teams > 15 && p.nt > 32) p.teams = 15;   // named barriers 1 .. 15
   const int chunks = CH * p.nt;
   p.pre = a.post != nullptr ? 16 * chunks : 0;
   p.gate = p.pre + (a.pre != nullptr ? 16 * chunks : 0);
@@ -739,7 +756,7 @@ cudaError_t run_fwd(const SandwichArgs& a, int num_sms, cudaStream_t stream) {
 BwdPlan bwd_plan(const SandwichBwdArgs& a, int num_sms, int ch, int e8, int rows, int maxt) {
   BwdPlan p = {};
   p.nt = row_threads(a.K / 8, ch);
-  p.teams = maxt / p.nt;
+  p.teams = maxt / p.nt;   // (at most 16, and of one warp each where above 8: named barriers 1 .. 15)
   const int most = (int)(((unsigned)a.T + rows * num_sms - 1) / (rows * num_sms));
   if (p.teams > most) p.teams = most;
   p.row = p.nt / 32 * ch * slots_bytes(a.gate_kind == 3, e8, a.dscale != nullptr);

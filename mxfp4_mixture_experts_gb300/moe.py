@@ -665,8 +665,10 @@ def sandwich_norm(x: torch.Tensor, residual: torch.Tensor, post_gamma: Optional[
         q = _empty(shape, torch.float8_e4m3fn, device, stream)
         qs = _empty((T, K // 32), torch.uint8, device, stream)
     if checkpoint8 is not None:
-        x8, h8 = _empty((2, T, K), torch.float8_e4m3fn, device, stream)
-        xs, hs = _empty((2, T, K // 32), torch.uint8, device, stream)
+        both = _empty((2, T, K), torch.float8_e4m3fn, device, stream)
+        x8, h8 = both[0], both[1]
+        both = _empty((2, T, K // 32), torch.uint8, device, stream)
+        xs, hs = both[0], both[1]
     if rstd:
         r = _empty((2, T), torch.float32, device, stream)
     rc = lib().mxfp4_moe_sandwich_norm(
