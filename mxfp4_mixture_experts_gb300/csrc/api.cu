@@ -798,7 +798,7 @@ int mxfp4_moe_combine_backward(const void* grad_out, const void* routes, const i
   a.E = n_experts;
   a.dw = grad_weights;
   a.droutes = static_cast<uint16_t*>(grad_routes);
-  return cuda_status(mxmoe::launch_combine_backward(a, static_cast<cudaStream_t>(stream)));
+  return cuda_status(mxmoe::launch_combine_backward(a, d->num_sms, static_cast<cudaStream_t>(stream)));
 }
 
 namespace {

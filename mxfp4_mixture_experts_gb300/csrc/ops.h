@@ -120,7 +120,7 @@ struct CombineBwdArgs {
   float* dw;                 // [T, topk]
   uint16_t* droutes;         // bf16 [T * topk, K] or null
 };
-cudaError_t launch_combine_backward(const CombineBwdArgs& a, cudaStream_t stream);
+cudaError_t launch_combine_backward(const CombineBwdArgs& a, int num_sms, cudaStream_t stream);
 
 constexpr int kLinearMaxAdapters = 1024;
 constexpr int kLinearMaxRank = 256;

@@ -154,7 +154,7 @@ template <int NPL>
 constexpr int kBalanceWarps = NPL > 16 ? 4 : 8;   // 32 KB of shared memory either way
 
 template <int NPL, bool VEC>
-__global__ void __launch_bounds__(kBalanceWarps<NPL> * 32)
+__global__ void __launch_bounds__(kBalanceWarps<NPL> * 32, 2)
     balance_pieces_kernel(const RouterBalanceArgs a, const BalanceScratch b, unsigned tile) {
   using Tok = Token<NPL, VEC>;
   constexpr int W = kBalanceWarps<NPL>;
