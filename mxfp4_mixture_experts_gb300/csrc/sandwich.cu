@@ -34,6 +34,7 @@
 namespace mxmoe {
 namespace {
 
+constexpr int kSwOneCta = 2;   // rows of a gradient that one CTA takes, without the second kernel
 constexpr int kSwRingBytes = 224 * 1024;   // shared memory of a gradient call, beside 1.7 KB of sums
 
 // A gate's value and its derivative, (s, s (1 - s)) of a sigmoid: one exponential of -|g|, so that
@@ -344,6 +345,34 @@ int slots_bytes(bool full_gate, int e8, bool res) {
   return 1024 + (e8 == 1 ? 512 : 1024) + (full_gate ? 512 : 0) + (res ? 512 : 0);
 }
 
+// What a column's second sum comes to, of post_gamma's (x) and of a channel gate's (y) gradient; its
+// gate and post_gamma as bits.
+__device__ __forceinline__ float2 finish_column(const SandwichBwdArgs& a, uint32_t gate, uint32_t post, float s1) {
+  const Gate g = a.gate_kind == 1 ? gate_of(__uint_as_float(gate << 16), a.gate_act) : Gate{1.f, 1.f};
+  return make_float2(g.v * s1, g.d * ((a.post != nullptr ? __uint_as_float(post << 16) : 1.f) * s1));
+}
+// Four neighbouring sums, the e-th four of a row of ws: finished where one CTA holds all rows.
+__device__ __forceinline__ void put_sums(const SandwichBwdArgs& a, float* row, bool all, int e, const float4& v) {
+  if (!all) {
+    reinterpret_cast<float4*>(row)[e] = v;
+    return;
+  }
+  const int k = 4 * e;
+  if (k < a.K) {
+    if (a.dpre != nullptr) *reinterpret_cast<float4*>(a.dpre + k) = v;
+    return;
+  }
+  const int c = k - a.K;
+  const uint2 g = a.gate_kind == 1 ? __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.gate) + c))
+                                   : make_uint2(0u, 0u);
+  const uint2 p = a.post != nullptr ? __ldg(reinterpret_cast<const uint2*>(a.post + c)) : make_uint2(0u, 0u);
+  const float2 o[4] = {finish_column(a, g.x & 0xFFFFu, p.x & 0xFFFFu, v.x), finish_column(a, g.x >> 16, p.x >> 16, v.y),
+                       finish_column(a, g.y & 0xFFFFu, p.y & 0xFFFFu, v.z), finish_column(a, g.y >> 16, p.y >> 16, v.w)};
+  if (a.dpost != nullptr) *reinterpret_cast<float4*>(a.dpost + c) = make_float4(o[0].x, o[1].x, o[2].x, o[3].x);
+  if (a.gate_kind == 1 && a.dgate != nullptr)
+    *reinterpret_cast<float4*>(static_cast<float*>(a.dgate) + c) = make_float4(o[0].y, o[1].y, o[2].y, o[3].y);
+}
+
 // Column sums of the CTA's rows go to ws [gridDim.x][2][K]: 0 dy * h^, 1 d x^ with
 // d = dn, or dh_total where the gate is a channel's (its gate and post_gamma take
 // their gradients from the one sum). After them ws holds a float a CTA, sum dh_total * res.
@@ -631,18 +660,25 @@ __global__ void __launch_bounds__(MAXT, 1)
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   float* sums = a.ws + (size_t)blockIdx.x * 2 * a.K;
   if (p.teams > 1) __syncthreads();
-  // one team: straight to ws; several: through shared memory, added up in order
-  float* to = p.teams > 1 ? reinterpret_cast<float*>(smem) + (size_t)team * 2 * a.K : sums;
+  // one team: straight out; several: through shared memory, added up in order
+  const bool all = gridDim.x == 1;
+  float4* const own = reinterpret_cast<float4*>(smem) + (size_t)team * (a.K / 2);
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const int c = c0 + 32 * i;
     if (c >= n8) continue;
 #pragma unroll
     for (int j = 0; j < 4; j += 2) {
-      *reinterpret_cast<float4*>(to + 8 * c + 2 * j) =
-          make_float4(s_pre[i][j].x, s_pre[i][j].y, s_pre[i][j + 1].x, s_pre[i][j + 1].y);
-      *reinterpret_cast<float4*>(to + a.K + 8 * c + 2 * j) =
-          make_float4(s_x[i][j].x, s_x[i][j].y, s_x[i][j + 1].x, s_x[i][j + 1].y);
+      const float4 v0 = make_float4(s_pre[i][j].x, s_pre[i][j].y, s_pre[i][j + 1].x, s_pre[i][j + 1].y);
+      const float4 v1 = make_float4(s_x[i][j].x, s_x[i][j].y, s_x[i][j + 1].x, s_x[i][j + 1].y);
+      const int e = 2 * c + j / 2;
+      if (p.teams > 1) {
+        own[e] = v0;
+        own[a.K / 4 + e] = v1;
+      } else {
+        put_sums(a, sums, all, e, v0);
+        put_sums(a, sums, all, a.K / 4 + e, v1);
+      }
     }
   }
   float sr = s_res.x + s_res.y;
@@ -663,13 +699,14 @@ __global__ void __launch_bounds__(MAXT, 1)
         v.z += o.z;
         v.w += o.w;
       }
-      reinterpret_cast<float4*>(sums)[e] = v;
+      put_sums(a, sums, all, e, v);
     }
   }
   if (has_res && threadIdx.x == 0) {
     sr = 0.f;
     for (int w = 0; w < (int)(blockDim.x >> 5); ++w) sr += last[w];
-    a.ws[(size_t)gridDim.x * 2 * a.K + blockIdx.x] = sr;
+    if (all) *a.dscale = sr;
+    else a.ws[(size_t)gridDim.x * 2 * a.K + blockIdx.x] = sr;
   }
 }
 
@@ -700,14 +737,10 @@ __global__ void __launch_bounds__(32 * kColWarps) sandwich_columns_kernel(const 
       s1 += part[1][w][lane];
     }
     if (a.dpre != nullptr) a.dpre[k] = s0;
-    Gate g = {1.f, 1.f};
-    if (a.gate_kind == 1)
-      g = gate_of(__uint_as_float((uint32_t)static_cast<const uint16_t*>(a.gate)[k] << 16), a.gate_act);
-    if (a.dpost != nullptr) a.dpost[k] = g.v * s1;
-    if (a.gate_kind == 1 && a.dgate != nullptr) {
-      const float p = a.post != nullptr ? __uint_as_float((uint32_t)a.post[k] << 16) : 1.f;
-      static_cast<float*>(a.dgate)[k] = g.d * (p * s1);
-    }
+    const float2 o = finish_column(a, a.gate_kind == 1 ? static_cast<const uint16_t*>(a.gate)[k] : 0u,
+                                   a.post != nullptr ? a.post[k] : 0u, s1);
+    if (a.dpost != nullptr) a.dpost[k] = o.x;
+    if (a.gate_kind == 1 && a.dgate != nullptr) static_cast<float*>(a.dgate)[k] = o.y;
   }
   if (a.dscale != nullptr && blockIdx.x == 0 && warp == 1) {
     float s = 0.f;
@@ -793,6 +826,7 @@ cudaError_t run_bwd(const SandwichBwdArgs& a, int num_sms, int* grid, cudaStream
   if (e != cudaSuccess) return e;
   const BwdPlan p = bwd_plan(a, num_sms, CH, E8, ROWS, MAXT);
   *grid = (int)(((unsigned)a.T + ROWS * p.teams - 1) / (ROWS * p.teams));   // (T + 15 may pass 2^31)
+  if (a.T <= kSwOneCta) *grid = 1;
   if (*grid > num_sms) *grid = num_sms;
   if (*grid > kSwMaxCtas) *grid = kSwMaxCtas;
   // copies that read nothing still name rows that are there
@@ -860,6 +894,7 @@ cudaError_t launch_sandwich_norm_backward(const SandwichBwdArgs& a, int num_sms,
                                             : run_bwd_form<4, 1, 512>(a, num_sms, &grid, stream);
     if (e != cudaSuccess) return e;
   }
+  if (grid == 1) return cudaSuccess;   // its CTA has finished the columns itself
   if (a.dpre != nullptr || a.dpost != nullptr || a.dscale != nullptr || (a.gate_kind == 1 && a.dgate != nullptr))
     return run_columns(a, grid, stream);
   return cudaSuccess;
