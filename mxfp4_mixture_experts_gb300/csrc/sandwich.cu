@@ -282,26 +282,34 @@ __device__ __forceinline__ float fold8(float v) {
   for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
-// Over a team of nt threads of the CTA (its own named barrier, none for one warp);
-// part: [3 ROWS][32], a place a warp of the CTA.
-template <int ROWS>
+// Over a team of nt threads of the CTA (its own named barrier, none for one warp), or over a pair of CTAs,
+// each of which writes its parts into both; part: [3 ROWS][32], a place a warp.
+template <int ROWS, bool PAIR>
 __device__ __forceinline__ void team_sum3(float (&v)[ROWS][3], float (*part)[32], int team, int nt, int lane,
                                           int warp, int warps) {
   float m[ROWS];
 #pragma unroll
   for (int r = 0; r < ROWS; ++r) m[r] = fold8(merge3(v[r][0], v[r][1], v[r][2], lane));
-  if (warps > 1) {
-    const int base = team * warps;
-    const bool there = lane < warps;
+  if (PAIR || warps > 1) {
+    const uint32_t rank = PAIR ? cluster_rank() : 0;
+    const int base = PAIR ? 16 * rank : team * warps;
     if ((lane & 7) == 0 && lane < 24) {
 #pragma unroll
-      for (int r = 0; r < ROWS; ++r) part[3 * r + (lane == 0 ? 0 : lane == 16 ? 1 : 2)][base + warp] = m[r];
+      for (int r = 0; r < ROWS; ++r) {
+        float* to = &part[3 * r + (lane == 0 ? 0 : lane == 16 ? 1 : 2)][base + warp];
+        *to = m[r];
+        if (PAIR)
+          asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr(to, rank ^ 1)), "f"(m[r]) : "memory");
+      }
     }
-    named_barrier(team + 1, nt);
+    if (PAIR) cluster_sync();
+    else named_barrier(team + 1, nt);
+    const bool there = (PAIR ? lane & 15 : lane) < warps;
+    const int at = PAIR ? lane : base + lane;
 #pragma unroll
     for (int r = 0; r < ROWS; ++r)
-      m[r] = fold8(merge3(there ? part[3 * r][base + lane] : 0.f, there ? part[3 * r + 1][base + lane] : 0.f,
-                          there ? part[3 * r + 2][base + lane] : 0.f, lane));
+      m[r] = fold8(merge3(there ? part[3 * r][at] : 0.f, there ? part[3 * r + 1][at] : 0.f,
+                          there ? part[3 * r + 2][at] : 0.f, lane));
   }
 #pragma unroll
   for (int r = 0; r < ROWS; ++r) {
@@ -324,7 +332,7 @@ __device__ __forceinline__ void slot8(const uint8_t* p, bool e4m3, float2 (&v)[4
   v[3] = e4m3x2_values((uint16_t)(q.y >> 16));
 }
 // Shared memory of the gradient: post_gamma, times a channel's gate (fp32, in two halves of
-// 4 values a chunk; not for the longest rows without such a gate), then for every team a ring of rows. A row's slots lie by warp and
+// 4 values a chunk), then for every team a ring of rows. A row's slots lie by warp and
 // chunk, [dh][dy][x][h][gate] of 32 lanes each, the residual's after the warp's chunks; a
 // thread fills and reads its own slots alone. What is not there (a gradient, lanes past
 // the row, rows past the last) is filled with zeros.
@@ -340,6 +348,9 @@ struct Slots {   // byte offsets
   static constexpr int dh = 0, dy = 512, x = 1024, h = x + (E8 == 1 ? 256 : 512), gate = h + (E8 == 1 ? 256 : 512),
                        size = gate + (GATE == 2 ? 512 : 0);
 };
+constexpr int kSwChunks = 2;   // chunks of a thread in the gradient
+// Chunks of the first half of a row whose columns a pair of CTAs shares (whole 32-value blocks).
+__host__ __device__ constexpr int half_chunks(int K) { return (K / 16 + 3) & ~3; }
 // Bytes of a warp's slots of one chunk.
 int slots_bytes(bool full_gate, int e8, bool res) {
   return 1024 + (e8 == 1 ? 512 : 1024) + (full_gate ? 512 : 0) + (res ? 512 : 0);
@@ -373,26 +384,31 @@ __device__ __forceinline__ void put_sums(const SandwichBwdArgs& a, float* row, b
     *reinterpret_cast<float4*>(static_cast<float*>(a.dgate) + c) = make_float4(o[0].y, o[1].y, o[2].y, o[3].y);
 }
 
-// Column sums of the CTA's rows go to ws [gridDim.x][2][K]: 0 dy * h^, 1 d x^ with
+// Column sums of the CTA's (the pair's) rows go to ws [CTAs or pairs][2][K]: 0 dy * h^, 1 d x^ with
 // d = dn, or dh_total where the gate is a channel's (its gate and post_gamma take
 // their gradients from the one sum). After them ws holds a float a CTA, sum dh_total * res.
 // GATE 0: none or a token's, 1: a channel's, 2: one for every value.
 // A warp holds CH * 32 chunks in a row, lane after lane, so that the chunks of a thread lie
 // at fixed distances. ROWS: rows that a team takes together, two independent chains of
 // work for a warp and half the waits (T = 8192, K = 6144, 8-bit x and h: 93 us for 117).
-template <int CH, int GATE, int E8, int ROWS, int MAXT>
+// PAIR: a row is the work of a cluster of two CTAs, half its columns each.
+template <int GATE, int E8, int ROWS, int MAXT, bool PAIR>
 __global__ void __launch_bounds__(MAXT, 1)
     sandwich_bwd_kernel(const SandwichBwdArgs a, const BwdPlan p) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float part[2][3 * ROWS][32];
   __shared__ float last[32];
   using L = Slots<GATE, E8>;
-  // pre_gamma in registers and the weights in shared memory. A spilled register is dear
+  // pre_gamma is in registers, the weights are in shared memory. A spilled register is dear
   // here: beside the ring L1 is a few KB, so that it comes back from L2.
-  constexpr bool kHold = CH <= 2, kWeights = kHold || GATE == 1;
+  constexpr int CH = kSwChunks;
   const int nt = p.nt, team = threadIdx.x / nt, tid = threadIdx.x - team * nt;
   const int lane = tid & 31, warp = tid >> 5, warps = nt >> 5;
-  const int n8 = a.K / 8, c0 = warp * (32 * CH) + lane;   // this thread's chunks: c0 + 32 i
+  // this CTA's columns: n8 chunks of 8 from chunk b0 on; this thread's: c0 + 32 i of them
+  const uint32_t rank = PAIR ? cluster_rank() : 0;
+  const unsigned unit = PAIR ? blockIdx.x >> 1 : blockIdx.x, units = PAIR ? gridDim.x >> 1 : gridDim.x;
+  const int b0 = rank * half_chunks(a.K), n8 = !PAIR ? a.K / 8 : rank == 0 ? half_chunks(a.K) : a.K / 8 - b0;
+  const int c0 = warp * (32 * CH) + lane, g0 = b0 + c0;
   const unsigned T = (unsigned)a.T;   // unsigned: T + the step may pass 2^31
   const bool scaled_res = a.rscale != nullptr;
   const float scale = scaled_res ? *a.rscale : 1.f;
@@ -406,19 +422,19 @@ __global__ void __launch_bounds__(MAXT, 1)
   float4* gch = reinterpret_cast<float4*>(smem);   // [2][chunks of a team]
   const int gch_half = CH * nt;
   bool valid[CH];
-  uint4 gn[kHold ? CH : 1];
+  uint4 gn[CH];
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const int c = c0 + 32 * i;
     valid[i] = c < n8;
-    if (kHold) gn[i] = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);   // 1
-    if (kWeights && team == 0) {
+    gn[i] = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);   // 1
+    if (team == 0) {
       float g[8], w[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) g[j] = w[j] = 1.f;
       if (valid[i]) {
-        if (GATE == 1) unpack8(ld_row16(gate16 + 8 * c), g);
-        if (has_post) unpack8(ld_row16(a.post + 8 * c), w);
+        if (GATE == 1) unpack8(ld_row16(gate16 + 8 * (b0 + c)), g);
+        if (has_post) unpack8(ld_row16(a.post + 8 * (b0 + c)), w);
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) g[j] = GATE == 1 ? gate_value(g[j], a.gate_act) * w[j] : w[j];
@@ -426,29 +442,17 @@ __global__ void __launch_bounds__(MAXT, 1)
       gch[gch_half + c] = make_float4(g[4], g[5], g[6], g[7]);
     }
     if (!valid[i]) continue;
-    if (kHold && has_dy) gn[i] = ld_row16(a.pre + 8 * c);
+    if (has_dy) gn[i] = ld_row16(a.pre + 8 * (b0 + c));
   }
-  if (kWeights) __syncthreads();
+  __syncthreads();
+  if (PAIR) cluster_sync();   // the other CTA has begun: its shared memory may be written
   // post_gamma, times the channel's gate
   auto weight_of = [&](int i, float2 (&v)[4]) {
-    if (kWeights) {
-      const float4 g0 = gch[c0 + 32 * i], g1 = gch[gch_half + c0 + 32 * i];
-      v[0] = make_float2(g0.x, g0.y);
-      v[1] = make_float2(g0.z, g0.w);
-      v[2] = make_float2(g1.x, g1.y);
-      v[3] = make_float2(g1.z, g1.w);
-    } else {
-      v[0] = v[1] = v[2] = v[3] = dup(1.f);
-      if (has_post && valid[i]) unpack4(ld_row16(a.post + 8 * (c0 + 32 * i)), v);
-    }
-  };
-  auto pre_of = [&](int i, float2 (&v)[4]) {
-    if (kHold) {
-      unpack4(gn[kHold ? i : 0], v);
-    } else {
-      v[0] = v[1] = v[2] = v[3] = dup(1.f);
-      if (has_dy && valid[i]) unpack4(ld_row16(a.pre + 8 * (c0 + 32 * i)), v);
-    }
+    const float4 w0 = gch[c0 + 32 * i], w1 = gch[gch_half + c0 + 32 * i];
+    v[0] = make_float2(w0.x, w0.y);
+    v[1] = make_float2(w0.z, w0.w);
+    v[2] = make_float2(w1.x, w1.y);
+    v[3] = make_float2(w1.z, w1.w);
   };
   // Rows t .. t + ROWS - 1 into stage st. Addresses stay inside the arrays' last row but for
   // lanes past its end, whose copies read nothing.
@@ -458,7 +462,7 @@ __global__ void __launch_bounds__(MAXT, 1)
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
       const int there = t + r < T ? 16 : 0;
-      const size_t at = (size_t)min(t + r, T - 1) * a.K + 8 * c0;
+      const size_t at = (size_t)min(t + r, T - 1) * a.K + 8 * g0;
       const uint32_t to = mine_addr + st * p.stage + r * p.row;
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
@@ -484,7 +488,7 @@ __global__ void __launch_bounds__(MAXT, 1)
   };
   int sc[CH];   // this thread's scale bytes
 #pragma unroll
-  for (int i = 0; i < CH; ++i) sc[i] = min(c0 + 32 * i, n8 - 1) >> 2;
+  for (int i = 0; i < CH; ++i) sc[i] = (b0 + min(c0 + 32 * i, n8 - 1)) >> 2;
   auto scalars = [&](unsigned t0, RowScalars& s) {
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
@@ -509,8 +513,8 @@ __global__ void __launch_bounds__(MAXT, 1)
   for (int i = 0; i < CH; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) s_pre[i][j] = s_x[i][j] = dup(0.f);
-  const unsigned step = gridDim.x * p.teams * ROWS;
-  const unsigned first = (blockIdx.x * p.teams + team) * ROWS;
+  const unsigned step = units * p.teams * ROWS;
+  const unsigned first = (unit * p.teams + team) * ROWS;
   grid_launch_dependents();
   RowScalars now = {}, next = {};
   scalars(first, next);
@@ -538,7 +542,7 @@ __global__ void __launch_bounds__(MAXT, 1)
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       float2 g[4], w0[4];
-      pre_of(i, g);
+      unpack4(gn[i], g);
       weight_of(i, w0);
 #pragma unroll
       for (int r = 0; r < ROWS; ++r) {
@@ -585,7 +589,7 @@ __global__ void __launch_bounds__(MAXT, 1)
     for (int r = 0; r < ROWS; ++r)
 #pragma unroll
       for (int n = 0; n < 3; ++n) s[r][n] = s2[r][n].x + s2[r][n].y;
-    team_sum3<ROWS>(s, part[odd], team, nt, lane, warp, warps);
+    team_sum3<ROWS, PAIR>(s, part[odd], team, nt, lane, warp, warps);
     float kh[ROWS], k1[ROWS], xr[ROWS];   // of h^, of x^ times the token's gate, of x
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
@@ -593,7 +597,7 @@ __global__ void __launch_bounds__(MAXT, 1)
       const float gt = GATE == 0 && a.gate_kind == 2 ? gate_value(now.g[r], a.gate_act) : 1.f;
       const float c2 = s[r][0] * r2 * inv_k * r2;                 // r2 mean(v h^)
       const float dot = r1 * (s[r][1] - c2 * (r2 * s[r][2]));     // sum of w x^ dh_total
-      if (GATE == 0 && a.gate_kind == 2 && a.dgate != nullptr && tid == 0 && t + r < T)
+      if (GATE == 0 && a.gate_kind == 2 && a.dgate != nullptr && tid == 0 && rank == 0 && t + r < T)
         static_cast<float*>(a.dgate)[t + r] = dot * gate_of(now.g[r], a.gate_act).d;
       kh[r] = -c2;
       k1[r] = has_post ? -r1 * (dot * inv_k) : 0.f;
@@ -601,7 +605,7 @@ __global__ void __launch_bounds__(MAXT, 1)
     }
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
-      const size_t out = (size_t)(t + r) * a.K + 8 * c0;
+      const size_t out = (size_t)(t + r) * a.K + 8 * g0;
       const bool there = t + r < T;
       const bool st_res = there && a.dres != nullptr, st_x = there && a.dx != nullptr;
 #pragma unroll
@@ -658,10 +662,10 @@ __global__ void __launch_bounds__(MAXT, 1)
     if (++st == p.depth) st = 0;
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
-  float* sums = a.ws + (size_t)blockIdx.x * 2 * a.K;
+  float* sums = a.ws + (size_t)unit * 2 * a.K;
   if (p.teams > 1) __syncthreads();
   // one team: straight out; several: through shared memory, added up in order
-  const bool all = gridDim.x == 1;
+  const bool all = gridDim.x == 1;   // (never a pair)
   float4* const own = reinterpret_cast<float4*>(smem) + (size_t)team * (a.K / 2);
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
@@ -671,7 +675,7 @@ __global__ void __launch_bounds__(MAXT, 1)
     for (int j = 0; j < 4; j += 2) {
       const float4 v0 = make_float4(s_pre[i][j].x, s_pre[i][j].y, s_pre[i][j + 1].x, s_pre[i][j + 1].y);
       const float4 v1 = make_float4(s_x[i][j].x, s_x[i][j].y, s_x[i][j + 1].x, s_x[i][j + 1].y);
-      const int e = 2 * c + j / 2;
+      const int e = 2 * (b0 + c) + j / 2;
       if (p.teams > 1) {
         own[e] = v0;
         own[a.K / 4 + e] = v1;
@@ -706,7 +710,7 @@ __global__ void __launch_bounds__(MAXT, 1)
     sr = 0.f;
     for (int w = 0; w < (int)(blockDim.x >> 5); ++w) sr += last[w];
     if (all) *a.dscale = sr;
-    else a.ws[(size_t)gridDim.x * 2 * a.K + blockIdx.x] = sr;
+    else a.ws[(size_t)units * 2 * a.K + blockIdx.x] = sr;
   }
 }
 
@@ -714,7 +718,7 @@ __global__ void __launch_bounds__(MAXT, 1)
 // columns a CTA, every 16th row a warp, so that few loads follow one another. Launched
 // while the rows' kernel still runs; waits for its end before it reads.
 constexpr int kColWarps = 16;
-__global__ void __launch_bounds__(32 * kColWarps) sandwich_columns_kernel(const SandwichBwdArgs a, int rows) {
+__global__ void __launch_bounds__(32 * kColWarps) sandwich_columns_kernel(const SandwichBwdArgs a, int rows, int scalars) {
   __shared__ float part[2][kColWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int k = blockIdx.x * 32 + lane;   // K is a multiple of 32
@@ -744,7 +748,7 @@ __global__ void __launch_bounds__(32 * kColWarps) sandwich_columns_kernel(const 
   }
   if (a.dscale != nullptr && blockIdx.x == 0 && warp == 1) {
     float s = 0.f;
-    for (int r = lane; r < rows; r += 32) s += a.ws[(size_t)rows * 2 * a.K + r];
+    for (int r = lane; r < scalars; r += 32) s += a.ws[(size_t)rows * 2 * a.K + r];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (lane == 0) *a.dscale = s;
@@ -798,15 +802,15 @@ cudaError_t run_fwd(const SandwichArgs& a, int num_sms, cudaStream_t stream) {
 
 // Threads, rows at a time and ring of a gradient call. One CTA a SM, so that an SM
 // leaves one row of column sums; short rows share it, several teams to a CTA.
-BwdPlan bwd_plan(const SandwichBwdArgs& a, int num_sms, int ch, int e8, int rows, int maxt) {
+BwdPlan bwd_plan(const SandwichBwdArgs& a, int num_sms, int e8, int rows, int maxt, bool pair) {
   BwdPlan p = {};
-  p.nt = row_threads(a.K / 8, ch);
-  p.teams = maxt / p.nt;   // (at most 16, and of one warp each where above 8: named barriers 1 .. 15)
+  p.nt = row_threads(pair ? half_chunks(a.K) : a.K / 8, kSwChunks);
+  p.teams = pair ? 1 : maxt / p.nt;   // (at most 16, and of one warp each where above 8: named barriers 1 .. 15)
   const int most = (int)(((unsigned)a.T + rows * num_sms - 1) / (rows * num_sms));
   if (p.teams > most) p.teams = most;
-  p.row = p.nt / 32 * ch * slots_bytes(a.gate_kind == 3, e8, a.dscale != nullptr);
+  p.row = p.nt / 32 * kSwChunks * slots_bytes(a.gate_kind == 3, e8, a.dscale != nullptr);
   p.stage = rows * p.row;
-  p.gate_bytes = ch <= 2 || a.gate_kind == 1 ? 32 * ch * p.nt : 0;
+  p.gate_bytes = 32 * kSwChunks * p.nt;
   p.depth = (kSwRingBytes - p.gate_bytes) / (p.teams * p.stage);
   if (p.depth > 4) p.depth = 4;
   p.has_dh = a.dh != nullptr;
@@ -817,18 +821,48 @@ BwdPlan bwd_plan(const SandwichBwdArgs& a, int num_sms, int ch, int e8, int rows
   return p;
 }
 
-template <int CH, int GATE, int E8, int ROWS, int MAXT>
-cudaError_t run_bwd(const SandwichBwdArgs& a, int num_sms, int* grid, cudaStream_t stream) {
+// Rows of column sums that a call leaves in ws (CTAs or pairs), and the CTAs.
+struct BwdGrid {
+  int units, ctas;
+};
+
+template <int GATE, int E8, int ROWS, int MAXT, bool PAIR>
+cudaError_t run_bwd(const SandwichBwdArgs& a, int num_sms, BwdGrid* grid, cudaStream_t stream) {
   static bool granted[kGrantDevices] = {};
+  static int resident[kGrantDevices] = {};   // pairs at a time
   static std::mutex mu;
-  const auto kernel = sandwich_bwd_kernel<CH, GATE, E8, ROWS, MAXT>;
-  const cudaError_t e = grant_smem(reinterpret_cast<const void*>(kernel), kSwRingBytes, granted, mu);
+  const auto kernel = sandwich_bwd_kernel<GATE, E8, ROWS, MAXT, PAIR>;
+  cudaError_t e = grant_smem(reinterpret_cast<const void*>(kernel), kSwRingBytes, granted, mu);
   if (e != cudaSuccess) return e;
-  const BwdPlan p = bwd_plan(a, num_sms, CH, E8, ROWS, MAXT);
-  *grid = (int)(((unsigned)a.T + ROWS * p.teams - 1) / (ROWS * p.teams));   // (T + 15 may pass 2^31)
-  if (a.T <= kSwOneCta) *grid = 1;
-  if (*grid > num_sms) *grid = num_sms;
-  if (*grid > kSwMaxCtas) *grid = kSwMaxCtas;
+  const BwdPlan p = bwd_plan(a, num_sms, E8, ROWS, MAXT, PAIR);
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(p.teams * p.nt);
+  cfg.dynamicSmemBytes = p.smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 2;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = PAIR ? 1 : 0;
+  int most = num_sms;
+  if (PAIR) {   // (whatever the size, one CTA an SM: rows past 8192 values have more than 8 warps of 128 registers)
+    int dev = 0;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lk(mu);
+    if (resident[dev] == 0) {
+      cfg.gridDim = dim3(num_sms / 2 * 2);
+      e = cudaOccupancyMaxActiveClusters(&resident[dev], kernel, &cfg);
+      if (e != cudaSuccess) return e;
+      if (resident[dev] < 1) return cudaErrorInvalidConfiguration;
+    }
+    most = resident[dev] < num_sms / 2 ? resident[dev] : num_sms / 2;
+  }
+  const unsigned want = ((unsigned)a.T + ROWS * p.teams - 1) / (ROWS * p.teams);   // (T + 15 may pass 2^31)
+  grid->units = want < (unsigned)most ? (int)want : most;
+  if (!PAIR && a.T <= kSwOneCta) grid->units = 1;
+  if (grid->units > kSwMaxCtas) grid->units = kSwMaxCtas;
+  grid->ctas = PAIR ? 2 * grid->units : grid->units;
   // copies that read nothing still name rows that are there
   SandwichBwdArgs k = a;
   if (!p.has_dh) k.dh = a.dy;
@@ -837,24 +871,25 @@ cudaError_t run_bwd(const SandwichBwdArgs& a, int num_sms, int* grid, cudaStream
     if (E8 == 1) k.h = a.x;
     else k.h = a.dh, k.hs = nullptr;
   }
-  kernel<<<*grid, p.teams * p.nt, p.smem, stream>>>(k, p);
-  return cudaGetLastError();
+  cfg.gridDim = dim3(grid->ctas);
+  return cudaLaunchKernelEx(&cfg, kernel, k, p);
 }
 
-template <int CH, int E8, int ROWS, int MAXT>
-cudaError_t run_bwd_gate(const SandwichBwdArgs& a, int num_sms, int* grid, cudaStream_t stream) {
-  if (a.gate_kind == 1) return run_bwd<CH, 1, E8, ROWS, MAXT>(a, num_sms, grid, stream);
-  if (a.gate_kind == 3) return run_bwd<CH, 2, E8, ROWS, MAXT>(a, num_sms, grid, stream);
-  return run_bwd<CH, 0, E8, ROWS, MAXT>(a, num_sms, grid, stream);
+template <int E8, int ROWS, int MAXT, bool PAIR>
+cudaError_t run_bwd_gate(const SandwichBwdArgs& a, int num_sms, BwdGrid* grid, cudaStream_t stream) {
+  if (a.gate_kind == 1) return run_bwd<1, E8, ROWS, MAXT, PAIR>(a, num_sms, grid, stream);
+  if (a.gate_kind == 3) return run_bwd<2, E8, ROWS, MAXT, PAIR>(a, num_sms, grid, stream);
+  return run_bwd<0, E8, ROWS, MAXT, PAIR>(a, num_sms, grid, stream);
 }
-template <int CH, int ROWS, int MAXT>
-cudaError_t run_bwd_form(const SandwichBwdArgs& a, int num_sms, int* grid, cudaStream_t stream) {
+template <int ROWS, int MAXT, bool PAIR>
+cudaError_t run_bwd_form(const SandwichBwdArgs& a, int num_sms, BwdGrid* grid, cudaStream_t stream) {
   const bool x8 = a.xs != nullptr, h8 = a.dy != nullptr ? a.hs != nullptr : x8;   // (without dy h is not read)
-  if (x8 != h8) return run_bwd_gate<CH, 2, ROWS, MAXT>(a, num_sms, grid, stream);
-  return x8 ? run_bwd_gate<CH, 1, ROWS, MAXT>(a, num_sms, grid, stream) : run_bwd_gate<CH, 0, ROWS, MAXT>(a, num_sms, grid, stream);
+  if (x8 != h8) return run_bwd_gate<2, ROWS, MAXT, PAIR>(a, num_sms, grid, stream);
+  return x8 ? run_bwd_gate<1, ROWS, MAXT, PAIR>(a, num_sms, grid, stream)
+            : run_bwd_gate<0, ROWS, MAXT, PAIR>(a, num_sms, grid, stream);
 }
 
-cudaError_t run_columns(const SandwichBwdArgs& a, int rows, cudaStream_t stream) {
+cudaError_t run_columns(const SandwichBwdArgs& a, int rows, int scalars, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.K / 32);
   cfg.blockDim = dim3(32 * kColWarps);
@@ -864,7 +899,7 @@ cudaError_t run_columns(const SandwichBwdArgs& a, int rows, cudaStream_t stream)
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = rows > 0 ? 1 : 0;   // (no rows: nothing of this call runs before it)
-  return cudaLaunchKernelEx(&cfg, sandwich_columns_kernel, a, rows);
+  return cudaLaunchKernelEx(&cfg, sandwich_columns_kernel, a, rows, scalars);
 }
 
 }  // namespace
@@ -880,23 +915,23 @@ cudaError_t launch_sandwich_norm(const SandwichArgs& a, int num_sms, cudaStream_
 
 size_t sandwich_bwd_workspace_bytes(int T, int K) {
   const size_t rows = T < kSwMaxCtas ? T : kSwMaxCtas;
-  return rows * (2 * (size_t)K + 1) * sizeof(float);
+  return rows * (2 * (size_t)K + 2) * sizeof(float);   // (a scalar each, of a pair two)
 }
 
 cudaError_t launch_sandwich_norm_backward(const SandwichBwdArgs& a, int num_sms, cudaStream_t stream) {
-  int grid = 0;
+  BwdGrid grid = {};
   if (a.T > 0) {   // (no rows: the sums are zero)
     // Two rows a team, 168 registers a thread; one (128 registers) where few rows would leave SMs
     // idle (T = 16, K = 2880: 5.4 us for 6.7; T = 150 8.4 for 9.3 the other way) and for rows past 6144
     // values, which take 16 warps.
-    const cudaError_t e = a.K <= 16 * 384 && a.T > num_sms / 2 ? run_bwd_form<2, 2, 384>(a, num_sms, &grid, stream)
-                          : a.K <= 16 * 512 ? run_bwd_form<2, 1, 512>(a, num_sms, &grid, stream)
-                                            : run_bwd_form<4, 1, 512>(a, num_sms, &grid, stream);
+    const cudaError_t e = a.K <= 16 * 384 && a.T > num_sms / 2 ? run_bwd_form<2, 384, false>(a, num_sms, &grid, stream)
+                          : a.K <= 16 * 512 ? run_bwd_form<1, 512, false>(a, num_sms, &grid, stream)
+                                            : run_bwd_form<1, 512, true>(a, num_sms, &grid, stream);
     if (e != cudaSuccess) return e;
   }
-  if (grid == 1) return cudaSuccess;   // its CTA has finished the columns itself
+  if (grid.ctas == 1) return cudaSuccess;   // its CTA has finished the columns itself
   if (a.dpre != nullptr || a.dpost != nullptr || a.dscale != nullptr || (a.gate_kind == 1 && a.dgate != nullptr))
-    return run_columns(a, grid, stream);
+    return run_columns(a, grid.units, grid.ctas, stream);
   return cudaSuccess;
 }
 

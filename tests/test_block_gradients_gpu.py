@@ -121,7 +121,7 @@ def check_forward(moe, d, act="linear", eps=1e-5, out8=None, ck=None, **kw):
 
 
 SHAPES = [(1, 32), (1, 2880), (3, 64), (2, 7168), (5, 8160), (2, 8192), (1, 16384), (33, 1056), (700, 96), (5, 4128),
-          (350, 512)]
+          (350, 512), (3, 8224), (190, 12320)]
 
 
 @pytest.mark.parametrize("T,K", SHAPES)
