@@ -189,3 +189,38 @@ def test_parameters_and_views_are_taken(moe):
         moe.sandwich_norm(**{**c, "x": c["x"].cpu()})
     with pytest.raises(ValueError):
         moe.sandwich_norm(**{**c, "pre_gamma": c["pre_gamma"].cpu()})
+
+
+FIRST = """
+import sys
+sys.path[:0] = [{root!r}, {tests!r}]
+import torch
+import test_block_gradients_gpu as B
+from mxfp4_mixture_experts_gb300 import moe
+K = {K}
+f, _ = B.calls(moe, T=40, K=K)[{op!r}] if {op!r} != "sandwich_norm_backward" else (None, 0)
+if f is None:
+    call, _ = B.make_backward(B.rows(40, K, 21, "full"), "sigmoid", seed=1)
+    call = {{n: v if isinstance(v, str) else B.cuda(v) for n, v in call.items()}}
+    f = lambda **kw: moe.sandwich_norm_backward(**call, **kw)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    out = f()
+g.replay()
+torch.cuda.synchronize()
+assert B.same(B.copies(out), B.copies(f()))
+print("same")
+"""
+
+
+@pytest.mark.parametrize("op,K", [("sandwich_norm", 640), ("sandwich_norm_backward", 640), ("sandwich_norm_backward", 8224),
+                                  ("router_backward", 640), ("combine_backward", 640)])
+def test_first_call_of_a_process_inside_a_capture(moe, op, K):
+    import os
+    import subprocess
+    import sys
+    tests = os.path.dirname(os.path.abspath(__file__))
+    r = subprocess.run([sys.executable, "-c", FIRST.format(root=os.path.dirname(tests), tests=tests, op=op, K=K)],
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
