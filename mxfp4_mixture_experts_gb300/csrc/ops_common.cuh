@@ -12,6 +12,20 @@ __device__ __forceinline__ uint32_t bf16x2_rn(float lo, float hi) {
   return r;
 }
 
+// exp(v) and 1 / v by the hardware's approximations (2^-22 and 1 ulp; the exponent's rounding adds
+// |v| 2^-24), results below 2^-126 as 0: without the steps that the functions of the same
+// precision take for those. exp(-inf) = 0, 1 / inf = 0; v of fast_rcp is not subnormal.
+__device__ __forceinline__ float fast_exp(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v * 1.4426950408889634f));
+  return r;
+}
+__device__ __forceinline__ float fast_rcp(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
 // Lets the next kernel of the stream, launched with programmatic
 // serialisation, start before this one has finished.
 __device__ __forceinline__ void grid_launch_dependents() {

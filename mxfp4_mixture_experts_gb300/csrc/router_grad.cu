@@ -24,7 +24,7 @@
 // One warp per token, its logits in registers, four neighbours a lane and 16-byte load where rows
 // allow it: the logits are read once, 4 T E bytes and as many written by the gradient. Both
 // kernels are bound by their instructions, so exponentials and reciprocals are the
-// hardware's (2^-22 and 1 ulp; the argument's rounding adds |x| 2^-24), a sigmoid and its
+// hardware's (a score below 2^-126 is 0), a sigmoid and its
 // complement come from one exponential, and a chosen expert's gradient is put
 // together in its slot's lane and written over the rest's, not searched for in the registers.
 // The losses' sums are per tile of tokens and sequence (a piece), written to scratch and added
@@ -48,9 +48,6 @@ __device__ __forceinline__ float warp_sum(float v) {
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
-// exp(v) and 1 / v; exp(-inf) = 0, 1 / inf = 0
-__device__ __forceinline__ float fast_exp(float v) { return __expf(v); }
-__device__ __forceinline__ float fast_rcp(float v) { return __fdividef(1.f, v); }
 // sigmoid(x) and sigmoid(-x), neither of which loses its last bits where the other is near 1
 struct Sigmoid {
   float s, rest;
@@ -204,7 +201,7 @@ struct Sums {
         for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
         total = __shfl_sync(0xffffffffu, v, 0);
         sum = __shfl_sync(0xffffffffu, v, 16);
-        inv = sum > 0.f ? fast_rcp(sum) : 0.f;
+        inv = sum >= FLT_MIN ? fast_rcp(sum) : 0.f;
       }
       const float lse = k.m + __logf(total);
       z = fmaf(lse, lse, z);
@@ -620,7 +617,7 @@ __global__ void __launch_bounds__(kRbWarps * 32) router_backward_kernel(const Ro
           rest[j] = g.rest;
         }
         sum = warp_sum(sum);
-        is = sum > 0.f ? fast_rcp(sum) : 0.f;
+        is = sum >= FLT_MIN ? fast_rcp(sum) : 0.f;
       }
 #pragma unroll
       for (int j = 0; j < NPL; ++j) dot = fmaf(p[j], sl[j], dot);

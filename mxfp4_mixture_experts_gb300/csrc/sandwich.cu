@@ -49,8 +49,7 @@ struct Gate {
 };
 __device__ __forceinline__ Gate gate_of(float g, int act) {
   if (!act) return Gate{g, 1.f};
-  const float e = __expf(-fabsf(g));
-  const float hi = __fdividef(1.f, 1.f + e), lo = e * hi;
+  const float e = fast_exp(-fabsf(g)), hi = fast_rcp(1.f + e), lo = e * hi;
   return Gate{g < 0.f ? lo : hi, hi * lo};
 }
 __device__ __forceinline__ float gate_value(float g, int act) { return gate_of(g, act).v; }
@@ -348,7 +347,7 @@ struct BwdPlan {
 template <int GATE, int E8>
 struct Slots {   // byte offsets
   static constexpr int dh = 0, dy = 512, x = 1024, h = x + (E8 == 1 ? 256 : 512), gate = h + (E8 == 1 ? 256 : 512),
-                       size = gate + (GATE == 2 ? 512 : 0);
+                       size = gate + (GATE >= 2 ? 512 : 0);
 };
 constexpr int kSwChunks = 2;   // chunks of a thread in the gradient
 // Chunks of the first half of a row whose columns a pair of CTAs shares (whole 32-value blocks).
@@ -389,7 +388,7 @@ __device__ __forceinline__ void put_sums(const SandwichBwdArgs& a, float* row, b
 // Column sums of the CTA's (the pair's) rows go to ws [CTAs or pairs][2][K]: 0 dy * h^, 1 d x^ with
 // d = dn, or dh_total where the gate is a channel's (its gate and post_gamma take
 // their gradients from the one sum). After them ws holds a float a CTA, sum dh_total * res.
-// GATE 0: none or a token's, 1: a channel's, 2: one for every value.
+// GATE 0: none or a token's, 1: a channel's, 2: one for every value, 3: the same through a sigmoid.
 // A warp holds CH * 32 chunks in a row, lane after lane, so that the chunks of a thread lie
 // at fixed distances. ROWS: rows that a team takes together, two independent chains of
 // work for a warp and half the waits (T = 8192, K = 6144, 8-bit x and h: 93 us for 117).
@@ -478,7 +477,7 @@ __global__ void __launch_bounds__(MAXT, 1)
         else copy16(base + L::h + lane_h, static_cast<const uint16_t*>(a.h) + at + 256 * i, n & n_dy);
         if (x8) copy8(base + L::x + lane_x, static_cast<const uint8_t*>(a.x) + at + 256 * i, n >> 1);
         else copy16(base + L::x + lane_x, static_cast<const uint16_t*>(a.x) + at + 256 * i, n);
-        if (GATE == 2) copy16(base + L::gate + lane16, gate16 + at + 256 * i, n);
+        if (GATE >= 2) copy16(base + L::gate + lane16, gate16 + at + 256 * i, n);
         if (has_res) copy16(to + res0 + 512 * i, a.residual + at + 256 * i, n);
       }
     }
@@ -560,12 +559,12 @@ __global__ void __launch_bounds__(MAXT, 1)
         float2 c2[3] = {dup(0.f), dup(0.f), dup(0.f)};
 #pragma unroll
         for (int j = 0; j < 4; ++j) w[j] = w0[j];
-        if (GATE == 2) {
+        if (GATE >= 2) {
           float2 f[4];
           unpack4(*reinterpret_cast<const uint4*>(at + L::gate + lane16), f);
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            w[j] = __fmul2_rn(w[j], make_float2(gate_value(f[j].x, a.gate_act), gate_value(f[j].y, a.gate_act)));
+            w[j] = __fmul2_rn(w[j], make_float2(gate_value(f[j].x, GATE == 3), gate_value(f[j].y, GATE == 3)));
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -638,11 +637,11 @@ __global__ void __launch_bounds__(MAXT, 1)
         uint4 o = pack4(v);
         if (st_res && valid[i]) st_row16(a.dres + out + 256 * i, o);
         // d becomes the gated gradient but for a channel's gate, whose sums take it without
-        if (GATE == 2) {
+        if (GATE >= 2) {
           unpack4(*reinterpret_cast<const uint4*>(at + L::gate + lane16), v);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const Gate gx = gate_of(v[j].x, a.gate_act), gy = gate_of(v[j].y, a.gate_act);
+            const Gate gx = gate_of(v[j].x, GATE == 3), gy = gate_of(v[j].y, GATE == 3);
             h[j] = __fmul2_rn(__fmul2_rn(d[j], make_float2(gx.d, gy.d)),
                               __fmul2_rn(__fmul2_rn(x[j], xrf), w[j]));
             d[j] = __fmul2_rn(d[j], make_float2(gx.v, gy.v));
@@ -819,6 +818,7 @@ BwdPlan bwd_plan(const SandwichBwdArgs& a, int num_sms, int e8, int rows, int ma
   if (p.depth > 4) p.depth = 4;
   p.has_dh = a.dh != nullptr;
   p.has_dy = a.dy != nullptr;
+  if (p.depth < 1) p.depth = 1;   // (never: every form has room for a row; the launch would be refused)
   p.smem = p.gate_bytes + p.teams * p.depth * p.stage;
   const int sums = p.teams > 1 ? p.teams * 8 * a.K : 0;
   if (p.smem < sums) p.smem = sums;
@@ -882,7 +882,9 @@ cudaError_t run_bwd(const SandwichBwdArgs& a, int num_sms, BwdGrid* grid, cudaSt
 template <int E8, int ROWS, int MAXT, bool PAIR>
 cudaError_t run_bwd_gate(const SandwichBwdArgs& a, int num_sms, BwdGrid* grid, cudaStream_t stream) {
   if (a.gate_kind == 1) return run_bwd<1, E8, ROWS, MAXT, PAIR>(a, num_sms, grid, stream);
-  if (a.gate_kind == 3) return run_bwd<2, E8, ROWS, MAXT, PAIR>(a, num_sms, grid, stream);
+  if (a.gate_kind == 3)
+    return a.gate_act ? run_bwd<3, E8, ROWS, MAXT, PAIR>(a, num_sms, grid, stream)
+                      : run_bwd<2, E8, ROWS, MAXT, PAIR>(a, num_sms, grid, stream);
   return run_bwd<0, E8, ROWS, MAXT, PAIR>(a, num_sms, grid, stream);
 }
 template <int ROWS, int MAXT, bool PAIR>
