@@ -29,8 +29,8 @@
 // together in its slot's lane and written over the rest's, not searched for in the registers.
 // The losses' sums are per tile of tokens and sequence (a piece), written to scratch and added
 // up in a fixed order: no floating-point atomics, every repeat gives the same bits.
-// 8192 tokens, 256 experts, 12 sequences, sigmoid, in a graph: losses 13.4 us (two kernels, the
-// first a chain of 3 or 4 tokens a warp), gradient 9.6 us; the launch alone is 2.
+// 8192 tokens, 256 experts, 12 sequences, sigmoid, in a graph: losses 12.9 us (two kernels, the
+// first a chain of 3 or 4 tokens a warp), gradient 7.8 us; the launch alone is 2.
 #include <cfloat>
 #include <cstdint>
 
@@ -231,7 +231,7 @@ __device__ __forceinline__ void finish_stats(const RouterBalanceArgs& a, float l
 }
 
 // All of it in one CTA, for few tokens in one or two sequences: one launch in place of two
-// (32 tokens, 128 experts in a graph 3.9 us for 6.2, 64 tokens, 256 experts 5.7 for 7.0; the host 3 us less).
+// (32 tokens, 128 experts in a graph 3.7 us for 6.2, 64 tokens, 256 experts 5.7 for 7.0; the host 3 us less).
 constexpr int kSmallTokens = 64, kSmallSequences = 2, kSmallWarps = 16;
 template <int NPL, bool VEC>
 __global__ void __launch_bounds__(32 * kSmallWarps) balance_small_kernel(const RouterBalanceArgs a) {
@@ -291,8 +291,8 @@ __global__ void __launch_bounds__(32 * kSmallWarps) balance_small_kernel(const R
   }
 }
 
-// Three CTAs an SM: 80 registers for 8 logits a lane (12 ragged sequences 13.4 us; left to itself the compiler
-// spills, with 116 registers 15.2).
+// Three CTAs an SM: 80 registers for 8 logits a lane (12 ragged sequences 12.9 us; with 116
+// registers 2 us more).
 template <int NPL, bool VEC>
 __global__ void __launch_bounds__(kBalanceWarps<NPL> * 32, 3)
     balance_pieces_kernel(const RouterBalanceArgs a, const BalanceScratch b, unsigned tile) {

@@ -42,8 +42,8 @@ constexpr int kSwRingBytes = 224 * 1024;   // shared memory of a gradient call, 
 // A gate's value and its derivative, (s, s (1 - s)) of a sigmoid: one exponential of -|g|, so that
 // neither overflows nor cancels, and a reciprocal, both approximate: a relative error below
 // 2^-21 + |g| 2^-23 (the exponent's rounding), far under the half step of 2^-8 that a bf16 gate
-// itself carries. (expf: the gradient of T = 4000, K = 2880 with a full gate and a trained scale
-// 68 us for 60.)
+// itself carries. (The gradient of T = 4000, K = 2880 with a full gate and a trained scale: expf 68 us,
+// without the steps for results below 2^-126 52.)
 struct Gate {
   float v, d;
 };
@@ -864,7 +864,7 @@ cudaError_t run_bwd(const SandwichBwdArgs& a, int num_sms, BwdGrid* grid, cudaSt
   }
   const unsigned want = ((unsigned)a.T + ROWS * p.teams - 1) / (ROWS * p.teams);   // (T + 15 may pass 2^31)
   grid->units = want < (unsigned)most ? (int)want : most;
-  if (!PAIR && a.T <= kSwOneCta) grid->units = 1;
+  if (!PAIR && ROWS == 1 && a.T <= kSwOneCta) grid->units = 1;
   if (grid->units > kSwMaxCtas) grid->units = kSwMaxCtas;
   grid->ctas = PAIR ? 2 * grid->units : grid->units;
   // copies that read nothing still name rows that are there
@@ -879,20 +879,32 @@ cudaError_t run_bwd(const SandwichBwdArgs& a, int num_sms, BwdGrid* grid, cudaSt
   return cudaLaunchKernelEx(&cfg, kernel, k, p);
 }
 
-template <int E8, int ROWS, int MAXT, bool PAIR>
+template <int E8, int MAXT, bool PAIR>
 cudaError_t run_bwd_gate(const SandwichBwdArgs& a, int num_sms, BwdGrid* grid, cudaStream_t stream) {
-  if (a.gate_kind == 1) return run_bwd<1, E8, ROWS, MAXT, PAIR>(a, num_sms, grid, stream);
-  if (a.gate_kind == 3)
-    return a.gate_act ? run_bwd<3, E8, ROWS, MAXT, PAIR>(a, num_sms, grid, stream)
-                      : run_bwd<2, E8, ROWS, MAXT, PAIR>(a, num_sms, grid, stream);
-  return run_bwd<0, E8, ROWS, MAXT, PAIR>(a, num_sms, grid, stream);
+  if (a.gate_kind == 1) return run_bwd<1, E8, 1, MAXT, PAIR>(a, num_sms, grid, stream);
+  if (a.gate_kind != 3) return run_bwd<0, E8, 1, MAXT, PAIR>(a, num_sms, grid, stream);
+  return a.gate_act ? run_bwd<3, E8, 1, MAXT, PAIR>(a, num_sms, grid, stream)
+                    : run_bwd<2, E8, 1, MAXT, PAIR>(a, num_sms, grid, stream);
 }
-template <int ROWS, int MAXT, bool PAIR>
+template <bool PAIR>
+cudaError_t run_bwd_rows(const SandwichBwdArgs& a, bool x8, bool h8, int num_sms, BwdGrid* grid, cudaStream_t stream) {
+  if (x8 != h8) return run_bwd_gate<2, 512, PAIR>(a, num_sms, grid, stream);
+  return x8 ? run_bwd_gate<1, 512, PAIR>(a, num_sms, grid, stream) : run_bwd_gate<0, 512, PAIR>(a, num_sms, grid, stream);
+}
 cudaError_t run_bwd_form(const SandwichBwdArgs& a, int num_sms, BwdGrid* grid, cudaStream_t stream) {
   const bool x8 = a.xs != nullptr, h8 = a.dy != nullptr ? a.hs != nullptr : x8;   // (without dy h is not read)
-  if (x8 != h8) return run_bwd_gate<2, ROWS, MAXT, PAIR>(a, num_sms, grid, stream);
-  return x8 ? run_bwd_gate<1, ROWS, MAXT, PAIR>(a, num_sms, grid, stream)
-            : run_bwd_gate<0, ROWS, MAXT, PAIR>(a, num_sms, grid, stream);
+  if (a.K > 16 * 512) return run_bwd_rows<true>(a, x8, h8, num_sms, grid, stream);
+  // Two rows a team, 168 registers a thread, for many long rows whose ring is then still two deep: no
+  // full gate, no residual, the same type of x and h. One row (16 warps of 128 registers) else. In a graph, one
+  // row / two: T = 4000, K = 6144 from bf16 58.8 / 54.9, with the residual 65.6 / 70.9, a full gate 76 / 83; K = 2880
+  // 32.4 / 30.5, T = 777 11.5 / 13.1; K = 512 11.3 / 12.2; T = 777, K = 6144 22.2 / 20.5.
+  if (a.gate_kind != 3 && a.dscale == nullptr && x8 == h8 && a.K > 2048 && a.K <= 16 * 384 &&
+      (size_t)a.T * a.K >= (size_t)9 << 19) {
+    if (a.gate_kind == 1)
+      return x8 ? run_bwd<1, 1, 2, 384, false>(a, num_sms, grid, stream) : run_bwd<1, 0, 2, 384, false>(a, num_sms, grid, stream);
+    return x8 ? run_bwd<0, 1, 2, 384, false>(a, num_sms, grid, stream) : run_bwd<0, 0, 2, 384, false>(a, num_sms, grid, stream);
+  }
+  return run_bwd_rows<false>(a, x8, h8, num_sms, grid, stream);
 }
 
 cudaError_t run_columns(const SandwichBwdArgs& a, int rows, int scalars, cudaStream_t stream) {
@@ -927,12 +939,7 @@ size_t sandwich_bwd_workspace_bytes(int T, int K) {
 cudaError_t launch_sandwich_norm_backward(const SandwichBwdArgs& a, int num_sms, cudaStream_t stream) {
   BwdGrid grid = {};
   if (a.T > 0) {   // (no rows: the sums are zero)
-    // Two rows a team, 168 registers a thread; one (128 registers) where few rows would leave SMs
-    // idle (T = 16, K = 2880: 5.4 us for 6.7; T = 150 8.4 for 9.3 the other way) and for rows past 6144
-    // values, which take 16 warps.
-    const cudaError_t e = a.K <= 16 * 384 && a.T > num_sms / 2 ? run_bwd_form<2, 384, false>(a, num_sms, &grid, stream)
-                          : a.K <= 16 * 512 ? run_bwd_form<1, 512, false>(a, num_sms, &grid, stream)
-                                            : run_bwd_form<1, 512, true>(a, num_sms, &grid, stream);
+    const cudaError_t e = run_bwd_form(a, num_sms, &grid, stream);
     if (e != cudaSuccess) return e;
   }
   if (grid.ctas == 1) return cudaSuccess;   // its CTA has finished the columns itself

@@ -29,6 +29,28 @@ def test_row_counts_around_the_forms(moe, T):
         check_backward(moe, *make_backward(d, "sigmoid", ck="ocp", seed=T))
 
 
+@pytest.mark.parametrize("gate,ck,kw", [(None, None, {}), ("token", "ocp", {}), ("channel", "nosat", {}),
+                                        ("token", None, dict(with_dy=False)), ("channel", None, dict(with_dh=False))])
+def test_two_rows_a_team_and_an_odd_one_left(moe, gate, ck, kw):
+    """The form for many long rows (T * K from 4.7 M on, rows past 2048 values), an odd number of them."""
+    d = rows(2235, 2112, 31, gate, scaled=False)
+    check_backward(moe, *make_backward(d, "sigmoid", ck=ck, seed=3, **kw))
+
+
+def test_two_rows_a_team_keep_nan_in_their_row(moe):
+    """A row of NaN beside a whole one, first and last: the other rows' gradients keep their bits."""
+    d = rows(2235, 2112, 32, "token", scaled=False)
+    call, _ = make_backward(d, "linear", seed=4)
+    run = lambda: moe.sandwich_norm_backward(**{k: v if isinstance(v, str) else cuda(v) for k, v in call.items()})
+    want = run()
+    for t in (0, 1001, 2234):
+        call["grad_y"][t, 7] = float("nan")
+    got = run()
+    keep = [t for t in range(2235) if t not in (0, 1001, 2234)]
+    assert same(got.x[keep], want.x[keep]) and same(got.residual[keep], want.residual[keep])
+    assert same(got.gate[keep], want.gate[keep]) and got.x[2234].isnan().all()
+
+
 @pytest.mark.parametrize("e", [-60, -30, 30, 50])
 def test_rows_far_from_one(moe, e):
     """Rows of magnitude 2^e without an eps: factors of 2^-e, whose squares are out of fp32's range at the ends."""
