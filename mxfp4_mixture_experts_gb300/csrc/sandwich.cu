@@ -138,7 +138,7 @@ __device__ __forceinline__ void store_mx8(const float2 (&v)[4], int nosat, bool 
 // A team of warps to a row, CH * 32 chunks in a row to a warp; short rows share a CTA.
 // A CTA has a row's two waits in each of its teams, the other teams and the other CTA of the SM
 // fill them (24 warps an SM at K = 6144; T = 8192 with 8-bit copies 84 us, a CTA a row 161).
-template <int CH, int MAXT, int PER_SM>
+template <int CH, int MAXT, int PER_SM, bool FULL>   // FULL: a gate for every value
 __global__ void __launch_bounds__(MAXT, PER_SM) sandwich_norm_kernel(const SandwichArgs a, const FwdPlan p) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float part[2][2][32];
@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(MAXT, PER_SM) sandwich_norm_kernel(const Sandw
       const int n = t < T && valid[i] ? 16 : 0;
       copy16(to + i * p.slot, a.x + at + 256 * i, n);
       copy16(to + i * p.slot + 512, a.residual + at + 256 * i, n);
-      if (a.gate_kind == 3) copy16(to + i * p.slot + 1024, gate16 + at + 256 * i, n);
+      if (FULL) copy16(to + i * p.slot + 1024, gate16 + at + 256 * i, n);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
@@ -228,13 +228,13 @@ __global__ void __launch_bounds__(MAXT, PER_SM) sandwich_norm_kernel(const Sandw
         for (int j = 0; j < 4; ++j) z[j] = __fmul2_rn(z[j], dup(scale));
       }
       float2 g[4] = {dup(gt), dup(gt), dup(gt), dup(gt)};
-      if (a.gate_kind == 1) {
+      if (!FULL && a.gate_kind == 1) {
         const float4 g0 = gch[c0 + 32 * i], g1 = gch[half + c0 + 32 * i];
         g[0] = make_float2(g0.x, g0.y);
         g[1] = make_float2(g0.z, g0.w);
         g[2] = make_float2(g1.x, g1.y);
         g[3] = make_float2(g1.z, g1.w);
-      } else if (a.gate_kind == 3) {
+      } else if (FULL) {
         unpack4(*reinterpret_cast<const uint4*>(slot + i * p.slot + 1024), g);
         if (a.gate_act) {
 #pragma unroll
@@ -779,12 +779,12 @@ cudaError_t grant_smem(const void* kernel, int bytes, bool (&granted)[kGrantDevi
   return e;
 }
 
-template <int CH, int MAXT, int PER_SM>
+template <int CH, int MAXT, int PER_SM, bool FULL>
 cudaError_t run_fwd(const SandwichArgs& a, int num_sms, cudaStream_t stream) {
   constexpr int kRing = PER_SM == 2 ? 110 * 1024 : kSwRingBytes;
   static bool granted[kGrantDevices] = {};
   static std::mutex mu;
-  const auto kernel = sandwich_norm_kernel<CH, MAXT, PER_SM>;
+  const auto kernel = sandwich_norm_kernel<CH, MAXT, PER_SM, FULL>;
   const cudaError_t e = grant_smem(reinterpret_cast<const void*>(kernel), kRing, granted, mu);
   if (e != cudaSuccess) return e;
   FwdPlan p = {};
@@ -931,9 +931,9 @@ cudaError_t launch_sandwich_norm(const SandwichArgs& a, int num_sms, cudaStream_
   // One row an SM at most: a chunk a thread, so that the row's chain is short (T = 32, K = 7168 with
   // 8-bit copies 5.9 us for 6.2, T = 1 with a full gate 5.4 for 6.9). Else two chunks a thread and two CTAs an
   // SM, or for rows past 6144 values four and one.
-  if (a.T <= num_sms && a.K <= 8 * 1024) return run_fwd<1, 1024, 1>(a, num_sms, stream);
-  if (a.K <= 16 * 384) return run_fwd<2, 384, 2>(a, num_sms, stream);
-  return run_fwd<4, 512, 1>(a, num_sms, stream);
+  if (a.T <= num_sms && a.K <= 8 * 1024) return a.gate_kind == 3 ? run_fwd<1, 1024, 1, true>(a, num_sms, stream) : run_fwd<1, 1024, 1, false>(a, num_sms, stream);
+  if (a.K <= 16 * 384) return a.gate_kind == 3 ? run_fwd<2, 384, 2, true>(a, num_sms, stream) : run_fwd<2, 384, 2, false>(a, num_sms, stream);
+  return a.gate_kind == 3 ? run_fwd<4, 512, 1, true>(a, num_sms, stream) : run_fwd<4, 512, 1, false>(a, num_sms, stream);
 }
 
 size_t sandwich_bwd_workspace_bytes(int T, int K) {
