@@ -665,10 +665,10 @@ def sandwich_norm(x: torch.Tensor, residual: torch.Tensor, post_gamma: Optional[
         q = _empty(shape, torch.float8_e4m3fn, device, stream)
         qs = _empty((T, K // 32), torch.uint8, device, stream)
     if checkpoint8 is not None:
-        both = _empty((2, T, K), torch.float8_e4m3fn, device, stream)
-        x8, h8 = both[0], both[1]
-        both = _empty((2, T, K // 32), torch.uint8, device, stream)
-        xs, hs = both[0], both[1]
+        x8 = _empty(shape, torch.float8_e4m3fn, device, stream)
+        xs = _empty((T, K // 32), torch.uint8, device, stream)
+        h8 = _like(x8, stream)
+        hs = _like(xs, stream)
     if rstd:
         r = _empty((2, T), torch.float32, device, stream)
     rc = lib().mxfp4_moe_sandwich_norm(
