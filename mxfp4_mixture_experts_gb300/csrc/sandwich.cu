@@ -894,7 +894,8 @@ cudaError_t run_bwd_gate(const SandwichBwdArgs& a, int num_sms, BwdGrid* grid, c
 template <bool PAIR>
 cudaError_t run_bwd_rows(const SandwichBwdArgs& a, bool x8, bool h8, int num_sms, BwdGrid* grid, cudaStream_t stream) {
   if (x8 != h8) return run_bwd_gate<2, 512, PAIR>(a, num_sms, grid, stream);
-  return x8 ? run_bwd_gate<1, 512, PAIR>(a, num_sms, grid, stream) : run_bwd_gate<0, 512, PAIR>(a, num_sms, grid, stream);
+  return x8 ? run_bwd_gate<1, 512, PAIR>(a, num_sms, grid, stream)
+            : run_bwd_gate<0, 512, PAIR>(a, num_sms, grid, stream);
 }
 cudaError_t run_bwd_form(const SandwichBwdArgs& a, int num_sms, BwdGrid* grid, cudaStream_t stream) {
   const bool x8 = a.xs != nullptr, h8 = a.dy != nullptr ? a.hs != nullptr : x8;   // (without dy h is not read)
@@ -906,8 +907,10 @@ cudaError_t run_bwd_form(const SandwichBwdArgs& a, int num_sms, BwdGrid* grid, c
   if (a.gate_kind != 3 && a.dscale == nullptr && x8 == h8 && a.K > 2048 && a.K <= 16 * 384 &&
       (size_t)a.T * a.K >= (size_t)9 << 19) {
     if (a.gate_kind == 1)
-      return x8 ? run_bwd<1, 1, 2, 384, false>(a, num_sms, grid, stream) : run_bwd<1, 0, 2, 384, false>(a, num_sms, grid, stream);
-    return x8 ? run_bwd<0, 1, 2, 384, false>(a, num_sms, grid, stream) : run_bwd<0, 0, 2, 384, false>(a, num_sms, grid, stream);
+      return x8 ? run_bwd<1, 1, 2, 384, false>(a, num_sms, grid, stream)
+                : run_bwd<1, 0, 2, 384, false>(a, num_sms, grid, stream);
+    return x8 ? run_bwd<0, 1, 2, 384, false>(a, num_sms, grid, stream)
+              : run_bwd<0, 0, 2, 384, false>(a, num_sms, grid, stream);
   }
   return run_bwd_rows<false>(a, x8, h8, num_sms, grid, stream);
 }
@@ -925,15 +928,20 @@ cudaError_t run_columns(const SandwichBwdArgs& a, int rows, int scalars, cudaStr
   return cudaLaunchKernelEx(&cfg, sandwich_columns_kernel, a, rows, scalars);
 }
 
+template <bool FULL>
+cudaError_t run_fwd_form(const SandwichArgs& a, int num_sms, cudaStream_t stream) {
+  // One row an SM at most: a chunk a thread, so that the row's chain is short (T = 32, K = 7168 with 8-bit
+  // copies 5.7 us for 6.2, T = 1 with a full gate 5.4 for 6.9). Else two chunks a thread and two CTAs an SM,
+  // or for rows past 6144 values four and one.
+  if (a.T <= num_sms && a.K <= 8 * 1024) return run_fwd<1, 1024, 1, FULL>(a, num_sms, stream);
+  if (a.K <= 16 * 384) return run_fwd<2, 384, 2, FULL>(a, num_sms, stream);
+  return run_fwd<4, 512, 1, FULL>(a, num_sms, stream);
+}
+
 }  // namespace
 
 cudaError_t launch_sandwich_norm(const SandwichArgs& a, int num_sms, cudaStream_t stream) {
-  // One row an SM at most: a chunk a thread, so that the row's chain is short (T = 32, K = 7168 with
-  // 8-bit copies 5.9 us for 6.2, T = 1 with a full gate 5.4 for 6.9). Else two chunks a thread and two CTAs an
-  // SM, or for rows past 6144 values four and one.
-  if (a.T <= num_sms && a.K <= 8 * 1024) return a.gate_kind == 3 ? run_fwd<1, 1024, 1, true>(a, num_sms, stream) : run_fwd<1, 1024, 1, false>(a, num_sms, stream);
-  if (a.K <= 16 * 384) return a.gate_kind == 3 ? run_fwd<2, 384, 2, true>(a, num_sms, stream) : run_fwd<2, 384, 2, false>(a, num_sms, stream);
-  return a.gate_kind == 3 ? run_fwd<4, 512, 1, true>(a, num_sms, stream) : run_fwd<4, 512, 1, false>(a, num_sms, stream);
+  return a.gate_kind == 3 ? run_fwd_form<true>(a, num_sms, stream) : run_fwd_form<false>(a, num_sms, stream);
 }
 
 size_t sandwich_bwd_workspace_bytes(int T, int K) {
