@@ -796,8 +796,10 @@ __global__ void __launch_bounds__(32 * kColWarps) sandwich_columns_kernel(const 
       s1 += part[1][w][lane];
     }
     if (a.dpre != nullptr) a.dpre[k] = s0;
-    const float2 o = finish_column(a, a.gate_kind == 1 ? static_cast<const uint16_t*>(a.gate)[k] : 0u,
-                                   a.post != nullptr ? a.post[k] : 0u, s1);
+    // (no rows: 0, whatever the weights hold)
+    const float2 o = rows == 0 ? dup(0.f)
+                               : finish_column(a, a.gate_kind == 1 ? static_cast<const uint16_t*>(a.gate)[k] : 0u,
+                                               a.post != nullptr ? a.post[k] : 0u, s1);
     if (a.dpost != nullptr) a.dpost[k] = o.x;
     if (a.gate_kind == 1 && a.dgate != nullptr) static_cast<float*>(a.dgate)[k] = o.y;
   }
