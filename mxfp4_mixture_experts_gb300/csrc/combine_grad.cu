@@ -47,7 +47,7 @@ __global__ void __launch_bounds__(32 * kCbWarps, 4) combine_backward_kernel(cons
     bool live = true;
     if (a.ids != nullptr) {
       const int id = a.ids[r];
-      live = id >= a.ebase && (a.E == 0 || id - a.ebase < a.E);
+      live = a.E == 0 ? id >= 0 : id >= a.ebase && id - a.ebase < a.E;
     }
     const uint16_t* dy = a.dy + (size_t)(r / (unsigned)a.topk) * a.K;
     const uint16_t* row = a.routes + (size_t)r * a.K;

@@ -316,7 +316,7 @@ def combine_backward(dy, routes, ids=None, weights=None, base: int = 0, experts:
     live = np.ones((T, k), bool)
     if ids is not None:
         i = np.asarray(ids)
-        live = (i >= base) & ((i < base + experts) if experts else True)
+        live = (i >= base) & (i < base + experts) if experts else i >= 0
     o = np.where(live[:, :, None], routes, 0.0)
     dw = np.einsum("tk,tjk->tj", dy, o)
     mag = np.einsum("tk,tjk->tj", np.abs(dy), np.abs(o))

@@ -23,3 +23,18 @@ def test_no_rows_and_weights_that_are_not_finite(moe, bad):
                                        torch.full((1,), bad, device="cuda"))
         for t in (r.post_gamma, r.pre_gamma, r.gate, r.residual_scale):
             assert torch.equal(t, torch.zeros_like(t))
+
+
+@pytest.mark.parametrize("base", [0, 3, 2 ** 31 - 1])
+def test_combination_without_a_window_takes_every_expert(moe, base):
+    """n_experts 0 is no window: expert_base then skips nothing; only negative ids are padding."""
+    T, k, K = 5, 4, 96
+    dy, o = torch.randn(T, K, generator=gen(1)).bfloat16(), torch.randn(T * k, K, generator=gen(2)).bfloat16()
+    ids = torch.tensor([0, 1, 2, 3, -1, 4, 2 ** 31 - 1, -2 ** 31, 5, 0] * 2, dtype=torch.int32).view(T, k)
+    w = torch.rand(T, k, generator=gen(3))
+    want = moe.combine_backward(dy.cuda(), o.cuda(), ids.cuda(), w.cuda(), True)
+    dw, do = moe.combine_backward(dy.cuda(), o.cuda(), ids.cuda(), w.cuda(), True, expert_base=base)
+    assert torch.equal(dw, want[0]) and torch.equal(do, want[1])
+    assert torch.equal(dw.cpu() != 0, ids >= 0)
+    ref, _, dref = P.combine_backward(f64(dy), f64(o).reshape(T, k, K), ids.numpy(), f64(w), base)
+    assert np.array_equal(ref != 0, ids.numpy() >= 0) and np.abs(f64(dw) - ref).max() <= 1e-4
