@@ -57,6 +57,11 @@ __device__ __forceinline__ Sigmoid sigmoid(float x) {
   return x < 0.f ? Sigmoid{lo, hi} : Sigmoid{hi, lo};
 }
 
+// Rows whose scores all leave fp32's range. Below kFaint a sigmoid is e^x to fp32's last bit, so that its quotients are a
+// softmax's, from the logits. They count where the router's own score of the largest logit is not 0.
+constexpr float kFaint = -17.f;
+__device__ __forceinline__ bool faint_scored(float x) { return expf(-x) < INFINITY; }
+
 // A token's logits in registers, masked ones as -inf, and what its softmax needs. Values
 // 4 i .. 4 i + 3 are neighbours (VEC), or 32 experts apart.
 template <int NPL, bool VEC>
@@ -201,7 +206,12 @@ struct Sums {
         for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
         total = __shfl_sync(0xffffffffu, v, 0);
         sum = __shfl_sync(0xffffffffu, v, 16);
-        inv = sum >= FLT_MIN ? fast_rcp(sum) : 0.f;
+        inv = fast_rcp(sum);
+        if (k.m < kFaint) {
+          inv = faint_scored(k.m) ? fast_rcp(total) : 0.f;
+#pragma unroll
+          for (int j = 0; j < NPL; ++j) s[j] = k.power(k.x[j]);
+        }
       }
       const float lse = k.m + __logf(total);
       z = fmaf(lse, lse, z);
@@ -556,10 +566,19 @@ __global__ void __launch_bounds__(kRbWarps * 32) router_backward_kernel(const Ro
     const bool soft = a.scoring == 0, there = v > -INFINITY;
     float common = 0.f;
     if (a.dw != nullptr) {
-      const float s = soft ? vx * inv : sv.s;
+      float s = soft ? vx * inv : sv.s;
       const float wv = there ? w : 0.f;   // (what is no part's gradient may be anything)
       if (a.renormalise) {
-        const float D = warp_sum(s), q = D > 0.f ? s / D : 0.f;
+        float D = warp_sum(s);
+        if (D < 0x1p-60f) {   // faint scores alone (a bias chose them): their quotients from the logits too
+          float most = v;
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+          const bool scored = soft ? __fdiv_rn(expf(most - k.m), total) > 0.f : faint_scored(most);
+          s = scored && there ? fast_exp(v - most) : 0.f;
+          D = warp_sum(s);
+        }
+        const float q = D > 0.f ? s / D : 0.f;
         val = q * (wv - warp_sum(q * wv));
       } else {
         val = s * wv;
@@ -602,7 +621,9 @@ __global__ void __launch_bounds__(kRbWarps * 32) router_backward_kernel(const Ro
         }
       }
       const float vsl = id >= 0 ? __ldg(slope + id) : 0.f;
-      if (soft) {
+      const bool faint = !soft && k.m < kFaint, powers = soft || faint;
+      if (powers) {
+        if (faint && !faint_scored(k.m)) is = 0.f;
 #pragma unroll
         for (int j = 0; j < NPL; ++j) {
           p[j] = ex[j];
@@ -617,7 +638,7 @@ __global__ void __launch_bounds__(kRbWarps * 32) router_backward_kernel(const Ro
           rest[j] = g.rest;
         }
         sum = warp_sum(sum);
-        is = sum >= FLT_MIN ? fast_rcp(sum) : 0.f;
+        is = fast_rcp(sum);
       }
 #pragma unroll
       for (int j = 0; j < NPL; ++j) dot = fmaf(p[j], sl[j], dot);
@@ -630,8 +651,8 @@ __global__ void __launch_bounds__(kRbWarps * 32) router_backward_kernel(const Ro
         d[j] = fmaf(u, rest[j], d[j]);
         d[j] = ex[j] > 0.f ? fmaf(zc, ex[j], d[j]) : d[j];   // (an infinite zc stays at the logits that have a part)
       }
-      const float u = gp * (soft ? vx : sv.s) * (vsl - dot);
-      vbase = fmaf(u, soft ? 1.f : sv.rest, vbase);
+      const float u = gp * (powers ? vx : sv.s) * (vsl - dot);
+      vbase = fmaf(u, powers ? 1.f : sv.rest, vbase);
       vbase = vx > 0.f ? fmaf(zc, vx, vbase) : vbase;
     }
     val = there ? val + vbase : 0.f;

@@ -207,6 +207,21 @@ def _masked(logits):
     return np.where(np.isnan(x), -np.inf, x)
 
 
+def _counts(most: float, row, scoring: str) -> bool:
+    """Whether the router's own fp32 score of the logit `most` of a row is not 0: expf(-x) does not overflow, or a
+    softmax's quotient does not vanish. Where the largest score of a sum is 0 there, its quotients are 0, and else
+    they are the formula's."""
+    if not most > -np.inf:
+        return False
+    with np.errstate(over="ignore"):
+        if scoring == "sigmoid":
+            return bool(np.isfinite(np.float32(np.exp(-most))))
+        m = row.max()
+        if not np.isfinite(m):
+            return most == m
+        return bool(np.float32(np.float32(np.exp(most - m)) / np.float32(np.sum(np.exp(row - m)))) > 0)
+
+
 def router_balance(logits, ids, scoring: str, offsets=None):
     """dict of stats [4], counts, prob, slope [S, E] and each token's sequence (-1: not counted)."""
     x, ids = _masked(logits), np.asarray(ids)
@@ -227,7 +242,7 @@ def router_balance(logits, ids, scoring: str, offsets=None):
             seq[t] = i
             for e in good:
                 counts[i, e] += 1
-            prob[i] += s[t] / s[t].sum() if s[t].sum() > 0 else 0.0
+            prob[i] += s[t] / s[t].sum() if _counts(x[t].max(), x[t], scoring) else 0.0
             m = x[t].max()
             z.append((m + math.log(np.sum(np.exp(x[t] - m)))) ** 2)
         if n:
@@ -249,7 +264,8 @@ def router_weights(logits, ids, scoring: str, renormalise: bool, route_scale: fl
             if 0 <= e < x.shape[1]:
                 w[t, j] = s[t, e]
         if renormalise:
-            w[t] = w[t] / w[t].sum() if w[t].sum() > 0 else 0.0
+            most = max((x[t, e] for e in ids[t] if 0 <= e < x.shape[1]), default=-np.inf)
+            w[t] = w[t] / w[t].sum() if _counts(most, x[t], scoring) else 0.0
     return w * route_scale
 
 
@@ -277,7 +293,7 @@ def router_backward(logits, ids, dw, scoring: str, renormalise: bool, route_scal
         if dw is not None:
             g, ga = np.zeros(E), np.zeros(E)
             D = sum(s[t, e] for _, e in good)
-            if renormalise and D > 0:
+            if renormalise and _counts(max((x[t, e] for _, e in good), default=-np.inf), x[t], scoring):
                 mean = sum(s[t, e] / D * dw[t, j] for j, e in good)
                 amean = sum(s[t, e] / D * abs(dw[t, j]) for j, e in good)
                 # q_j (dw_j - mean): through the quotient, whose softmax denominators cancel
@@ -294,7 +310,7 @@ def router_backward(logits, ids, dw, scoring: str, renormalise: bool, route_scal
         if dloss is not None and balance["seq"][t] >= 0:
             slope = balance["slope"][balance["seq"][t]]
             tot = s[t].sum()
-            if tot > 0:
+            if _counts(x[t].max(), x[t], scoring):
                 p = s[t] / tot
                 f = p * rest[t] if scoring == "sigmoid" else p
                 b = dloss[0] / balance["stats"][3]

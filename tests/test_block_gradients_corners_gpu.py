@@ -38,3 +38,62 @@ def test_combination_without_a_window_takes_every_expert(moe, base):
     assert torch.equal(dw.cpu() != 0, ids >= 0)
     ref, _, dref = P.combine_backward(f64(dy), f64(o).reshape(T, k, K), ids.numpy(), f64(w), base)
     assert np.array_equal(ref != 0, ids.numpy() >= 0) and np.abs(f64(dw) - ref).max() <= 1e-4
+
+
+@pytest.mark.parametrize("T,E,k", [(9, 17, 3), (40, 128, 4), (333, 256, 8), (70, 1024, 32)])
+def test_rows_of_faint_scores_keep_their_quotients(moe, T, E, k):
+    """Sigmoid scores far below 1 in every expert, down to where the router's own fp32 score is 0 (a logit of -88.7),
+    and softmax scores that a bias chose from the far end: what is divided by their sum stays what it is."""
+    g = gen(T + E)
+    for low in (-16.9, -17.5, -40.0, -84.0):
+        x = low - 4 * torch.rand(T, E, generator=g)
+        ids = torch.argsort(torch.rand(T, E, generator=g), 1)[:, :k].int()
+        ids[T // 2] = -1
+        off = [0, T // 3, T - 1]
+        check_balance(moe, x, ids, "sigmoid", off)
+        for renorm in (True, False):
+            if renorm or low > -60:
+                check_router_backward(moe, x, ids, "sigmoid", renorm, off)
+    # one row of each kind beside the others
+    x = 3 * torch.randn(T, E, generator=g)
+    x[::2] -= 90 - x[::2].amax(1, keepdim=True).neg() - 8
+    x[::2] = torch.minimum(x[::2], torch.tensor(-70.0))
+    x[::2, 0] = -82.0
+    check_balance(moe, x, ids, "sigmoid")
+    check_router_backward(moe, x, ids, "sigmoid", True)
+    # chosen experts 50 to 95 below a row's largest logit
+    x = torch.randn(T, E, generator=g)
+    far = torch.argsort(torch.rand(T, E - 1, generator=g), 1)[:, :min(k, E - 1)] + 1
+    x[:, 0] = 1.0
+    x.scatter_(1, far, -50 - 45 * torch.rand(T, 1, generator=g) + torch.randn(T, far.shape[1], generator=g))
+    check_router_backward(moe, x, far.int(), "softmax", True)
+    check_router_backward(moe, x, far.int(), "softmax", True, losses=False)
+
+
+def test_gradient_of_weights_of_faint_scores_that_a_bias_chose(moe):
+    """Through router_scored: where its weights are normalised and not 0, so are the gradient's."""
+    for scoring, x in (("sigmoid", -86 + torch.rand(6, 32, generator=gen(1))),
+                       ("softmax", torch.cat((torch.full((6, 1), 80.0), torch.rand(6, 31, generator=gen(2)) * 2), 1))):
+        bias = torch.zeros(32)
+        bias[5:20] = 2.0
+        dw = torch.randn(6, 4, generator=gen(3))
+        ids, w = moe.router_scored(x.cuda(), 4, scoring, bias.cuda(), route_scale=2.5)
+        assert (w > 0).all() and torch.allclose(w.sum(1), torch.full((6,), 2.5).cuda())
+        got = f64(moe.router_backward(x.cuda(), ids, dw.cuda(), scoring, route_scale=2.5))
+        ref, mag = P.router_backward(x.numpy(), ids.cpu().numpy(), f64(dw), scoring, True, 2.5)
+        assert np.all(np.abs(got - ref) <= 2.0 ** -16 * mag) and np.abs(got).max() > 0.05
+
+
+def test_scores_that_the_router_has_as_0(moe):
+    """Logits below -88.8, or a chosen softmax score below fp32's least: no weights, no gradient, no share of p."""
+    x = torch.full((2, 8), -90.0)
+    x[1] = -89.0
+    ids = torch.tensor([[1, 2], [3, 4]], dtype=torch.int32)
+    b = moe.router_balance(x.cuda(), ids.cuda(), "sigmoid")
+    assert not b.prob.any() and float(b.stats[2]) == 2
+    g = moe.router_backward(x.cuda(), ids.cuda(), torch.ones(2, 2).cuda(), "sigmoid", stats=b.stats, slope=b.slope,
+                            grad_losses=torch.tensor([1.0, 0.0]).cuda())
+    assert not g.any()
+    x = torch.zeros(1, 8)
+    x[0, 1:3] = torch.tensor([-106.0, -107.0])
+    assert not moe.router_backward(x.cuda(), ids[:1].cuda(), torch.tensor([[1.0, 2.0]]).cuda(), "softmax").any()
