@@ -213,7 +213,7 @@ struct Sums {
           for (int j = 0; j < NPL; ++j) s[j] = k.power(k.x[j]);
         }
       }
-      const float lse = k.m + __logf(total);
+      const float lse = k.m + logf(total);   // (near 1 the hardware's logarithm is off by more than the sum is)
       z = fmaf(lse, lse, z);
 #pragma unroll
       for (int j = 0; j < NPL; ++j) acc[j] = fmaf(s[j], inv, acc[j]);
@@ -644,7 +644,7 @@ __global__ void __launch_bounds__(kRbWarps * 32) router_backward_kernel(const Ro
       for (int j = 0; j < NPL; ++j) dot = fmaf(p[j], sl[j], dot);
       dot = warp_sum(dot) * is;
       const float gp = gb * is;
-      const float zc = gz != 0.f ? gz * (k.m + __logf(total)) * inv : 0.f;
+      const float zc = gz != 0.f ? gz * (k.m + logf(total)) * inv : 0.f;
 #pragma unroll
       for (int j = 0; j < NPL; ++j) {
         const float u = gp * p[j] * (sl[j] - dot);

@@ -97,3 +97,32 @@ def test_scores_that_the_router_has_as_0(moe):
     x = torch.zeros(1, 8)
     x[0, 1:3] = torch.tensor([-106.0, -107.0])
     assert not moe.router_backward(x.cuda(), ids[:1].cuda(), torch.tensor([[1.0, 2.0]]).cuda(), "softmax").any()
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_z_loss_of_confident_rows(moe, scoring):
+    """One logit of 0 and others far below: log(1 + d), d the others' exponentials. d is off by 2^-20 of itself, 1 + d
+    by half a step of 2^-23, the logarithm by 2^-23 of itself; z is its square."""
+    a = np.linspace(2.0, 15.0, 53).astype(np.float32)
+    for E in (2, 8):
+        for many in (False, True):
+            x = torch.full((len(a), E), -INF)
+            x[:, 0] = 0
+            x[:, E - 1] = -torch.from_numpy(a)
+            ids = torch.zeros(len(a), 1, dtype=torch.int32)
+            off = torch.arange(len(a) + 1, dtype=torch.int32)
+            d = np.exp(-a.astype(np.float64))
+            lse = np.log1p(d)
+            e = 2.0 ** -20 * d + 2.0 ** -24 + 2.0 ** -23 * lse
+            if many:
+                z = f64(moe.router_balance(x.cuda(), ids.cuda(), scoring, off.cuda()).stats[1])
+                assert abs(z - np.mean(lse ** 2)) <= np.mean(2 * lse * e + e * e) + 2.0 ** -20 * np.mean(lse ** 2)
+                continue
+            for t in range(len(a)):
+                b = moe.router_balance(x[t:t + 1].cuda(), ids[:1].cuda(), scoring)
+                assert abs(float(b.stats[1]) - lse[t] ** 2) <= 2 * lse[t] * e[t] + e[t] ** 2 + 2.0 ** -22 * lse[t] ** 2
+                g = f64(moe.router_backward(x[t:t + 1].cuda(), ids[:1].cuda(), None, scoring, stats=b.stats, slope=b.slope,
+                                            grad_losses=torch.tensor([0.0, 1.0]).cuda()))[0]
+                want = 2 * lse[t] / (1 + d[t]) * np.array([1.0, d[t]])
+                tol = 2 * e[t] / (1 + d[t]) * np.array([1.0, d[t]]) + 2.0 ** -19 * want
+                assert np.all(np.abs(g[[0, E - 1]] - want) <= tol)
