@@ -301,10 +301,13 @@ __global__ void __launch_bounds__(32 * kSmallWarps) balance_small_kernel(const R
   }
 }
 
-// Three CTAs an SM: 80 registers for 8 logits a lane (12 ragged sequences 12.9 us; with 116
-// registers 2 us more).
+// CTAs an SM: three to 8 logits a lane (80 registers; 12 ragged sequences of 256 experts 12.9 us, with 116
+// registers 2 us more), two past that, where three would spill (8192 tokens, 12 sequences, three / two: 384 experts
+// 16.4 / 15.5, 1024 20.7 / 18.9; softmax of 1024 in one sequence 14.4 / 15.2).
+template <int NPL>
+constexpr int kBalanceCtas = NPL > 8 ? 2 : 3;
 template <int NPL, bool VEC>
-__global__ void __launch_bounds__(kBalanceWarps<NPL> * 32, 3)
+__global__ void __launch_bounds__(kBalanceWarps<NPL> * 32, kBalanceCtas<NPL>)
     balance_pieces_kernel(const RouterBalanceArgs a, const BalanceScratch b, unsigned tile) {
   using Tok = Token<NPL, VEC>;
   constexpr int W = kBalanceWarps<NPL>;
