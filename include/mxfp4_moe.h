@@ -467,6 +467,7 @@ int mxfp4_moe_router_backward(const float* logits, const int32_t* topk_ids,
  *   topk_ids int32 [T, topk] or NULL (every route counts). A negative id, or one outside
  *   expert_base .. expert_base + n_experts - 1 (n_experts 0: no window, whatever expert_base
  *   is), is a skipped route: its row is not read, its gradients are 0
+ * No output may overlap an input (MXFP4_MOE_ERR_ARG).
  * Limits (MXFP4_MOE_ERR_SHAPE): K as above, 1 <= topk <= 32, T * topk < 2^31.
  * bf16 rows 16-byte aligned, the rest 4. T == 0 enqueues nothing. */
 int mxfp4_moe_combine_backward(const void* grad_out, const void* routes, const int32_t* topk_ids,

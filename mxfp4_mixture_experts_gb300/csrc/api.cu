@@ -770,6 +770,14 @@ int mxfp4_moe_router_backward(const float* logits, const int32_t* topk_ids,
   return cuda_status(mxmoe::launch_router_backward(a, static_cast<cudaStream_t>(stream)));
 }
 
+namespace {
+// Whether n bytes at a and m at b share one (null: no bytes).
+bool overlap(const void* a, size_t n, const void* b, size_t m) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a != nullptr && b != nullptr && (x < y ? y - x < n : x - y < m);
+}
+}  // namespace
+
 int mxfp4_moe_combine_backward(const void* grad_out, const void* routes, const int32_t* topk_ids,
                                const float* topk_weights, int T, int K, int topk, int expert_base,
                                int n_experts, float* grad_weights, void* grad_routes,
@@ -784,6 +792,13 @@ int mxfp4_moe_combine_backward(const void* grad_out, const void* routes, const i
   if (!aligned(grad_out, 16) || !aligned(routes, 16) || !aligned(topk_ids, 4) ||
       !aligned(topk_weights, 4) || !aligned(grad_weights, 4) || !aligned(grad_routes, 16))
     return MXFP4_MOE_ERR_ALIGN;
+  // inputs are read past the coherent path while other warps write
+  const size_t slots = (size_t)T * topk, row = (size_t)K * 2;
+  const void* ins[4] = {grad_out, routes, topk_ids, topk_weights};
+  const size_t sizes[4] = {T * row, slots * row, slots * 4, slots * 4};
+  for (int i = 0; i < 4; ++i)
+    if (overlap(grad_weights, slots * 4, ins[i], sizes[i]) || overlap(grad_routes, slots * row, ins[i], sizes[i]))
+      return MXFP4_MOE_ERR_ARG;
   DeviceInfo* d = nullptr;
   if (int rc = current_device(&d)) return rc;
   mxmoe::CombineBwdArgs a = {};

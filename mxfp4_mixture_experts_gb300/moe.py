@@ -871,7 +871,8 @@ def combine_backward(grad_out: torch.Tensor, routes: torch.Tensor,
     (``forward_window(per_route=True)``): (fp32 [T, topk], and with routes_too bf16 [T * topk, K],
     else None). topk is topk_ids' or topk_weights' second size. Routes with a negative id, or
     outside expert_base .. expert_base + n_experts - 1 when n_experts is not 0, are skipped: gradients
-    0. topk_weights fp32 [T, topk] are needed with routes_too only."""
+    0. topk_weights fp32 [T, topk] are needed with routes_too only. grad_routes may be given as an output
+    that overlaps no input."""
     dev = _first(grad_out, "grad_out", torch.bfloat16)
     _first(routes, "routes", torch.bfloat16)
     T, K = grad_out.shape
