@@ -584,10 +584,24 @@ def _scratch(nbytes: int, workspace: Optional[torch.Tensor], device, stream, dev
 GATE_ACTS = {"linear": 0, "sigmoid": 1}
 
 
-def _gate(gate: Optional[torch.Tensor], gate_act: str, T: int, K: int, dev: int):
-    """(kind, activation) of a gate: bf16 [1, K], fp32 [T, 1] or bf16 [T, K]."""
+GATE_PER = {"channel": 1, "token": 2, "value": 3}
+
+
+def _gate(gate: Optional[torch.Tensor], gate_act: str, T: int, K: int, dev: int, per: Optional[str] = None):
+    """(kind, activation) of a gate: bf16 [1, K], fp32 [T, 1] or bf16 [T, K], as its shape or ``per`` says."""
     if gate_act not in GATE_ACTS:
         raise ValueError(f"gate_act must be one of {sorted(GATE_ACTS)}")
+    if per is not None:
+        if per not in GATE_PER:
+            raise ValueError(f"gate_per must be None or one of {sorted(GATE_PER)}")
+        if gate is None:
+            raise ValueError("gate_per needs gate")
+        kind = GATE_PER[per]
+        if kind == 2:
+            _want(gate, "gate", torch.float32, (T, 1), dev)
+        else:
+            _want(gate, "gate", torch.bfloat16, (T if kind == 3 else 1, K), dev)
+        return kind, GATE_ACTS[gate_act]
     if gate is None:
         return 0, GATE_ACTS[gate_act]
     if not isinstance(gate, torch.Tensor):
@@ -622,14 +636,14 @@ def sandwich_norm(x: torch.Tensor, residual: torch.Tensor, post_gamma: Optional[
                   eps: float = 1e-5, out8: Optional[str] = None, bf16: bool = True,
                   checkpoint8: Optional[str] = None, rstd: bool = False,
                   residual_out: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
-                  stream=None) -> SandwichNorm:
+                  stream=None, gate_per: Optional[str] = None) -> SandwichNorm:
     """The norm after a block, its gate, the scaled residual and the next block's norm, for bf16 rows
     [T, K]: n = x * rsqrt(mean(x^2) + eps) * post_gamma, h = residual_scale * residual + g * n,
     y = h * rsqrt(mean(h^2) + eps) * pre_gamma.
 
     Without post_gamma n = x; without pre_gamma there is no y. gate: bf16 [1, K] (a
-    channel's), fp32 [T, 1] (a token's) or bf16 [T, K]; with one row a bf16 gate is a channel's.
-    g is the gate, or its sigmoid with gate_act "sigmoid". residual_scale fp32 [1]. residual_out
+    channel's), fp32 [T, 1] (a token's) or bf16 [T, K]; with one row a bf16 gate is a channel's
+    unless gate_per ("channel", "token" or "value") says otherwise, as a batch of any size should. g is the gate, or its sigmoid with gate_act "sigmoid". residual_scale fp32 [1]. residual_out
     may be x or residual. out8 and bf16 as in ``add_rmsnorm``. For
     ``sandwich_norm_backward``: rstd True keeps both norms' factors, checkpoint8 "ocp" or "nosat"
     writes x and the unrounded h in MXFP8 beside the rest."""
@@ -643,7 +657,7 @@ def sandwich_norm(x: torch.Tensor, residual: torch.Tensor, post_gamma: Optional[
     _want(pre_gamma, "pre_gamma", torch.bfloat16, (K,), dev)
     _want(residual_scale, "residual_scale", torch.float32, (1,), dev)
     _want(residual_out, "residual_out", torch.bfloat16, shape, dev)
-    kind, act = _gate(gate, gate_act, T, K, dev)
+    kind, act = _gate(gate, gate_act, T, K, dev, gate_per)
     for name, rule in (("out8", out8), ("checkpoint8", checkpoint8)):
         if rule is not None and rule not in MX8_RULES:
             raise ValueError(f"{name} must be None or one of {sorted(MX8_RULES)}")
@@ -708,10 +722,10 @@ def sandwich_norm_backward(grad_h: Optional[torch.Tensor], grad_y: Optional[torc
                            grad_x: Optional[torch.Tensor] = None,
                            grad_residual: Optional[torch.Tensor] = None,
                            workspace: Optional[torch.Tensor] = None,
-                           stream=None) -> SandwichNormGrads:
+                           stream=None, gate_per: Optional[str] = None) -> SandwichNormGrads:
     """Gradient of ``sandwich_norm`` from the gradients of its h and y (bf16 [T, K], either None) and
     from what it kept: x and h in bf16, or as x8 / h8 with x_scale / h_scale, and rstd [2, T]. h is
-    needed with grad_y, rstd with grad_y or post_gamma. gate, gate_act, gammas and residual_scale as
+    needed with grad_y, rstd with grad_y or post_gamma. gate, gate_act, gate_per, gammas and residual_scale as
     in the forward call; with residual (its bf16 rows) residual_scale gets a gradient too.
     grad_x and grad_residual may be given as outputs that overlap no input."""
     dev = _first(x, "x", torch.bfloat16 if x_scale is None else torch.float8_e4m3fn)
@@ -739,7 +753,7 @@ def sandwich_norm_backward(grad_h: Optional[torch.Tensor], grad_y: Optional[torc
     _want(residual, "residual", torch.bfloat16, shape, dev)
     _want(grad_x, "grad_x", torch.bfloat16, shape, dev)
     _want(grad_residual, "grad_residual", torch.bfloat16, shape, dev)
-    kind, act = _gate(gate, gate_act, T, K, dev)
+    kind, act = _gate(gate, gate_act, T, K, dev, gate_per)
     device = x.device
     rows = grad_h if grad_h is not None else grad_y
     if grad_x is None:
