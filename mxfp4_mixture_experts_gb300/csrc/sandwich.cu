@@ -328,8 +328,8 @@ __device__ __forceinline__ void team_sum3(float (&v)[ROWS][3], float (*part)[32]
 // A sum as a value and its remainder, so that what cancels in the value is kept. The gradient of the residual's scale
 // adds up T K products of both signs: T = 777, K = 2880, magnitudes of 5000 that come to about 4. One fp32 value
 // a thread, a warp and a CTA left that off by 6.8e-7 in the median and 3.1e-6 at worst of 300 input sets, a
-// relative 2e-5 where little is left; with remainders 2.6e-7 and 1.2e-6, what the roundings of dh_total itself
-// come to (calls that ask for this gradient take 2 to 6% longer).
+// relative 2e-5 where little is left; with remainders 2.6e-7 and 1.2e-6, what the roundings of dh_total
+// itself come to (calls that ask for this gradient take 1 to 5% longer).
 struct Sum {
   float hi, lo;
   __device__ __forceinline__ void add(const Sum& v) {
@@ -346,11 +346,12 @@ struct Sum {
   // (the remainder of a sum that is not finite is none)
   __device__ __forceinline__ float value() const { return fabsf(hi) < INFINITY ? __fadd_rn(hi, lo) : hi; }
 };
+__device__ __forceinline__ float2 sub2(const float2& a, const float2& b) { return __ffma2_rn(b, dup(-1.f), a); }
 // sum += a b, and e += what that rounds off: exactly where the sum is the larger part, else to a rounding of a b, as
 // a itself has one.
 __device__ __forceinline__ void add_product(float2& sum, float2& e, const float2& a, const float2& b) {
   const float2 to = __ffma2_rn(a, b, sum);
-  e = __fadd2_rn(e, __ffma2_rn(a, b, __ffma2_rn(to, dup(-1.f), sum)));
+  e = __fadd2_rn(e, __ffma2_rn(a, b, sub2(sum, to)));
   sum = to;
 }
 
@@ -546,9 +547,11 @@ __global__ void __launch_bounds__(MAXT, 1)
     }
   };
   float2 s_pre[CH][4], s_x[CH][4];
-  // Of dh_total * res: two sums and one remainder of both, or, for full gates, a chunk's added to one sum
-  // (a register less; with the other form eight bytes are spilled: T = 4096, K = 2880 45 us for 42).
-  constexpr bool kFold = GATE >= 2;
+  // dscale = sum dh_total res, with q = dh + r2 v sum q res - c2 r2 sum h res. The first pass adds up both, so that
+  // the rounding of dh_total stays out of it (the same for every value of an 8-bit code: T = 1151, K = 3008 off by
+  // 3.7e-7 for 7.2e-7). Full gates, mixed types and pairs leave the first pass no register for it (eight bytes
+  // spilled cost T = 4096, K = 2880 3 us of 42): the second adds up dh_total res, with a full gate a chunk's sums into one.
+  constexpr bool kFull = GATE >= 2, kFirst = !kFull && !PAIR && E8 != 2;
   float2 s_res = dup(0.f);
   Sum s_all = {0.f, 0.f};
 #pragma unroll
@@ -579,6 +582,9 @@ __global__ void __launch_bounds__(MAXT, 1)
     // v h, w x (dh + r2 v), w x h; w without a token's gate. An 8-bit block's factor is taken
     // into the sums of its chunk and into the row's factors, not into every value.
     float2 s2[ROWS][3];
+    float s_h[ROWS];   // h * res of this thread's part of the row
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) s_h[r] = 0.f;
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) s2[r][0] = s2[r][1] = s2[r][2] = dup(0.f);
 #pragma unroll
@@ -621,6 +627,17 @@ __global__ void __launch_bounds__(MAXT, 1)
           s2[r][1] = __ffma2_rn(c2[1], dup(fx[r][i]), s2[r][1]);
           s2[r][2] = __ffma2_rn(__fmul2_rn(c2[2], dup(fx[r][i])), dup(fh[r][i]), s2[r][2]);
         }
+        if (kFirst && has_res) {
+          float2 z[4], e = dup(0.f), hz = dup(0.f);
+          unpack4(*reinterpret_cast<const uint4*>(slot + r * p.row + res0 + 512 * i), z);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            add_product(s_res, e, q[j], z[j]);
+            hz = __ffma2_rn(h[j], z[j], hz);
+          }
+          s_all.lo += e.x + e.y;
+          s_h[r] = fmaf(hz.x + hz.y, fh[r][i], s_h[r]);
+        }
         // dh + r2 v goes where dh and dy were, for the second pass
         *reinterpret_cast<float4*>(at + L::dh + lane16) = make_float4(q[0].x, q[0].y, q[1].x, q[1].y);
         *reinterpret_cast<float4*>(at + L::dy + lane16) = make_float4(q[2].x, q[2].y, q[3].x, q[3].y);
@@ -642,6 +659,10 @@ __global__ void __launch_bounds__(MAXT, 1)
       if (GATE == 0 && a.gate_kind == 2 && a.dgate != nullptr && tid == 0 && rank == 0 && t + r < T)
         static_cast<float*>(a.dgate)[t + r] = dot * gate_of(now.g[r], a.gate_act).d;
       kh[r] = -c2;
+      if (kFirst && has_res) {   // (an infinite residual is in the first sum, with its sign)
+        const bool in = fabsf(s_h[r]) < INFINITY || !(fabsf(c2) < INFINITY);
+        s_all.add(Sum{in ? -(c2 * s_h[r]) * r2 : 0.f, 0.f});
+      }
       k1[r] = has_post ? -r1 * (dot * inv_k) : 0.f;
       xr[r] = r1 * gt;
     }
@@ -666,12 +687,12 @@ __global__ void __launch_bounds__(MAXT, 1)
         slot8(at + L::x + lane_x, x8, x);
 #pragma unroll
         for (int j = 0; j < 4; ++j) d[j] = __ffma2_rn(dup(kh[r]), __fmul2_rn(h[j], hr2), d[j]);
-        if (has_res) {
+        if (!kFirst && has_res) {
           unpack4(*reinterpret_cast<const uint4*>(slot + r * p.row + res0 + 512 * i), v);
-          float2 e = dup(0.f), to = kFold ? dup(0.f) : s_res;
+          float2 e = dup(0.f), to = kFull ? dup(0.f) : s_res;
 #pragma unroll
           for (int j = 0; j < 4; ++j) add_product(to, e, d[j], v[j]);
-          if (kFold) {
+          if (kFull) {
             s_all.add(Sum{to.x, e.x});
             s_all.add(Sum{to.y, e.y});
           } else {
@@ -737,7 +758,7 @@ __global__ void __launch_bounds__(MAXT, 1)
   }
   if (has_res) {
     Sum sr = s_all;
-    if (!kFold) {
+    if (!kFull) {
       sr.add(Sum{s_res.x, 0.f});
       sr.add(Sum{s_res.y, 0.f});
     }

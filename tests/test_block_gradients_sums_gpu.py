@@ -71,3 +71,26 @@ def test_gradient_of_the_residual_scale_out_of_range(moe):
         assert np.isnan(run(bad, x)) and np.isnan(run(x, bad))
         bad[39, 63] = float("inf")
         assert run(bad, x) == float("inf") and run(x, -bad) == -float("inf")
+
+
+@pytest.mark.parametrize("gate", [None, "channel", "full"])
+@pytest.mark.parametrize("ck", [None, "ocp"])
+def test_gradient_of_the_residual_scale_with_values_that_are_not_finite(moe, gate, ck):
+    """An infinite residual beside a finite kept h: its term's sign. A NaN of h makes its row NaN."""
+    call, v = make_backward(rows(20, 96, 3, gate), "linear", ck=ck, seed=4)
+    run = lambda: float(moe.sandwich_norm_backward(**{k: t if isinstance(t, str) else cuda(t) for k, t in call.items()})
+                        .residual_scale)
+    sign = np.sign(P.sandwich_norm_backward(**v)["residual"] / v["scale"])
+    for at in ((0, 0), (7, 50), (19, 95)):
+        keep = call["residual"]
+        for big in (float("inf"), -float("inf"), float("nan")):
+            call["residual"] = keep.clone()
+            call["residual"][at] = big
+            got = run()
+            assert got == sign[at] * big or (np.isnan(big) and np.isnan(got))
+        call["residual"] = keep
+    if ck is None:
+        call["h"][7, 50] = float("nan")
+    else:
+        call["h_scale"][7, 1] = 255
+    assert np.isnan(run())
