@@ -340,7 +340,8 @@ int mxfp4_moe_add_rmsnorm(const void* x, const void* residual, const void* gamma
  *   n = x * r1 * post_gamma, r1 = rsqrt(mean(x^2) + eps)   (post_gamma NULL: n = x)
  *   h = residual_scale * residual + g * n (fp32)            residual_out = bf16(h)
  *   y = h * r2 * pre_gamma, r2 = rsqrt(mean(h^2) + eps), from the unrounded h
- *   out = bf16(y); out8, scale8: MXFP8 of y as mxfp4_moe_add_rmsnorm writes it
+ *   out = bf16(y); out8, scale8: MXFP8 of y in mxfp4_moe_add_rmsnorm's format and rules. y
+ *   is two fp32 products here, where that call rounds once: codes beside a tie may differ
  *   x, residual    bf16 [T, K]
  *   post_gamma, pre_gamma  bf16 [K]; pre_gamma NULL: no y, out and out8 NULL
  *   gate           gate_kind 0: NULL (g = 1); 1: bf16 [K], a channel's; 2: fp32 [T],
@@ -418,7 +419,9 @@ int mxfp4_moe_router_scored(const float* logits, const float* bias, int T, int E
                             float* topk_weights, void* stream);
 
 /* Balance losses and expert counts of a routing. s as mxfp4_moe_router_scored
- * scores the logits (NaN and -inf: masked, s = 0), p_e = s_e / sum s. A token counts when
+ * scores the logits (NaN and -inf: masked, s = 0), p_e = s_e / sum s; rows of scores too
+ * small for fp32 keep their quotients, but for one whose every score that call has as 0
+ * (sigmoid, no logit above -88.7): p = 0. A token counts when
  * it has an id in [0, E) and a logit that is not masked; other ids are skipped,
  * the same id twice counts twice. Per sequence, over its n counting tokens:
  *   counts int32 [n_seq, E]  routes to each expert (C: their sum)
@@ -445,7 +448,9 @@ int mxfp4_moe_router_balance(const float* logits, const int32_t* topk_ids, int T
  * fixed) and of mxfp4_moe_router_balance's losses (the counts are):
  *   sum grad_weights * topk_weights + grad_losses[0] * stats[0] + grad_losses[1] * stats[1]
  *   topk_ids      the chosen experts; an id outside [0, E) or of a masked expert
- *                 takes no part, the same id twice twice
+ *                 takes no part, the same id twice twice. Renormalised weights have
+ *                 their gradient where the largest chosen score is not 0 in fp32; the
+ *                 others' is 0 for scores below 2^-126
  *   grad_weights  fp32 [T, topk] or NULL (zero)
  *   grad_losses   fp32 [2] or NULL (zero; stats, slope and seq_offsets are then not
  *                 read); stats, slope, seq_offsets, n_seq as that call's
@@ -461,7 +466,8 @@ int mxfp4_moe_router_backward(const float* logits, const int32_t* topk_ids,
 /* Gradient of the layer's combination y_t = sum_j w_tj o_tj of its routes'
  * outputs o (mxfp4_moe_forward_window with per_route):
  *   grad_weights fp32 [T, topk]       sum over the row of grad_out_t * o_tj
- *   grad_routes  bf16 [T * topk, K] or NULL   bf16(w_tj * grad_out_t)
+ *   grad_routes  bf16 [T * topk, K] or NULL   bf16(w_tj * grad_out_t): for a caller whose
+ *   routes come from something that trains; the MXFP4 experts have no gradient here
  *   grad_out bf16 [T, K], routes bf16 [T * topk, K], topk_weights fp32 [T, topk]
  *   (needed with grad_routes)
  *   topk_ids int32 [T, topk] or NULL (every route counts). A negative id, or one outside

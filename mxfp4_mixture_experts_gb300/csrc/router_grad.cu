@@ -24,13 +24,13 @@
 // One warp per token, its logits in registers, four neighbours a lane and 16-byte load where rows
 // allow it: the logits are read once, 4 T E bytes and as many written by the gradient. Both
 // kernels are bound by their instructions, so exponentials and reciprocals are the
-// hardware's (a score below 2^-126 is 0), a sigmoid and its
+// hardware's (a score below 2^-126 is 0; rows of nothing else go through the logits), a sigmoid and its
 // complement come from one exponential, and a chosen expert's gradient is put
 // together in its slot's lane and written over the rest's, not searched for in the registers.
 // The losses' sums are per tile of tokens and sequence (a piece), written to scratch and added
 // up in a fixed order: no floating-point atomics, every repeat gives the same bits.
-// 8192 tokens, 256 experts, 12 sequences, sigmoid, in a graph: losses 12.9 us (two kernels, the
-// first a chain of 3 or 4 tokens a warp), gradient 7.8 us; the launch alone is 2.
+// 8192 tokens, 256 experts, 12 sequences, sigmoid, in a graph: losses 13.1 us (two kernels, the
+// first a chain of 3 or 4 tokens a warp), gradient 8.0 us; the launch alone is 2.
 #include <cfloat>
 #include <cstdint>
 
@@ -241,7 +241,7 @@ __device__ __forceinline__ void finish_stats(const RouterBalanceArgs& a, float l
 }
 
 // All of it in one CTA, for few tokens in one or two sequences: one launch in place of two
-// (32 tokens, 128 experts in a graph 3.7 us for 6.2, 64 tokens, 256 experts 5.7 for 7.0; the host 3 us less).
+// (32 tokens, 128 experts in a graph 3.6 us for 6.1, 64 tokens, 256 experts 5.6 for 6.9; the host 3 us less).
 constexpr int kSmallTokens = 64, kSmallSequences = 2, kSmallWarps = 16;
 template <int NPL, bool VEC>
 __global__ void __launch_bounds__(32 * kSmallWarps) balance_small_kernel(const RouterBalanceArgs a) {
@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(32 * kSmallWarps) balance_small_kernel(const R
   }
 }
 
-// CTAs an SM: three to 8 logits a lane (80 registers; 12 ragged sequences of 256 experts 12.9 us, with 116
+// CTAs an SM: three to 8 logits a lane (80 registers; 12 ragged sequences of 256 experts 13.1 us, with 116
 // registers 2 us more), two past that, where three would spill (8192 tokens, 12 sequences, three / two: 384 experts
 // 16.4 / 15.5, 1024 20.7 / 18.9; softmax of 1024 in one sequence 14.4 / 15.2).
 template <int NPL>

@@ -52,7 +52,7 @@ __device__ __forceinline__ Gate gate_of(float g, int act) {
 __device__ __forceinline__ float gate_value(float g, int act) { return gate_of(g, act).v; }
 // The same for a full gate's bf16 values, a thread's 8 of every row: both steps approximate, a relative
 // error below 2^-21 + |g| 2^-23 (the exponent's rounding), far under the half step of 2^-8 that the gate
-// itself carries. (The gradient of T = 4000, K = 2880 with a full gate and a trained scale: 68 us with expf, 52.)
+// itself carries. (The gradient of T = 4096, K = 2880 with a full gate and a trained scale: 78 us with expf, 44.)
 __device__ __forceinline__ Gate full_gate(float g, bool act) {
   if (!act) return Gate{g, 1.f};
   const float e = fast_exp(-fabsf(g)), hi = fast_rcp(1.f + e), lo = e * hi;
@@ -428,7 +428,7 @@ __device__ __forceinline__ void put_sums(const SandwichBwdArgs& a, float* row, b
 // at fixed distances. ROWS: rows that a team takes together, two independent chains of
 // work for a warp and half the waits (T = 8192, K = 6144, 8-bit x and h: 93 us for 117).
 // PAIR: a row is the work of a cluster of two CTAs, half its columns each, whose sums meet in both CTAs'
-// shared memory (T = 2048, K = 16384: 88 us from bf16, 86 from 8 bits; four chunks a thread in one CTA spill, 110 and
+// shared memory (T = 2048, K = 16384: 92 us from bf16, 89 from 8 bits; four chunks a thread in one CTA spill, 110 and
 // 130).
 template <int GATE, int E8, int ROWS, int MAXT, bool PAIR>
 __global__ void __launch_bounds__(MAXT, 1)

@@ -824,7 +824,8 @@ def router_balance(logits: torch.Tensor, topk_ids: torch.Tensor, scoring: str = 
     that went to e) * (its tokens' mean p_e), 1 for an even routing; stats[0] is the mean over the
     sequences, stats[1] the mean over tokens of logsumexp(logits)^2. seq_offsets int32 [S + 1]: rows
     of sequence i are seq_offsets[i] up to seq_offsets[i + 1] (not decreasing), None: one of all rows.
-    Rows without an id in [0, E) (padding) or with every logit masked (NaN, -inf) do not count."""
+    Rows without an id in [0, E) (padding) or with every logit masked (NaN, -inf) do not count. p of a
+    row whose every sigmoid ``router_scored`` has as 0 (no logit above -88.7) is 0."""
     T, E, k, S, dev = _routing(logits, topk_ids, scoring, seq_offsets)
     device = logits.device
     stats = _empty(4, torch.float32, device, stream)
@@ -852,7 +853,9 @@ def router_backward(logits: torch.Tensor, topk_ids: torch.Tensor,
     """Gradient fp32 [T, E] of the logits: of ``router_scored``'s weights for the ids it chose, by
     grad_weights fp32 [T, topk], and of ``router_balance``'s two losses, by grad_losses fp32 [2] with
     that call's stats, slope and seq_offsets. Ids outside [0, E) and masked experts take no part;
-    rows without a valid id get zeros. scoring, renormalise and route_scale as in ``router_scored``."""
+    rows without a valid id get zeros. scoring, renormalise and route_scale as in ``router_scored``.
+    Renormalised weights have their gradient where the largest chosen score is not 0 in fp32, the others'
+    is 0 for scores below 2^-126."""
     T, E, k, S, dev = _routing(logits, topk_ids, scoring, seq_offsets)
     if grad_weights is None and grad_losses is None:
         raise ValueError("grad_weights or grad_losses is needed")
@@ -883,7 +886,7 @@ def combine_backward(grad_out: torch.Tensor, routes: torch.Tensor,
                      grad_routes: Optional[torch.Tensor] = None, stream=None):
     """Gradient of y_t = sum_j w_tj o_tj by its weights and its routes' outputs o, bf16 [T * topk, K]
     (``forward_window(per_route=True)``): (fp32 [T, topk], and with routes_too bf16 [T * topk, K],
-    else None). topk is topk_ids' or topk_weights' second size. Routes with a negative id, or
+    else None). The latter is for routes that come from something that trains: the MXFP4 experts have no gradient. topk is topk_ids' or topk_weights' second size. Routes with a negative id, or
     outside expert_base .. expert_base + n_experts - 1 when n_experts is not 0, are skipped: gradients
     0. topk_weights fp32 [T, topk] are needed with routes_too only. grad_routes may be given as an output
     that overlaps no input."""
