@@ -328,8 +328,8 @@ __device__ __forceinline__ void team_sum3(float (&v)[ROWS][3], float (*part)[32]
 // A sum as a value and its remainder, so that what cancels in the value is kept. The gradient of the residual's scale
 // adds up T K products of both signs: T = 777, K = 2880, magnitudes of 5000 that come to about 4. One fp32 value
 // a thread, a warp and a CTA left that off by 6.8e-7 in the median and 3.1e-6 at worst of 300 input sets, a
-// relative 2e-5 where little is left; with remainders 2.6e-7 and 1.2e-6, what the roundings of dh_total
-// itself come to (calls that ask for this gradient take 1 to 5% longer).
+// relative 2e-5 where little is left; with remainders 2.0e-7 and 0.9e-6, what the roundings of
+// dh + r2 v and of the row's mean come to (calls that ask for this gradient take 1 to 5% longer).
 struct Sum {
   float hi, lo;
   __device__ __forceinline__ void add(const Sum& v) {
@@ -437,8 +437,11 @@ __global__ void __launch_bounds__(MAXT, 1)
   __shared__ float part[2][3 * ROWS][32];
   __shared__ Sum last[32];
   using L = Slots<GATE, E8>;
-  // pre_gamma is in registers, the weights are in shared memory. A spilled register is dear
-  // here: beside the ring L1 is a few KB, so that it comes back from L2.
+  // pre_gamma is in registers, the weights are in shared memory as fp32; where registers are short and no
+  // channel's gate is in the weights, both gammas are there as bf16, the same bytes. A spilled register is dear
+  // here: beside the ring L1 is a few KB, so that it comes back from L2 (a full gate's sigmoid with 8-bit x and h,
+  // T = 4096, K = 7168: 124 us with 20 bytes spilled, 87 without; K = 16384: 159, 111).
+  constexpr bool kBf16 = GATE >= 2 || (GATE == 0 && (PAIR || E8 == 2));
   constexpr int CH = kSwChunks;
   const int nt = p.nt, team = threadIdx.x / nt, tid = threadIdx.x - team * nt;
   const int lane = tid & 31, warp = tid >> 5, warps = nt >> 5;
@@ -459,6 +462,7 @@ __global__ void __launch_bounds__(MAXT, 1)
   const int res0 = CH * L::size + lane16;
   float4* gch = reinterpret_cast<float4*>(smem);   // [2][chunks of a team]
   const int gch_half = CH * nt;
+  uint4* wbf = reinterpret_cast<uint4*>(smem);     // or [post_gamma, pre_gamma][chunks of a team]
   bool valid[CH];
   uint4 gn[CH];
 #pragma unroll
@@ -466,7 +470,11 @@ __global__ void __launch_bounds__(MAXT, 1)
     const int c = c0 + 32 * i;
     valid[i] = c < n8;
     gn[i] = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);   // 1
-    if (team == 0) {
+    if (kBf16 && team == 0) {
+      wbf[c] = valid[i] && has_post ? ld_row16(a.post + 8 * (b0 + c)) : gn[i];
+      wbf[gch_half + c] = valid[i] && has_dy ? ld_row16(a.pre + 8 * (b0 + c)) : gn[i];
+    }
+    if (!kBf16 && team == 0) {
       float g[8], w[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) g[j] = w[j] = 1.f;
@@ -479,13 +487,16 @@ __global__ void __launch_bounds__(MAXT, 1)
       gch[c] = make_float4(g[0], g[1], g[2], g[3]);
       gch[gch_half + c] = make_float4(g[4], g[5], g[6], g[7]);
     }
-    if (!valid[i]) continue;
-    if (has_dy) gn[i] = ld_row16(a.pre + 8 * (b0 + c));
+    if (!kBf16 && valid[i] && has_dy) gn[i] = ld_row16(a.pre + 8 * (b0 + c));
   }
   __syncthreads();
   if (PAIR) cluster_sync();   // the other CTA has begun: its shared memory may be written
   // post_gamma, times the channel's gate
   auto weight_of = [&](int i, float2 (&v)[4]) {
+    if (kBf16) {
+      unpack4(wbf[c0 + 32 * i], v);
+      return;
+    }
     const float4 w0 = gch[c0 + 32 * i], w1 = gch[gch_half + c0 + 32 * i];
     v[0] = make_float2(w0.x, w0.y);
     v[1] = make_float2(w0.z, w0.w);
@@ -549,9 +560,9 @@ __global__ void __launch_bounds__(MAXT, 1)
   float2 s_pre[CH][4], s_x[CH][4];
   // dscale = sum dh_total res, with q = dh + r2 v sum q res - c2 r2 sum h res. The first pass adds up both, so that
   // the rounding of dh_total stays out of it (the same for every value of an 8-bit code: T = 1151, K = 3008 off by
-  // 3.7e-7 for 7.2e-7). Full gates, mixed types and pairs leave the first pass no register for it (eight bytes
-  // spilled cost T = 4096, K = 2880 3 us of 42): the second adds up dh_total res, with a full gate a chunk's sums into one.
-  constexpr bool kFull = GATE >= 2, kFirst = !kFull && !PAIR && E8 != 2;
+  // 3.7e-7 for 7.2e-7). Channel gates of pairs and of mixed types and sigmoids of pairs leave it no
+  // register for that: the second pass adds up dh_total res.
+  constexpr bool kFirst = PAIR ? GATE == 0 || GATE == 2 : GATE != 1 || E8 != 2;
   float2 s_res = dup(0.f);
   Sum s_all = {0.f, 0.f};
 #pragma unroll
@@ -590,7 +601,7 @@ __global__ void __launch_bounds__(MAXT, 1)
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       float2 g[4], w0[4];
-      unpack4(gn[i], g);
+      unpack4(kBf16 ? wbf[gch_half + c0 + 32 * i] : gn[i], g);
       weight_of(i, w0);
 #pragma unroll
       for (int r = 0; r < ROWS; ++r) {
@@ -689,16 +700,10 @@ __global__ void __launch_bounds__(MAXT, 1)
         for (int j = 0; j < 4; ++j) d[j] = __ffma2_rn(dup(kh[r]), __fmul2_rn(h[j], hr2), d[j]);
         if (!kFirst && has_res) {
           unpack4(*reinterpret_cast<const uint4*>(slot + r * p.row + res0 + 512 * i), v);
-          float2 e = dup(0.f), to = kFull ? dup(0.f) : s_res;
+          float2 e = dup(0.f);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) add_product(to, e, d[j], v[j]);
-          if (kFull) {
-            s_all.add(Sum{to.x, e.x});
-            s_all.add(Sum{to.y, e.y});
-          } else {
-            s_res = to;
-            s_all.lo += e.x + e.y;
-          }
+          for (int j = 0; j < 4; ++j) add_product(s_res, e, d[j], v[j]);
+          s_all.lo += e.x + e.y;
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] = __fmul2_rn(d[j], dup(scale));
@@ -758,10 +763,8 @@ __global__ void __launch_bounds__(MAXT, 1)
   }
   if (has_res) {
     Sum sr = s_all;
-    if (!kFull) {
-      sr.add(Sum{s_res.x, 0.f});
-      sr.add(Sum{s_res.y, 0.f});
-    }
+    sr.add(Sum{s_res.x, 0.f});
+    sr.add(Sum{s_res.y, 0.f});
     sr.add_lanes();
     if (lane == 0) last[threadIdx.x >> 5] = sr;
   }
