@@ -13,7 +13,7 @@ __device__ __forceinline__ uint32_t bf16x2_rn(float lo, float hi) {
 }
 
 // exp(v) and 1 / v by the hardware's approximations (2^-22 and 1 ulp; the exponent's rounding adds
-// |v| 2^-24), results below 2^-126 as 0: without the steps that the functions of the same
+// |v| 2^-24 and the constant's |v| 2^-26), results below 2^-126 as 0: without the steps that the functions of the same
 // precision take for those. exp(-inf) = 0, 1 / inf = 0; v of fast_rcp is not subnormal.
 __device__ __forceinline__ float fast_exp(float v) {
   float r;
